@@ -9,6 +9,7 @@ no method arithmetic; the tests hand those inputs to the oracle.
 
 Modules:
   attend  -- attention over contiguous latent rows (and over listed rows) in fp64 (C, via ctypes)
+  blocks  -- mean rows and scores of 64-row blocks, and attention over a list of them
   fp8     -- E4M3 codes from their bit fields, per-row quantization and dequantization
   paged   -- expected pool images after appends and kept-state copies
   plan    -- the kv_pool plan arithmetic in integers

@@ -88,6 +88,16 @@ _SIGS = {
     "tf_paged_mla_plan_info": (ctypes.c_int, [_I32, _I32, _I32, _P, _I32, _I32, _P, _P, _P]),
     "tf_topk_workspace_bytes": (_SZ, [_I64, _I64, _I32]),
     "tf_topk_blocked": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _I32, _P, _P, _P, _SZ, _P]),
+    "tf_block_keys_bytes": (_SZ, [_P]),
+    "tf_block_keys_update": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _P, _I32, _P, _P]),
+    "tf_block_scores": (ctypes.c_int, [_P, _P, _P, _I32, _P, _I32, _I32, _I32, _P, _P, _F, _I32, _I32, _P, _I64, _P,
+                                       _P]),
+    "tf_paged_mla_blocks_workspace_bytes": (_SZ, [_P, _I32, _I32, _I32, _P, _I32]),
+    "tf_paged_mla_attend_blocks": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _P, _F, _P, _P,
+                                                  _P, _SZ, _P]),
+    "tf_paged_mla_shared_workspace_bytes": (_SZ, [_P, _I32, _I32, _I32, _P, _P, _I32, _P]),
+    "tf_paged_mla_attend_shared": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _P, _I32, _P, _I32, _I32, _I32, _P, _F, _P,
+                                                  _P, _P, _SZ, _P]),
     "tf_profile_enable": (ctypes.c_int, [_P, _I32]),
     "tf_profile_read": (ctypes.c_int, [_P, _I32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_I64)]),
 }
@@ -340,6 +350,102 @@ def tf_topk_blocked(logits, k: int, idx, val, lens=None, n: int | None = None, w
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check(lib().tf_topk_blocked(_ptr(logits), rows, n, ld, _ptr(lens), int(k), _ptr(idx), _ptr(val), _ptr(ws),
                                  ws_bytes, _stream(stream)), "tf_topk_blocked")
+
+
+TF_BLOCK_ROWS = 64
+
+
+def _given(what: str, ok: bool) -> None:
+    """Refuse what the library cannot see: host arrays of another length, tensors of another type or layout."""
+    if not ok:
+        raise TFError(TF_E_ARG, what)
+
+
+def _dense(t, dtype: str, shape=None) -> bool:
+    return t is None or (str(t.dtype) == dtype and t.is_contiguous() and (shape is None or tuple(t.shape) == shape))
+
+
+def _qout(q, out, lse) -> bool:
+    lead = tuple(q.shape[:3])
+    return (q.dim() == 4 and q.shape[3] == 576 and _dense(q, "torch.bfloat16") and
+            _dense(out, "torch.bfloat16", lead + (512,)) and _dense(lse, "torch.float32", lead))
+
+
+def tf_block_keys_bytes(pool: KVPool) -> int:
+    """Bytes of one cache's block keys: bf16 [pages][8][576]."""
+    return int(lib().tf_block_keys_bytes(pool.handle))
+
+
+def tf_block_keys_update(pool: KVPool, cache: int, pt, max_pages: int, start, lens, bkeys, stream=None) -> None:
+    """Average again every 64-row block of each stream s that holds rows of [start[s], lens[s]); bkeys: bf16 CUDA
+    tensor [pages][8][576]."""
+    a, p = _i64(start)
+    b, pl = _i64(lens)
+    _given("tf_block_keys_update", len(a) == len(b) and (pt is None or pt.shape[0] >= len(b)) and
+           _dense(bkeys, "torch.bfloat16", (pool.num_pages, 8, 576)))
+    _check(lib().tf_block_keys_update(pool.handle, cache, _ptr(pt), max_pages, p, pl, len(b), _ptr(bkeys),
+                                      _stream(stream)), "tf_block_keys_update")
+
+
+def tf_block_scores(pool: KVPool, bkeys, pt, max_pages: int, lens, q, scale: float, scores, w=None, nblk=None,
+                    sink: int = 1, local: int = 1, stream=None) -> None:
+    """q: bf16 [S][R][H][576]; w: fp32 [S][R][H] or None (ones); scores: fp32 [S * R][ld] (row stride ld, a multiple
+    of 4, at least the longest stream's blocks); nblk: int32 [S * R] or None, each row's visible blocks."""
+    S, R, H = int(q.shape[0]), int(q.shape[1]), int(q.shape[2])
+    a, p = _i64(lens)
+    _given("tf_block_scores", len(a) == S and _dense(q, "torch.bfloat16") and _dense(w, "torch.float32", (S, R, H)) and
+           _dense(bkeys, "torch.bfloat16", (pool.num_pages, 8, 576)) and str(scores.dtype) == "torch.float32" and
+           scores.dim() == 2 and scores.shape[0] == S * R and scores.stride(1) == 1 and
+           scores.shape[1] >= -(-int(a.max()) // TF_BLOCK_ROWS) and
+           (nblk is None or (_dense(nblk, "torch.int32") and nblk.numel() == S * R)))
+    _check(lib().tf_block_scores(pool.handle, _ptr(bkeys), _ptr(pt), max_pages, p, S, R, H, _ptr(q), _ptr(w),
+                                 float(scale), int(sink), int(local), _ptr(scores), int(scores.stride(0)), _ptr(nblk),
+                                 _stream(stream)), "tf_block_scores")
+
+
+def tf_paged_mla_blocks_workspace_bytes(pool, S: int, R: int, H: int, lens, max_blk: int) -> int:
+    a, p = _i64(lens)
+    _given("tf_paged_mla_blocks_workspace_bytes", len(a) == S)
+    return int(lib().tf_paged_mla_blocks_workspace_bytes(pool.handle if pool is not None else None, S, R, H, p,
+                                                         int(max_blk)))
+
+
+def tf_paged_mla_attend_blocks(pool: KVPool, cache: int, pt, max_pages: int, lens, blk, q, scale: float, out,
+                               lse=None, ws=None, stream=None) -> None:
+    """blk: int32 CUDA tensor [S][R][max_blk] (or [S * R][max_blk]) of block numbers, -1 for none; q, out, lse, ws
+    as in tf_paged_mla_attend."""
+    S, R, H = int(q.shape[0]), int(q.shape[1]), int(q.shape[2])
+    a, p = _i64(lens)
+    _given("tf_paged_mla_attend_blocks", len(a) == S and _qout(q, out, lse) and _dense(blk, "torch.int32") and
+           blk.numel() == S * R * int(blk.shape[-1]))
+    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(lib().tf_paged_mla_attend_blocks(pool.handle, cache, _ptr(pt), max_pages, p, _ptr(blk), int(blk.shape[-1]),
+                                            S, R, H, _ptr(q), float(scale), _ptr(out), _ptr(lse), _ptr(ws), ws_bytes,
+                                            _stream(stream)), "tf_paged_mla_attend_blocks")
+
+
+def tf_paged_mla_shared_workspace_bytes(pool, S: int, R: int, H: int, lens, group_sizes, prefixes) -> int:
+    a, p = _i64(lens)
+    g, pg = _i32(group_sizes)
+    f, pf = _i64(prefixes)
+    _given("tf_paged_mla_shared_workspace_bytes", len(a) == S and len(g) == len(f))
+    return int(lib().tf_paged_mla_shared_workspace_bytes(pool.handle if pool is not None else None, S, R, H, p, pg,
+                                                         len(g), pf))
+
+
+def tf_paged_mla_attend_shared(pool: KVPool, cache: int, pt, max_pages: int, lens, group_sizes, prefixes, q,
+                               scale: float, out, lse=None, ws=None, stream=None) -> None:
+    """group_sizes: streams of each group, in order; prefixes: the rows each group's streams have in common; the rest
+    as in tf_paged_mla_attend."""
+    S, R, H = int(q.shape[0]), int(q.shape[1]), int(q.shape[2])
+    a, p = _i64(lens)
+    g, pg = _i32(group_sizes)
+    f, pf = _i64(prefixes)
+    _given("tf_paged_mla_attend_shared", len(a) == S and len(g) == len(f) and _qout(q, out, lse))
+    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(lib().tf_paged_mla_attend_shared(pool.handle, cache, _ptr(pt), max_pages, p, pg, len(g), pf, S, R, H,
+                                            _ptr(q), float(scale), _ptr(out), _ptr(lse), _ptr(ws), ws_bytes,
+                                            _stream(stream)), "tf_paged_mla_attend_shared")
 
 
 def tf_paged_mla_plan_info(S: int, R: int, H: int, lens, sms: int = 0, invariant: bool = False) -> dict:

@@ -49,6 +49,7 @@
 #include <memory>
 #include <mutex>
 #include <numeric>
+#include <type_traits>
 
 #include "ptx.cuh"
 #include "tf_internal.h"
@@ -171,9 +172,20 @@ static_assert(SMEM_TOTAL <= 232448, "shared memory budget");
 //    result has the same bits whatever else is in the batch.
 //  - SPARSE (tf_paged_mla_attend_sparse).  RANGES over the tiles of each stream's list
 //    of rows; the key tiles are gathered row by row (TMA gather4) through the table.
-enum { MODE_RANGES = 0, MODE_UNITS = 1, MODE_SPLITS = 2, MODE_SPARSE = 3 };
+//  - BLOCKS (tf_paged_mla_attend_blocks).  A unit is a query row's group of at most 64 heads and
+//    its tiles are the row's listed 64-row blocks, one TMA tile each, numbered and cut like UNITS
+//    but anywhere: rows choose blocks on their own, so there are no common positions to keep.
+//  - SHARED (tf_paged_mla_attend_shared).  Entries instead of streams: one for each stream's own
+//    rows and one for each group's shared rows, whose columns are the (stream, row, head) columns
+//    of the whole group one after another, so a tile of shared rows is loaded once for 64 of them
+//    whatever stream they belong to.  A column's partials over both are merged.
+enum { MODE_RANGES = 0, MODE_UNITS = 1, MODE_SPLITS = 2, MODE_SPARSE = 3, MODE_BLOCKS = 4, MODE_SHARED = 5 };
+// the modes whose segments carry their own columns
+__host__ __device__ constexpr bool own_cols(int mode) { return mode == MODE_BLOCKS || mode == MODE_SHARED; }
 
-// One entry per stream, in the caller's order.
+// One entry per stream, in the caller's order.  SHARED: entry s is stream s's own rows (keys from
+// the shared ones on), entries S and up the groups' shared rows; the fields then hold what
+// SharedEntry names.
 struct StreamPlan {
     int64_t len;
     int64_t toff;     // RANGES: first numbered key tile of the stream
@@ -185,13 +197,27 @@ struct StreamPlan {
     int32_t pad;
 };
 
+// SHARED: the fields of an entry, by the names they have there.
+struct SharedEntry {
+    int64_t len;      // end of the entry's keys
+    int64_t alone;    // 1: its columns have no other entry
+    int32_t nt;       // key tiles (0: the stream has no rows of its own)
+    int32_t tile0;    // first key tile
+    int32_t ncols;    // columns
+    int32_t unit0;    // first unit (64 columns each)
+    int32_t col0;     // first column of the batch, numbered (stream, row, head)
+    int32_t row;      // the page table's row
+};
+static_assert(sizeof(SharedEntry) == sizeof(StreamPlan), "entries take the streams' place");
+
 struct Params {
     CUtensorMap tm_lat;   // 4D {512, 512 rows, pages, caches}, box {64, 64, 1, 1}
     CUtensorMap tm_rope;  // 4D {64, 512 rows, pages, caches}, box {64, 64, 1, 1}
     CUtensorMap tm_q;     // 2D {576, S*R*H}, box {64, 64}
     CUtensorMap tm_lat_rows;    // SPARSE: 2D {512, pool rows}, 1,024-byte rows (576 a page), box {64, 1}
     CUtensorMap tm_rope_rows;   // SPARSE: 2D {64, pool rows}, 128-byte rows (4,608 a page), box {64, 1}
-    const int32_t *idx;         // SPARSE: [S][max_idx] row numbers of each stream's listed keys
+    const int32_t *idx;         // SPARSE: [S][max_idx] row numbers of each stream's listed keys;
+                                // BLOCKS: [S][R][max_idx] block numbers of each row
     int32_t max_idx;
     const int32_t *pt;
     const __nv_bfloat16 *q;     // [S*R*H][576]: the TMEM part of each column group is read from here
@@ -207,10 +233,21 @@ struct Params {
     int32_t mode;
     int32_t nranges;      // RANGES: ranges of the numbering
     int32_t rep;          // RANGES: CTAs a range (the column groups)
+    int32_t nent;         // SHARED: entries
     int64_t rb[MAX_CTAS + 1];        // RANGES: range i is tiles [rb[i], rb[i+1]); UNITS: positions
-    StreamPlan st[TF_MAX_STREAMS];
-    int16_t order[TF_MAX_STREAMS];   // SPLITS: launch order (streams with longer splits first)
+    union {
+        StreamPlan st[TF_MAX_STREAMS];
+        SharedEntry se[TF_MAX_STREAMS];
+    };
+    int16_t order[TF_MAX_STREAMS];   // SPLITS: launch order (streams with longer splits first);
+                                     // SHARED: the stream's entry of shared rows, or -1
 };
+
+// BLOCKS: blocks a query row at position pos takes from its list: no more than it can see
+__host__ __device__ __forceinline__ int64_t row_blocks(int64_t pos, int max_blk) {
+    const int64_t seen = pos / BK + 1;
+    return seen < max_blk ? seen : max_blk;
+}
 
 // UNITS: keys unit (stream of `len` keys, column group g) reads, up to the last key its last
 // column sees (the R rows are the stream's last R positions; column c is row c / H).  len >= R.
@@ -238,7 +275,27 @@ struct Seg {
     int slot;          // workspace slot of a partial result; -1: the segment is its whole unit
     int64_t kb, ke;    // keys [kb, ke)
     int64_t len;
+    // BLOCKS and SHARED
+    int64_t gcol;           // first of the segment's columns among the batch's S * R * H
+    int nc;                 // its columns
+    int row;                // the page table's row
+    bool causal;            // SHARED: own rows (shared ones are visible to every column)
+    int64_t pos;            // BLOCKS: the query row's position
+    const int32_t *list;    // BLOCKS: the segment's part of the row's list
 };
+template <int MODE>
+__device__ __forceinline__ int64_t seg_gcol(const Seg &q, int ncols_all) {
+    return own_cols(MODE) ? q.gcol : (int64_t)q.s * ncols_all + q.g * NCOL;
+}
+// the segment's columns (the older modes: those left from its first on, 64 of which it takes)
+template <int MODE>
+__device__ __forceinline__ int seg_cols(const Seg &q, int ncols_all) {
+    return own_cols(MODE) ? q.nc : ncols_all - q.g * NCOL;
+}
+template <int MODE>
+__device__ __forceinline__ int seg_row(const Seg &q) {
+    return own_cols(MODE) ? q.row : q.s;
+}
 
 __device__ __forceinline__ Seg seg_at(const Params &p, int64_t x, int64_t x0, int64_t x1) {
     int lo = 0, hi = p.S - 1;
@@ -272,7 +329,7 @@ struct SegIter {
     int64_t x, x0, x1;
     int k;
     __device__ __forceinline__ explicit SegIter(const Params &p) : x(0), x0(0), x1(0), k(0) {
-        if (MODE == MODE_RANGES || MODE == MODE_SPARSE || MODE == MODE_UNITS) {
+        if (MODE != MODE_SPLITS) {
             const int range = (int)blockIdx.x / p.rep;
             x0 = p.rb[range];
             x1 = p.rb[range + 1];
@@ -281,7 +338,7 @@ struct SegIter {
     }
     // after next() returned a segment: is it this CTA's last?
     __device__ __forceinline__ bool last(const Params &p) const {
-        if (MODE == MODE_RANGES || MODE == MODE_SPARSE || MODE == MODE_UNITS) return x >= x1;
+        if (MODE != MODE_SPLITS) return x >= x1;
         return true;
     }
     __device__ __forceinline__ bool next(const Params &p, Seg &q) {
@@ -307,6 +364,54 @@ struct SegIter {
             q.slot = (t == 0 && te == nt) ? -1 : 2 * (int)blockIdx.x + (k == 0 ? 0 : 1);
             ++k;
             x = te == nt ? unit_pos(u + 1, 0) : unit_pos(u, te);
+            return true;
+        }
+        if (MODE == MODE_BLOCKS) {
+            if (x >= x1) return false;
+            const int64_t u = x >> 32, t = x & 0xffffffffll;
+            const int hg = (p.H + NCOL - 1) / NCOL;   // head groups a query row; p.groups = R * hg
+            q.s = (int)(u / p.groups);
+            q.g = (int)(u - (int64_t)q.s * p.groups);
+            const int r = q.g / hg, h0 = (q.g - r * hg) * NCOL;
+            q.len = p.st[q.s].len;
+            q.pos = q.len - p.R + r;
+            q.row = q.s;
+            q.gcol = (int64_t)q.s * p.ncols + r * p.H + h0;
+            q.nc = min(NCOL, p.H - h0);
+            const int64_t nt = row_blocks(q.pos, p.max_idx);
+            const int64_t te = (x1 >> 32) == u ? (x1 & 0xffffffffll) : nt;
+            q.nt = (int)(te - t);
+            q.list = p.idx + ((int64_t)q.s * p.R + r) * p.max_idx + t;
+            q.slot = (t == 0 && te == nt) ? -1 : 2 * (int)blockIdx.x + (k == 0 ? 0 : 1);
+            ++k;
+            x = te == nt ? unit_pos(u + 1, 0) : unit_pos(u, te);
+            return true;
+        }
+        if (MODE == MODE_SHARED) {
+            if (x >= x1) return false;
+            const int64_t u = x >> 32, t = x & 0xffffffffll;
+            // the last entry whose first unit is not after u (entries without units share the
+            // next one's first unit and come before it)
+            int lo = 0, hi = p.nent - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (p.se[mid].unit0 <= u) lo = mid; else hi = mid - 1;
+            }
+            const SharedEntry &e = p.se[lo];
+            q.g = (int)(u - e.unit0);
+            q.causal = lo < p.S;
+            q.row = e.row;
+            q.len = e.len;
+            q.gcol = (int64_t)e.col0 + q.g * NCOL;
+            q.nc = min(NCOL, e.ncols - q.g * NCOL);
+            const int64_t te = (x1 >> 32) == u ? (x1 & 0xffffffffll) : e.nt;
+            q.nt = (int)(te - t);
+            q.kb = ((int64_t)e.tile0 + t) * BK;
+            q.ke = min(e.len, ((int64_t)e.tile0 + te) * BK);
+            // every segment of a CTA can be a partial: unit + CTA numbers them without gaps or
+            // repeats (of two segments the later one has the larger unit, CTA or both)
+            q.slot = e.alone && t == 0 && te == e.nt ? -1 : (int)u + (int)blockIdx.x;
+            x = te == e.nt ? unit_pos(u + 1, 0) : unit_pos(u, te);
             return true;
         }
         // SPLITS: one item a CTA
@@ -629,7 +734,7 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
             ptx::prefetch_tmap(&p.tm_q);
             // a key tile read by one column group streams through L2; tiles that other
             // groups of the same stream read too are kept
-            const uint64_t pol_kv = ngroups > 2 ? ptx::policy_evict_last() : ptx::policy_evict_first();
+            uint64_t pol_kv = ngroups > 2 ? ptx::policy_evict_last() : ptx::policy_evict_first();
             const uint64_t pol_q = ptx::policy_evict_last();
             int gt = 0, si = 0;
             SegIter<MODE> it(p);
@@ -638,18 +743,53 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
                 // the queries' shared-memory boxes are reloaded once the previous segment's QK^T has read them
                 if (si > 0 && !ptx::mbar_wait(&c.q_free, (si - 1) & 1, abort, errp, 15)) break;
                 ptx::mbar_arrive_expect_tx(&c.q_full, Q_SMEM_BOXES * QBOX_BYTES);
-                const int qrow = q.s * R_ * H_ + q.g * NCOL;
+                const int qrow = own_cols(MODE) ? (int)q.gcol : q.s * R_ * H_ + q.g * NCOL;
+                const int trow = seg_row<MODE>(q);
+                // SHARED: the group's other columns read the shared rows too
+                if (MODE == MODE_SHARED) pol_kv = q.causal ? ptx::policy_evict_first() : ptx::policy_evict_last();
                 for (int b = 0; b < Q_SMEM_BOXES; ++b)
                     ptx::tma_load_2d(smem + SMEM_Q + b * QBOX_BYTES, &p.tm_q, &c.q_full, (Q_TMEM_BOXES + b) * 64, qrow,
                                      pol_q);
                 q_armed = si;
                 int cur_lp = -1, page = 0;
+                // BLOCKS: the list entries run two tiles and their pages one tile ahead of the
+                // copies, so that these dependent loads do not delay a tile
+                int bc = 0, bn = 0, bnn = 0, pgn = 0;
+                auto block_page = [&](int b) -> int {
+                    if (b < 0 || (int64_t)b * BK >= q.len) return 0;
+                    const int lp = b >> 3;
+                    return windowed ? trow * max_pages + lp : __ldg(pt + (int64_t)trow * max_pages + lp);
+                };
+                if (MODE == MODE_BLOCKS) {
+                    bn = __ldg(q.list);
+                    bnn = q.nt > 1 ? __ldg(q.list + 1) : 0;
+                    pgn = block_page(bn);
+                }
                 for (int tl = 0; tl < q.nt; ++tl, ++gt) {
                     const int rs = rope_slot(gt);
-                    const int64_t k0 = q.kb + (int64_t)tl * BK;
+                    int64_t k0 = q.kb + (int64_t)tl * BK;
+                    int pg_blk = 0;
+                    if (MODE == MODE_BLOCKS) {
+                        bc = bn;
+                        pg_blk = pgn;
+                        bn = bnn;
+                        bnn = tl + 2 < q.nt ? __ldg(q.list + tl + 2) : 0;
+                        pgn = tl + 1 < q.nt ? block_page(bn) : 0;
+                        if (bc < -1 || (int64_t)bc * BK >= q.len) {
+                            ptx::record_error(errp, TF_E_DEVICE, bc);
+                            *abort = 1;
+                            stop = true;
+                            break;
+                        }
+                        // -1: no block.  Any tile will do (QK^T's issuer zeroes all its rows).
+                        k0 = bc < 0 ? 0 : (int64_t)bc * BK;
+                        cur_lp = -1;
+                    }
                     const int lp = (int)(k0 >> 9), row = (int)(k0 & 511);
                     if (lp != cur_lp) {
-                        const int raw = windowed ? q.s * max_pages + lp : __ldg(pt + (int64_t)q.s * max_pages + lp);
+                        const int raw = MODE == MODE_BLOCKS ? pg_blk
+                                        : windowed          ? trow * max_pages + lp
+                                                            : __ldg(pt + (int64_t)trow * max_pages + lp);
                         cur_lp = lp;
                         if (raw < 0 || raw >= num_pages) {
                             ptx::record_error(errp, TF_E_DEVICE, raw);
@@ -726,15 +866,15 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
         // QK^T of global tile tq (tile tl of segment q): S[64 columns][64 keys] (M = 64: rows
         // 16w..16w+15 in lanes 0-15 of TMEM quadrant w; buffer tq % 2).  Box order: rope (queries'
         // rope box in shared memory), latent pairs 0-1 (queries in TMEM), pairs 2-3 (shared memory).
-        auto qk_tile = [&](int tq, int tl, const Seg &q) -> bool {
+        // rem: the tile's rows that the stream holds (64 or more: all).
+        auto qk_tile = [&](int tq, int tl, const Seg &q, int64_t rem) -> bool {
             const int rs = rope_slot(tq);
             // the tile's S buffer has been read out (by the softmax of tile tq - 2)
             if (tq >= 2 && !ptx::mbar_wait_warp(&c.s_free[tq & 1], ((tq - 2) >> 1) & 1, abort, errp, 4)) return false;
-            const int64_t rem = q.len - (q.kb + (int64_t)tl * BK);
             // rows past the stream's end may hold NaN poison: zero them in latent boxes [b0, b1) and
             // the rope box, so that P = 0 times V stays 0 in the PV contraction
             auto zero_box = [&](int b) {
-                const int valid = (int)rem;
+                const int valid = MODE == MODE_BLOCKS && rem < 0 ? 0 : (int)rem;
                 uint4 *bx = reinterpret_cast<uint4 *>(smem + box_off(tq, b));
                 for (int k = lane; k < (BK - valid) * 8; k += 32) bx[valid * 8 + k] = make_uint4(0, 0, 0, 0);
             };
@@ -812,12 +952,22 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
         SegIter<MODE> it(p);
         Seg q;
         for (; ok && it.next(p, q); ++si) {
-            const int ncols = min(NCOL, ncols_all - q.g * NCOL);
+            const int ncols = min(NCOL, seg_cols<MODE>(q, ncols_all));
             const uint32_t idesc_pv = ptx::idesc_bf16_f32(128, (ncols + 15) & ~15, true, false);
             if (qk_role) {
                 ok = ptx::mbar_wait_warp(&c.q_full, si & 1, abort, errp, 2) &&
                      ptx::mbar_wait_warp(&c.q_tmem_full, si & 1, abort, errp, 2);
-                for (int tl = 0; ok && tl < q.nt; ++tl) ok = qk_tile(gt + tl, tl, q);
+                int bn = MODE == MODE_BLOCKS ? __ldg(q.list) : 0;   // the next tile's block
+                for (int tl = 0; ok && tl < q.nt; ++tl) {
+                    int64_t rem;
+                    if (MODE == MODE_BLOCKS) {
+                        rem = bn < 0 ? 0 : q.len - (int64_t)bn * BK;
+                        bn = tl + 1 < q.nt ? __ldg(q.list + tl + 1) : 0;
+                    } else {
+                        rem = q.len - (q.kb + (int64_t)tl * BK);
+                    }
+                    ok = qk_tile(gt + tl, tl, q, rem);
+                }
             } else {
                 for (int tl = 0; ok && tl < q.nt; ++tl) ok = pv_tile(gt + tl, tl, idesc_pv);
             }
@@ -1018,14 +1168,15 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
         Seg q;
         for (; ok && it.next(p, q); ++si) {
             const int col0 = q.g * NCOL;
-            const int ncols = ncols_all - col0;
+            const int ncols = seg_cols<MODE>(q, ncols_all);
+            const int64_t gcol = seg_gcol<MODE>(q, ncols_all);
             {
                 // The segment's queries, latent values 0-255, into TMEM (A of QK^T): lane i < 16 of
                 // this quadrant holds column 16 q4 + i.  Every QK^T of the previous segment has
                 // completed: this warp has seen its last S.
                 const int m = 16 * q4 + (lane & 15);
                 const bool live = lane < 16 && m < ncols;
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + ((size_t)q.s * ncols_all + col0 + (live ? m : 0)) * kDk);
+                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (size_t)(gcol + (live ? m : 0)) * kDk);
 #pragma unroll 1
                 for (int c2 = 0; c2 < Q_TMEM_BOXES; c2 += 2) {
                     uint32_t v[2][32];
@@ -1049,13 +1200,23 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
             }
             const bool act0 = r0 < ncols, act1 = r1 < ncols;
             // last visible key of each row's column
-            const int64_t pos0 = q.len - R_ + (act0 ? (col0 + r0) / H_ : 0);
-            const int64_t pos1 = q.len - R_ + (act1 ? (col0 + r1) / H_ : 0);
+            const bool all_seen = MODE == MODE_SHARED && !q.causal;
+            const int64_t pos0 = MODE == MODE_BLOCKS ? q.pos
+                                 : all_seen          ? q.len - 1
+                                                     : q.len - R_ + (act0 ? (col0 + r0) / H_ : 0);
+            const int64_t pos1 = MODE == MODE_BLOCKS ? q.pos
+                                 : all_seen          ? q.len - 1
+                                                     : q.len - R_ + (act1 ? (col0 + r1) / H_ : 0);
+            int bn = MODE == MODE_BLOCKS ? __ldg(q.list) : 0;   // the next tile's block
             float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
             for (int tl = 0; tl < q.nt; ++tl) {
                 const int t = gt + tl;
                 const int rs = rope_slot(t);
-                const int64_t k0 = q.kb + (int64_t)tl * BK;
+                int64_t k0 = q.kb + (int64_t)tl * BK;
+                if (MODE == MODE_BLOCKS) {
+                    k0 = bn < 0 ? q.len : (int64_t)bn * BK;   // -1: no key is visible
+                    bn = tl + 1 < q.nt ? __ldg(q.list + tl + 1) : 0;
+                }
                 if (!ptx::mbar_wait_warp(&c.s_full[t & 1], (t >> 1) & 1, abort, errp, 7)) {
                     ok = false;
                     break;
@@ -1070,8 +1231,9 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
                 // keys outside a row's range become -inf; the maximum is taken before
                 // scaling (the scale is positive) and the scale is folded into the
                 // exponent's FFMA: p = 2^(s * scale*log2(e) - m_ref)
-                const int64_t lim0 = (pos0 + 1 < q.ke ? pos0 + 1 : q.ke) - k0;
-                const int64_t lim1 = (pos1 + 1 < q.ke ? pos1 + 1 : q.ke) - k0;
+                const int64_t kend = MODE == MODE_BLOCKS ? q.len : q.ke;
+                const int64_t lim0 = (pos0 + 1 < kend ? pos0 + 1 : kend) - k0;
+                const int64_t lim1 = (pos1 + 1 < kend ? pos1 + 1 : kend) - k0;
                 const int nv0 = act0 ? (lim0 < 0 ? 0 : (lim0 > BK ? BK : (int)lim0)) : 0;
                 const int nv1 = act1 ? (lim1 < 0 ? 0 : (lim1 > BK ? BK : (int)lim1)) : 0;
                 float x0[16], x1[16];
@@ -1168,7 +1330,7 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
                     const float m = h ? m1 : m0, l = h ? l1 : l0;
                     if (!(h ? act1 : act0)) continue;
                     if (q.slot < 0) {
-                        if (lsep) lsep[(size_t)q.s * ncols_all + col0 + rr] = (m + log2f(l)) * 0.69314718055994531f;
+                        if (lsep) lsep[(size_t)gcol + rr] = (m + log2f(l)) * 0.69314718055994531f;
                     } else {
                         ws_ml[((size_t)q.slot * NCOL + rr) * 2 + 0] = m;
                         ws_ml[((size_t)q.slot * NCOL + rr) * 2 + 1] = l;
@@ -1188,8 +1350,7 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
         SegIter<MODE> it(p);
         Seg q;
         for (; ok && it.next(p, q); ++si) {
-            const int col0 = q.g * NCOL;
-            const int ncols = min(NCOL, ncols_all - col0);
+            const int ncols = min(NCOL, seg_cols<MODE>(q, ncols_all));
             const int npv = (ncols + 15) & ~15;
             for (int tl = 0; tl < q.nt; ++tl) {
                 const int t = gt + tl;
@@ -1276,7 +1437,7 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
                             if (col >= ncols) continue;
                             const float o = __uint_as_float(v[k]);
                             if (q.slot < 0) {
-                                const size_t orow = (size_t)q.s * ncols_all + col0 + col;
+                                const size_t orow = (size_t)seg_gcol<MODE>(q, ncols_all) + col;
                                 outp[orow * kLat + dim] = __float2bfloat16_rn(o * inv_l[col]);
                             } else {
                                 ws_o[((size_t)q.slot * NCOL + col) * kLat + dim] = o;
@@ -1320,13 +1481,15 @@ constexpr int COMBINE_NARROW_MAX = 8;   // partials a unit that form takes
 // key order: slot_of(j) for j < n.  False: nothing to merge (the unit is whole).
 struct CombineUnit {
     int s, g, c0, n, first_slot, rg;
+    int col0, nc;   // the unit's first column in its stream, and its columns
     bool ranges;
-    __device__ __forceinline__ int slot_of(const Params &p, int j) const {
-        return j == 0 ? first_slot : ranges ? 2 * ((c0 + j) * p.rep + rg) : first_slot + j;
+    // the slot of partial j, times the slot's columns, plus column col's place in it
+    __device__ __forceinline__ size_t place(const Params &p, int j, int col) const {
+        return (size_t)(j == 0 ? first_slot : ranges ? 2 * ((c0 + j) * p.rep + rg) : first_slot + j) * NCOL + col;
     }
 };
 __device__ __forceinline__ bool combine_unit(const Params &p, CombineUnit &cu) {
-    if (p.mode == MODE_UNITS) {
+    if (p.mode == MODE_UNITS || p.mode == MODE_BLOCKS) {
         const int64_t x = p.rb[blockIdx.y + 1], xp = p.rb[blockIdx.y];
         const int64_t u = x >> 32;
         if ((x & 0xffffffffll) == 0 || ((xp >> 32) == u && (xp & 0xffffffffll) != 0)) return false;
@@ -1338,6 +1501,8 @@ __device__ __forceinline__ bool combine_unit(const Params &p, CombineUnit &cu) {
     }
     const StreamPlan &sp = p.st[cu.s];
     int c1;
+    cu.col0 = cu.g * NCOL;
+    cu.nc = min(NCOL, p.ncols - cu.col0);
     cu.rg = cu.g;
     if (p.mode == MODE_RANGES || p.mode == MODE_SPARSE) {
         // the ranges that hold the unit; their CTAs' partial slots
@@ -1345,10 +1510,19 @@ __device__ __forceinline__ bool combine_unit(const Params &p, CombineUnit &cu) {
         cu.c0 = range_of(p, ub);
         c1 = range_of(p, ue - 1);
         cu.first_slot = 2 * (cu.c0 * p.rep + cu.g) + (ub == p.rb[cu.c0] ? 0 : 1);
-    } else if (p.mode == MODE_UNITS) {
+    } else if (p.mode == MODE_UNITS || p.mode == MODE_BLOCKS) {
         // the same over positions (unit, tile), one CTA a range
         const int64_t u = (int64_t)cu.s * p.groups + cu.g;
-        const int64_t nt = (unit_keys(sp.len, p.R, p.H, p.ncols, cu.g) + BK - 1) / BK;
+        int64_t nt;
+        if (p.mode == MODE_BLOCKS) {
+            const int hg = (p.H + NCOL - 1) / NCOL;
+            const int r = cu.g / hg, h0 = (cu.g - r * hg) * NCOL;
+            cu.col0 = r * p.H + h0;
+            cu.nc = min(NCOL, p.H - h0);
+            nt = row_blocks(sp.len - p.R + r, p.max_idx);
+        } else {
+            nt = (unit_keys(sp.len, p.R, p.H, p.ncols, cu.g) + BK - 1) / BK;
+        }
         const int64_t ub = unit_pos(u, 0);
         cu.c0 = range_of(p, ub);
         c1 = range_of(p, unit_pos(u, nt - 1));
@@ -1365,10 +1539,40 @@ __device__ __forceinline__ bool combine_unit(const Params &p, CombineUnit &cu) {
     return cu.n > 1;
 }
 
-__device__ __forceinline__ void combine_store(const Params &p, const CombineUnit &cu, int gc, int lane, float M,
-                                              float L, const float4 (&acc)[4]) {
-    const float inv = 1.f / L;
-    const size_t orow = (size_t)cu.s * p.ncols + gc;
+// SHARED: the partials of one column of stream s: those over the group's shared rows (a unit of
+// the group's packed columns), then those over the stream's own.  False: the column was written whole.
+struct CombineColumn {
+    int n, n1, first1, first2, col1, col2;
+    __device__ __forceinline__ size_t place(const Params &, int j, int) const {
+        return j < n1 ? (size_t)(first1 + j) * NCOL + col1 : (size_t)(first2 + j - n1) * NCOL + col2;
+    }
+};
+__device__ __forceinline__ bool combine_column(const Params &p, int s, int c, CombineColumn &cc) {
+    // the slots of unit u of an entry: u + the CTAs that hold a piece of it
+    auto pieces = [&](const SharedEntry &e, int64_t u, int &first) {
+        const int c0 = range_of(p, unit_pos(u, 0));
+        first = (int)u + c0;
+        return range_of(p, unit_pos(u, e.nt - 1)) - c0 + 1;
+    };
+    cc.n1 = 0;
+    int n2 = 0;
+    const int pe = p.order[s];
+    if (pe >= 0) {
+        const int k = s * p.ncols + c - p.se[pe].col0;
+        cc.n1 = pieces(p.se[pe], p.se[pe].unit0 + k / NCOL, cc.first1);
+        cc.col1 = k % NCOL;
+    }
+    if (p.se[s].nt > 0) {
+        n2 = pieces(p.se[s], p.se[s].unit0 + c / NCOL, cc.first2);
+        cc.col2 = c % NCOL;
+    }
+    cc.n = cc.n1 + n2;
+    return pe >= 0 || n2 > 1;
+}
+
+__device__ __forceinline__ void combine_store(const Params &p, size_t orow, int lane, float M, float L,
+                                              const float4 (&acc)[4]) {
+    const float inv = L > 0.f ? 1.f / L : 0.f;   // BLOCKS: a row whose list leaves no key is zero
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         __nv_bfloat162 *o2 = reinterpret_cast<__nv_bfloat162 *>(p.out + orow * kLat) + 2 * (lane + 32 * i);
@@ -1393,16 +1597,23 @@ __device__ __forceinline__ void combine_add(float4 (&acc)[4], const float *o, in
     }
 }
 
-template <bool WIDE>
+template <bool WIDE, bool SHARED>
 __global__ void __launch_bounds__(WIDE ? COMBINE_THREADS : COMBINE_COLS * 32) mla_combine_kernel(const __grid_constant__ Params p) {
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    CombineUnit cu;
-    if (!combine_unit(p, cu)) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = WIDE ? (int)blockIdx.x : (int)blockIdx.x * COMBINE_COLS + warp;   // column of the group
-    const int gc = cu.g * NCOL + col;
-    if (gc >= p.ncols) return;   // WIDE: the whole block
+    std::conditional_t<SHARED, CombineColumn, CombineUnit> cu;
+    size_t orow;
+    if constexpr (SHARED) {
+        const int c = (int)blockIdx.y * NCOL + col;
+        if (c >= p.ncols || !combine_column(p, (int)blockIdx.z, c, cu)) return;   // WIDE: the whole block
+        orow = (size_t)blockIdx.z * p.ncols + c;
+    } else {
+        if (!combine_unit(p, cu)) return;
+        if (col >= cu.nc) return;   // WIDE: the whole block
+        orow = (size_t)cu.s * p.ncols + cu.col0 + col;
+    }
     const int n = cu.n;
     float4 acc[4];
 #pragma unroll
@@ -1414,7 +1625,7 @@ __global__ void __launch_bounds__(WIDE ? COMBINE_THREADS : COMBINE_COLS * 32) ml
             m = -INFINITY;
             l = 0.f;
             if (j < n) {
-                const size_t base = (size_t)cu.slot_of(p, j) * NCOL + col;
+                const size_t base = cu.place(p, j, col);
                 m = __ldg(p.ws_ml + base * 2);
                 l = __ldg(p.ws_ml + base * 2 + 1);
             }
@@ -1435,18 +1646,18 @@ __global__ void __launch_bounds__(WIDE ? COMBINE_THREADS : COMBINE_COLS * 32) ml
 #pragma unroll 4
             for (int k = 0; k < cnt; ++k) {
                 const float w = __shfl_sync(0xffffffffu, wj, k);
-                combine_add(acc, p.ws_o + ((size_t)cu.slot_of(p, j0 + k) * NCOL + col) * kLat, lane, w);
+                combine_add(acc, p.ws_o + cu.place(p, j0 + k, col) * kLat, lane, w);
                 L = __fmaf_rn(w, __shfl_sync(0xffffffffu, lj, k), L);
             }
         }
-        combine_store(p, cu, gc, lane, M, L, acc);
+        combine_store(p, orow, lane, M, L, acc);
     } else {
         __shared__ float red_m[COMBINE_THREADS / 32];
         __shared__ float red_l[COMBINE_THREADS / 32];
         __shared__ float4 red_o[COMBINE_THREADS / 32][128];
         float m = -INFINITY;
         for (int j = threadIdx.x; j < n; j += COMBINE_THREADS)
-            m = fmaxf(m, __ldg(p.ws_ml + ((size_t)cu.slot_of(p, j) * NCOL + col) * 2));
+            m = fmaxf(m, __ldg(p.ws_ml + cu.place(p, j, col) * 2));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (lane == 0) red_m[warp] = m;
@@ -1456,7 +1667,7 @@ __global__ void __launch_bounds__(WIDE ? COMBINE_THREADS : COMBINE_COLS * 32) ml
         for (int w = 1; w < COMBINE_THREADS / 32; ++w) M = fmaxf(M, red_m[w]);
 #pragma unroll 2
         for (int j = warp; j < n; j += COMBINE_THREADS / 32) {
-            const size_t base = (size_t)cu.slot_of(p, j) * NCOL + col;
+            const size_t base = cu.place(p, j, col);
             const float mj = __ldg(p.ws_ml + base * 2), lj = __ldg(p.ws_ml + base * 2 + 1);
             const float w = (mj == -INFINITY) ? 0.f : ptx::ex2(mj - M);
             combine_add(acc, p.ws_o + base * kLat, lane, w);
@@ -1482,7 +1693,7 @@ __global__ void __launch_bounds__(WIDE ? COMBINE_THREADS : COMBINE_COLS * 32) ml
             }
             Lt += red_l[w];
         }
-        combine_store(p, cu, gc, lane, M, Lt, acc);
+        combine_store(p, orow, lane, M, Lt, acc);
     }
 }
 
@@ -1681,6 +1892,112 @@ inline Plan plan_of(int S, int R, int H, const int64_t *h_len, int sms, bool inv
     return pl;
 }
 
+// Ranges over units of nt[u] tiles (no tile: no unit), cut anywhere: bound i at weighted position
+// i W / n, a unit's start weighing `seg` tiles (a bound that falls into that weight moves to the
+// unit's start).  Writes b[0..n] as unit_pos values and returns n; *cut: a bound inside a unit.
+inline int cut_units(const std::vector<int32_t> &nt, int64_t seg, int min_tiles, int sms, int64_t *b, bool *cut) {
+    const int64_t units = (int64_t)nt.size();
+    int64_t W = 0, tiles = 0;
+    for (int32_t t : nt) tiles += t;
+    W = tiles + seg * units;
+    const int64_t want = (tiles + min_tiles - 1) / min_tiles;
+    int n = (int)(want < sms ? want : sms);
+    if (n < 1) n = 1;
+    *cut = false;
+    b[0] = 0;
+    int64_t u = 0, w = 0;   // unit u starts at weight w
+    int m = 0;              // bounds written
+    for (int i = 1; i < n; ++i) {
+        const int64_t tau = i * W / n;
+        while (w + seg + nt[u] <= tau) w += seg + nt[u++];
+        const int64_t t = tau - w - seg;
+        const int64_t x = t > 0 ? unit_pos(u, t) : unit_pos(u, 0);
+        if (x <= b[m]) continue;   // no empty range
+        b[++m] = x;
+        *cut |= t > 0;
+    }
+    b[++m] = unit_pos(units, 0);
+    return m;
+}
+
+constexpr int64_t BLOCKS_SEG_COST = 3;   // BLOCKS: a unit's start, in key tiles
+
+inline Plan plan_blocks(int S, int R, int H, const int64_t *h_len, int max_blk, int sms, int64_t *rb) {
+    Plan pl;
+    const int hg = (H + NCOL - 1) / NCOL;
+    std::vector<int32_t> nt((size_t)S * R * hg);
+    size_t u = 0;
+    for (int s = 0; s < S; ++s)
+        for (int r = 0; r < R; ++r) {
+            const int32_t n = (int32_t)row_blocks(h_len[s] - R + r, max_blk);
+            for (int h = 0; h < hg; ++h) nt[u++] = n;
+        }
+    bool cut = false;
+    pl.mode = MODE_BLOCKS;
+    pl.total = (int64_t)nt.size();
+    pl.rep = 1;
+    pl.nranges = cut_units(nt, BLOCKS_SEG_COST, MIN_TILES, sms, rb, &cut);
+    pl.nctas = pl.nranges;
+    pl.slots = cut ? 2 * (size_t)pl.nctas : 0;
+    return pl;
+}
+
+constexpr int64_t SHARED_SEG_COST = 5;   // SHARED: a unit's start, in key tiles
+
+// The entries of a shared call: own rows of each stream, then the shared rows of each group that
+// shares any (in whole tiles; the rest of a prefix counts as each stream's own).  order[s]: the
+// entry of stream s's shared rows or -1.  Returns the entries, or -1 when they pass the table.
+inline int shared_entries(int S, int R, int H, const int64_t *h_len, const int32_t *h_gsize, int G,
+                          const int64_t *h_prefix, SharedEntry *e, int16_t *order, std::vector<int32_t> *nt) {
+    const int ncols = R * H;
+    const int groups = (ncols + NCOL - 1) / NCOL;
+    int n = S, units = 0;
+    for (int g = 0, s = 0; g < G; ++g) {
+        const int64_t whole = h_gsize[g] > 1 ? h_prefix[g] / BK * BK : 0;
+        if (whole > 0) {
+            if (n >= TF_MAX_STREAMS) return -1;
+            e[n].len = whole;
+            e[n].alone = 0;
+            e[n].nt = (int32_t)(whole / BK);
+            e[n].tile0 = 0;
+            e[n].ncols = h_gsize[g] * ncols;
+            e[n].col0 = s * ncols;
+            e[n].row = s;
+        }
+        for (int k = 0; k < h_gsize[g]; ++k, ++s) {
+            e[s].len = h_len[s];
+            e[s].alone = whole == 0;
+            e[s].tile0 = (int32_t)(whole / BK);
+            e[s].nt = (int32_t)((h_len[s] - whole + BK - 1) / BK);
+            e[s].ncols = ncols;
+            e[s].col0 = s * ncols;
+            e[s].row = s;
+            order[s] = (int16_t)(whole > 0 ? n : -1);
+        }
+        if (whole > 0) ++n;
+    }
+    for (int i = 0; i < n; ++i) {
+        e[i].unit0 = units;
+        if (e[i].nt == 0) continue;
+        const int k = i < S ? groups : (e[i].ncols + NCOL - 1) / NCOL;
+        units += k;
+        if (nt) nt->insert(nt->end(), k, e[i].nt);
+    }
+    return n;
+}
+
+inline Plan plan_shared(const std::vector<int32_t> &nt, int nshared, int sms, int64_t *rb) {
+    Plan pl;
+    bool cut = false;
+    pl.mode = MODE_SHARED;
+    pl.total = (int64_t)nt.size();
+    pl.rep = 1;
+    pl.nranges = cut_units(nt, SHARED_SEG_COST, MIN_TILES, sms, rb, &cut);
+    pl.nctas = pl.nranges;
+    pl.slots = cut || nshared > 0 ? nt.size() + (size_t)pl.nctas : 0;
+    return pl;
+}
+
 inline size_t slot_bytes() { return (size_t)NCOL * kLat * sizeof(float); }
 
 // The most partials any unit of this launch leaves (the combine's form depends on it).
@@ -1688,7 +2005,7 @@ inline int max_partials(const Params &p, const Plan &pl) {
     int most = 1;
     if (pl.mode == MODE_SPLITS) {
         for (int s = 0; s < p.S; ++s) most = std::max(most, (int)p.st[s].nsplit);
-    } else if (pl.mode == MODE_UNITS) {
+    } else if (pl.mode == MODE_UNITS || pl.mode == MODE_BLOCKS) {
         // consecutive bounds inside one unit
         int run = 0;
         for (int i = 1; i < pl.nranges; ++i) {
@@ -1697,6 +2014,20 @@ inline int max_partials(const Params &p, const Plan &pl) {
             run = inside ? (((xp >> 32) == (x >> 32) && (xp & 0xffffffffll) != 0) ? run + 1 : 1) : 0;
             most = std::max(most, run + 1);
         }
+    } else if (pl.mode == MODE_SHARED) {
+        // pieces of the longest own unit plus pieces of the longest shared one
+        const int64_t *b = p.rb, *e = p.rb + pl.nranges + 1;
+        int kind[2] = {0, 0};
+        for (int i = 0; i < p.nent; ++i) {
+            const SharedEntry &x = p.se[i];
+            const int units = x.nt > 0 ? (x.ncols + NCOL - 1) / NCOL : 0;
+            for (int k = 0; k < units; ++k) {
+                const int c0 = (int)(std::upper_bound(b, e, unit_pos(x.unit0 + k, 0)) - b);
+                const int c1 = (int)(std::upper_bound(b, e, unit_pos(x.unit0 + k, x.nt - 1)) - b);
+                kind[i >= p.S] = std::max(kind[i >= p.S], c1 - c0 + 1);
+            }
+        }
+        most = std::max(most, kind[0] + kind[1]);
     } else {
         for (int s = 0; s < p.S; ++s) {
             const int64_t *b = p.rb, *e = p.rb + pl.nranges + 1;
@@ -1727,13 +2058,32 @@ static int device_sms() {
     return n < attn::MAX_CTAS ? n : attn::MAX_CTAS;
 }
 
-size_t attend_workspace_bytes(bool invariant, int S, int R, int H, const int64_t *h_len, bool sparse) {
-    const attn::Plan pl = attn::plan_of(S, R, H, h_len, device_sms(), invariant, nullptr, sparse);
-    if (pl.slots == 0) return 0;
-    const size_t slots = pl.slots;
+static size_t slots_bytes(size_t slots) {
+    if (slots == 0) return 0;
     const size_t o = slots * attn::slot_bytes();
     const size_t ml = slots * attn::NCOL * 2 * sizeof(float);
     return o + ((ml + 255) & ~size_t(255));
+}
+
+size_t attend_workspace_bytes(bool invariant, int S, int R, int H, const int64_t *h_len, bool sparse) {
+    return slots_bytes(attn::plan_of(S, R, H, h_len, device_sms(), invariant, nullptr, sparse).slots);
+}
+
+size_t blocks_workspace_bytes(int S, int R, int H, const int64_t *h_len, int max_blk) {
+    int64_t rb[attn::MAX_CTAS + 1];
+    return slots_bytes(attn::plan_blocks(S, R, H, h_len, max_blk, device_sms(), rb).slots);
+}
+
+int shared_workspace_bytes(int S, int R, int H, const int64_t *h_len, const int32_t *h_gsize, int G,
+                           const int64_t *h_prefix, size_t *bytes) {
+    attn::SharedEntry e[TF_MAX_STREAMS];
+    int16_t order[TF_MAX_STREAMS];
+    std::vector<int32_t> nt;
+    const int n = attn::shared_entries(S, R, H, h_len, h_gsize, G, h_prefix, e, order, &nt);
+    if (n < 0) return TF_E_UNSUPPORTED;
+    int64_t rb[attn::MAX_CTAS + 1];
+    *bytes = slots_bytes(attn::plan_shared(nt, n - S, device_sms(), rb).slots);
+    return TF_OK;
 }
 
 // The plan a call would use, for tf_paged_mla_plan_info (host arithmetic only).
@@ -1783,6 +2133,18 @@ static bool encode(CUtensorMap *tm, void *base, int rank, const cuuint64_t *dims
     CUresult r = fn(tm, type, rank, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
+}
+
+bool encode_tmap_bf16(CUtensorMap *tm, void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                      const uint32_t *box) {
+    cuuint64_t d[4], st[3];
+    cuuint32_t bx[4];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        bx[i] = box[i];
+        if (i + 1 < rank) st[i] = strides[i];
+    }
+    return encode(tm, base, rank, d, st, bx);
 }
 
 static int ensure_pool_maps(tf_kvpool *pool) {
@@ -1859,35 +2221,32 @@ static int ensure_pool_maps(tf_kvpool *pool) {
     return TF_OK;
 }
 
-int launch_attend(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_len, int S, int R,
-                  int H, const void *d_q, float scale, void *d_out, float *d_lse, void *d_ws, size_t ws_bytes,
-                  cudaStream_t st, const int32_t *d_idx, int max_idx, const int32_t *h_nidx) {
+// Every instance opted in to its shared memory once, whichever host thread comes first.
+static bool attend_ready() {
     using namespace attn;
-    if (prepare_launch(pool, st) != TF_OK) return TF_E_CUDA;
-    // every instance opted in to its shared memory once, whichever host thread comes first
     static std::once_flag attr_once;
     static bool attr_ok = false;
     std::call_once(attr_once, [] {
-        attr_ok = !(cudaFuncSetAttribute(mla_attend_kernel<MODE_RANGES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 SMEM_TOTAL) != cudaSuccess ||
-            cudaFuncSetAttribute(mla_attend_kernel<MODE_UNITS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 SMEM_TOTAL) != cudaSuccess ||
-            cudaFuncSetAttribute(mla_attend_kernel<MODE_SPLITS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 SMEM_TOTAL) != cudaSuccess ||
-            cudaFuncSetAttribute(mla_attend_kernel<MODE_SPARSE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 SMEM_TOTAL) != cudaSuccess ||
-            cudaFuncSetAttribute(mla_attend_kernel<MODE_RANGES, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 SMEM_TOTAL) != cudaSuccess ||
-            cudaFuncSetAttribute(mla_attend_kernel<MODE_UNITS, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 SMEM_TOTAL) != cudaSuccess ||
-            cudaFuncSetAttribute(mla_attend_kernel<MODE_SPARSE, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 SMEM_TOTAL) != cudaSuccess);
+        attr_ok = true;
+        for (auto *kern : {mla_attend_kernel<MODE_RANGES>, mla_attend_kernel<MODE_UNITS>, mla_attend_kernel<MODE_SPLITS>,
+                           mla_attend_kernel<MODE_SPARSE>, mla_attend_kernel<MODE_BLOCKS>, mla_attend_kernel<MODE_SHARED>,
+                           mla_attend_kernel<MODE_RANGES, true>, mla_attend_kernel<MODE_UNITS, true>,
+                           mla_attend_kernel<MODE_SPARSE, true>, mla_attend_kernel<MODE_BLOCKS, true>,
+                           mla_attend_kernel<MODE_SHARED, true>})
+            attr_ok = attr_ok && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL) ==
+                                     cudaSuccess;
     });
-    if (!attr_ok) return TF_E_CUDA;
+    return attr_ok;
+}
+
+// The parameters every mode takes.  Params is large (tensor maps + the per-stream plan); there is
+// one per host thread.
+static int fill_params(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, int S, int R, int H,
+                       const void *d_q, float scale, void *d_out, float *d_lse, attn::Params *&out) {
+    using namespace attn;
+    if (!attend_ready()) return TF_E_CUDA;
     int rc = ensure_pool_maps(pool);
     if (rc != TF_OK) return rc;
-
-    // Params is large (tensor maps + the per-stream plan); keep one per host thread.
     thread_local std::unique_ptr<Params> pp;
     if (!pp) pp.reset(new Params());
     Params &p = *pp;
@@ -1895,8 +2254,8 @@ int launch_attend(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages
     p.tm_rope = pool->tm_rope[0];
     p.tm_lat_rows = pool->tm_lat[1];
     p.tm_rope_rows = pool->tm_rope[1];
-    p.idx = d_idx;
-    p.max_idx = max_idx;
+    p.idx = nullptr;
+    p.max_idx = 0;
     {
         cuuint64_t dims[2] = {(cuuint64_t)kDk, (cuuint64_t)S * R * H};
         cuuint64_t strides[1] = {(cuuint64_t)kDk * 2};
@@ -1919,6 +2278,70 @@ int launch_attend(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages
     p.ncols = R * H;
     p.groups = (R * H + NCOL - 1) / NCOL;
     p.windowed = d_pt ? 0 : 1;
+    p.nent = 0;
+    out = &p;
+    return TF_OK;
+}
+
+// Launch the attention of plan pl and, when it leaves partials, their merge.
+static int launch_plan(tf_kvpool *pool, attn::Params &p, const attn::Plan &pl, void *d_ws, cudaStream_t st) {
+    using namespace attn;
+    p.mode = pl.mode;
+    p.total = pl.total;
+    p.nranges = pl.nranges;
+    p.rep = pl.rep;
+    const size_t slots = pl.slots;
+    p.ws_o = slots ? static_cast<float *>(d_ws) : nullptr;
+    p.ws_ml = slots ? reinterpret_cast<float *>(static_cast<char *>(d_ws) + slots * slot_bytes()) : nullptr;
+    {
+        ProfScope prof(pool, kProfAttend, st);
+        const bool f8 = is_fp8(pool->desc);
+        if (f8 && pl.mode == MODE_SPLITS) return TF_E_UNSUPPORTED;
+        auto *kern = f8 ? (pl.mode == MODE_RANGES   ? mla_attend_kernel<MODE_RANGES, true>
+                           : pl.mode == MODE_UNITS  ? mla_attend_kernel<MODE_UNITS, true>
+                           : pl.mode == MODE_BLOCKS ? mla_attend_kernel<MODE_BLOCKS, true>
+                           : pl.mode == MODE_SHARED ? mla_attend_kernel<MODE_SHARED, true>
+                                                    : mla_attend_kernel<MODE_SPARSE, true>)
+                   : pl.mode == MODE_RANGES ? mla_attend_kernel<MODE_RANGES>
+                   : pl.mode == MODE_UNITS  ? mla_attend_kernel<MODE_UNITS>
+                   : pl.mode == MODE_SPARSE ? mla_attend_kernel<MODE_SPARSE>
+                   : pl.mode == MODE_BLOCKS ? mla_attend_kernel<MODE_BLOCKS>
+                   : pl.mode == MODE_SHARED ? mla_attend_kernel<MODE_SHARED>
+                                            : mla_attend_kernel<MODE_SPLITS>;
+        const int threads = f8 || pl.mode == MODE_SPARSE ? THREADS + 128 : THREADS;
+        const cudaError_t e = launch_pdl(kern, dim3(pl.nctas), dim3(threads), SMEM_TOTAL, st, p);
+        launch_counter()++;
+        if (e != cudaSuccess) return TF_E_CUDA;
+    }
+    if (slots) {
+        ProfScope prof(pool, kProfCombine, st);
+        const bool wide = max_partials(p, pl) > COMBINE_NARROW_MAX;
+        const int groups = (p.ncols + NCOL - 1) / NCOL;
+        const int gx = wide ? NCOL : NCOL / COMBINE_COLS;
+        // UNITS, BLOCKS: blockIdx.y runs over the range bounds (only cut units merge)
+        const bool bounds = pl.mode == MODE_UNITS || pl.mode == MODE_BLOCKS;
+        const dim3 grid = bounds ? dim3(gx, pl.nranges - 1) : dim3(gx, groups, p.S);
+        auto *kern = pl.mode == MODE_SHARED ? (wide ? mla_combine_kernel<true, true> : mla_combine_kernel<false, true>)
+                                            : (wide ? mla_combine_kernel<true, false> : mla_combine_kernel<false, false>);
+        const cudaError_t e = launch_pdl(kern, grid, dim3(wide ? COMBINE_THREADS : COMBINE_COLS * 32), 0, st, p);
+        launch_counter()++;
+        if (e != cudaSuccess) return TF_E_CUDA;
+    }
+    return TF_OK;
+}
+
+int launch_attend(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_len, int S, int R,
+                  int H, const void *d_q, float scale, void *d_out, float *d_lse, void *d_ws, size_t ws_bytes,
+                  cudaStream_t st, const int32_t *d_idx, int max_idx, const int32_t *h_nidx) {
+    using namespace attn;
+    (void)ws_bytes;
+    if (prepare_launch(pool, st) != TF_OK) return TF_E_CUDA;
+    Params *pp;
+    const int rc = fill_params(pool, cache, d_pt, max_pages, S, R, H, d_q, scale, d_out, d_lse, pp);
+    if (rc != TF_OK) return rc;
+    Params &p = *pp;
+    p.idx = d_idx;
+    p.max_idx = max_idx;
     const bool sparse = d_idx != nullptr;
     // the keys of a sparse call are the listed rows: plan over the list lengths
     int64_t nkeys[TF_MAX_STREAMS];
@@ -1930,10 +2353,6 @@ int launch_attend(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages
     const bool invariant = !sparse && (pool->desc.flags & TF_POOL_BATCH_INVARIANT) != 0;
     Plan pl = plan_of(S, R, H, keys, device_sms(), invariant, p.rb, sparse);
     if (sparse) pl.mode = MODE_SPARSE;   // ranges over the lists (few column groups: R = 1, H <= 128)
-    p.mode = pl.mode;
-    p.total = pl.total;
-    p.nranges = pl.nranges;
-    p.rep = pl.rep;
     int64_t off = 0;
     for (int s = 0; s < S; ++s) {
         StreamPlan &sp = p.st[s];
@@ -1963,40 +2382,38 @@ int launch_attend(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages
             if (p.st[s].nsplit > 1) slots += p.groups * p.st[s].nsplit;
         }
     }
-    const size_t slots = pl.slots;
-    p.ws_o = slots ? static_cast<float *>(d_ws) : nullptr;
-    p.ws_ml = slots ? reinterpret_cast<float *>(static_cast<char *>(d_ws) + slots * slot_bytes()) : nullptr;
-    (void)ws_bytes;
-    {
-        ProfScope prof(pool, kProfAttend, st);
-        const bool f8 = is_fp8(pool->desc);
-        if (f8 && pl.mode == MODE_SPLITS) return TF_E_UNSUPPORTED;
-        auto *kern = f8 ? (pl.mode == MODE_RANGES  ? mla_attend_kernel<MODE_RANGES, true>
-                           : pl.mode == MODE_UNITS ? mla_attend_kernel<MODE_UNITS, true>
-                                                   : mla_attend_kernel<MODE_SPARSE, true>)
-                   : pl.mode == MODE_RANGES ? mla_attend_kernel<MODE_RANGES>
-                   : pl.mode == MODE_UNITS  ? mla_attend_kernel<MODE_UNITS>
-                   : pl.mode == MODE_SPARSE ? mla_attend_kernel<MODE_SPARSE>
-                                            : mla_attend_kernel<MODE_SPLITS>;
-        const int threads = f8 || pl.mode == MODE_SPARSE ? THREADS + 128 : THREADS;
-        const cudaError_t e = launch_pdl(kern, dim3(pl.nctas), dim3(threads), SMEM_TOTAL, st, p);
-        launch_counter()++;
-        if (e != cudaSuccess) return TF_E_CUDA;
-    }
-    if (slots) {
-        ProfScope prof(pool, kProfCombine, st);
-        // UNITS: only the units a range bound cuts
-        // UNITS: blockIdx.y runs over the range bounds (only cut units merge)
-        const bool wide = max_partials(p, pl) > COMBINE_NARROW_MAX;
-        const int groups = (R * H + NCOL - 1) / NCOL;
-        const int gx = wide ? NCOL : NCOL / COMBINE_COLS;
-        const dim3 grid = pl.mode == MODE_UNITS ? dim3(gx, pl.nranges - 1) : dim3(gx, groups, S);
-        const cudaError_t e = launch_pdl(wide ? mla_combine_kernel<true> : mla_combine_kernel<false>, grid,
-                                         dim3(wide ? COMBINE_THREADS : COMBINE_COLS * 32), 0, st, p);
-        launch_counter()++;
-        if (e != cudaSuccess) return TF_E_CUDA;
-    }
-    return TF_OK;
+    return launch_plan(pool, p, pl, d_ws, st);
+}
+
+int launch_attend_blocks(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_len,
+                         const int32_t *d_blk, int max_blk, int S, int R, int H, const void *d_q, float scale,
+                         void *d_out, float *d_lse, void *d_ws, cudaStream_t st) {
+    using namespace attn;
+    if (prepare_launch(pool, st) != TF_OK) return TF_E_CUDA;
+    Params *pp;
+    const int rc = fill_params(pool, cache, d_pt, max_pages, S, R, H, d_q, scale, d_out, d_lse, pp);
+    if (rc != TF_OK) return rc;
+    pp->idx = d_blk;
+    pp->max_idx = max_blk;
+    pp->groups = R * ((H + NCOL - 1) / NCOL);   // a unit's columns are of one query row
+    for (int s = 0; s < S; ++s) pp->st[s].len = h_len[s];
+    const Plan pl = plan_blocks(S, R, H, h_len, max_blk, device_sms(), pp->rb);
+    return launch_plan(pool, *pp, pl, d_ws, st);
+}
+
+int launch_attend_shared(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_len,
+                         const int32_t *h_gsize, int G, const int64_t *h_prefix, int S, int R, int H, const void *d_q,
+                         float scale, void *d_out, float *d_lse, void *d_ws, cudaStream_t st) {
+    using namespace attn;
+    if (prepare_launch(pool, st) != TF_OK) return TF_E_CUDA;
+    Params *pp;
+    const int rc = fill_params(pool, cache, d_pt, max_pages, S, R, H, d_q, scale, d_out, d_lse, pp);
+    if (rc != TF_OK) return rc;
+    std::vector<int32_t> nt;
+    pp->nent = shared_entries(S, R, H, h_len, h_gsize, G, h_prefix, pp->se, pp->order, &nt);
+    if (pp->nent < 0) return TF_E_UNSUPPORTED;
+    const Plan pl = plan_shared(nt, pp->nent - S, device_sms(), pp->rb);
+    return launch_plan(pool, *pp, pl, d_ws, st);
 }
 
 }  // namespace tf

@@ -1,0 +1,535 @@
+// Choosing blocks of rows for sparse attention: the mean row ("key") of every 64-row block of a
+// paged latent cache, and the score of each visible block for every query row.  The scores go to
+// the blocked top-k, whose lists tf_paged_mla_attend_blocks takes.
+//
+//   k_b        = mean of the rows of block b that the stream holds         (576 wide, bf16)
+//   score[r,b] = sum_h w[r,h] max(0, scale q[r,h] . k_b)                    (fp32)
+//
+// Pooled index keys and the weighted sum of rectified products over heads are the TensorFold pages'
+// (issue #1142, "What happens now": one pooled index key every few tokens; issue #1142, piece 2: the kernels that pool keys and score
+// them take the page table).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <memory>
+#include <mutex>
+
+#include "ptx.cuh"
+#include "tf_internal.h"
+
+namespace tf {
+
+namespace blk {
+
+constexpr int ROWS = TF_BLOCK_ROWS;
+constexpr int PER_PAGE = kPageRows / ROWS;   // 8 blocks a page
+
+// ---- block keys ----
+struct KeysParams {
+    const int32_t *pt;       // [S][max_pages] or null (windows)
+    const char *cache_base;  // page 0 of this cache
+    uint16_t *bkeys;         // [pages][8][576] bf16
+    DevErr *err;
+    int32_t max_pages, num_pages, S;
+    int64_t off[TF_MAX_STREAMS + 1];   // first numbered block of each stream
+    int64_t len[TF_MAX_STREAMS];
+    int32_t first[TF_MAX_STREAMS];     // first block to average
+};
+
+__device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// One CTA a block: thread (g, c) adds 16-byte chunk c of rows g, g + G, ... in fp32; the G sums of a
+// value are added in order and divided by the rows the block holds, rounded once to bf16.
+// BF16 pages: 72 chunks of 8 values, 4 row groups.  FP8: 32 chunks of 16 codes (each value is
+// bf16(code * scale), as the attention takes it) and 8 rope chunks, 8 row groups.
+template <bool FP8>
+struct KeysShape {
+    static constexpr int C = FP8 ? 40 : 72;
+    static constexpr int G = FP8 ? 8 : 4;
+    static constexpr int T = C * G;
+    static constexpr int V = FP8 ? 16 : 8;   // values a latent chunk
+};
+
+template <bool FP8>
+__global__ void __launch_bounds__(KeysShape<FP8>::T) block_keys_kernel(const __grid_constant__ KeysParams p) {
+    using K = KeysShape<FP8>;
+    __shared__ float part[K::G][kDk];
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    const int64_t n = blockIdx.x;
+    int s = 0;
+    for (int a = p.S - 1; s < a;) {   // the stream whose blocks hold number n
+        const int mid = (s + a + 1) >> 1;
+        if (p.off[mid] <= n) s = mid; else a = mid - 1;
+    }
+    const int64_t b = p.first[s] + (n - p.off[s]);
+    const int lp = (int)(b / PER_PAGE), ib = (int)(b % PER_PAGE);
+    const int page = p.pt ? __ldg(p.pt + (int64_t)s * p.max_pages + lp) : s * p.max_pages + lp;
+    if (page < 0 || page >= p.num_pages) {
+        if (threadIdx.x == 0) ptx::record_error(p.err, TF_E_DEVICE, page);
+        return;
+    }
+    const int64_t left = p.len[s] - b * ROWS;
+    const int rows = left < ROWS ? (int)left : ROWS;
+    const int c = (int)threadIdx.x % K::C, g = (int)threadIdx.x / K::C;
+    const char *pg = p.cache_base + (size_t)page * (FP8 ? kF8PageBytes : kPageBytes);
+    const int row0 = ib * ROWS;
+    constexpr int LC = FP8 ? kLat / 16 : kLat / 8;   // latent chunks
+    const bool rope = c >= LC;
+    const size_t lat_stride = FP8 ? kLat : kLat * 2;
+    const char *src = rope ? pg + (FP8 ? kF8RopeOff : kLatBlockBytes) + (size_t)row0 * (kRope * 2) + (c - LC) * 16
+                           : pg + (size_t)row0 * lat_stride + c * 16;
+    const size_t stride = rope ? (size_t)kRope * 2 : lat_stride;
+    const float *scales = reinterpret_cast<const float *>(pg + kF8ScaleOff) + row0;
+    float acc[K::V];
+#pragma unroll
+    for (int i = 0; i < K::V; ++i) acc[i] = 0.f;
+    constexpr int N = ROWS / K::G;   // rows a thread
+    constexpr int U = 8;             // loads in flight
+#pragma unroll
+    for (int i0 = 0; i0 < N; i0 += U) {
+        uint4 v[U];
+        float sc[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = (i0 + u) * K::G + g;
+            v[u] = make_uint4(0, 0, 0, 0);
+            sc[u] = 0.f;
+            if (r < rows) {
+                v[u] = __ldg(reinterpret_cast<const uint4 *>(src + (size_t)r * stride));
+                if (FP8) sc[u] = __ldg(scales + r);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+            if (!FP8 || rope) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    acc[2 * k] += lo(w[k]);
+                    acc[2 * k + 1] += hi(w[k]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < K::V / 2; ++k) {
+                    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
+                        (__nv_fp8x2_storage_t)((w[k / 2] >> (16 * (k & 1))) & 0xFFFFu), __NV_E4M3);
+                    const float2 f = __half22float2(__half2(hr));
+                    const uint32_t x = ptx::pack_bf16x2(f.x * sc[u], f.y * sc[u]);
+                    acc[2 * k] += lo(x);
+                    acc[2 * k + 1] += hi(x);
+                }
+            }
+        }
+    }
+    const int v0 = rope ? kLat + (c - LC) * 8 : c * K::V;
+#pragma unroll
+    for (int i = 0; i < K::V; ++i)
+        if (!rope || i < 8) part[g][v0 + i] = acc[i];
+    __syncthreads();
+    uint32_t *dst = reinterpret_cast<uint32_t *>(p.bkeys + ((size_t)page * PER_PAGE + ib) * kDk);
+    for (int i = threadIdx.x; i < kDk / 2; i += K::T) {
+        float a = 0.f, d = 0.f;
+#pragma unroll
+        for (int k = 0; k < K::G; ++k) {
+            a += part[k][2 * i];
+            d += part[k][2 * i + 1];
+        }
+        dst[i] = ptx::pack_bf16x2(__fdiv_rn(a, (float)rows), __fdiv_rn(d, (float)rows));
+    }
+}
+
+// ---- block scores ----
+// A GEMM of the block keys with the queries, blocks on the accumulator's lanes:
+//   D[128 blocks][N columns] = K[128][576] . Q[N][576]^T      tcgen05.mma M = 128, K in 9 boxes of 64
+// so a thread of the epilogue holds one block and adds the rectified products of a query row's
+// heads, which lie along its columns, in registers; a warp's stores are 128 bytes of a score row.
+// A tile's columns are as many whole query rows as fit 128 columns.  A CTA walks a run of tiles,
+// block tile by block tile, so the block keys (144 KB) stay in shared memory while query tiles
+// stream through a ring of 64-wide boxes; two accumulators let a tile's products run under the
+// last one's epilogue.
+constexpr int M = 128;                        // blocks a tile: 16 pages of 8
+constexpr int TILE_PAGES = M / PER_PAGE;
+constexpr int NMAX = 128;                     // columns a tile
+constexpr int KBOX = kDk / 64;                // 9
+constexpr int PAGE_KEYS = PER_PAGE * kDk * 2; // 9,216 bytes: [9 boxes][8 blocks][64 values], swizzled
+constexpr int STAGES = 4;
+constexpr int STAGE_BYTES = NMAX * 128;
+constexpr int SMEM_A = 0;
+constexpr int SMEM_B = SMEM_A + TILE_PAGES * PAGE_KEYS;
+constexpr int SMEM_CTRL = SMEM_B + STAGES * STAGE_BYTES;
+constexpr int THREADS = 192;                  // 4 epilogue warps, the TMA warp, the MMA warp
+constexpr int TCOLS = 2 * NMAX;
+
+struct Ctrl {
+    uint64_t a_full, a_free;
+    uint64_t b_full[STAGES], b_free[STAGES];
+    uint64_t d_full[2], d_free[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+    float w[2][NMAX];
+};
+constexpr int SMEM_TOTAL = SMEM_CTRL + (int)sizeof(Ctrl) + 1024;
+static_assert(SMEM_TOTAL <= 232448, "shared memory budget");
+
+struct ScoreParams {
+    CUtensorMap tm_k;   // 3D {576, 8 blocks, pages}, box {64, 8, 1}
+    CUtensorMap tm_q;   // 2D {576, S*R*H}, box {64, npad}
+    const int32_t *pt;
+    const float *w;
+    float *scores;
+    int32_t *nblk;
+    DevErr *err;
+    float scale;
+    int32_t max_pages, num_pages, S, R, H;
+    int32_t rpt;        // query rows a tile
+    int32_t nrt;        // row tiles a stream
+    int32_t npad;       // columns a tile, rounded up to 16
+    int32_t sink, local;
+    int64_t cols, ld;   // columns written, row stride
+    int64_t items;      // (stream, block tile, row tile)
+    int64_t item0[TF_MAX_STREAMS];
+    int64_t len[TF_MAX_STREAMS];
+};
+
+// The CTA's items: a run of the numbering, block tile by block tile of each stream.
+struct Items {
+    int64_t i, i1;
+    int s = -1;
+    int64_t bt = -1, rt = 0;
+    bool fresh = false;   // another block tile than the last item's
+    __device__ __forceinline__ explicit Items(const ScoreParams &p)
+        : i(p.items * blockIdx.x / gridDim.x), i1(p.items * (blockIdx.x + 1) / gridDim.x) {}
+    __device__ __forceinline__ bool next(const ScoreParams &p) {
+        if (i >= i1) return false;
+        if (s >= 0 && rt + 1 < p.nrt) {
+            ++rt;
+            fresh = false;
+        } else {
+            int a = s < 0 ? 0 : s, z = p.S - 1;
+            while (a < z) {
+                const int mid = (a + z + 1) >> 1;
+                if (p.item0[mid] <= i) a = mid; else z = mid - 1;
+            }
+            s = a;
+            const int64_t k = i - p.item0[s];
+            bt = k / p.nrt;
+            rt = k - bt * p.nrt;
+            fresh = true;
+        }
+        ++i;
+        return true;
+    }
+    // after next(): the last item of its block tile here
+    __device__ __forceinline__ bool last_of_tile(const ScoreParams &p) const { return i >= i1 || rt + 1 == p.nrt; }
+};
+
+// 64 values from x on of a page's eight block keys: one 1 KB atom of the 128-byte swizzle.
+__device__ __forceinline__ void tma_page_keys(void *dst, const CUtensorMap *tm, uint64_t *bar, int x, int page) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(ptx::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(ptx::smem_u32(bar)), "r"(x), "r"(0), "r"(page)
+        : "memory");
+}
+
+__global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_constant__ ScoreParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Ctrl &c = *reinterpret_cast<Ctrl *>(smem + SMEM_CTRL);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    ptx::griddep_launch_dependents();
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(&c.a_full, 1);
+        ptx::mbar_init(&c.a_free, 1);
+        for (int i = 0; i < STAGES; ++i) {
+            ptx::mbar_init(&c.b_full[i], 1);
+            ptx::mbar_init(&c.b_free[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&c.d_full[i], 1);
+            ptx::mbar_init(&c.d_free[i], 4);
+        }
+        ptx::mbar_init(&c.drain, 1);
+        c.abort = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 5) {
+        ptx::tmem_alloc(&c.tmem_base, TCOLS);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = c.tmem_base;
+    volatile int *abort = &c.abort;
+    ptx::griddep_wait();
+
+    if (warp == 4) {
+        // ================= TMA =================
+        // Lane 0 waits and loads the query boxes; a block tile's pages are loaded by a lane each (nine
+        // one-atom boxes of 8 blocks x 64 values a page, to where the 128-byte-swizzled tile has them).
+        if (lane == 0) {
+            ptx::prefetch_tmap(&p.tm_k);
+            ptx::prefetch_tmap(&p.tm_q);
+        }
+        const uint64_t pol_q = ptx::policy_evict_last();
+        int na = 0;        // block tiles loaded
+        int64_t nb = 0;    // query boxes loaded
+        bool ok = true;
+        for (Items it(p); ok && it.next(p);) {
+            if (it.fresh) {
+                if (na > 0) ok = ptx::mbar_wait_warp(&c.a_free, (na - 1) & 1, abort, p.err, 30);
+                if (!ok) break;
+                // the pages that hold blocks of the stream.  One out of the pool is left out (its scores
+                // are undefined); other lanes of the product do not see it.
+                const int64_t lp = it.bt * TILE_PAGES + lane;
+                bool load = lane < TILE_PAGES && lp < (p.len[it.s] + kPageRows - 1) / kPageRows;
+                int id = 0;
+                if (load) {
+                    id = p.pt ? __ldg(p.pt + (int64_t)it.s * p.max_pages + lp) : it.s * p.max_pages + (int)lp;
+                    if (id < 0 || id >= p.num_pages) {
+                        ptx::record_error(p.err, TF_E_DEVICE, id);
+                        load = false;
+                    }
+                }
+                const unsigned who = __ballot_sync(0xffffffffu, load);
+                if (lane == 0) ptx::mbar_arrive_expect_tx(&c.a_full, __popc(who) * PAGE_KEYS);
+                __syncwarp();
+                if (load)
+                    for (int k = 0; k < KBOX; ++k)
+                        tma_page_keys(smem + SMEM_A + lane * PAGE_KEYS + k * 1024, &p.tm_k, &c.a_full, k * 64, id);
+                ++na;
+            }
+            if (lane == 0) {
+                const int qrow = (int)(((int64_t)it.s * p.R + it.rt * p.rpt) * p.H);
+                for (int kb = 0; ok && kb < KBOX; ++kb) {
+                    const int64_t n = nb + kb;
+                    const int st = (int)(n % STAGES);
+                    if (n >= STAGES && !ptx::mbar_wait(&c.b_free[st], (uint32_t)(n / STAGES - 1) & 1, abort, p.err, 31)) {
+                        ok = false;
+                        nb -= KBOX - kb;   // the boxes that were not armed
+                        break;
+                    }
+                    ptx::mbar_arrive_expect_tx(&c.b_full[st], p.npad * 128);
+                    ptx::tma_load_2d(smem + SMEM_B + st * STAGE_BYTES, &p.tm_q, &c.b_full[st], kb * 64, qrow, pol_q);
+                }
+            }
+            nb += KBOX;
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        }
+        // no copy may still be writing shared memory when the CTA exits
+        if (lane == 0) {
+            if (na > 0) ptx::mbar_wait(&c.a_full, (na - 1) & 1, abort, p.err, 32, 1ll << 28);
+            for (int k = 0; k < STAGES; ++k)
+                if (nb > k) {
+                    const int64_t last = nb - 1 - k;
+                    ptx::mbar_wait(&c.b_full[last % STAGES], (uint32_t)(last / STAGES) & 1, abort, p.err, 32, 1ll << 28);
+                }
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        // ================= MMA =================
+        const uint64_t a0 = ptx::sdesc_sw128(ptx::smem_u32(smem + SMEM_A), 16, PAGE_KEYS);
+        const uint64_t b0 = ptx::sdesc_sw128(ptx::smem_u32(smem + SMEM_B), 16, 1024);
+        const uint32_t idesc = ptx::idesc_bf16_f32(M, p.npad, false, false);
+        int na = 0;
+        int64_t nb = 0, nd = 0;
+        bool ok = true;
+        for (Items it(p); ok && it.next(p); ++nd) {
+            if (it.fresh) {
+                if (!ptx::mbar_wait_warp(&c.a_full, na & 1, abort, p.err, 33)) break;
+                ++na;
+            }
+            const int buf = (int)(nd & 1);
+            if (nd >= 2 && !ptx::mbar_wait_warp(&c.d_free[buf], (uint32_t)(nd / 2 - 1) & 1, abort, p.err, 34)) break;
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int kb = 0; kb < KBOX; ++kb, ++nb) {
+                const int st = (int)(nb % STAGES);
+                if (!ptx::mbar_wait_warp(&c.b_full[st], (uint32_t)(nb / STAGES) & 1, abort, p.err, 35)) {
+                    ok = false;
+                    break;
+                }
+                ptx::mma4_bf16_ss_warp(tmem + buf * NMAX, a0 + (uint64_t)((kb * 1024) >> 4),
+                                       b0 + (uint64_t)((st * STAGE_BYTES) >> 4), idesc, kb == 0);
+                ptx::mma_commit_warp(&c.b_free[st]);
+            }
+            if (!ok) break;
+            ptx::mma_commit_warp(&c.d_full[buf]);
+            if (it.last_of_tile(p)) ptx::mma_commit_warp(&c.a_free);
+        }
+        // no MMA may still run when TMEM is freed
+        if (lane == 0) {
+            ptx::mma_commit(&c.drain);
+            ptx::mbar_wait(&c.drain, 0, abort, p.err, 36, 1ll << 29);
+        }
+        __syncwarp();
+    } else {
+        // ================= epilogue: a block a thread =================
+        const int tid = (int)threadIdx.x;
+        const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+        int64_t nd = 0;
+        bool ok = true;
+        for (Items it(p); it.next(p); ++nd) {
+            const int buf = (int)(nd & 1);
+            const int64_t r0 = it.rt * p.rpt;
+            const int nr = (int)(p.R - r0 < p.rpt ? p.R - r0 : p.rpt);
+            const int ncols = nr * p.H;
+            // the buffer's last readers (two items back) are past the previous item's barrier
+            if (p.w) c.w[buf][tid] = tid < ncols ? __ldg(p.w + ((int64_t)it.s * p.R + r0) * p.H + tid) : 0.f;
+            // the four warps leave together when a wait ran out
+            if (ptx::named_bar_or(1, 128, !ok || *abort)) break;
+            const float *w = c.w[buf];
+            if (!ptx::mbar_wait_warp(&c.d_full[buf], (uint32_t)(nd / 2) & 1, abort, p.err, 37)) {
+                ok = false;
+                continue;
+            }
+            ptx::tc_fence_after();
+            const int64_t b = it.bt * M + tid;
+            float *dst = p.scores + ((int64_t)it.s * p.R + r0) * p.ld + b;
+            int64_t pos = p.len[it.s] - p.R + r0;   // the row's position
+            float acc = 0.f;
+            int left = p.H;
+            for (int n0 = 0; n0 < ncols; n0 += 32) {
+                uint32_t v[32];
+                ptx::tmem_ld32(lane_base + buf * NMAX + n0, v);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    if (n0 + k >= ncols) break;
+                    const float x = fmaxf(__uint_as_float(v[k]), 0.f);
+                    acc = p.w ? fmaf(w[n0 + k], x, acc) : acc + x;
+                    if (--left == 0) {
+                        const int64_t mine = pos / ROWS;
+                        float y = acc * p.scale;
+                        if (b < p.sink || b > mine - p.local) y = INFINITY;
+                        if (b > mine) y = -INFINITY;
+                        if (b < p.cols) *dst = y;
+                        dst += p.ld;
+                        ++pos;
+                        acc = 0.f;
+                        left = p.H;
+                    }
+                }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&c.d_free[buf]);
+        }
+        // rows of streams with fewer block tiles than the longest: no block there; and every row's
+        // visible blocks
+        for (int64_t r = blockIdx.x; r < (int64_t)p.S * p.R; r += gridDim.x) {
+            const int s = (int)(r / p.R);
+            const int64_t len = p.len[s];
+            const int64_t nb = (len + ROWS - 1) / ROWS;
+            for (int64_t b = (nb + M - 1) / M * M + tid; b < p.cols; b += 128) p.scores[r * p.ld + b] = -INFINITY;
+            if (p.nblk && tid == 0) p.nblk[r] = (int32_t)((len - p.R + (r - (int64_t)s * p.R)) / ROWS + 1);
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == 5) ptx::tmem_dealloc(tmem, TCOLS);
+}
+
+}  // namespace blk
+
+int launch_block_keys(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_from,
+                      const int64_t *h_len, int S, void *d_bkeys, cudaStream_t st) {
+    using namespace blk;
+    KeysParams p;
+    const bool f8 = is_fp8(pool->desc);
+    p.pt = d_pt;
+    p.cache_base = pool->base + (size_t)cache * pool->desc.num_pages * page_bytes(pool->desc);
+    p.bkeys = static_cast<uint16_t *>(d_bkeys);
+    p.err = pool->err;
+    p.max_pages = max_pages;
+    p.num_pages = pool->desc.num_pages;
+    p.S = S;
+    int64_t n = 0;
+    for (int s = 0; s < S; ++s) {
+        p.off[s] = n;
+        p.len[s] = h_len[s];
+        p.first[s] = (int32_t)(h_from[s] / ROWS);
+        if (h_from[s] < h_len[s]) n += (h_len[s] + ROWS - 1) / ROWS - p.first[s];
+    }
+    p.off[S] = n;
+    if (n == 0) return TF_OK;
+    if (n > 0x7FFFFFFF) return TF_E_UNSUPPORTED;
+    if (prepare_launch(pool, st) != TF_OK) return TF_E_CUDA;
+    const cudaError_t e = f8 ? launch_pdl(block_keys_kernel<true>, dim3((unsigned)n), dim3(KeysShape<true>::T), 0, st, p)
+                             : launch_pdl(block_keys_kernel<false>, dim3((unsigned)n), dim3(KeysShape<false>::T), 0, st, p);
+    launch_counter()++;
+    return e == cudaSuccess ? TF_OK : TF_E_CUDA;
+}
+
+int launch_block_scores(tf_kvpool *pool, const void *d_bkeys, const int32_t *d_pt, int max_pages, const int64_t *h_len,
+                        int S, int R, int H, const void *d_q, const float *d_w, float scale, int sink, int local,
+                        float *d_scores, int64_t ld, int32_t *d_nblk, cudaStream_t st) {
+    using namespace blk;
+    static std::once_flag once;
+    static int ready_sms = 0;
+    std::call_once(once, [] {
+        int dev = 0, n = 0;
+        if (cudaFuncSetAttribute(block_scores_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL) ==
+                cudaSuccess &&
+            cudaGetDevice(&dev) == cudaSuccess &&
+            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+            ready_sms = n;
+    });
+    if (ready_sms <= 0) return TF_E_CUDA;
+    thread_local std::unique_ptr<ScoreParams> pp;
+    if (!pp) pp.reset(new ScoreParams());
+    ScoreParams &p = *pp;
+    {
+        const uint64_t dims[3] = {(uint64_t)kDk, (uint64_t)PER_PAGE, (uint64_t)pool->desc.num_pages};
+        const uint64_t strides[2] = {(uint64_t)kDk * 2, (uint64_t)PAGE_KEYS};
+        const uint32_t box[3] = {64, (uint32_t)PER_PAGE, 1};
+        if (!encode_tmap_bf16(&p.tm_k, const_cast<void *>(d_bkeys), 3, dims, strides, box)) return TF_E_CUDA;
+    }
+    p.rpt = std::min(R, std::max(1, NMAX / H));
+    p.nrt = (R + p.rpt - 1) / p.rpt;
+    p.npad = (p.rpt * H + 15) / 16 * 16;
+    {
+        const uint64_t dims[2] = {(uint64_t)kDk, (uint64_t)S * R * H};
+        const uint64_t strides[1] = {(uint64_t)kDk * 2};
+        const uint32_t box[2] = {64, (uint32_t)p.npad};
+        if (!encode_tmap_bf16(&p.tm_q, const_cast<void *>(d_q), 2, dims, strides, box)) return TF_E_CUDA;
+    }
+    p.pt = d_pt;
+    p.w = d_w;
+    p.scores = d_scores;
+    p.nblk = d_nblk;
+    p.err = pool->err;
+    p.scale = scale;
+    p.max_pages = max_pages;
+    p.num_pages = pool->desc.num_pages;
+    p.S = S;
+    p.R = R;
+    p.H = H;
+    p.sink = sink;
+    p.local = local;
+    p.ld = ld;
+    p.cols = 0;
+    p.items = 0;
+    for (int s = 0; s < S; ++s) {
+        const int64_t nb = (h_len[s] + ROWS - 1) / ROWS;
+        p.cols = std::max(p.cols, nb);
+        p.len[s] = h_len[s];
+        p.item0[s] = p.items;
+        p.items += (nb + M - 1) / M * p.nrt;
+    }
+    const int ctas = (int)std::min<int64_t>(p.items, ready_sms);
+    if (prepare_launch(pool, st) != TF_OK) return TF_E_CUDA;
+    const cudaError_t e = launch_pdl(block_scores_kernel, dim3((unsigned)ctas), dim3(THREADS), SMEM_TOTAL, st, p);
+    launch_counter()++;
+    return e == cudaSuccess ? TF_OK : TF_E_CUDA;
+}
+
+}  // namespace tf

@@ -3,6 +3,7 @@
 // error word and launch profiling.  Nothing here touches device memory except the
 // error word (zeroed before the first launch, read by tf_last_error) and the
 // kernels it launches.
+#include <algorithm>
 #include <cstdio>
 #include <cstring>
 #include <new>
@@ -312,6 +313,156 @@ extern "C" int tf_paged_mla_attend_sparse(tf_kvpool *p, int32_t cache, const int
         return d_ws && ws_bytes < need ? TF_E_NOMEM : TF_E_ARG;
     return launch_attend(p, cache, d_pt, max_pages, h_len, S, 1, H, d_q, scale, d_out, d_lse, d_ws, ws_bytes,
                          (cudaStream_t)stream, d_idx, max_idx, h_nidx);
+}
+
+// ---- attention over listed blocks, and of streams that share a prefix ----
+// What both calls and their workspace sizes refuse about the batch.
+static int batch_checks(int32_t S, int32_t R, int32_t H, const int64_t *h_len) {
+    if (!h_len || S < 1 || S > TF_MAX_STREAMS || R < 1 || H < 1 || H > TF_MAX_HEADS) return TF_E_ARG;
+    if ((int64_t)S * R * H > (int64_t)1 << 30) return TF_E_UNSUPPORTED;
+    for (int s = 0; s < S; ++s) {
+        if (h_len[s] < R) return TF_E_RANGE;
+        if (h_len[s] > kMaxStreamRows) return TF_E_UNSUPPORTED;
+    }
+    return TF_OK;
+}
+
+// What both calls refuse beyond that, but for the workspace.
+static int call_checks(const tf_kvpool *p, int32_t cache, const int32_t *d_pt, int32_t max_pages, const int64_t *h_len,
+                       int32_t S, const void *d_q, float scale, const void *d_out) {
+    if (!p || !d_q || !d_out || max_pages < 1) return TF_E_ARG;
+    if (!(scale > 0.0f) || scale == 1.0f / 0.0f) return TF_E_ARG;
+    if (cache < 0 || cache >= p->desc.num_caches) return TF_E_RANGE;
+    if (!d_pt && (int64_t)S * max_pages > p->desc.num_pages) return TF_E_RANGE;
+    for (int s = 0; s < S; ++s)
+        if (h_len[s] > (int64_t)max_pages * kPageRows) return TF_E_RANGE;
+    if ((reinterpret_cast<uintptr_t>(d_q) & 15u) != 0 || (reinterpret_cast<uintptr_t>(d_out) & 15u) != 0)
+        return TF_E_ARG;
+    return TF_OK;
+}
+
+static int ws_check(size_t need, const void *d_ws, size_t ws_bytes) {
+    if (need == 0) return TF_OK;
+    if (!d_ws || (reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0) return TF_E_ARG;
+    return ws_bytes < need ? TF_E_NOMEM : TF_OK;
+}
+
+// Host arithmetic on caller sizes allocates (the plan's unit table), and no exception leaves a C entry.
+template <typename F>
+static int no_throw(F &&f) {
+    try {
+        return f();
+    } catch (const std::bad_alloc &) {
+        return TF_E_NOMEM;
+    }
+}
+
+static int blocks_size(int32_t S, int32_t R, int32_t H, const int64_t *h_len, int32_t max_blk, size_t *bytes) {
+    const int rc = batch_checks(S, R, H, h_len);
+    if (rc != TF_OK) return rc;
+    if (max_blk < 1) return TF_E_ARG;
+    return no_throw([&] {
+        *bytes = blocks_workspace_bytes(S, R, H, h_len, max_blk);
+        return TF_OK;
+    });
+}
+
+extern "C" size_t tf_paged_mla_blocks_workspace_bytes(const tf_kvpool *, int32_t S, int32_t R, int32_t H,
+                                                      const int64_t *h_len, int32_t max_blk) {
+    size_t n = 0;
+    return blocks_size(S, R, H, h_len, max_blk, &n) == TF_OK ? n : 0;
+}
+
+extern "C" int tf_paged_mla_attend_blocks(tf_kvpool *p, int32_t cache, const int32_t *d_pt, int32_t max_pages,
+                                          const int64_t *h_len, const int32_t *d_blk, int32_t max_blk, int32_t S,
+                                          int32_t R, int32_t H, const void *d_q, float scale, void *d_out,
+                                          float *d_lse, void *d_ws, size_t ws_bytes, void *stream) {
+    size_t need = 0;
+    int rc = blocks_size(S, R, H, h_len, max_blk, &need);
+    if (rc == TF_OK) rc = call_checks(p, cache, d_pt, max_pages, h_len, S, d_q, scale, d_out);
+    if (rc == TF_OK && !d_blk) rc = TF_E_ARG;
+    if (rc == TF_OK) rc = ws_check(need, d_ws, ws_bytes);
+    if (rc != TF_OK) return rc;
+    return no_throw([&] {
+        return launch_attend_blocks(p, cache, d_pt, max_pages, h_len, d_blk, max_blk, S, R, H, d_q, scale, d_out,
+                                    d_lse, d_ws, (cudaStream_t)stream);
+    });
+}
+
+static int shared_size(int32_t S, int32_t R, int32_t H, const int64_t *h_len, const int32_t *h_gsize, int32_t G,
+                       const int64_t *h_prefix, size_t *bytes) {
+    const int rc = batch_checks(S, R, H, h_len);
+    if (rc != TF_OK) return rc;
+    if (!h_gsize || !h_prefix || G < 1 || G > S) return TF_E_ARG;
+    int64_t sum = 0;
+    for (int g = 0; g < G; ++g) {
+        if (h_gsize[g] < 1) return TF_E_ARG;
+        sum += h_gsize[g];
+    }
+    if (sum != S) return TF_E_ARG;
+    // every row of every stream of the group sees the whole prefix
+    for (int g = 0, s = 0; g < G; ++g)
+        for (int k = 0; k < h_gsize[g]; ++k, ++s)
+            if (h_prefix[g] < 0 || h_prefix[g] > h_len[s] - R + 1) return TF_E_RANGE;
+    return no_throw([&] { return shared_workspace_bytes(S, R, H, h_len, h_gsize, G, h_prefix, bytes); });
+}
+
+extern "C" size_t tf_paged_mla_shared_workspace_bytes(const tf_kvpool *, int32_t S, int32_t R, int32_t H,
+                                                      const int64_t *h_len, const int32_t *h_gsize, int32_t G,
+                                                      const int64_t *h_prefix) {
+    size_t n = 0;
+    return shared_size(S, R, H, h_len, h_gsize, G, h_prefix, &n) == TF_OK ? n : 0;
+}
+
+extern "C" int tf_paged_mla_attend_shared(tf_kvpool *p, int32_t cache, const int32_t *d_pt, int32_t max_pages,
+                                          const int64_t *h_len, const int32_t *h_gsize, int32_t G,
+                                          const int64_t *h_prefix, int32_t S, int32_t R, int32_t H, const void *d_q,
+                                          float scale, void *d_out, float *d_lse, void *d_ws, size_t ws_bytes,
+                                          void *stream) {
+    size_t need = 0;
+    int rc = shared_size(S, R, H, h_len, h_gsize, G, h_prefix, &need);
+    if (rc == TF_OK) rc = call_checks(p, cache, d_pt, max_pages, h_len, S, d_q, scale, d_out);
+    if (rc == TF_OK) rc = ws_check(need, d_ws, ws_bytes);
+    if (rc != TF_OK) return rc;
+    return no_throw([&] {
+        return launch_attend_shared(p, cache, d_pt, max_pages, h_len, h_gsize, G, h_prefix, S, R, H, d_q, scale, d_out,
+                                    d_lse, d_ws, (cudaStream_t)stream);
+    });
+}
+
+// ---- block keys and scores ----
+extern "C" size_t tf_block_keys_bytes(const tf_kvpool *p) {
+    return p ? (size_t)p->desc.num_pages * (kPageRows / TF_BLOCK_ROWS) * kDk * 2 : 0;
+}
+
+extern "C" int tf_block_keys_update(tf_kvpool *p, int32_t cache, const int32_t *d_pt, int32_t max_pages,
+                                    const int64_t *h_from, const int64_t *h_len, int32_t S, void *d_bkeys,
+                                    void *stream) {
+    if (!p || !h_from || !h_len || !d_bkeys || S < 1 || S > TF_MAX_STREAMS || max_pages < 1) return TF_E_ARG;
+    if ((reinterpret_cast<uintptr_t>(d_bkeys) & 15u) != 0) return TF_E_ARG;
+    if (cache < 0 || cache >= p->desc.num_caches) return TF_E_RANGE;
+    if (!d_pt && (int64_t)S * max_pages > p->desc.num_pages) return TF_E_RANGE;
+    for (int s = 0; s < S; ++s)
+        if (h_from[s] < 0 || h_from[s] > h_len[s] || h_len[s] > (int64_t)max_pages * kPageRows) return TF_E_RANGE;
+    for (int s = 0; s < S; ++s)
+        if (h_len[s] > kMaxStreamRows) return TF_E_UNSUPPORTED;
+    return launch_block_keys(p, cache, d_pt, max_pages, h_from, h_len, S, d_bkeys, (cudaStream_t)stream);
+}
+
+extern "C" int tf_block_scores(tf_kvpool *p, const void *d_bkeys, const int32_t *d_pt, int32_t max_pages,
+                               const int64_t *h_len, int32_t S, int32_t R, int32_t H, const void *d_q, const float *d_w,
+                               float scale, int32_t sink, int32_t local, float *d_scores, int64_t ld, int32_t *d_nblk,
+                               void *stream) {
+    int rc = batch_checks(S, R, H, h_len);
+    // the scores' checks of pool, table, queries, scale and output are the attention's
+    if (rc == TF_OK) rc = call_checks(p, 0, d_pt, max_pages, h_len, S, d_q, scale, d_scores);
+    if (rc != TF_OK) return rc;
+    if (!d_bkeys || (reinterpret_cast<uintptr_t>(d_bkeys) & 15u) != 0 || sink < 0 || local < 1) return TF_E_ARG;
+    int64_t cols = 0;
+    for (int s = 0; s < S; ++s) cols = std::max(cols, (h_len[s] + TF_BLOCK_ROWS - 1) / TF_BLOCK_ROWS);
+    if (ld % 4 != 0 || ld < cols) return TF_E_ARG;
+    return launch_block_scores(p, d_bkeys, d_pt, max_pages, h_len, S, R, H, d_q, d_w, scale, sink, local, d_scores, ld,
+                               d_nblk, (cudaStream_t)stream);
 }
 
 extern "C" int tf_state_copy_rows(tf_kvpool *p, int32_t cache, const int32_t *d_src, const int32_t *d_dst,

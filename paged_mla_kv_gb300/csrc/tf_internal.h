@@ -10,6 +10,7 @@
 #include <utility>
 #include <vector>
 
+#include "../../include/tf_blocks.h"
 #include "../../include/tf_paged_mla.h"
 
 namespace tf {
@@ -142,5 +143,26 @@ int launch_attend(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages
                   int R, int H, const void *d_q, float scale, void *d_out, float *d_lse, void *d_ws,
                   size_t ws_bytes, cudaStream_t st, const int32_t *d_idx = nullptr, int max_idx = 0,
                   const int32_t *h_nidx = nullptr);
+// Attention over listed blocks, and of streams that share a prefix (attend.cu).
+size_t blocks_workspace_bytes(int S, int R, int H, const int64_t *h_len, int max_blk);
+int launch_attend_blocks(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_len,
+                         const int32_t *d_blk, int max_blk, int S, int R, int H, const void *d_q, float scale,
+                         void *d_out, float *d_lse, void *d_ws, cudaStream_t st);
+// TF_E_UNSUPPORTED: too many streams and sharing groups for one launch.
+int shared_workspace_bytes(int S, int R, int H, const int64_t *h_len, const int32_t *h_gsize, int G,
+                           const int64_t *h_prefix, size_t *bytes);
+int launch_attend_shared(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_len,
+                         const int32_t *h_gsize, int G, const int64_t *h_prefix, int S, int R, int H, const void *d_q,
+                         float scale, void *d_out, float *d_lse, void *d_ws, cudaStream_t st);
+// Block keys and their scores (blocks.cu).
+int launch_block_keys(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_from,
+                      const int64_t *h_len, int S, void *d_bkeys, cudaStream_t st);
+int launch_block_scores(tf_kvpool *pool, const void *d_bkeys, const int32_t *d_pt, int max_pages, const int64_t *h_len,
+                        int S, int R, int H, const void *d_q, const float *d_w, float scale, int sink, int local,
+                        float *d_scores, int64_t ld, int32_t *d_nblk, cudaStream_t st);
+
+// The driver's tensor-map encoder (attend.cu); null without a driver.
+bool encode_tmap_bf16(CUtensorMap *tm, void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                      const uint32_t *box);
 
 }  // namespace tf
