@@ -171,9 +171,10 @@ struct Ctrl {
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
-    float w[2][NMAX];
+    alignas(16) float w[2][NMAX];
 };
 constexpr int SMEM_TOTAL = SMEM_CTRL + (int)sizeof(Ctrl) + 1024;
+static_assert(ROWS == 64, "positions are shifted by 6");
 static_assert(SMEM_TOTAL <= 232448, "shared memory budget");
 
 struct ScoreParams {
@@ -237,6 +238,19 @@ __device__ __forceinline__ void tma_page_keys(void *dst, const CUtensorMap *tm, 
         : "memory");
 }
 
+// a * b + c on two values at once
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+// C: a divisor of H that the epilogue adds up without asking whether the query row ends (32, 8 or 1;
+// at C = 1 the 128 questions a tile cost more than its products).
+template <int C>
 __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_constant__ ScoreParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -393,26 +407,40 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
             const int64_t b = it.bt * M + tid;
             float *dst = p.scores + ((int64_t)it.s * p.R + r0) * p.ld + b;
             int64_t pos = p.len[it.s] - p.R + r0;   // the row's position
-            float acc = 0.f;
+            float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             int left = p.H;
             for (int n0 = 0; n0 < ncols; n0 += 32) {
                 uint32_t v[32];
                 ptx::tmem_ld32(lane_base + buf * NMAX + n0, v);
                 ptx::tmem_ld_wait();
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    if (n0 + k >= ncols) break;
-                    const float x = fmaxf(__uint_as_float(v[k]), 0.f);
-                    acc = p.w ? fmaf(w[n0 + k], x, acc) : acc + x;
-                    if (--left == 0) {
-                        const int64_t mine = pos / ROWS;
-                        float y = acc * p.scale;
+                for (int j = 0; j < 32; j += C) {
+                    if (n0 + j >= ncols) break;
+                    if (C == 1) {
+                        acc[0].x = fmaf(p.w ? w[n0 + j] : 1.f, fmaxf(__uint_as_float(v[j]), 0.f), acc[0].x);
+                    } else {
+#pragma unroll
+                        for (int k = j; k < j + C; k += 4) {
+                            const float4 wk = p.w ? *reinterpret_cast<const float4 *>(w + n0 + k)
+                                                  : make_float4(1.f, 1.f, 1.f, 1.f);
+                            acc[0] = fma2(make_float2(wk.x, wk.y),
+                                          make_float2(fmaxf(__uint_as_float(v[k]), 0.f),
+                                                      fmaxf(__uint_as_float(v[k + 1]), 0.f)), acc[0]);
+                            acc[1] = fma2(make_float2(wk.z, wk.w),
+                                          make_float2(fmaxf(__uint_as_float(v[k + 2]), 0.f),
+                                                      fmaxf(__uint_as_float(v[k + 3]), 0.f)), acc[1]);
+                        }
+                    }
+                    left -= C;
+                    if (left == 0) {
+                        const int mine = (int)(pos >> 6);
+                        float y = ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) * p.scale;
                         if (b < p.sink || b > mine - p.local) y = INFINITY;
                         if (b > mine) y = -INFINITY;
                         if (b < p.cols) *dst = y;
                         dst += p.ld;
                         ++pos;
-                        acc = 0.f;
+                        acc[0] = acc[1] = make_float2(0.f, 0.f);
                         left = p.H;
                     }
                 }
@@ -477,9 +505,10 @@ int launch_block_scores(tf_kvpool *pool, const void *d_bkeys, const int32_t *d_p
     static int ready_sms = 0;
     std::call_once(once, [] {
         int dev = 0, n = 0;
-        if (cudaFuncSetAttribute(block_scores_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL) ==
-                cudaSuccess &&
-            cudaGetDevice(&dev) == cudaSuccess &&
+        bool ok = true;
+        for (auto *kern : {block_scores_kernel<32>, block_scores_kernel<8>, block_scores_kernel<1>})
+            ok = ok && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL) == cudaSuccess;
+        if (ok && cudaGetDevice(&dev) == cudaSuccess &&
             cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
             ready_sms = n;
     });
@@ -527,7 +556,8 @@ int launch_block_scores(tf_kvpool *pool, const void *d_bkeys, const int32_t *d_p
     }
     const int ctas = (int)std::min<int64_t>(p.items, ready_sms);
     if (prepare_launch(pool, st) != TF_OK) return TF_E_CUDA;
-    const cudaError_t e = launch_pdl(block_scores_kernel, dim3((unsigned)ctas), dim3(THREADS), SMEM_TOTAL, st, p);
+    auto *kern = H % 32 == 0 ? block_scores_kernel<32> : H % 8 == 0 ? block_scores_kernel<8> : block_scores_kernel<1>;
+    const cudaError_t e = launch_pdl(kern, dim3((unsigned)ctas), dim3(THREADS), SMEM_TOTAL, st, p);
     launch_counter()++;
     return e == cudaSuccess ? TF_OK : TF_E_CUDA;
 }
