@@ -362,7 +362,7 @@ def _given(what: str, ok: bool) -> None:
 
 
 def _dense(t, dtype: str, shape=None) -> bool:
-    return t is None or (str(t.dtype) == dtype and t.is_contiguous() and (shape is None or tuple(t.shape) == shape))
+    return t is None or (str(t.dtype) == dtype and t.is_contiguous() and (shape is None or t.shape == shape))
 
 
 def _qout(q, out, lse) -> bool:
@@ -396,7 +396,7 @@ def tf_block_scores(pool: KVPool, bkeys, pt, max_pages: int, lens, q, scale: flo
     _given("tf_block_scores", len(a) == S and _dense(q, "torch.bfloat16") and _dense(w, "torch.float32", (S, R, H)) and
            _dense(bkeys, "torch.bfloat16", (pool.num_pages, 8, 576)) and str(scores.dtype) == "torch.float32" and
            scores.dim() == 2 and scores.shape[0] == S * R and scores.stride(1) == 1 and
-           scores.shape[1] >= -(-int(a.max()) // TF_BLOCK_ROWS) and
+           scores.shape[1] * TF_BLOCK_ROWS >= (max(lens) if type(lens) is list else int(a.max())) and
            (nblk is None or (_dense(nblk, "torch.int32") and nblk.numel() == S * R)))
     _check(lib().tf_block_scores(pool.handle, _ptr(bkeys), _ptr(pt), max_pages, p, S, R, H, _ptr(q), _ptr(w),
                                  float(scale), int(sink), int(local), _ptr(scores), int(scores.stride(0)), _ptr(nblk),

@@ -144,30 +144,37 @@ __global__ void __launch_bounds__(KeysShape<FP8>::T) block_keys_kernel(const __g
 
 // ---- block scores ----
 // A GEMM of the block keys with the queries, blocks on the accumulator's lanes:
-//   D[128 blocks][N columns] = K[128][576] . Q[N][576]^T      tcgen05.mma M = 128, K in 9 boxes of 64
+//   D[256 blocks][N columns] = K[256][576] . Q[N][576]^T      tcgen05.mma cta_group::2, M = 256,
+//                                                             K in 9 boxes of 64
 // so a thread of the epilogue holds one block and adds the rectified products of a query row's
 // heads, which lie along its columns, in registers; a warp's stores are 128 bytes of a score row.
-// A tile's columns are as many whole query rows as fit 128 columns.  A CTA walks a run of tiles,
-// block tile by block tile, so the block keys (144 KB) stay in shared memory while query tiles
-// stream through a ring of 64-wide boxes; two accumulators let a tile's products run under the
-// last one's epilogue.
-constexpr int M = 128;                        // blocks a tile: 16 pages of 8
+// A tile's columns are as many whole query rows as fit 256 columns.  A pair of CTAs walks a run of
+// tiles, block tile by block tile, so the block keys (128 a CTA, 144 KB) stay in shared memory while
+// query tiles stream through a ring of 64-wide boxes; two accumulators let a tile's products run
+// under the last one's epilogue.  Why a pair: each CTA holds and loads half of a query box, so a box
+// of 16 KB feeds 512 cycles of products instead of 256.  One CTA alone (M = 128, N = 128) needs 64
+// bytes a cycle of its queries from L2 and 128 + 64 of shared memory's 128, and took 323 us for 2,048
+// rows of 64 heads against 1,595 blocks, where the products alone take 126 us.
+constexpr int M = 128;                        // blocks a CTA: 16 pages of 8
+constexpr int MP = 2 * M;                     // blocks a pair
 constexpr int TILE_PAGES = M / PER_PAGE;
-constexpr int NMAX = 128;                     // columns a tile
+constexpr int NMAX = 256;                     // columns a tile
 constexpr int KBOX = kDk / 64;                // 9
 constexpr int PAGE_KEYS = PER_PAGE * kDk * 2; // 9,216 bytes: [9 boxes][8 blocks][64 values], swizzled
 constexpr int STAGES = 4;
-constexpr int STAGE_BYTES = NMAX * 128;
+constexpr int STAGE_BYTES = NMAX / 2 * 128;
 constexpr int SMEM_A = 0;
 constexpr int SMEM_B = SMEM_A + TILE_PAGES * PAGE_KEYS;
 constexpr int SMEM_CTRL = SMEM_B + STAGES * STAGE_BYTES;
 constexpr int THREADS = 192;                  // 4 epilogue warps, the TMA warp, the MMA warp
 constexpr int TCOLS = 2 * NMAX;
 
+// Barriers marked L are waited on in the leader (rank 0) only and reached from both CTAs; the
+// others are each CTA's own, and the MMA warp's commits arrive on both.
 struct Ctrl {
-    uint64_t a_full, a_free;
-    uint64_t b_full[STAGES], b_free[STAGES];
-    uint64_t d_full[2], d_free[2];
+    uint64_t a_full, a_free;                    // L: both CTAs' block keys landed; the tile's products are done
+    uint64_t b_full[STAGES], b_free[STAGES];    // L: both halves of a query box landed; its products are done
+    uint64_t d_full[2], d_free[2];              // accumulator computed; L: read by the eight epilogue warps
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
@@ -179,7 +186,7 @@ static_assert(SMEM_TOTAL <= 232448, "shared memory budget");
 
 struct ScoreParams {
     CUtensorMap tm_k;   // 3D {576, 8 blocks, pages}, box {64, 8, 1}
-    CUtensorMap tm_q;   // 2D {576, S*R*H}, box {64, npad}
+    CUtensorMap tm_q;   // 2D {576, S*R*H}, box {64, npad / 2}
     const int32_t *pt;
     const float *w;
     float *scores;
@@ -189,7 +196,7 @@ struct ScoreParams {
     int32_t max_pages, num_pages, S, R, H;
     int32_t rpt;        // query rows a tile
     int32_t nrt;        // row tiles a stream
-    int32_t npad;       // columns a tile, rounded up to 16
+    int32_t npad;       // columns a tile, rounded up to 32
     int32_t sink, local;
     int64_t cols, ld;   // columns written, row stride
     int64_t items;      // (stream, block tile, row tile)
@@ -197,14 +204,14 @@ struct ScoreParams {
     int64_t len[TF_MAX_STREAMS];
 };
 
-// The CTA's items: a run of the numbering, block tile by block tile of each stream.
+// The pair's items: a run of the numbering, block tile by block tile of each stream.
 struct Items {
     int64_t i, i1;
     int s = -1;
     int64_t bt = -1, rt = 0;
     bool fresh = false;   // another block tile than the last item's
     __device__ __forceinline__ explicit Items(const ScoreParams &p)
-        : i(p.items * blockIdx.x / gridDim.x), i1(p.items * (blockIdx.x + 1) / gridDim.x) {}
+        : i(p.items * (blockIdx.x / 2) / (gridDim.x / 2)), i1(p.items * (blockIdx.x / 2 + 1) / (gridDim.x / 2)) {}
     __device__ __forceinline__ bool next(const ScoreParams &p) {
         if (i >= i1) return false;
         if (s >= 0 && rt + 1 < p.nrt) {
@@ -229,12 +236,81 @@ struct Items {
     __device__ __forceinline__ bool last_of_tile(const ScoreParams &p) const { return i >= i1 || rt + 1 == p.nrt; }
 };
 
+// ---- a pair of CTAs ----
+__device__ __forceinline__ uint32_t pair_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// the address, in the pair's shared memory, of this CTA's `p` in the leader
+__device__ __forceinline__ uint32_t leader_addr(const void *p) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(ptx::smem_u32(p)));
+    return a;
+}
+__device__ __forceinline__ void pair_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// TMA into this CTA's shared memory, completing on a barrier of the pair.
 // 64 values from x on of a page's eight block keys: one 1 KB atom of the 128-byte swizzle.
-__device__ __forceinline__ void tma_page_keys(void *dst, const CUtensorMap *tm, uint64_t *bar, int x, int page) {
+__device__ __forceinline__ void tma_page_keys(void *dst, const CUtensorMap *tm, uint32_t bar, int x, int page) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(ptx::smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(ptx::smem_u32(bar)), "r"(x), "r"(0), "r"(page)
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(x), "r"(0), "r"(page)
+        : "memory");
+}
+__device__ __forceinline__ void tma_queries(void *dst, const CUtensorMap *tm, uint32_t bar, int x, int row,
+                                            uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(ptx::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(x), "r"(row), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t *dst, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(ptx::smem_u32(dst)), "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// Four MMAs along K on one 64-value box (32 bytes of each operand's rows a step); one elected lane
+// issues for the pair; `first` = 1 starts the accumulator.
+__device__ __forceinline__ void pair_mma4_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t first) {
+    asm volatile(
+        "{\n\t.reg .pred e, p;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+        "add.u64 a1, %1, 2;\n\tadd.u64 a2, %1, 4;\n\tadd.u64 a3, %1, 6;\n\t"
+        "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"
+        "setp.eq.b32 p, %4, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %3, 1;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %3, 1;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %3, 1;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(first)
+        : "memory");
+}
+// Arrive once on this CTA's `bar` when the pair's MMAs issued so far complete.
+__device__ __forceinline__ void pair_commit_own_warp(uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(ptx::smem_u32(bar))
+        : "memory");
+}
+// The same on `bar` of both CTAs.
+__device__ __forceinline__ void pair_commit_warp(uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .b16 both;\n\tmov.b16 both, 3;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], both;\n\t}" ::"r"(
+            ptx::smem_u32(bar))
         : "memory");
 }
 
@@ -257,6 +333,7 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
     Ctrl &c = *reinterpret_cast<Ctrl *>(smem + SMEM_CTRL);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     ptx::griddep_launch_dependents();
+    const uint32_t rank = pair_rank();
     if (threadIdx.x == 0) {
         ptx::mbar_init(&c.a_full, 1);
         ptx::mbar_init(&c.a_free, 1);
@@ -266,18 +343,16 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&c.d_full[i], 1);
-            ptx::mbar_init(&c.d_free[i], 4);
+            ptx::mbar_init(&c.d_free[i], 8);
         }
         ptx::mbar_init(&c.drain, 1);
         c.abort = 0;
         ptx::fence_mbar_init();
     }
-    if (warp == 5) {
-        ptx::tmem_alloc(&c.tmem_base, TCOLS);
-        ptx::tmem_relinquish();
-    }
+    if (warp == 5) pair_tmem_alloc(&c.tmem_base, TCOLS);
     ptx::tc_fence_before();
     __syncthreads();
+    pair_sync();   // the peer's barriers are ready
     ptx::tc_fence_after();
     const uint32_t tmem = c.tmem_base;
     volatile int *abort = &c.abort;
@@ -285,13 +360,16 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
 
     if (warp == 4) {
         // ================= TMA =================
-        // Lane 0 waits and loads the query boxes; a block tile's pages are loaded by a lane each (nine
-        // one-atom boxes of 8 blocks x 64 values a page, to where the 128-byte-swizzled tile has them).
+        // Lane 0 waits and loads this CTA's half of each query box; its half of a block tile is
+        // loaded a page a lane (nine one-atom boxes of 8 blocks x 64 values, to where the
+        // 128-byte-swizzled tile has them).  All land on the leader's barriers, which the leader arms
+        // with the bytes of both halves.
         if (lane == 0) {
             ptx::prefetch_tmap(&p.tm_k);
             ptx::prefetch_tmap(&p.tm_q);
         }
         const uint64_t pol_q = ptx::policy_evict_last();
+        const uint32_t a_bar = leader_addr(&c.a_full);
         int na = 0;        // block tiles loaded
         int64_t nb = 0;    // query boxes loaded
         bool ok = true;
@@ -299,61 +377,70 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
             if (it.fresh) {
                 if (na > 0) ok = ptx::mbar_wait_warp(&c.a_free, (na - 1) & 1, abort, p.err, 30);
                 if (!ok) break;
-                // the pages that hold blocks of the stream.  One out of the pool is left out (its scores
-                // are undefined); other lanes of the product do not see it.
-                const int64_t lp = it.bt * TILE_PAGES + lane;
-                bool load = lane < TILE_PAGES && lp < (p.len[it.s] + kPageRows - 1) / kPageRows;
-                int id = 0;
-                if (load) {
-                    id = p.pt ? __ldg(p.pt + (int64_t)it.s * p.max_pages + lp) : it.s * p.max_pages + (int)lp;
+                // a lane past the stream's pages takes its last one again (no score is made of it); for a
+                // page out of the pool page 0 stands in (the scores are undefined)
+                if (lane < TILE_PAGES) {
+                    const int64_t pages = (p.len[it.s] + kPageRows - 1) / kPageRows;
+                    int64_t lp = it.bt * (2 * TILE_PAGES) + rank * TILE_PAGES + lane;
+                    const bool there = lp < pages;
+                    if (!there) lp = pages - 1;
+                    int id = p.pt ? __ldg(p.pt + (int64_t)it.s * p.max_pages + lp) : it.s * p.max_pages + (int)lp;
                     if (id < 0 || id >= p.num_pages) {
-                        ptx::record_error(p.err, TF_E_DEVICE, id);
-                        load = false;
+                        if (there) ptx::record_error(p.err, TF_E_DEVICE, id);
+                        id = 0;
                     }
-                }
-                const unsigned who = __ballot_sync(0xffffffffu, load);
-                if (lane == 0) ptx::mbar_arrive_expect_tx(&c.a_full, __popc(who) * PAGE_KEYS);
-                __syncwarp();
-                if (load)
+                    if (lane == 0 && rank == 0) ptx::mbar_arrive_expect_tx(&c.a_full, 2 * TILE_PAGES * PAGE_KEYS);
                     for (int k = 0; k < KBOX; ++k)
-                        tma_page_keys(smem + SMEM_A + lane * PAGE_KEYS + k * 1024, &p.tm_k, &c.a_full, k * 64, id);
+                        tma_page_keys(smem + SMEM_A + lane * PAGE_KEYS + k * 1024, &p.tm_k, a_bar, k * 64, id);
+                }
+                __syncwarp();
                 ++na;
             }
             if (lane == 0) {
-                const int qrow = (int)(((int64_t)it.s * p.R + it.rt * p.rpt) * p.H);
+                const int qrow = (int)(((int64_t)it.s * p.R + it.rt * p.rpt) * p.H) + (int)rank * (p.npad / 2);
                 for (int kb = 0; ok && kb < KBOX; ++kb) {
                     const int64_t n = nb + kb;
                     const int st = (int)(n % STAGES);
                     if (n >= STAGES && !ptx::mbar_wait(&c.b_free[st], (uint32_t)(n / STAGES - 1) & 1, abort, p.err, 31)) {
                         ok = false;
-                        nb -= KBOX - kb;   // the boxes that were not armed
+                        nb -= KBOX - kb;   // the boxes that were not loaded
                         break;
                     }
-                    ptx::mbar_arrive_expect_tx(&c.b_full[st], p.npad * 128);
-                    ptx::tma_load_2d(smem + SMEM_B + st * STAGE_BYTES, &p.tm_q, &c.b_full[st], kb * 64, qrow, pol_q);
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(&c.b_full[st], p.npad * 128);
+                    tma_queries(smem + SMEM_B + st * STAGE_BYTES, &p.tm_q, leader_addr(&c.b_full[st]), kb * 64, qrow, pol_q);
                 }
             }
             nb += KBOX;
             ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
         }
-        // no copy may still be writing shared memory when the CTA exits
+        // No copy may still be writing shared memory when a CTA exits, nor a commit of the leader's be
+        // on its way to a barrier of the peer's: what was loaded last has to be released.
         if (lane == 0) {
-            if (na > 0) ptx::mbar_wait(&c.a_full, (na - 1) & 1, abort, p.err, 32, 1ll << 28);
+            if (na > 0) ptx::mbar_wait(&c.a_free, (na - 1) & 1, abort, p.err, 32, 1ll << 28);
             for (int k = 0; k < STAGES; ++k)
                 if (nb > k) {
                     const int64_t last = nb - 1 - k;
-                    ptx::mbar_wait(&c.b_full[last % STAGES], (uint32_t)(last / STAGES) & 1, abort, p.err, 32, 1ll << 28);
+                    ptx::mbar_wait(&c.b_free[last % STAGES], (uint32_t)(last / STAGES) & 1, abort, p.err, 32, 1ll << 28);
                 }
+            // after a wait that ran out: the copies themselves (all land on the leader's barriers)
+            if (*abort && rank == 0) {
+                if (na > 0) ptx::mbar_wait(&c.a_full, (na - 1) & 1, abort, p.err, 32, 1ll << 28);
+                for (int k = 0; k < STAGES; ++k)
+                    if (nb > k) {
+                        const int64_t last = nb - 1 - k;
+                        ptx::mbar_wait(&c.b_full[last % STAGES], (uint32_t)(last / STAGES) & 1, abort, p.err, 32, 1ll << 28);
+                    }
+            }
         }
         __syncwarp();
     } else if (warp == 5) {
-        // ================= MMA =================
+        // ================= MMA (the leader, for the pair) =================
         const uint64_t a0 = ptx::sdesc_sw128(ptx::smem_u32(smem + SMEM_A), 16, PAGE_KEYS);
         const uint64_t b0 = ptx::sdesc_sw128(ptx::smem_u32(smem + SMEM_B), 16, 1024);
-        const uint32_t idesc = ptx::idesc_bf16_f32(M, p.npad, false, false);
+        const uint32_t idesc = ptx::idesc_bf16_f32(MP, p.npad, false, false);
         int na = 0;
         int64_t nb = 0, nd = 0;
-        bool ok = true;
+        bool ok = rank == 0;
         for (Items it(p); ok && it.next(p); ++nd) {
             if (it.fresh) {
                 if (!ptx::mbar_wait_warp(&c.a_full, na & 1, abort, p.err, 33)) break;
@@ -369,18 +456,18 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
                     ok = false;
                     break;
                 }
-                ptx::mma4_bf16_ss_warp(tmem + buf * NMAX, a0 + (uint64_t)((kb * 1024) >> 4),
-                                       b0 + (uint64_t)((st * STAGE_BYTES) >> 4), idesc, kb == 0);
-                ptx::mma_commit_warp(&c.b_free[st]);
+                pair_mma4_warp(tmem + buf * NMAX, a0 + (uint64_t)((kb * 1024) >> 4),
+                               b0 + (uint64_t)((st * STAGE_BYTES) >> 4), idesc, kb == 0);
+                pair_commit_warp(&c.b_free[st]);
             }
             if (!ok) break;
-            ptx::mma_commit_warp(&c.d_full[buf]);
-            if (it.last_of_tile(p)) ptx::mma_commit_warp(&c.a_free);
+            pair_commit_warp(&c.d_full[buf]);
+            if (it.last_of_tile(p)) pair_commit_warp(&c.a_free);
         }
         // no MMA may still run when TMEM is freed
-        if (lane == 0) {
-            ptx::mma_commit(&c.drain);
-            ptx::mbar_wait(&c.drain, 0, abort, p.err, 36, 1ll << 29);
+        if (rank == 0) {
+            pair_commit_own_warp(&c.drain);
+            if (lane == 0) ptx::mbar_wait(&c.drain, 0, abort, p.err, 36, 1ll << 29);
         }
         __syncwarp();
     } else {
@@ -395,7 +482,8 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
             const int nr = (int)(p.R - r0 < p.rpt ? p.R - r0 : p.rpt);
             const int ncols = nr * p.H;
             // the buffer's last readers (two items back) are past the previous item's barrier
-            if (p.w) c.w[buf][tid] = tid < ncols ? __ldg(p.w + ((int64_t)it.s * p.R + r0) * p.H + tid) : 0.f;
+            if (p.w)
+                for (int n = tid; n < ncols; n += 128) c.w[buf][n] = __ldg(p.w + ((int64_t)it.s * p.R + r0) * p.H + n);
             // the four warps leave together when a wait ran out
             if (ptx::named_bar_or(1, 128, !ok || *abort)) break;
             const float *w = c.w[buf];
@@ -404,7 +492,7 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
                 continue;
             }
             ptx::tc_fence_after();
-            const int64_t b = it.bt * M + tid;
+            const int64_t b = it.bt * MP + rank * M + tid;
             float *dst = p.scores + ((int64_t)it.s * p.R + r0) * p.ld + b;
             int64_t pos = p.len[it.s] - p.R + r0;   // the row's position
             float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -447,7 +535,7 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
             }
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&c.d_free[buf]);
+            if (lane == 0) arrive_at(leader_addr(&c.d_free[buf]));
         }
         // rows of streams with fewer block tiles than the longest: no block there; and every row's
         // visible blocks
@@ -455,15 +543,16 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
             const int s = (int)(r / p.R);
             const int64_t len = p.len[s];
             const int64_t nb = (len + ROWS - 1) / ROWS;
-            for (int64_t b = (nb + M - 1) / M * M + tid; b < p.cols; b += 128) p.scores[r * p.ld + b] = -INFINITY;
+            for (int64_t b = (nb + MP - 1) / MP * MP + tid; b < p.cols; b += 128) p.scores[r * p.ld + b] = -INFINITY;
             if (p.nblk && tid == 0) p.nblk[r] = (int32_t)((len - p.R + (r - (int64_t)s * p.R)) / ROWS + 1);
         }
     }
 
     ptx::tc_fence_before();
     __syncthreads();
+    pair_sync();   // both CTAs are done with each other's barriers and TMEM
     ptx::tc_fence_after();
-    if (warp == 5) ptx::tmem_dealloc(tmem, TCOLS);
+    if (warp == 5) pair_tmem_dealloc(tmem, TCOLS);
 }
 
 }  // namespace blk
@@ -524,11 +613,11 @@ int launch_block_scores(tf_kvpool *pool, const void *d_bkeys, const int32_t *d_p
     }
     p.rpt = std::min(R, std::max(1, NMAX / H));
     p.nrt = (R + p.rpt - 1) / p.rpt;
-    p.npad = (p.rpt * H + 15) / 16 * 16;
+    p.npad = (p.rpt * H + 31) / 32 * 32;
     {
         const uint64_t dims[2] = {(uint64_t)kDk, (uint64_t)S * R * H};
         const uint64_t strides[1] = {(uint64_t)kDk * 2};
-        const uint32_t box[2] = {64, (uint32_t)p.npad};
+        const uint32_t box[2] = {64, (uint32_t)p.npad / 2};
         if (!encode_tmap_bf16(&p.tm_q, const_cast<void *>(d_q), 2, dims, strides, box)) return TF_E_CUDA;
     }
     p.pt = d_pt;
@@ -552,12 +641,12 @@ int launch_block_scores(tf_kvpool *pool, const void *d_bkeys, const int32_t *d_p
         p.cols = std::max(p.cols, nb);
         p.len[s] = h_len[s];
         p.item0[s] = p.items;
-        p.items += (nb + M - 1) / M * p.nrt;
+        p.items += (nb + MP - 1) / MP * p.nrt;
     }
-    const int ctas = (int)std::min<int64_t>(p.items, ready_sms);
+    const int ctas = 2 * (int)std::min<int64_t>(p.items, std::max(1, ready_sms / 2));
     if (prepare_launch(pool, st) != TF_OK) return TF_E_CUDA;
     auto *kern = H % 32 == 0 ? block_scores_kernel<32> : H % 8 == 0 ? block_scores_kernel<8> : block_scores_kernel<1>;
-    const cudaError_t e = launch_pdl(kern, dim3((unsigned)ctas), dim3(THREADS), SMEM_TOTAL, st, p);
+    const cudaError_t e = launch_pdl_pairs(kern, dim3((unsigned)ctas), dim3(THREADS), SMEM_TOTAL, st, p);
     launch_counter()++;
     return e == cudaSuccess ? TF_OK : TF_E_CUDA;
 }
