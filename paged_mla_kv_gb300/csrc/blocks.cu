@@ -161,12 +161,13 @@ constexpr int TILE_PAGES = M / PER_PAGE;
 constexpr int NMAX = 256;                     // columns a tile
 constexpr int KBOX = kDk / 64;                // 9
 constexpr int PAGE_KEYS = PER_PAGE * kDk * 2; // 9,216 bytes: [9 boxes][8 blocks][64 values], swizzled
-constexpr int STAGES = 4;
+constexpr int STAGES = 5;
 constexpr int STAGE_BYTES = NMAX / 2 * 128;
 constexpr int SMEM_A = 0;
 constexpr int SMEM_B = SMEM_A + TILE_PAGES * PAGE_KEYS;
 constexpr int SMEM_CTRL = SMEM_B + STAGES * STAGE_BYTES;
-constexpr int THREADS = 192;                  // 4 epilogue warps, the TMA warp, the MMA warp
+constexpr int EPI = 256;                      // 8 epilogue warps: two a TMEM quadrant
+constexpr int THREADS = EPI + 64;             // and the TMA warp, the MMA warp
 constexpr int TCOLS = 2 * NMAX;
 
 // Barriers marked L are waited on in the leader (rank 0) only and reached from both CTAs; the
@@ -174,11 +175,11 @@ constexpr int TCOLS = 2 * NMAX;
 struct Ctrl {
     uint64_t a_full, a_free;                    // L: both CTAs' block keys landed; the tile's products are done
     uint64_t b_full[STAGES], b_free[STAGES];    // L: both halves of a query box landed; its products are done
-    uint64_t d_full[2], d_free[2];              // accumulator computed; L: read by the eight epilogue warps
+    uint64_t d_full[2], d_free[2];              // accumulator computed; L: read by both CTAs' epilogue warps
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
-    alignas(16) float w[2][NMAX];
+    alignas(16) float w[NMAX];
 };
 constexpr int SMEM_TOTAL = SMEM_CTRL + (int)sizeof(Ctrl) + 1024;
 static_assert(ROWS == 64, "positions are shifted by 6");
@@ -204,36 +205,64 @@ struct ScoreParams {
     int64_t len[TF_MAX_STREAMS];
 };
 
-// The pair's items: a run of the numbering, block tile by block tile of each stream.
+// The pair's items: a run of the numbering (stream, block tile, place in the block tile's order), in
+// which a block tile stands for as many runs as share it.  The places of a block tile are its row
+// tiles in the order of (time, pair): the j-th items of all its pairs come before the (j+1)-th ones.
+// So all pairs, whatever their block tile, go through the query rows side by side and each query
+// tile comes from DRAM once: read run by run instead, 2,048 rows against 7 block tiles took 1.04 GB
+// of DRAM reads for 151 MB of queries.
 struct Items {
-    int64_t i, i1;
-    int s = -1;
-    int64_t bt = -1, rt = 0;
-    bool fresh = false;   // another block tile than the last item's
-    __device__ __forceinline__ explicit Items(const ScoreParams &p)
-        : i(p.items * (blockIdx.x / 2) / (gridDim.x / 2)), i1(p.items * (blockIdx.x / 2 + 1) / (gridDim.x / 2)) {}
+    int64_t len, more;     // items a pair, and how many of the first pairs have one more
+    int64_t i, i1;         // next item, end
+    int64_t first;         // the pair's first item
+    int64_t i0 = 0;        // the block tile's first item
+    int p0 = 0;            // the pair that holds it
+    int pair, s = -1;
+    int64_t bt = -1;
+    bool fresh = false;    // another block tile than the last item's
+    __device__ __forceinline__ int64_t start(int64_t q) const { return q * len + (q < more ? q : more); }
+    __device__ __forceinline__ explicit Items(const ScoreParams &p) {
+        const int pairs = gridDim.x / 2;
+        pair = blockIdx.x / 2;
+        len = p.items / pairs;
+        more = p.items - len * pairs;
+        first = i = start(pair);
+        i1 = start(pair + 1);
+    }
     __device__ __forceinline__ bool next(const ScoreParams &p) {
         if (i >= i1) return false;
-        if (s >= 0 && rt + 1 < p.nrt) {
-            ++rt;
-            fresh = false;
-        } else {
+        fresh = s < 0 || i == i0 + p.nrt;
+        if (fresh) {
             int a = s < 0 ? 0 : s, z = p.S - 1;
             while (a < z) {
                 const int mid = (a + z + 1) >> 1;
                 if (p.item0[mid] <= i) a = mid; else z = mid - 1;
             }
             s = a;
-            const int64_t k = i - p.item0[s];
-            bt = k / p.nrt;
-            rt = k - bt * p.nrt;
-            fresh = true;
+            bt = (i - p.item0[s]) / p.nrt;
+            i0 = p.item0[s] + bt * p.nrt;
+            p0 = pair;
+            while (start(p0) > i0) --p0;
         }
         ++i;
         return true;
     }
+    // after next(): the item's row tile
+    __device__ __forceinline__ int64_t row_tile(const ScoreParams &p) const {
+        if (p.nrt == 1) return 0;
+        const int64_t t = i - 1 - first, end = i0 + p.nrt;
+        int64_t rank = 0;
+        int64_t at = start(p0);
+        for (int q = p0; at < end; ++q) {   // items of pair q in this block tile: times [a, e)
+            const int64_t to = start(q + 1);
+            const int64_t a = (at > i0 ? at : i0) - at, e = (to < end ? to : end) - at;
+            rank += t < a ? 0 : t >= e ? e - a : t - a + (q < pair);
+            at = to;
+        }
+        return rank;
+    }
     // after next(): the last item of its block tile here
-    __device__ __forceinline__ bool last_of_tile(const ScoreParams &p) const { return i >= i1 || rt + 1 == p.nrt; }
+    __device__ __forceinline__ bool last_of_tile(const ScoreParams &p) const { return i >= i1 || i == i0 + p.nrt; }
 };
 
 // ---- a pair of CTAs ----
@@ -270,6 +299,12 @@ __device__ __forceinline__ void tma_queries(void *dst, const CUtensorMap *tm, ui
         " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(ptx::smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(x), "r"(row), "l"(policy)
         : "memory");
+}
+// Ask for a box of queries in L2.
+__device__ __forceinline__ void prefetch_queries(const CUtensorMap *tm, int x, int row) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(tm)),
+                 "r"(x), "r"(row)
+                 : "memory");
 }
 __device__ __forceinline__ void pair_tmem_alloc(uint32_t *dst, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(ptx::smem_u32(dst)), "r"(ncols)
@@ -343,13 +378,13 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&c.d_full[i], 1);
-            ptx::mbar_init(&c.d_free[i], 8);
+            ptx::mbar_init(&c.d_free[i], 2 * EPI / 32);
         }
         ptx::mbar_init(&c.drain, 1);
         c.abort = 0;
         ptx::fence_mbar_init();
     }
-    if (warp == 5) pair_tmem_alloc(&c.tmem_base, TCOLS);
+    if (warp == EPI / 32 + 1) pair_tmem_alloc(&c.tmem_base, TCOLS);
     ptx::tc_fence_before();
     __syncthreads();
     pair_sync();   // the peer's barriers are ready
@@ -358,7 +393,7 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
     volatile int *abort = &c.abort;
     ptx::griddep_wait();
 
-    if (warp == 4) {
+    if (warp == EPI / 32) {
         // ================= TMA =================
         // Lane 0 waits and loads this CTA's half of each query box; its half of a block tile is
         // loaded a page a lane (nine one-atom boxes of 8 blocks x 64 values, to where the
@@ -373,7 +408,16 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
         int na = 0;        // block tiles loaded
         int64_t nb = 0;    // query boxes loaded
         bool ok = true;
-        for (Items it(p); ok && it.next(p);) {
+        Items it(p), ahead(p);   // ahead: an item further, whose queries are asked for in L2
+        bool more = ahead.next(p);
+        auto row_of = [&](const Items &x) {
+            return (int)(((int64_t)x.s * p.R + x.row_tile(p) * p.rpt) * p.H) + (int)rank * (p.npad / 2);
+        };
+        int qrow = 0, qnext = more ? row_of(ahead) : 0;
+        while (ok && it.next(p)) {
+            qrow = qnext;
+            more = ahead.next(p);
+            if (more) qnext = row_of(ahead);
             if (it.fresh) {
                 if (na > 0) ok = ptx::mbar_wait_warp(&c.a_free, (na - 1) & 1, abort, p.err, 30);
                 if (!ok) break;
@@ -397,7 +441,6 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
                 ++na;
             }
             if (lane == 0) {
-                const int qrow = (int)(((int64_t)it.s * p.R + it.rt * p.rpt) * p.H) + (int)rank * (p.npad / 2);
                 for (int kb = 0; ok && kb < KBOX; ++kb) {
                     const int64_t n = nb + kb;
                     const int st = (int)(n % STAGES);
@@ -408,6 +451,7 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
                     }
                     if (rank == 0) ptx::mbar_arrive_expect_tx(&c.b_full[st], p.npad * 128);
                     tma_queries(smem + SMEM_B + st * STAGE_BYTES, &p.tm_q, leader_addr(&c.b_full[st]), kb * 64, qrow, pol_q);
+                    if (more) prefetch_queries(&p.tm_q, kb * 64, qnext);
                 }
             }
             nb += KBOX;
@@ -433,7 +477,7 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
             }
         }
         __syncwarp();
-    } else if (warp == 5) {
+    } else if (warp == EPI / 32 + 1) {
         // ================= MMA (the leader, for the pair) =================
         const uint64_t a0 = ptx::sdesc_sw128(ptx::smem_u32(smem + SMEM_A), 16, PAGE_KEYS);
         const uint64_t b0 = ptx::sdesc_sw128(ptx::smem_u32(smem + SMEM_B), 16, 1024);
@@ -471,36 +515,60 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
         }
         __syncwarp();
     } else {
-        // ================= epilogue: a block a thread =================
+        // ================= epilogue: a block a thread, half of the item's query rows a warp =================
         const int tid = (int)threadIdx.x;
-        const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+        const int half = warp >> 2;
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         int64_t nd = 0;
         bool ok = true;
-        for (Items it(p); it.next(p); ++nd) {
+        // The weights of an item's columns go to shared memory for all to read; those of the next are
+        // fetched while this one's products run (a column a thread).
+        Items it(p);
+        bool more = it.next(p);
+        int64_t r0 = 0, r0n = more ? it.row_tile(p) * p.rpt : 0;   // first query row: this item's, the next one's
+        int s = 0, sn = it.s;
+        int64_t bt = 0, btn = it.bt;
+        float wn = 0.f;
+        auto fetch = [&]() {
+            const int n = (int)(p.R - r0n < p.rpt ? p.R - r0n : p.rpt) * p.H;
+            if (p.w && tid < n) wn = __ldg(p.w + ((int64_t)sn * p.R + r0n) * p.H + tid);
+        };
+        if (more) fetch();
+        for (; more; ++nd) {
             const int buf = (int)(nd & 1);
-            const int64_t r0 = it.rt * p.rpt;
-            const int nr = (int)(p.R - r0 < p.rpt ? p.R - r0 : p.rpt);
-            const int ncols = nr * p.H;
-            // the buffer's last readers (two items back) are past the previous item's barrier
-            if (p.w)
-                for (int n = tid; n < ncols; n += 128) c.w[buf][n] = __ldg(p.w + ((int64_t)it.s * p.R + r0) * p.H + n);
-            // the four warps leave together when a wait ran out
-            if (ptx::named_bar_or(1, 128, !ok || *abort)) break;
-            const float *w = c.w[buf];
+            r0 = r0n;
+            s = sn;
+            bt = btn;
+            // the previous item's weights are read; the warps leave together when a wait ran out
+            if (ptx::named_bar_or(1, EPI, !ok || *abort)) break;
+            if (p.w) {
+                c.w[tid] = wn;
+                ptx::named_bar(1, EPI);
+            }
+            more = it.next(p);
+            if (more) {
+                r0n = it.row_tile(p) * p.rpt;
+                sn = it.s;
+                btn = it.bt;
+                fetch();
+            }
             if (!ptx::mbar_wait_warp(&c.d_full[buf], (uint32_t)(nd / 2) & 1, abort, p.err, 37)) {
                 ok = false;
                 continue;
             }
             ptx::tc_fence_after();
-            const int64_t b = it.bt * MP + rank * M + tid;
-            float *dst = p.scores + ((int64_t)it.s * p.R + r0) * p.ld + b;
-            int64_t pos = p.len[it.s] - p.R + r0;   // the row's position
+            const int nr = (int)(p.R - r0 < p.rpt ? p.R - r0 : p.rpt);
+            const int ra = half ? (nr + 1) / 2 : 0;                    // this warp's rows
+            const int ncols = ((half ? nr : (nr + 1) / 2) - ra) * p.H;  // and its columns
+            const float *w = c.w + ra * p.H;
+            const uint32_t col = lane_base + buf * NMAX + ra * p.H;
+            const int64_t b = bt * MP + rank * M + (tid & (M - 1));
+            float *dst = p.scores + ((int64_t)s * p.R + r0 + ra) * p.ld + b;
+            int64_t pos = p.len[s] - p.R + r0 + ra;   // the row's position
             float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             int left = p.H;
-            for (int n0 = 0; n0 < ncols; n0 += 32) {
-                uint32_t v[32];
-                ptx::tmem_ld32(lane_base + buf * NMAX + n0, v);
-                ptx::tmem_ld_wait();
+            // 32 columns at n0
+            auto add = [&](int n0, const uint32_t (&v)[32]) {
 #pragma unroll
                 for (int j = 0; j < 32; j += C) {
                     if (n0 + j >= ncols) break;
@@ -532,6 +600,18 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
                         left = p.H;
                     }
                 }
+            };
+            // the next 32 columns are on their way from TMEM while these are added
+            uint32_t va[32], vb[32];
+            if (ncols > 0) ptx::tmem_ld32(col, va);
+            for (int n0 = 0; n0 < ncols; n0 += 64) {
+                ptx::tmem_ld_wait();
+                if (n0 + 32 < ncols) ptx::tmem_ld32(col + n0 + 32, vb);
+                add(n0, va);
+                if (n0 + 32 >= ncols) break;
+                ptx::tmem_ld_wait();
+                if (n0 + 64 < ncols) ptx::tmem_ld32(col + n0 + 64, va);
+                add(n0 + 32, vb);
             }
             ptx::tc_fence_before();
             __syncwarp();
@@ -543,7 +623,7 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
             const int s = (int)(r / p.R);
             const int64_t len = p.len[s];
             const int64_t nb = (len + ROWS - 1) / ROWS;
-            for (int64_t b = (nb + MP - 1) / MP * MP + tid; b < p.cols; b += 128) p.scores[r * p.ld + b] = -INFINITY;
+            for (int64_t b = (nb + MP - 1) / MP * MP + tid; b < p.cols; b += EPI) p.scores[r * p.ld + b] = -INFINITY;
             if (p.nblk && tid == 0) p.nblk[r] = (int32_t)((len - p.R + (r - (int64_t)s * p.R)) / ROWS + 1);
         }
     }
@@ -552,7 +632,7 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
     __syncthreads();
     pair_sync();   // both CTAs are done with each other's barriers and TMEM
     ptx::tc_fence_after();
-    if (warp == 5) pair_tmem_dealloc(tmem, TCOLS);
+    if (warp == EPI / 32 + 1) pair_tmem_dealloc(tmem, TCOLS);
 }
 
 }  // namespace blk
@@ -612,6 +692,10 @@ int launch_block_scores(tf_kvpool *pool, const void *d_bkeys, const int32_t *d_p
         if (!encode_tmap_bf16(&p.tm_k, const_cast<void *>(d_bkeys), 3, dims, strides, box)) return TF_E_CUDA;
     }
     p.rpt = std::min(R, std::max(1, NMAX / H));
+    // a warp of the epilogue reads 32 columns at a time from its first row on, up to the buffer's end
+    auto reach = [&](int nr) { return (nr + 1) / 2 * H + (nr / 2 * H + 31) / 32 * 32; };
+    for (int nr = 1; nr <= p.rpt; ++nr)
+        if (reach(nr) > NMAX) p.rpt = nr - 1;
     p.nrt = (R + p.rpt - 1) / p.rpt;
     p.npad = (p.rpt * H + 31) / 32 * 32;
     {

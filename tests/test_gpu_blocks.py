@@ -145,7 +145,8 @@ def run_scores(res, w, bk, q, weights=None, sink=1, local=1, extra=0, lens=None)
     ([1], 1, 1, 0, 1, False), ([64], 1, 16, 1, 1, True), ([65, 1, 9000], 1, 64, 0, 1, False),
     ([8192, 8193, 300], 2, 16, 1, 2, True), ([20000, 513], 2, 128, 2, 3, True), ([5000], 7, 100, 0, 1, False),
     ([3000, 2000], 33, 5, 1, 1, True), ([9000, 300], 131, 64, 1, 4, True), ([700], 700, 20, 3, 1, False),
-    ([17000] * 3, 3, 96, 0, 5, True)])
+    ([17000] * 3, 3, 96, 0, 5, True), ([700], 7, 85, 0, 1, True), ([9000], 60, 5, 0, 1, False), ([600], 9, 127, 1, 1, True),
+    ([40000], 500, 8, 1, 1, True)])
 def test_block_scores(lens, R, H, sink, local, weighted):
     w = Y.custom("sc", 90 + R + H, lens=lens, R=R, H=H)
     res = Resident(w, caches=[])
@@ -169,7 +170,7 @@ def test_block_scores(lens, R, H, sink, local, weighted):
         # 576 products and H terms, each rounded; the scale once more
         mag = np.abs(qs[s]) @ np.abs(k).T
         mag = (mag if ws is None else mag * np.abs(ws)[..., None]).sum(1)
-        assert np.all(np.abs(got[:, :nb] - ref)[fin] <= (w.scale * (580 + H) * F * mag)[fin])
+        assert np.all(np.abs(got[:, :nb][fin] - ref[fin]) <= (w.scale * (580 + H) * F * mag)[fin])
 
 
 def test_block_scores_same_bits_and_null_outputs():
