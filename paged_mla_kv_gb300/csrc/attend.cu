@@ -148,7 +148,7 @@ struct Ctrl {
     int abort;
     int flag[NROPE];
     float alpha[NROPE][NCOL];
-    float row_inv_l[2][NCOL];          // by segment parity
+    alignas(16) float row_inv_l[2][NCOL];   // by segment parity
 };
 constexpr int SMEM_TOTAL = SMEM_CTRL + (int)sizeof(Ctrl) + 1024;
 static_assert(SMEM_TOTAL <= 232448, "shared memory budget");
@@ -751,6 +751,13 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
                     ptx::tma_load_2d(smem + SMEM_Q + b * QBOX_BYTES, &p.tm_q, &c.q_full, (Q_TMEM_BOXES + b) * 64, qrow,
                                      pol_q);
                 q_armed = si;
+                {   // the next segment's queries on their way to L2
+                    SegIter<MODE> ahead = it;
+                    Seg n;
+                    if (ahead.next(p, n))
+                        ptx::bulk_prefetch_l2(p.q + (size_t)seg_gcol<MODE>(n, ncols_all) * kDk,
+                                              min(NCOL, seg_cols<MODE>(n, ncols_all)) * kDk * 2);
+                }
                 int cur_lp = -1, page = 0;
                 // BLOCKS: the list entries run two tiles and their pages one tile ahead of the
                 // copies, so that these dependent loads do not delay a tile
@@ -1173,26 +1180,25 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
             {
                 // The segment's queries, latent values 0-255, into TMEM (A of QK^T): lane i < 16 of
                 // this quadrant holds column 16 q4 + i.  Every QK^T of the previous segment has
-                // completed: this warp has seen its last S.
-                const int m = 16 * q4 + (lane & 15);
-                const bool live = lane < 16 && m < ncols;
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (size_t)(gcol + (live ? m : 0)) * kDk);
-#pragma unroll 1
-                for (int c2 = 0; c2 < Q_TMEM_BOXES; c2 += 2) {
-                    uint32_t v[2][32];
+                // completed: this warp has seen its last S.  A thread takes 8 bytes of rows r0 and r1 in
+                // each 16 values (the layout of the 16x256b store), all loads in flight together.
+                const bool live0 = r0 < ncols, live1 = r1 < ncols;
+                const uint2 *s0 = reinterpret_cast<const uint2 *>(p.q + (size_t)(gcol + (live0 ? r0 : 0)) * kDk) + (lane & 3);
+                const uint2 *s1 = reinterpret_cast<const uint2 *>(p.q + (size_t)(gcol + (live1 ? r1 : 0)) * kDk) + (lane & 3);
+                uint32_t v[2][32];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const uint4 x = live ? __ldg(src + (c2 + h) * 8 + i) : make_uint4(0, 0, 0, 0);
-                            v[h][4 * i] = x.x;
-                            v[h][4 * i + 1] = x.y;
-                            v[h][4 * i + 2] = x.z;
-                            v[h][4 * i + 3] = x.w;
-                        }
-                    ptx::tmem_st32(lane_base + TMEM_Q + 32 * c2, v[0]);
-                    ptx::tmem_st32(lane_base + TMEM_Q + 32 * (c2 + 1), v[1]);
-                }
+                    for (int j = 0; j < 8; ++j) {
+                        const uint2 a = live0 ? __ldg(s0 + 4 * (8 * h + j)) : make_uint2(0, 0);
+                        const uint2 b = live1 ? __ldg(s1 + 4 * (8 * h + j)) : make_uint2(0, 0);
+                        v[h][4 * j] = a.x;
+                        v[h][4 * j + 1] = a.y;
+                        v[h][4 * j + 2] = b.x;
+                        v[h][4 * j + 3] = b.y;
+                    }
+                ptx::tmem_st_16x256b_x8(lane_base + TMEM_Q, v[0]);
+                ptx::tmem_st_16x256b_x8(lane_base + TMEM_Q + 64, v[1]);
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before();
                 __syncwarp();
@@ -1424,25 +1430,49 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
                     ptx::bulk_s2g(ws_o + (size_t)q.slot * NCOL * kLat, stage, nst * kLat * sizeof(float));
                     ptx::bulk_s2g_wait();
                 }
-            } else {
+            } else if (q.slot >= 0) {
+                // a partial with segments after it: the columns' fp32 values, 128 bytes a warp store
                 for (int jm = 0; jm < 4; ++jm)
                     for (int h2 = 0; h2 < npv; h2 += 32) {
                         uint32_t v[32];
                         ptx::tmem_ld32(lane_base + TMEM_O + jm * 64 + h2, v);
                         ptx::tmem_ld_wait();
-                        const int dim = jm * 128 + q4 * 32 + lane;
-    #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const int col = h2 + k;
-                            if (col >= ncols) continue;
-                            const float o = __uint_as_float(v[k]);
-                            if (q.slot < 0) {
-                                const size_t orow = (size_t)seg_gcol<MODE>(q, ncols_all) + col;
-                                outp[orow * kLat + dim] = __float2bfloat16_rn(o * inv_l[col]);
-                            } else {
-                                ws_o[((size_t)q.slot * NCOL + col) * kLat + dim] = o;
-                            }
+                        float *dst = ws_o + ((size_t)q.slot * NCOL + h2) * kLat + jm * 128 + q4 * 32 + lane;
+                        if (h2 + 32 <= ncols) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) dst[k * kLat] = __uint_as_float(v[k]);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (h2 + k < ncols) dst[k * kLat] = __uint_as_float(v[k]);
                         }
+                    }
+            } else {
+                // a whole unit: bf16 output.  A lane holds one value of 32 columns; exchanged among
+                // eight lanes it stores 16 bytes of a column, 4 stores instead of 32 two-byte ones (a
+                // segment's epilogue took 21,000 cycles of its SM with those, eight tiles' time).
+                for (int jm = 0; jm < 4; ++jm)
+                    for (int h2 = 0; h2 < npv; h2 += 32) {
+                        uint32_t v[32];
+                        ptx::tmem_ld32(lane_base + TMEM_O + jm * 64 + h2, v);
+                        float f[32];
+                        uint4 o[4];
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4) {
+                            const float4 il = *reinterpret_cast<const float4 *>(inv_l + h2 + k);
+                            f[k] = __uint_as_float(v[k]) * il.x;
+                            f[k + 1] = __uint_as_float(v[k + 1]) * il.y;
+                            f[k + 2] = __uint_as_float(v[k + 2]) * il.z;
+                            f[k + 3] = __uint_as_float(v[k + 3]) * il.w;
+                        }
+                        ptx::transpose_bf16(f, o, lane);
+                        const int col = h2 + (lane & 7);
+                        __nv_bfloat16 *dst = outp + (size_t)(seg_gcol<MODE>(q, ncols_all) + col) * kLat + jm * 128 +
+                                             q4 * 32 + (lane & 24);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (col + 8 * i < ncols) *reinterpret_cast<uint4 *>(dst + 8 * i * kLat) = o[i];
                     }
             }
             // the statistics are read: the softmax may post the next segment's

@@ -198,6 +198,11 @@ __device__ __forceinline__ void bulk_s2g_wait() {
     asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
 }
 
+// Ask for `bytes` bytes (a multiple of 16, 16-byte aligned) in L2.
+__device__ __forceinline__ void bulk_prefetch_l2(const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap *tm) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
 }
@@ -388,6 +393,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         TF_W8(0), TF_W8(8), TF_W8(16), TF_W8(24)
         : "memory");
 }
+// The store to the layout that tmem_ld_16x256b_x8 reads (16 lanes, 64 columns).
+__device__ __forceinline__ void tmem_st_16x256b_x8(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        TF_W8(0), TF_W8(8), TF_W8(16), TF_W8(24)
+        : "memory");
+}
 #undef TF_W8
 
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -398,6 +412,39 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x via the hardware approxi
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// 32 columns of 32 values, value `lane` of column k in v[k] -> bf16 with eight values of a column a
+// lane: o[i] holds values 8 (lane / 8) .. + 7 of column 8 i + lane % 8.  Three exchanges with the
+// lanes 1, 2 and 4 away, each of which halves a lane's columns and doubles its values.
+__device__ __forceinline__ void transpose_bf16(const float (&v)[32], uint4 (&o)[4], int lane) {
+    const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
+    const uint32_t lo = b0 ? 0x1054u : 0x5410u, hi = b0 ? 0x3276u : 0x7632u;
+    uint32_t w[16];   // column 2 i + b0, values lane & ~1, + 1
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+        uint32_t a, b;   // columns 4 m, 4 m + 2 and 4 m + 1, 4 m + 3
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(a) : "f"(v[4 * m + 2]), "f"(v[4 * m]));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b) : "f"(v[4 * m + 3]), "f"(v[4 * m + 1]));
+        const uint32_t keep = b0 ? b : a, got = __shfl_xor_sync(0xffffffffu, b0 ? a : b, 1);
+        w[2 * m] = __byte_perm(keep, got, lo);
+        w[2 * m + 1] = __byte_perm(keep, got, hi);
+    }
+    uint32_t x[8], y[8];   // column 4 i + 2 b1 + b0, values lane & ~3 .. + 3
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t keep = b1 ? w[2 * i + 1] : w[2 * i];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, b1 ? w[2 * i] : w[2 * i + 1], 2);
+        x[i] = b1 ? got : keep;
+        y[i] = b1 ? keep : got;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t kx = b2 ? x[2 * i + 1] : x[2 * i], ky = b2 ? y[2 * i + 1] : y[2 * i];
+        const uint32_t gx = __shfl_xor_sync(0xffffffffu, b2 ? x[2 * i] : x[2 * i + 1], 4);
+        const uint32_t gy = __shfl_xor_sync(0xffffffffu, b2 ? y[2 * i] : y[2 * i + 1], 4);
+        o[i] = b2 ? make_uint4(gx, gy, kx, ky) : make_uint4(kx, ky, gx, gy);
+    }
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
