@@ -112,6 +112,7 @@ static_assert(4 * F8_BOX_BYTES == PAIR_BYTES && F8_BLK_BYTES == PAIR_BYTES, "a p
 constexpr int MIN_TILES = 4;                    // fewest key tiles a CTA is given
 constexpr int SPLIT_UNIT = 256;                 // batch-invariant split sizes are multiples of this
 static_assert(SPLIT_UNIT % BK == 0, "splits must be tile-aligned");
+constexpr int MAX_MERGE = 8;                    // CTAs of a (portable) cluster that merges partials
 constexpr int MAX_CTAS = 240;                   // CTAs a launch (one a SM); sizes the workspace
 constexpr uint32_t IDESC_QK = ptx::idesc_bf16_f32(64, BK, false, false);
 
@@ -148,7 +149,8 @@ struct Ctrl {
     int abort;
     int flag[NROPE];
     float alpha[NROPE][NCOL];
-    alignas(16) float row_inv_l[2][NCOL];   // by segment parity
+    alignas(16) float row_inv_l[2][NCOL];   // by segment parity (BLOCKS, merged in a cluster: the
+                                            // CTA's one segment's maxima and sums)
 };
 constexpr int SMEM_TOTAL = SMEM_CTRL + (int)sizeof(Ctrl) + 1024;
 static_assert(SMEM_TOTAL <= 232448, "shared memory budget");
@@ -234,6 +236,8 @@ struct Params {
     int32_t nranges;      // RANGES: ranges of the numbering
     int32_t rep;          // RANGES: CTAs a range (the column groups)
     int32_t nent;         // SHARED: entries
+    int32_t merge;        // BLOCKS: CTAs a unit, side by side in a cluster that merges their partials
+                          // (0: CTAs take ranges of the numbering, a combine pass merges)
     int64_t rb[MAX_CTAS + 1];        // RANGES: range i is tiles [rb[i], rb[i+1]); UNITS: positions
     union {
         StreamPlan st[TF_MAX_STREAMS];
@@ -368,10 +372,11 @@ struct SegIter {
         }
         if (MODE == MODE_BLOCKS) {
             if (x >= x1) return false;
-            const int64_t u = x >> 32, t = x & 0xffffffffll;
+            const int u = (int)(x >> 32);             // S * R * hg <= 2^30
+            const int64_t t = x & 0xffffffffll;
             const int hg = (p.H + NCOL - 1) / NCOL;   // head groups a query row; p.groups = R * hg
-            q.s = (int)(u / p.groups);
-            q.g = (int)(u - (int64_t)q.s * p.groups);
+            q.s = u / p.groups;
+            q.g = u - q.s * p.groups;
             const int r = q.g / hg, h0 = (q.g - r * hg) * NCOL;
             q.len = p.st[q.s].len;
             q.pos = q.len - p.R + r;
@@ -382,9 +387,11 @@ struct SegIter {
             const int64_t te = (x1 >> 32) == u ? (x1 & 0xffffffffll) : nt;
             q.nt = (int)(te - t);
             q.list = p.idx + ((int64_t)q.s * p.R + r) * p.max_idx + t;
-            q.slot = (t == 0 && te == nt) ? -1 : 2 * (int)blockIdx.x + (k == 0 ? 0 : 1);
+            q.slot = p.merge                ? (int)blockIdx.x
+                     : t == 0 && te == nt ? -1
+                                          : 2 * (int)blockIdx.x + (k == 0 ? 0 : 1);
             ++k;
-            x = te == nt ? unit_pos(u + 1, 0) : unit_pos(u, te);
+            x = te == nt ? unit_pos(u + 1ll, 0) : unit_pos(u, te);
             return true;
         }
         if (MODE == MODE_SHARED) {
@@ -446,6 +453,20 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *tm, ui
         "l"(reinterpret_cast<uint64_t>(tm)), "r"(ptx::smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
         "l"(policy)
         : "memory");
+}
+
+// A merged column: lane l holds its sums at values 4 (l + 32 i) .. + 3, M and L the maximum (log2
+// units) and the sum over its partials.
+__device__ __forceinline__ void store_column(const Params &p, size_t orow, int lane, float M, float L,
+                                              const float4 (&acc)[4]) {
+    const float inv = L > 0.f ? 1.f / L : 0.f;   // BLOCKS: a row whose list leaves no key is zero
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        __nv_bfloat162 *o2 = reinterpret_cast<__nv_bfloat162 *>(p.out + orow * kLat) + 2 * (lane + 32 * i);
+        o2[0] = __floats2bfloat162_rn(acc[i].x * inv, acc[i].y * inv);
+        o2[1] = __floats2bfloat162_rn(acc[i].z * inv, acc[i].w * inv);
+    }
+    if (lane == 0 && p.lse) p.lse[orow] = (M + log2f(L)) * 0.69314718055994531f;
 }
 
 #define ALLW(x) __all_sync(0xffffffffu, (x))
@@ -516,6 +537,10 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
         ptx::mbar_init(&c.drain, 2);
         c.abort = 0;
         ptx::fence_mbar_init();
+    }
+    if (MODE == MODE_BLOCKS && threadIdx.x < NCOL) {   // a CTA without a tile adds nothing to its unit
+        c.row_inv_l[0][threadIdx.x] = -INFINITY;
+        c.row_inv_l[1][threadIdx.x] = 0.f;
     }
     if (warp == 9) {
         ptx::tmem_alloc(&c.tmem_base, TMEM_COLS);
@@ -1337,6 +1362,9 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
                     if (!(h ? act1 : act0)) continue;
                     if (q.slot < 0) {
                         if (lsep) lsep[(size_t)gcol + rr] = (m + log2f(l)) * 0.69314718055994531f;
+                    } else if (MODE == MODE_BLOCKS && p.merge) {
+                        c.row_inv_l[0][rr] = m;
+                        c.row_inv_l[1][rr] = l;
                     } else {
                         ws_ml[((size_t)q.slot * NCOL + rr) * 2 + 0] = m;
                         ws_ml[((size_t)q.slot * NCOL + rr) * 2 + 1] = l;
@@ -1413,10 +1441,16 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
                 // staged in the key ring, which no tile uses any more (the last PV is done and the
                 // TMA warp loads nothing after it).  Every CTA ends with this write at about the
                 // same time; one bulk copy a CTA moves it faster than 4,096 warp stores.
+                // 32 columns (64 KB) a copy, the next ones staged meanwhile.  In a cluster that merges, a
+                // half of columns that are all this CTA's to merge is staged last and stays here.
                 float *stage = reinterpret_cast<float *>(smem + SMEM_PAIR);
                 const int nst = (npv + 31) & ~31;
-                for (int jm = 0; jm < 4; ++jm)
-                    for (int h2 = 0; h2 < nst; h2 += 32) {
+                const bool merge2 = MODE == MODE_BLOCKS && p.merge == 2;
+                const int mine = merge2 && nst == NCOL ? (int)ptx::cluster_rank() * 32 : -1;
+#pragma unroll 1
+                for (int i = 0; i < nst; i += 32) {
+                    const int h2 = mine == 0 ? 32 - i : i;
+                    for (int jm = 0; jm < 4; ++jm) {
                         uint32_t v[32];
                         ptx::tmem_ld32(lane_base + TMEM_O + jm * 64 + h2, v);
                         ptx::tmem_ld_wait();
@@ -1424,12 +1458,14 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
 #pragma unroll
                         for (int k = 0; k < 32; ++k) stage[(h2 + k) * kLat + dim] = __uint_as_float(v[k]);
                     }
-                ptx::fence_proxy_async_smem();
-                ptx::named_bar(1, 128);
-                if (threadIdx.x == 0) {
-                    ptx::bulk_s2g(ws_o + (size_t)q.slot * NCOL * kLat, stage, nst * kLat * sizeof(float));
-                    ptx::bulk_s2g_wait();
+                    if (h2 == mine) continue;
+                    ptx::fence_proxy_async_smem();
+                    ptx::named_bar(1, 128);
+                    if (threadIdx.x == 0)
+                        ptx::bulk_s2g(ws_o + ((size_t)q.slot * NCOL + h2) * kLat, stage + h2 * kLat,
+                                      32 * kLat * sizeof(float));
                 }
+                if (threadIdx.x == 0) ptx::bulk_s2g_wait();
             } else if (q.slot >= 0) {
                 // a partial with segments after it: the columns' fp32 values, 128 bytes a warp store
                 for (int jm = 0; jm < 4; ++jm)
@@ -1486,6 +1522,101 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
+    if (MODE == MODE_BLOCKS && p.merge) {
+        // The cluster's CTAs hold the partials of one unit: a warp a column, the columns dealt out to
+        // the CTAs, each adding up the column's partials in key order: its own from shared memory, the
+        // others' from the workspace.  This is the combine pass without its launch and its wait for
+        // the last CTA of the grid.  (Read from the other CTAs' shared memory the partials came at about
+        // 10 bytes a cycle: 6,800 cycles for the half of a 128 KB partial.)
+        ptx::cluster_sync();
+        const int n = p.merge, mine = (int)ptx::cluster_rank(), u = (int)blockIdx.x / n;
+        const int hg = (H_ + NCOL - 1) / NCOL;
+        const int s = u / ngroups, r = (u - s * ngroups) / hg, h0 = ((u - s * ngroups) - r * hg) * NCOL;
+        const int nc = min(NCOL, H_ - h0);
+        const uint32_t m0 = ptx::smem_u32(c.row_inv_l[0]), l0 = ptx::smem_u32(c.row_inv_l[1]);
+        const float *stage = reinterpret_cast<const float *>(smem + SMEM_PAIR);
+        // A thread a column first: the weights of its partials over its sum (kept behind the partial), and its lse
+        float *wts = reinterpret_cast<float *>(smem + SMEM_PAIR + NCOL * kLat * 4);   // [MAX_MERGE][NCOL]
+        const int per = n == 2 ? NCOL / 2 : (nc + n - 1) / n;   // columns a CTA, side by side
+        const int c1 = min(nc, (mine + 1) * per);
+        if (threadIdx.x < nc) {
+            const int col = (int)threadIdx.x;
+            float w[MAX_MERGE], l[MAX_MERGE], M = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int j = 0; j < MAX_MERGE; ++j) {
+                w[j] = j < n ? ptx::ld_cluster1(ptx::cluster_addr(m0 + col * 4, j)) : -INFINITY;
+                l[j] = j < n ? ptx::ld_cluster1(ptx::cluster_addr(l0 + col * 4, j)) : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < MAX_MERGE; ++j) M = fmaxf(M, w[j]);
+#pragma unroll
+            for (int j = 0; j < MAX_MERGE; ++j) {
+                w[j] = w[j] == -INFINITY ? 0.f : ptx::ex2(w[j] - M);
+                L = __fmaf_rn(w[j], l[j], L);
+            }
+            const float inv = L > 0.f ? 1.f / L : 0.f;
+#pragma unroll
+            for (int j = 0; j < MAX_MERGE; ++j) wts[j * NCOL + col] = w[j] * inv;
+            if (lsep && col >= mine * per && col < c1)
+                lsep[(size_t)s * ncols_all + r * H_ + h0 + col] = (M + log2f(L)) * 0.69314718055994531f;
+        }
+        __syncthreads();
+        // NC columns a warp and NP of their partials in flight at a time
+        const int warps = (int)blockDim.x / 32;
+        auto merge = [&](auto nc_, auto np_) {
+            constexpr int NC = decltype(nc_)::value, NP = decltype(np_)::value;
+            for (int ca = mine * per + warp; ca < c1; ca += NC * warps) {
+                float4 acc[NC][4];
+#pragma unroll
+                for (int h = 0; h < NC; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[h][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int j0 = 0; j0 < n; j0 += NP) {
+                    float4 v[NC][NP][4];
+                    float w[NC][NP];
+#pragma unroll
+                    for (int h = 0; h < NC; ++h)
+#pragma unroll
+                        for (int j = 0; j < NP; ++j) {
+                            const int col = ca + h * warps, jj = j0 + j;
+                            w[h][j] = col < c1 && jj < n ? wts[jj * NCOL + col] : 0.f;
+                            const float4 *src = reinterpret_cast<const float4 *>(
+                                jj == mine ? stage + col * kLat : ws_o + ((size_t)(u * n + jj) * NCOL + col) * kLat) + lane;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)   // weight 0: nothing there (a CTA without a tile has no partial)
+                                v[h][j][i] = w[h][j] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                             : jj == mine   ? src[32 * i]
+                                                            : __ldcg(src + 32 * i);
+                        }
+#pragma unroll
+                    for (int h = 0; h < NC; ++h)
+#pragma unroll
+                        for (int j = 0; j < NP; ++j)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                acc[h][i].x = __fmaf_rn(w[h][j], v[h][j][i].x, acc[h][i].x);
+                                acc[h][i].y = __fmaf_rn(w[h][j], v[h][j][i].y, acc[h][i].y);
+                                acc[h][i].z = __fmaf_rn(w[h][j], v[h][j][i].z, acc[h][i].z);
+                                acc[h][i].w = __fmaf_rn(w[h][j], v[h][j][i].w, acc[h][i].w);
+                            }
+                }
+#pragma unroll
+                for (int h = 0; h < NC; ++h) {
+                    const int col = ca + h * warps;
+                    if (col >= c1) break;
+                    uint2 *dst = reinterpret_cast<uint2 *>(outp + ((size_t)s * ncols_all + r * H_ + h0 + col) * kLat) + lane;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        dst[32 * i] = make_uint2(ptx::pack_bf16x2(acc[h][i].x, acc[h][i].y),
+                                                 ptx::pack_bf16x2(acc[h][i].z, acc[h][i].w));
+                }
+            }
+        };
+        using One = std::integral_constant<int, 1>;
+        if (n == 2) merge(std::integral_constant<int, 2>(), std::integral_constant<int, 2>());
+        else merge(One(), std::integral_constant<int, 4>());
+        ptx::cluster_sync();   // the others are done with this CTA's shared memory
+    }
     if (warp == 9) ptx::tmem_dealloc(tmem, TMEM_COLS);
 }
 
@@ -1600,18 +1731,6 @@ __device__ __forceinline__ bool combine_column(const Params &p, int s, int c, Co
     return pe >= 0 || n2 > 1;
 }
 
-__device__ __forceinline__ void combine_store(const Params &p, size_t orow, int lane, float M, float L,
-                                              const float4 (&acc)[4]) {
-    const float inv = L > 0.f ? 1.f / L : 0.f;   // BLOCKS: a row whose list leaves no key is zero
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        __nv_bfloat162 *o2 = reinterpret_cast<__nv_bfloat162 *>(p.out + orow * kLat) + 2 * (lane + 32 * i);
-        o2[0] = __floats2bfloat162_rn(acc[i].x * inv, acc[i].y * inv);
-        o2[1] = __floats2bfloat162_rn(acc[i].z * inv, acc[i].w * inv);
-    }
-    if (lane == 0 && p.lse) p.lse[orow] = (M + log2f(L)) * 0.69314718055994531f;
-}
-
 // acc += w * o_j (the column's 512 values, lane's share)
 __device__ __forceinline__ void combine_add(float4 (&acc)[4], const float *o, int lane, float w) {
     const float4 *o4 = reinterpret_cast<const float4 *>(o);
@@ -1630,7 +1749,6 @@ __device__ __forceinline__ void combine_add(float4 (&acc)[4], const float *o, in
 template <bool WIDE, bool SHARED>
 __global__ void __launch_bounds__(WIDE ? COMBINE_THREADS : COMBINE_COLS * 32) mla_combine_kernel(const __grid_constant__ Params p) {
     ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = WIDE ? (int)blockIdx.x : (int)blockIdx.x * COMBINE_COLS + warp;   // column of the group
     std::conditional_t<SHARED, CombineColumn, CombineUnit> cu;
@@ -1644,6 +1762,8 @@ __global__ void __launch_bounds__(WIDE ? COMBINE_THREADS : COMBINE_COLS * 32) ml
         if (col >= cu.nc) return;   // WIDE: the whole block
         orow = (size_t)cu.s * p.ncols + cu.col0 + col;
     }
+    // where the partials lie follows from the parameters alone; the wait comes before the first of them
+    ptx::griddep_wait();
     const int n = cu.n;
     float4 acc[4];
 #pragma unroll
@@ -1680,7 +1800,7 @@ __global__ void __launch_bounds__(WIDE ? COMBINE_THREADS : COMBINE_COLS * 32) ml
                 L = __fmaf_rn(w, __shfl_sync(0xffffffffu, lj, k), L);
             }
         }
-        combine_store(p, orow, lane, M, L, acc);
+        store_column(p, orow, lane, M, L, acc);
     } else {
         __shared__ float red_m[COMBINE_THREADS / 32];
         __shared__ float red_l[COMBINE_THREADS / 32];
@@ -1723,7 +1843,7 @@ __global__ void __launch_bounds__(WIDE ? COMBINE_THREADS : COMBINE_COLS * 32) ml
             }
             Lt += red_l[w];
         }
-        combine_store(p, orow, lane, M, Lt, acc);
+        store_column(p, orow, lane, M, Lt, acc);
     }
 }
 
@@ -1735,7 +1855,8 @@ struct Plan {
     int mode;
     int64_t total;
     int nranges, rep, nctas;
-    size_t slots;   // workspace slots of partials (0: no combine pass)
+    size_t slots;   // workspace slots of partials
+    int merge = 0;  // BLOCKS: CTAs a unit, in a cluster that merges (0: a combine pass if there are slots)
 };
 
 // SPLITS: a function of the stream's own (len, R, H) only.  Splits are whole
@@ -1922,10 +2043,22 @@ inline Plan plan_of(int S, int R, int H, const int64_t *h_len, int sms, bool inv
     return pl;
 }
 
+// What a CTA pays for a segment beyond its tiles, in tiles (queries, the pipeline's refill, the
+// epilogue), from a trace of the kernel: 8,000 cycles of 2,600-cycle tiles.  A CTA's load is its tiles
+// plus this for each segment.
+constexpr int64_t UNIT_SEG_COST = 3;
+constexpr int UNIT_MIN_TILES = 2;
+// What merging cut units takes, in tiles: a combine pass (5 to 9 us from the last CTA's end to its own,
+// more with more columns), or a cluster's merge.  Measured: 64 streams of 32 tiles in clusters of 2 take
+// 37.3 us against 39.6 with a combine pass, 16 units of 16 tiles in clusters of 8 16.3 against 18.0; one
+// stream of 32 tiles takes 16.5 us in a cluster of 8 and 13.5 on 16 CTAs with a combine pass.
+inline int64_t combine_cost(size_t units) { return 4 + std::min<int64_t>(3, (int64_t)units / 16); }
+constexpr int64_t MERGE_COST = 4;
+
 // Ranges over units of nt[u] tiles (no tile: no unit), cut anywhere: bound i at weighted position
 // i W / n, a unit's start weighing `seg` tiles (a bound that falls into that weight moves to the
 // unit's start).  Writes b[0..n] as unit_pos values and returns n; *cut: a bound inside a unit.
-inline int cut_units(const std::vector<int32_t> &nt, int64_t seg, int min_tiles, int sms, int64_t *b, bool *cut) {
+inline int cut_evenly(const std::vector<int32_t> &nt, int64_t seg, int min_tiles, int sms, int64_t *b, bool *cut) {
     const int64_t units = (int64_t)nt.size();
     int64_t W = 0, tiles = 0;
     for (int32_t t : nt) tiles += t;
@@ -1950,9 +2083,72 @@ inline int cut_units(const std::vector<int32_t> &nt, int64_t seg, int min_tiles,
     return m;
 }
 
-constexpr int64_t BLOCKS_SEG_COST = 3;   // BLOCKS: a unit's start, in key tiles
+// The same with a unit cut only if it does not fit a range, and then into equal parts that are ranges
+// of their own; smaller units share a range, whole, while it holds them.  Ranges hold at most `lim`
+// (tiles + seg a segment).  Returns the ranges, sms + 1 if there are more than sms; b may be null.
+inline int cut_by_limit(const std::vector<int32_t> &nt, int64_t seg, int64_t lim, int sms, int64_t *b, bool *cut) {
+    int n = 0;
+    int64_t load = 0;   // of the range that is open (0: none)
+    for (int64_t u = 0; u < (int64_t)nt.size(); ++u) {
+        const int64_t t = nt[u];
+        if (load > 0 && load + t + seg <= lim) {
+            load += t + seg;
+            continue;
+        }
+        const int64_t k = (t + lim - seg - 1) / (lim - seg);   // parts
+        if (n + k > sms) return sms + 1;
+        for (int64_t i = 0; i < k; ++i)
+            if (b) b[n + i] = unit_pos(u, t * i / k);
+        n += (int)k;
+        if (k > 1 && cut) *cut = true;
+        load = k > 1 ? lim : t + seg;
+    }
+    if (b) b[n] = unit_pos((int64_t)nt.size(), 0);
+    return n;
+}
 
-inline Plan plan_blocks(int S, int R, int H, const int64_t *h_len, int max_blk, int sms, int64_t *rb) {
+// Both ways of cutting, whichever leaves the smaller largest load.  Even cuts fit many units a CTA (a
+// prefill chunk's 2,048 rows: whole rows would leave 14 a CTA against 13.5); cuts by limit fit few: 64
+// streams of 32 tiles are 128 CTAs of one segment, where even cuts give 152 CTAs two segments each
+// and more partials to merge.
+// *largest: that load, with the combine pass where a unit is cut.
+inline int cut_units(const std::vector<int32_t> &nt, int min_tiles, int sms, int64_t *b, bool *cut, int64_t *largest) {
+    const int64_t seg = UNIT_SEG_COST;
+    int64_t tiles = 0, most = 0;
+    for (int32_t t : nt) {
+        tiles += t;
+        most = std::max<int64_t>(most, t);
+    }
+    const int n = cut_evenly(nt, seg, min_tiles, sms, b, cut);
+    int64_t load = 0;
+    for (int i = 0; i < n; ++i) {   // tiles and segments of [b[i], b[i + 1])
+        int64_t u = b[i] >> 32, t = b[i] & 0xffffffffll, w = 0;
+        const int64_t ue = b[i + 1] >> 32, te = b[i + 1] & 0xffffffffll;
+        for (; u < ue; ++u, t = 0) w += nt[u] - t + seg;
+        if (te > t) w += te - t + seg;
+        load = std::max(load, w);
+    }
+    *largest = load + (*cut ? combine_cost(nt.size()) : 0);
+    // the smallest limit that needs at most sms ranges and cuts nothing below min_tiles
+    int64_t lo = std::max<int64_t>(seg + std::min<int64_t>(most, min_tiles), (tiles + sms - 1) / sms + seg);
+    int64_t hi = *largest;
+    if (lo > hi || cut_by_limit(nt, seg, hi, sms, nullptr, nullptr) > sms) return n;
+    while (lo < hi) {
+        const int64_t mid = lo + (hi - lo) / 2;
+        if (cut_by_limit(nt, seg, mid, sms, nullptr, nullptr) <= sms) hi = mid; else lo = mid + 1;
+    }
+    bool c2 = false;
+    cut_by_limit(nt, seg, lo, sms, nullptr, &c2);
+    const int64_t cost = lo + (c2 ? combine_cost(nt.size()) : 0);
+    if (cost > *largest) return n;
+    *largest = cost;
+    *cut = c2;
+    return cut_by_limit(nt, seg, lo, sms, b, nullptr);
+}
+
+// clusters[k]: clusters of k CTAs that the device runs at a time.
+inline Plan plan_blocks(int S, int R, int H, const int64_t *h_len, int max_blk, int sms, const int *clusters,
+                        int64_t *rb) {
     Plan pl;
     const int hg = (H + NCOL - 1) / NCOL;
     std::vector<int32_t> nt((size_t)S * R * hg);
@@ -1966,13 +2162,29 @@ inline Plan plan_blocks(int S, int R, int H, const int64_t *h_len, int max_blk, 
     pl.mode = MODE_BLOCKS;
     pl.total = (int64_t)nt.size();
     pl.rep = 1;
-    pl.nranges = cut_units(nt, BLOCKS_SEG_COST, MIN_TILES, sms, rb, &cut);
+    int64_t load = 0;
+    pl.nranges = cut_units(nt, UNIT_MIN_TILES, sms, rb, &cut, &load);
     pl.nctas = pl.nranges;
     pl.slots = cut ? 2 * (size_t)pl.nctas : 0;
+    // few units: k CTAs each, one cluster, for the k that ends first
+    int32_t most = 0;
+    for (int32_t t : nt) most = std::max(most, t);
+    for (int k = 2; k <= MAX_MERGE && k <= most; ++k) {
+        const int64_t l = (most + k - 1) / k + UNIT_SEG_COST + MERGE_COST;
+        if ((int64_t)nt.size() <= clusters[k] && l < load) {
+            load = l;
+            pl.merge = k;
+        }
+    }
+    if (pl.merge) {
+        for (size_t v = 0; v < nt.size(); ++v)
+            for (int i = 0; i < pl.merge; ++i) rb[v * pl.merge + i] = unit_pos((int64_t)v, (int64_t)nt[v] * i / pl.merge);
+        pl.nranges = pl.nctas = (int)nt.size() * pl.merge;
+        rb[pl.nranges] = unit_pos((int64_t)nt.size(), 0);
+        pl.slots = (size_t)pl.nctas;
+    }
     return pl;
 }
-
-constexpr int64_t SHARED_SEG_COST = 5;   // SHARED: a unit's start, in key tiles
 
 // The entries of a shared call: own rows of each stream, then the shared rows of each group that
 // shares any (in whole tiles; the rest of a prefix counts as each stream's own).  order[s]: the
@@ -2022,7 +2234,8 @@ inline Plan plan_shared(const std::vector<int32_t> &nt, int nshared, int sms, in
     pl.mode = MODE_SHARED;
     pl.total = (int64_t)nt.size();
     pl.rep = 1;
-    pl.nranges = cut_units(nt, SHARED_SEG_COST, MIN_TILES, sms, rb, &cut);
+    int64_t load = 0;
+    pl.nranges = cut_units(nt, UNIT_MIN_TILES, sms, rb, &cut, &load);
     pl.nctas = pl.nranges;
     pl.slots = cut || nshared > 0 ? nt.size() + (size_t)pl.nctas : 0;
     return pl;
@@ -2088,6 +2301,10 @@ static int device_sms() {
     return n < attn::MAX_CTAS ? n : attn::MAX_CTAS;
 }
 
+// Clusters of k = 0 .. MAX_MERGE attention CTAs that the current device runs at a time (0 for k < 2,
+// and without a device).  One resident CTA a SM in every instance, so one instance is asked.
+static const int *device_clusters();
+
 static size_t slots_bytes(size_t slots) {
     if (slots == 0) return 0;
     const size_t o = slots * attn::slot_bytes();
@@ -2101,7 +2318,7 @@ size_t attend_workspace_bytes(bool invariant, int S, int R, int H, const int64_t
 
 size_t blocks_workspace_bytes(int S, int R, int H, const int64_t *h_len, int max_blk) {
     int64_t rb[attn::MAX_CTAS + 1];
-    return slots_bytes(attn::plan_blocks(S, R, H, h_len, max_blk, device_sms(), rb).slots);
+    return slots_bytes(attn::plan_blocks(S, R, H, h_len, max_blk, device_sms(), device_clusters(), rb).slots);
 }
 
 int shared_workspace_bytes(int S, int R, int H, const int64_t *h_len, const int32_t *h_gsize, int G,
@@ -2269,6 +2486,35 @@ static bool attend_ready() {
     return attr_ok;
 }
 
+static const int *device_clusters() {
+    using namespace attn;
+    static int n[MAX_MERGE + 1] = {};
+    static std::once_flag once;
+    std::call_once(once, [] {
+        if (!attend_ready()) {
+            cudaGetLastError();
+            return;
+        }
+        for (int k = 2; k <= MAX_MERGE; ++k) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)k);
+            cfg.blockDim = dim3(kernel_threads<MODE_BLOCKS, true>());
+            cfg.dynamicSmemBytes = SMEM_TOTAL;
+            cudaLaunchAttribute a;
+            a.id = cudaLaunchAttributeClusterDimension;
+            a.val.clusterDim.x = (unsigned)k;
+            a.val.clusterDim.y = a.val.clusterDim.z = 1;
+            cfg.attrs = &a;
+            cfg.numAttrs = 1;
+            int c = 0;
+            if (cudaOccupancyMaxActiveClusters(&c, mla_attend_kernel<MODE_BLOCKS, true>, &cfg) == cudaSuccess) n[k] = c;
+            else cudaGetLastError();
+            n[k] = std::min(n[k], MAX_CTAS / k);   // the bounds' table
+        }
+    });
+    return n;
+}
+
 // The parameters every mode takes.  Params is large (tensor maps + the per-stream plan); there is
 // one per host thread.
 static int fill_params(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, int S, int R, int H,
@@ -2320,6 +2566,7 @@ static int launch_plan(tf_kvpool *pool, attn::Params &p, const attn::Plan &pl, v
     p.total = pl.total;
     p.nranges = pl.nranges;
     p.rep = pl.rep;
+    p.merge = pl.merge;
     const size_t slots = pl.slots;
     p.ws_o = slots ? static_cast<float *>(d_ws) : nullptr;
     p.ws_ml = slots ? reinterpret_cast<float *>(static_cast<char *>(d_ws) + slots * slot_bytes()) : nullptr;
@@ -2339,11 +2586,11 @@ static int launch_plan(tf_kvpool *pool, attn::Params &p, const attn::Plan &pl, v
                    : pl.mode == MODE_SHARED ? mla_attend_kernel<MODE_SHARED>
                                             : mla_attend_kernel<MODE_SPLITS>;
         const int threads = f8 || pl.mode == MODE_SPARSE ? THREADS + 128 : THREADS;
-        const cudaError_t e = launch_pdl(kern, dim3(pl.nctas), dim3(threads), SMEM_TOTAL, st, p);
+        const cudaError_t e = launch_pdl_cluster(std::max(1, pl.merge), kern, dim3(pl.nctas), dim3(threads), SMEM_TOTAL, st, p);
         launch_counter()++;
         if (e != cudaSuccess) return TF_E_CUDA;
     }
-    if (slots) {
+    if (slots && !pl.merge) {
         ProfScope prof(pool, kProfCombine, st);
         const bool wide = max_partials(p, pl) > COMBINE_NARROW_MAX;
         const int groups = (p.ncols + NCOL - 1) / NCOL;
@@ -2427,7 +2674,7 @@ int launch_attend_blocks(tf_kvpool *pool, int cache, const int32_t *d_pt, int ma
     pp->max_idx = max_blk;
     pp->groups = R * ((H + NCOL - 1) / NCOL);   // a unit's columns are of one query row
     for (int s = 0; s < S; ++s) pp->st[s].len = h_len[s];
-    const Plan pl = plan_blocks(S, R, H, h_len, max_blk, device_sms(), pp->rb);
+    const Plan pl = plan_blocks(S, R, H, h_len, max_blk, device_sms(), device_clusters(), pp->rb);
     return launch_plan(pool, *pp, pl, d_ws, st);
 }
 

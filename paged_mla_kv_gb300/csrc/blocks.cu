@@ -266,20 +266,8 @@ struct Items {
 };
 
 // ---- a pair of CTAs ----
-__device__ __forceinline__ uint32_t pair_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
 // the address, in the pair's shared memory, of this CTA's `p` in the leader
-__device__ __forceinline__ uint32_t leader_addr(const void *p) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(ptx::smem_u32(p)));
-    return a;
-}
-__device__ __forceinline__ void pair_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ uint32_t leader_addr(const void *p) { return ptx::cluster_addr(ptx::smem_u32(p), 0); }
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -368,7 +356,7 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
     Ctrl &c = *reinterpret_cast<Ctrl *>(smem + SMEM_CTRL);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     ptx::griddep_launch_dependents();
-    const uint32_t rank = pair_rank();
+    const uint32_t rank = ptx::cluster_rank();
     if (threadIdx.x == 0) {
         ptx::mbar_init(&c.a_full, 1);
         ptx::mbar_init(&c.a_free, 1);
@@ -387,7 +375,7 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
     if (warp == EPI / 32 + 1) pair_tmem_alloc(&c.tmem_base, TCOLS);
     ptx::tc_fence_before();
     __syncthreads();
-    pair_sync();   // the peer's barriers are ready
+    ptx::cluster_sync();   // the peer's barriers are ready
     ptx::tc_fence_after();
     const uint32_t tmem = c.tmem_base;
     volatile int *abort = &c.abort;
@@ -630,7 +618,7 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
 
     ptx::tc_fence_before();
     __syncthreads();
-    pair_sync();   // both CTAs are done with each other's barriers and TMEM
+    ptx::cluster_sync();   // both CTAs are done with each other's barriers and TMEM
     ptx::tc_fence_after();
     if (warp == EPI / 32 + 1) pair_tmem_dealloc(tmem, TCOLS);
 }
