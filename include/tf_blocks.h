@@ -89,10 +89,11 @@ int tf_block_scores(tf_kvpool *pool, const void *d_bkeys, const int32_t *d_pt, i
  * a table entry outside the pool; the call's output is then undefined.
  * d_blk: int32 [S][R][max_blk]; everything else as in tf_paged_mla_attend, BF16 and FP8 pages alike.  The
  * blocks are dealt out by the default plan whatever the pool's flags: a row's bits may differ (within
- * rounding) between batches and are the same on every call of one batch.
+ * rounding) between batches and are the same on every call of one batch.  The rows of an FP8 pool that many
+ * query rows read are first expanded to BF16 pages in the workspace, whose size then includes them.
  * Errors: as for tf_paged_mla_attend, and TF_E_ARG for max_blk < 1 or a null d_blk. */
 size_t tf_paged_mla_blocks_workspace_bytes(const tf_kvpool *pool, int32_t S, int32_t R, int32_t H, const int64_t *h_len,
-                                           int32_t max_blk);   /* pool may be NULL */
+                                           int32_t max_blk);   /* pool may be NULL: a BF16 pool */
 
 int tf_paged_mla_attend_blocks(tf_kvpool *pool, int32_t cache, const int32_t *d_pt, int32_t max_pages,
                                const int64_t *h_len, const int32_t *d_blk, int32_t max_blk, int32_t S, int32_t R,
@@ -110,12 +111,13 @@ int tf_paged_mla_attend_blocks(tf_kvpool *pool, int32_t cache, const int32_t *d_
  * Both arrays have G entries, 1 <= G <= S.  All else as in tf_paged_mla_attend, BF16 and FP8 pages alike;
  * the keys are dealt out by a plan of their own whatever the pool's flags, so bits may differ (within
  * rounding) from tf_paged_mla_attend and between batches, and are the same on every call of one batch.
- * The workspace can be larger than that call's.
+ * The workspace can be larger than that call's (and holds a BF16 copy of the rows of an FP8 pool that
+ * many columns read).
  * Errors: as for tf_paged_mla_attend; TF_E_ARG for a null array, a size below 1 or sizes that do not add up;
  * TF_E_RANGE for a prefix outside its bounds; TF_E_UNSUPPORTED if S plus the groups that share passes
  * TF_MAX_STREAMS. */
 size_t tf_paged_mla_shared_workspace_bytes(const tf_kvpool *pool, int32_t S, int32_t R, int32_t H, const int64_t *h_len,
-                                           const int32_t *h_gsize, int32_t G, const int64_t *h_prefix);   /* pool may be NULL */
+                                           const int32_t *h_gsize, int32_t G, const int64_t *h_prefix);   /* pool may be NULL: a BF16 pool */
 
 int tf_paged_mla_attend_shared(tf_kvpool *pool, int32_t cache, const int32_t *d_pt, int32_t max_pages,
                                const int64_t *h_len, const int32_t *h_gsize, int32_t G, const int64_t *h_prefix, int32_t S,

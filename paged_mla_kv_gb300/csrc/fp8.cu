@@ -11,6 +11,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <functional>
 #include <mutex>
 
 #include "ptx.cuh"
@@ -112,68 +113,74 @@ struct DequantParams {
     DevErr *err;
     int32_t max_pages, num_pages, S, maxp;
     int64_t len[TF_MAX_STREAMS];
-    int32_t off[TF_MAX_STREAMS];  // the stream's first shadow page
+    int32_t off[TF_MAX_STREAMS];  // the shadow page of the stream's logical page 0
+    int32_t from[TF_MAX_STREAMS]; // the stream's first page to expand
 };
 
-// grid (maxp, S): logical page j of stream s, rows [0, min(512, len - 512 j)), expanded to a
-// BF16 page: latent value = bf16(code * scale), rope copied.
+// grid (8 maxp, S): 64 rows of logical page j of stream s, as many as the stream holds, expanded to a
+// BF16 page: latent value = bf16(code * scale), rope copied.  An eighth of a page a block: whole
+// pages left most SMs idle for short streams (8,192 rows took 28 us more than on a BF16 pool).
 constexpr int kDequantThreads = 512;
+constexpr int kDequantRows = 64;
 
 __global__ void __launch_bounds__(kDequantThreads) dequant_kernel(const __grid_constant__ DequantParams p) {
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    const int j = blockIdx.x, s = blockIdx.y;
-    const int64_t rem = p.len[s] - (int64_t)j * kPageRows;
-    if (rem <= 0) return;
-    const int rows = rem < kPageRows ? (int)rem : kPageRows;
+    constexpr int kParts = kPageRows / kDequantRows;
+    const int j = blockIdx.x / kParts, r0 = (int)blockIdx.x % kParts * kDequantRows, s = blockIdx.y;
+    const int64_t rem = p.len[s] - (int64_t)j * kPageRows - r0;
+    if (rem <= 0 || j < p.from[s]) return;
+    const int rows = rem < kDequantRows ? (int)rem : kDequantRows;
     const int page = p.pt ? __ldg(p.pt + (int64_t)s * p.max_pages + j) : s * p.max_pages + j;
     if (page < 0 || page >= p.num_pages) {
         if (threadIdx.x == 0) ptx::record_error(p.err, TF_E_DEVICE, page);
         return;
     }
     const int dpage = p.off[s] + j;
-    if (threadIdx.x == 0) p.shadow_pt[(int64_t)s * p.maxp + j] = dpage;
+    if (threadIdx.x == 0 && r0 == 0) p.shadow_pt[(int64_t)s * p.maxp + j] = dpage;
     const char *src = p.cache_base + (size_t)page * kF8PageBytes;
     char *dst = p.shadow + (size_t)dpage * kPageBytes;
-    const float *scales = reinterpret_cast<const float *>(src + kF8ScaleOff);
+    const float *scales = reinterpret_cast<const float *>(src + kF8ScaleOff) + r0;
+    const uint4 *codes = reinterpret_cast<const uint4 *>(src + (size_t)r0 * kLat);
+    uint4 *lat = reinterpret_cast<uint4 *>(dst + (size_t)r0 * kLat * 2);
+    const uint4 *rope = reinterpret_cast<const uint4 *>(src + kF8RopeOff + (size_t)r0 * kRope * 2);
+    uint4 *drope = reinterpret_cast<uint4 *>(dst + kLatBlockBytes + (size_t)r0 * kRope * 2);
     const int nc = rows * (kLat / 16);  // 16 codes a unit
-    constexpr int U = 4;                // units a thread has in flight
-    for (int k0 = threadIdx.x; k0 < nc; k0 += U * kDequantThreads) {
-        uint4 c[U];
-        float sc[U];
+    constexpr int U = kDequantRows * (kLat / 16) / kDequantThreads;   // units a thread, all in flight
+    static_assert(U * kDequantThreads == kDequantRows * (kLat / 16) && kDequantThreads == kDequantRows * kRope * 2 / 16,
+                  "a round of units and one of rope chunks");
+    uint4 c[U];
+    float sc[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = k0 + u * kDequantThreads;
-            if (k < nc) {
-                c[u] = __ldg(reinterpret_cast<const uint4 *>(src) + k);
-                sc[u] = __ldg(scales + (k >> 5));
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = k0 + u * kDequantThreads;
-            if (k >= nc) break;
-            const uint32_t cw[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
-            uint32_t o[8];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
-                        (__nv_fp8x2_storage_t)((cw[q] >> (16 * h)) & 0xFFFFu), __NV_E4M3);
-                    const float2 f = __half22float2(__half2(hr));
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * sc[u], f.y * sc[u]);
-                    o[2 * q + h] = *reinterpret_cast<const uint32_t *>(&b);
-                }
-            }
-            uint4 *d = reinterpret_cast<uint4 *>(dst) + 2 * k;
-            d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-            d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    for (int u = 0; u < U; ++u) {
+        const int k = threadIdx.x + u * kDequantThreads;
+        if (k < nc) {
+            c[u] = __ldg(codes + k);
+            sc[u] = __ldg(scales + (k >> 5));
         }
     }
     const int nr = rows * (kRope * 2 / 16);
-    for (int k = threadIdx.x; k < nr; k += blockDim.x)
-        reinterpret_cast<uint4 *>(dst + kLatBlockBytes)[k] = __ldg(reinterpret_cast<const uint4 *>(src + kF8RopeOff) + k);
+    if ((int)threadIdx.x < nr) drope[threadIdx.x] = __ldg(rope + threadIdx.x);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int k = threadIdx.x + u * kDequantThreads;
+        if (k >= nc) break;
+        const uint32_t cw[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
+                    (__nv_fp8x2_storage_t)((cw[q] >> (16 * h)) & 0xFFFFu), __NV_E4M3);
+                const float2 f = __half22float2(__half2(hr));
+                const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * sc[u], f.y * sc[u]);
+                o[2 * q + h] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+        }
+        lat[2 * k] = make_uint4(o[0], o[1], o[2], o[3]);
+        lat[2 * k + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
 }
 
 int launch_append_fp8(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_pos, int S,
@@ -218,11 +225,12 @@ struct ShadowPlan {
     int32_t maxp = 0;    // most pages of one stream
     size_t table_bytes = 0;
 };
-ShadowPlan shadow_plan(int S, const int64_t *h_len) {
+// h_from: the first page of each stream to expand (null: 0).
+ShadowPlan shadow_plan(int S, const int64_t *h_len, const int32_t *h_from) {
     ShadowPlan sp;
     for (int s = 0; s < S; ++s) {
         const int64_t np = (h_len[s] + kPageRows - 1) / kPageRows;
-        sp.pages += np;
+        sp.pages += std::max<int64_t>(0, np - (h_from ? h_from[s] : 0));
         sp.maxp = std::max<int32_t>(sp.maxp, (int32_t)np);
     }
     sp.table_bytes = ((size_t)S * sp.maxp * 4 + 1023) / 1024 * 1024;
@@ -231,15 +239,15 @@ ShadowPlan shadow_plan(int S, const int64_t *h_len) {
 }  // namespace
 
 // The expanded rows: a page table and the BF16 pages, with room to align the pages to 1 KiB.
-size_t fp8_shadow_bytes(int S, const int64_t *h_len) {
-    const ShadowPlan sp = shadow_plan(S, h_len);
+size_t fp8_shadow_bytes(int S, const int64_t *h_len, const int32_t *h_from) {
+    const ShadowPlan sp = shadow_plan(S, h_len, h_from);
     return sp.table_bytes + 1024 + (size_t)sp.pages * kPageBytes;
 }
 
-int launch_attend_fp8(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_len, int S,
-                      int R, int H, const void *d_q, float scale, void *d_out, float *d_lse, void *d_ws,
-                      size_t ws_bytes, size_t attend_ws, cudaStream_t st) {
-    const ShadowPlan sp = shadow_plan(S, h_len);
+int launch_over_expanded(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_len,
+                         const int32_t *h_from, int S, void *d_ws, size_t ws_bytes, size_t attend_ws, cudaStream_t st,
+                         const std::function<int(tf_kvpool *, const int32_t *, int)> &attend) {
+    const ShadowPlan sp = shadow_plan(S, h_len, h_from);
     if (sp.pages * (int64_t)kPageBytes / (int64_t)kPageBytes != sp.pages || sp.pages >= (1ll << 31))
         return TF_E_UNSUPPORTED;
     const size_t part = (attend_ws + 1023) / 1024 * 1024;  // partials first, as on a BF16 pool
@@ -282,16 +290,28 @@ int launch_attend_fp8(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_p
     int32_t off = 0;
     for (int s = 0; s < S; ++s) {
         p.len[s] = h_len[s];
-        p.off[s] = off;
-        off += (int32_t)((h_len[s] + kPageRows - 1) / kPageRows);
+        p.from[s] = h_from ? h_from[s] : 0;
+        p.off[s] = off - p.from[s];
+        off += std::max<int32_t>(0, (int32_t)((h_len[s] + kPageRows - 1) / kPageRows) - p.from[s]);
     }
     if (prepare_launch(pool, st) != TF_OK) return TF_E_CUDA;
     ProfScope prof(pool, kProfAttend, st);  // the expansion and the attention together
     const cudaError_t e =
-        launch_pdl(dequant_kernel, dim3((unsigned)sp.maxp, (unsigned)S), dim3(kDequantThreads), 0, st, p);
+        launch_pdl(dequant_kernel, dim3((unsigned)sp.maxp * (kPageRows / kDequantRows), (unsigned)S), dim3(kDequantThreads),
+                   0, st, p);
     launch_counter()++;
     if (e != cudaSuccess) return TF_E_CUDA;
-    return launch_attend(sh, 0, spt, sp.maxp, h_len, S, R, H, d_q, scale, d_out, d_lse, d_ws, attend_ws, st);
+    return attend(sh, spt, sp.maxp);
+}
+
+int launch_attend_fp8(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_len, int S,
+                      int R, int H, const void *d_q, float scale, void *d_out, float *d_lse, void *d_ws,
+                      size_t ws_bytes, size_t attend_ws, cudaStream_t st) {
+    return launch_over_expanded(pool, cache, d_pt, max_pages, h_len, nullptr, S, d_ws, ws_bytes, attend_ws, st,
+                                [&](tf_kvpool *sh, const int32_t *spt, int maxp) {
+                                    return launch_attend(sh, 0, spt, maxp, h_len, S, R, H, d_q, scale, d_out, d_lse,
+                                                         d_ws, attend_ws, st);
+                                });
 }
 
 }  // namespace tf

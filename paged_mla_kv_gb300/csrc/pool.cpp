@@ -357,20 +357,20 @@ static int no_throw(F &&f) {
     }
 }
 
-static int blocks_size(int32_t S, int32_t R, int32_t H, const int64_t *h_len, int32_t max_blk, size_t *bytes) {
+static int blocks_size(const tf_kvpool *p, int32_t S, int32_t R, int32_t H, const int64_t *h_len, int32_t max_blk, size_t *bytes) {
     const int rc = batch_checks(S, R, H, h_len);
     if (rc != TF_OK) return rc;
     if (max_blk < 1) return TF_E_ARG;
     return no_throw([&] {
-        *bytes = blocks_workspace_bytes(S, R, H, h_len, max_blk);
+        *bytes = blocks_workspace_bytes(p && is_fp8(p->desc), S, R, H, h_len, max_blk);
         return TF_OK;
     });
 }
 
-extern "C" size_t tf_paged_mla_blocks_workspace_bytes(const tf_kvpool *, int32_t S, int32_t R, int32_t H,
+extern "C" size_t tf_paged_mla_blocks_workspace_bytes(const tf_kvpool *p, int32_t S, int32_t R, int32_t H,
                                                       const int64_t *h_len, int32_t max_blk) {
     size_t n = 0;
-    return blocks_size(S, R, H, h_len, max_blk, &n) == TF_OK ? n : 0;
+    return blocks_size(p, S, R, H, h_len, max_blk, &n) == TF_OK ? n : 0;
 }
 
 extern "C" int tf_paged_mla_attend_blocks(tf_kvpool *p, int32_t cache, const int32_t *d_pt, int32_t max_pages,
@@ -378,18 +378,18 @@ extern "C" int tf_paged_mla_attend_blocks(tf_kvpool *p, int32_t cache, const int
                                           int32_t R, int32_t H, const void *d_q, float scale, void *d_out,
                                           float *d_lse, void *d_ws, size_t ws_bytes, void *stream) {
     size_t need = 0;
-    int rc = blocks_size(S, R, H, h_len, max_blk, &need);
+    int rc = blocks_size(p, S, R, H, h_len, max_blk, &need);
     if (rc == TF_OK) rc = call_checks(p, cache, d_pt, max_pages, h_len, S, d_q, scale, d_out);
     if (rc == TF_OK && !d_blk) rc = TF_E_ARG;
     if (rc == TF_OK) rc = ws_check(need, d_ws, ws_bytes);
     if (rc != TF_OK) return rc;
     return no_throw([&] {
         return launch_attend_blocks(p, cache, d_pt, max_pages, h_len, d_blk, max_blk, S, R, H, d_q, scale, d_out,
-                                    d_lse, d_ws, (cudaStream_t)stream);
+                                    d_lse, d_ws, ws_bytes, (cudaStream_t)stream);
     });
 }
 
-static int shared_size(int32_t S, int32_t R, int32_t H, const int64_t *h_len, const int32_t *h_gsize, int32_t G,
+static int shared_size(const tf_kvpool *p, int32_t S, int32_t R, int32_t H, const int64_t *h_len, const int32_t *h_gsize, int32_t G,
                        const int64_t *h_prefix, size_t *bytes) {
     const int rc = batch_checks(S, R, H, h_len);
     if (rc != TF_OK) return rc;
@@ -404,14 +404,14 @@ static int shared_size(int32_t S, int32_t R, int32_t H, const int64_t *h_len, co
     for (int g = 0, s = 0; g < G; ++g)
         for (int k = 0; k < h_gsize[g]; ++k, ++s)
             if (h_prefix[g] < 0 || h_prefix[g] > h_len[s] - R + 1) return TF_E_RANGE;
-    return no_throw([&] { return shared_workspace_bytes(S, R, H, h_len, h_gsize, G, h_prefix, bytes); });
+    return no_throw([&] { return shared_workspace_bytes(p && is_fp8(p->desc), S, R, H, h_len, h_gsize, G, h_prefix, bytes); });
 }
 
-extern "C" size_t tf_paged_mla_shared_workspace_bytes(const tf_kvpool *, int32_t S, int32_t R, int32_t H,
+extern "C" size_t tf_paged_mla_shared_workspace_bytes(const tf_kvpool *p, int32_t S, int32_t R, int32_t H,
                                                       const int64_t *h_len, const int32_t *h_gsize, int32_t G,
                                                       const int64_t *h_prefix) {
     size_t n = 0;
-    return shared_size(S, R, H, h_len, h_gsize, G, h_prefix, &n) == TF_OK ? n : 0;
+    return shared_size(p, S, R, H, h_len, h_gsize, G, h_prefix, &n) == TF_OK ? n : 0;
 }
 
 extern "C" int tf_paged_mla_attend_shared(tf_kvpool *p, int32_t cache, const int32_t *d_pt, int32_t max_pages,
@@ -420,13 +420,13 @@ extern "C" int tf_paged_mla_attend_shared(tf_kvpool *p, int32_t cache, const int
                                           float scale, void *d_out, float *d_lse, void *d_ws, size_t ws_bytes,
                                           void *stream) {
     size_t need = 0;
-    int rc = shared_size(S, R, H, h_len, h_gsize, G, h_prefix, &need);
+    int rc = shared_size(p, S, R, H, h_len, h_gsize, G, h_prefix, &need);
     if (rc == TF_OK) rc = call_checks(p, cache, d_pt, max_pages, h_len, S, d_q, scale, d_out);
     if (rc == TF_OK) rc = ws_check(need, d_ws, ws_bytes);
     if (rc != TF_OK) return rc;
     return no_throw([&] {
         return launch_attend_shared(p, cache, d_pt, max_pages, h_len, h_gsize, G, h_prefix, S, R, H, d_q, scale, d_out,
-                                    d_lse, d_ws, (cudaStream_t)stream);
+                                    d_lse, d_ws, ws_bytes, (cudaStream_t)stream);
     });
 }
 

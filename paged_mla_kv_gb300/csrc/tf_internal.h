@@ -6,6 +6,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <functional>
 #include <mutex>
 #include <utility>
 #include <vector>
@@ -144,7 +145,13 @@ int launch_append_fp8(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_p
                       int S, int n, const void *d_lat, const void *d_rope, cudaStream_t st);
 int launch_state_copy_fp8(tf_kvpool *pool, int cache, const int32_t *d_src, const int32_t *d_dst, int64_t at,
                           cudaStream_t st);
-size_t fp8_shadow_bytes(int S, const int64_t *h_len);
+// Rows expanded to BF16 pages in the workspace, stream s from its page h_from[s] on (null: 0), and the
+// attention that `attend` launches over that view (a pool, its page table and the table's width).  A
+// stream's table entries before h_from[s] are not set.
+size_t fp8_shadow_bytes(int S, const int64_t *h_len, const int32_t *h_from = nullptr);
+int launch_over_expanded(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_len,
+                         const int32_t *h_from, int S, void *d_ws, size_t ws_bytes, size_t attend_ws, cudaStream_t st,
+                         const std::function<int(tf_kvpool *, const int32_t *, int)> &attend);
 int launch_attend_fp8(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_len, int S,
                       int R, int H, const void *d_q, float scale, void *d_out, float *d_lse, void *d_ws,
                       size_t ws_bytes, size_t attend_ws, cudaStream_t st);
@@ -158,16 +165,16 @@ int launch_attend(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages
                   size_t ws_bytes, cudaStream_t st, const int32_t *d_idx = nullptr, int max_idx = 0,
                   const int32_t *h_nidx = nullptr);
 // Attention over listed blocks, and of streams that share a prefix (attend.cu).
-size_t blocks_workspace_bytes(int S, int R, int H, const int64_t *h_len, int max_blk);
+size_t blocks_workspace_bytes(bool fp8, int S, int R, int H, const int64_t *h_len, int max_blk);
 int launch_attend_blocks(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_len,
                          const int32_t *d_blk, int max_blk, int S, int R, int H, const void *d_q, float scale,
-                         void *d_out, float *d_lse, void *d_ws, cudaStream_t st);
+                         void *d_out, float *d_lse, void *d_ws, size_t ws_bytes, cudaStream_t st);
 // TF_E_UNSUPPORTED: too many streams and sharing groups for one launch.
-int shared_workspace_bytes(int S, int R, int H, const int64_t *h_len, const int32_t *h_gsize, int G,
+int shared_workspace_bytes(bool fp8, int S, int R, int H, const int64_t *h_len, const int32_t *h_gsize, int G,
                            const int64_t *h_prefix, size_t *bytes);
 int launch_attend_shared(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_len,
                          const int32_t *h_gsize, int G, const int64_t *h_prefix, int S, int R, int H, const void *d_q,
-                         float scale, void *d_out, float *d_lse, void *d_ws, cudaStream_t st);
+                         float scale, void *d_out, float *d_lse, void *d_ws, size_t ws_bytes, cudaStream_t st);
 // Block keys and their scores (blocks.cu).
 int launch_block_keys(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_from,
                       const int64_t *h_len, int S, void *d_bkeys, cudaStream_t st);

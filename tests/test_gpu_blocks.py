@@ -476,7 +476,8 @@ def check_dense(w, out, lse, fp8=False, rows=None):
     ([(512, [1, 64, 65]), (0, [300]), (2048, [2, 600])], 2, 64),
     ([(1536, [3, 3])], 3, 128), ([(512, [40, 90, 41])], 40, 5), ([(2560, [1] * 30)], 1, 5),
     ([(512, [100]), (1024, [100])], 1, 64),           # groups of one stream share nothing
-    ([(16384, [1, 900, 17])], 1, 64)])
+    ([(16384, [1, 900, 17])], 1, 64),
+    ([(4096, [9, 70, 600]), (2560, [5, 5])], 5, 128)])   # rows that many columns read: FP8 pages are expanded first
 def test_attend_shared(groups, R, H, fp8):
     w, sizes, prefixes = shared_workload("sh", 140 + R + H, groups, R, H)
     res = Resident(w, fp8=fp8)
