@@ -8,6 +8,7 @@ library has not been built.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -154,6 +155,12 @@ def _stream(stream):
 
 
 def _i64(a):
+    if type(a) is list:
+        try:
+            a = array.array("q", a)   # about half of what numpy takes for a short list
+            return a, a.buffer_info()[0]
+        except TypeError:
+            pass
     if not (isinstance(a, np.ndarray) and a.dtype == np.int64 and a.flags.c_contiguous):
         a = np.ascontiguousarray(a, dtype=np.int64)
     return a, a.ctypes.data
@@ -304,6 +311,12 @@ def tf_paged_mla_attend_static(pool: KVPool, cache: int, pt, max_pages: int, len
 
 
 def _i32(a):
+    if type(a) is list:
+        try:
+            a = array.array("i", a)
+            return a, a.buffer_info()[0]
+        except (TypeError, OverflowError):
+            pass
     if not (isinstance(a, np.ndarray) and a.dtype == np.int32 and a.flags.c_contiguous):
         a = np.ascontiguousarray(a, dtype=np.int32)
     return a, a.ctypes.data
@@ -355,20 +368,30 @@ def tf_topk_blocked(logits, k: int, idx, val, lens=None, n: int | None = None, w
 TF_BLOCK_ROWS = 64
 
 
-def _given(what: str, ok: bool) -> None:
-    """Refuse what the library cannot see: host arrays of another length, tensors of another type or layout."""
-    if not ok:
-        raise TFError(TF_E_ARG, what)
+# What the library cannot see is refused here: host arrays of another length, tensors of another type,
+# size or layout.  A check is on every call's path, so it asks for as little as it can.
+_types = None
 
 
-def _dense(t, dtype: str, shape=None) -> bool:
-    return t is None or (str(t.dtype) == dtype and t.is_contiguous() and (shape is None or t.shape == shape))
+def _dtypes():
+    global _types
+    if _types is None:
+        import torch
+        _types = (torch.bfloat16, torch.float32, torch.int32)
+    return _types
 
 
-def _qout(q, out, lse) -> bool:
-    lead = tuple(q.shape[:3])
-    return (q.dim() == 4 and q.shape[3] == 576 and _dense(q, "torch.bfloat16") and
-            _dense(out, "torch.bfloat16", lead + (512,)) and _dense(lse, "torch.float32", lead))
+def _refuse(what: str):
+    raise TFError(TF_E_ARG, what)
+
+
+def _dense(t, dtype, n: int) -> bool:
+    return t.dtype is dtype and t.numel() == n and t.is_contiguous()
+
+
+def _qout(q, out, lse, cols: int, bf16, f32) -> bool:
+    """q of 576, out of 512 and lse (or None) of one value for each of `cols` (stream, row, head)."""
+    return (_dense(q, bf16, cols * 576) and _dense(out, bf16, cols * 512) and (lse is None or _dense(lse, f32, cols)))
 
 
 def tf_block_keys_bytes(pool: KVPool) -> int:
@@ -381,9 +404,9 @@ def tf_block_keys_update(pool: KVPool, cache: int, pt, max_pages: int, start, le
     tensor [pages][8][576]."""
     a, p = _i64(start)
     b, pl = _i64(lens)
-    _given("tf_block_keys_update", len(a) == len(b) and (pt is None or pt.shape[0] >= len(b)) and
-           _dense(bkeys, "torch.bfloat16", (pool.num_pages, 8, 576)))
-    _check(lib().tf_block_keys_update(pool.handle, cache, _ptr(pt), max_pages, p, pl, len(b), _ptr(bkeys),
+    if not (len(a) == len(b) and _dense(bkeys, _dtypes()[0], pool.num_pages * 4608)):
+        _refuse("tf_block_keys_update")
+    _check(lib().tf_block_keys_update(pool.handle, cache, _ptr(pt), max_pages, p, pl, len(b), bkeys.data_ptr(),
                                       _stream(stream)), "tf_block_keys_update")
 
 
@@ -391,21 +414,24 @@ def tf_block_scores(pool: KVPool, bkeys, pt, max_pages: int, lens, q, scale: flo
                     sink: int = 1, local: int = 1, stream=None) -> None:
     """q: bf16 [S][R][H][576]; w: fp32 [S][R][H] or None (ones); scores: fp32 [S * R][ld] (row stride ld, a multiple
     of 4, at least the longest stream's blocks); nblk: int32 [S * R] or None, each row's visible blocks."""
-    S, R, H = int(q.shape[0]), int(q.shape[1]), int(q.shape[2])
+    S, R, H, _ = q.shape
+    bf16, f32, i32 = _dtypes()
     a, p = _i64(lens)
-    _given("tf_block_scores", len(a) == S and _dense(q, "torch.bfloat16") and _dense(w, "torch.float32", (S, R, H)) and
-           _dense(bkeys, "torch.bfloat16", (pool.num_pages, 8, 576)) and str(scores.dtype) == "torch.float32" and
-           scores.dim() == 2 and scores.shape[0] == S * R and scores.stride(1) == 1 and
-           scores.shape[1] * TF_BLOCK_ROWS >= (max(lens) if type(lens) is list else int(a.max())) and
-           (nblk is None or (_dense(nblk, "torch.int32") and nblk.numel() == S * R)))
-    _check(lib().tf_block_scores(pool.handle, _ptr(bkeys), _ptr(pt), max_pages, p, S, R, H, _ptr(q), _ptr(w),
-                                 float(scale), int(sink), int(local), _ptr(scores), int(scores.stride(0)), _ptr(nblk),
-                                 _stream(stream)), "tf_block_scores")
+    rows, cols = scores.shape
+    ld, one = scores.stride()
+    if not (len(a) == S and _dense(q, bf16, S * R * H * 576) and _dense(bkeys, bf16, pool.num_pages * 4608) and
+            (w is None or _dense(w, f32, S * R * H)) and (nblk is None or _dense(nblk, i32, S * R)) and
+            scores.dtype is f32 and rows == S * R and (one == 1 or cols == 1) and cols * TF_BLOCK_ROWS >= (max(a) if type(a) is array.array else a.max())):
+        _refuse("tf_block_scores")
+    _check(lib().tf_block_scores(pool.handle, bkeys.data_ptr(), _ptr(pt), max_pages, p, S, R, H, q.data_ptr(), _ptr(w),
+                                 scale, sink, local, scores.data_ptr(), ld, _ptr(nblk), _stream(stream)),
+           "tf_block_scores")
 
 
 def tf_paged_mla_blocks_workspace_bytes(pool, S: int, R: int, H: int, lens, max_blk: int) -> int:
     a, p = _i64(lens)
-    _given("tf_paged_mla_blocks_workspace_bytes", len(a) == S)
+    if len(a) != S:
+        _refuse("tf_paged_mla_blocks_workspace_bytes")
     return int(lib().tf_paged_mla_blocks_workspace_bytes(pool.handle if pool is not None else None, S, R, H, p,
                                                          int(max_blk)))
 
@@ -414,21 +440,24 @@ def tf_paged_mla_attend_blocks(pool: KVPool, cache: int, pt, max_pages: int, len
                                lse=None, ws=None, stream=None) -> None:
     """blk: int32 CUDA tensor [S][R][max_blk] (or [S * R][max_blk]) of block numbers, -1 for none; q, out, lse, ws
     as in tf_paged_mla_attend."""
-    S, R, H = int(q.shape[0]), int(q.shape[1]), int(q.shape[2])
+    S, R, H, _ = q.shape
+    bf16, f32, i32 = _dtypes()
     a, p = _i64(lens)
-    _given("tf_paged_mla_attend_blocks", len(a) == S and _qout(q, out, lse) and _dense(blk, "torch.int32") and
-           blk.numel() == S * R * int(blk.shape[-1]))
-    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check(lib().tf_paged_mla_attend_blocks(pool.handle, cache, _ptr(pt), max_pages, p, _ptr(blk), int(blk.shape[-1]),
-                                            S, R, H, _ptr(q), float(scale), _ptr(out), _ptr(lse), _ptr(ws), ws_bytes,
-                                            _stream(stream)), "tf_paged_mla_attend_blocks")
+    max_blk = blk.shape[-1]
+    if not (len(a) == S and _qout(q, out, lse, S * R * H, bf16, f32) and _dense(blk, i32, S * R * max_blk)):
+        _refuse("tf_paged_mla_attend_blocks")
+    _check(lib().tf_paged_mla_attend_blocks(pool.handle, cache, _ptr(pt), max_pages, p, blk.data_ptr(), max_blk, S, R, H,
+                                            q.data_ptr(), scale, out.data_ptr(), _ptr(lse), _ptr(ws),
+                                            0 if ws is None else ws.nbytes, _stream(stream)),
+           "tf_paged_mla_attend_blocks")
 
 
 def tf_paged_mla_shared_workspace_bytes(pool, S: int, R: int, H: int, lens, group_sizes, prefixes) -> int:
     a, p = _i64(lens)
     g, pg = _i32(group_sizes)
     f, pf = _i64(prefixes)
-    _given("tf_paged_mla_shared_workspace_bytes", len(a) == S and len(g) == len(f))
+    if not (len(a) == S and len(g) == len(f)):
+        _refuse("tf_paged_mla_shared_workspace_bytes")
     return int(lib().tf_paged_mla_shared_workspace_bytes(pool.handle if pool is not None else None, S, R, H, p, pg,
                                                          len(g), pf))
 
@@ -437,15 +466,17 @@ def tf_paged_mla_attend_shared(pool: KVPool, cache: int, pt, max_pages: int, len
                                scale: float, out, lse=None, ws=None, stream=None) -> None:
     """group_sizes: streams of each group, in order; prefixes: the rows each group's streams have in common; the rest
     as in tf_paged_mla_attend."""
-    S, R, H = int(q.shape[0]), int(q.shape[1]), int(q.shape[2])
+    S, R, H, _ = q.shape
+    bf16, f32, _ = _dtypes()
     a, p = _i64(lens)
     g, pg = _i32(group_sizes)
     f, pf = _i64(prefixes)
-    _given("tf_paged_mla_attend_shared", len(a) == S and len(g) == len(f) and _qout(q, out, lse))
-    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    if not (len(a) == S and len(g) == len(f) and _qout(q, out, lse, S * R * H, bf16, f32)):
+        _refuse("tf_paged_mla_attend_shared")
     _check(lib().tf_paged_mla_attend_shared(pool.handle, cache, _ptr(pt), max_pages, p, pg, len(g), pf, S, R, H,
-                                            _ptr(q), float(scale), _ptr(out), _ptr(lse), _ptr(ws), ws_bytes,
-                                            _stream(stream)), "tf_paged_mla_attend_shared")
+                                            q.data_ptr(), scale, out.data_ptr(), _ptr(lse), _ptr(ws),
+                                            0 if ws is None else ws.nbytes, _stream(stream)),
+           "tf_paged_mla_attend_shared")
 
 
 def tf_paged_mla_plan_info(S: int, R: int, H: int, lens, sms: int = 0, invariant: bool = False) -> dict:

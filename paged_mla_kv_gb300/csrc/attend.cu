@@ -2702,6 +2702,12 @@ int launch_attend(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages
     return launch_plan(pool, p, pl, d_ws, st);
 }
 
+static int check_workspace(size_t need, const void *d_ws, size_t ws_bytes) {
+    if (need == 0) return TF_OK;
+    if (!d_ws || (reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0) return TF_E_ARG;
+    return ws_bytes < need ? TF_E_NOMEM : TF_OK;
+}
+
 static int attend_blocks(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_len,
                          const int32_t *d_blk, int max_blk, int S, int R, int H, const void *d_q, float scale,
                          void *d_out, float *d_lse, void *d_ws, const attn::Plan &pl, const int64_t *rb, cudaStream_t st) {
@@ -2721,12 +2727,16 @@ int launch_attend_blocks(tf_kvpool *pool, int cache, const int32_t *d_pt, int ma
                          const int32_t *d_blk, int max_blk, int S, int R, int H, const void *d_q, float scale,
                          void *d_out, float *d_lse, void *d_ws, size_t ws_bytes, cudaStream_t st) {
     using namespace attn;
-    if (prepare_launch(pool, st) != TF_OK) return TF_E_CUDA;
     int64_t rb[MAX_CTAS + 1];
     const Plan pl = plan_blocks(S, R, H, h_len, max_blk, device_sms(), device_clusters(), rb);
-    if (is_fp8(pool->desc) && expand_blocks(S, R, H, h_len, max_blk))
-        return launch_over_expanded(pool, cache, d_pt, max_pages, h_len, nullptr, S, d_ws, ws_bytes, slots_bytes(pl.slots),
-                                    st, [&](tf_kvpool *sh, const int32_t *spt, int maxp) {
+    const bool expand = is_fp8(pool->desc) && expand_blocks(S, R, H, h_len, max_blk);
+    const size_t part = slots_bytes(pl.slots);
+    const int rc = check_workspace(expand ? with_expanded(part, fp8_shadow_bytes(S, h_len)) : part, d_ws, ws_bytes);
+    if (rc != TF_OK) return rc;
+    if (prepare_launch(pool, st) != TF_OK) return TF_E_CUDA;
+    if (expand)
+        return launch_over_expanded(pool, cache, d_pt, max_pages, h_len, nullptr, S, d_ws, ws_bytes, part, st,
+                                    [&](tf_kvpool *sh, const int32_t *spt, int maxp) {
                                         return attend_blocks(sh, 0, spt, maxp, h_len, d_blk, max_blk, S, R, H, d_q, scale,
                                                              d_out, d_lse, d_ws, pl, rb, st);
                                     });
@@ -2752,7 +2762,6 @@ int launch_attend_shared(tf_kvpool *pool, int cache, const int32_t *d_pt, int ma
                          const int32_t *h_gsize, int G, const int64_t *h_prefix, int S, int R, int H, const void *d_q,
                          float scale, void *d_out, float *d_lse, void *d_ws, size_t ws_bytes, cudaStream_t st) {
     using namespace attn;
-    if (prepare_launch(pool, st) != TF_OK) return TF_E_CUDA;
     SharedEntry e[TF_MAX_STREAMS];
     int16_t order[TF_MAX_STREAMS];
     std::vector<int32_t> nt;
@@ -2761,8 +2770,13 @@ int launch_attend_shared(tf_kvpool *pool, int cache, const int32_t *d_pt, int ma
     int64_t rb[MAX_CTAS + 1];
     const Plan pl = plan_shared(nt, n - S, device_sms(), rb);
     int32_t from[TF_MAX_STREAMS];
-    if (is_fp8(pool->desc) && expand_shared(S, h_gsize, G, e, order, n, from))
-        return launch_over_expanded(pool, cache, d_pt, max_pages, h_len, from, S, d_ws, ws_bytes, slots_bytes(pl.slots), st,
+    const bool expand = is_fp8(pool->desc) && expand_shared(S, h_gsize, G, e, order, n, from);
+    const size_t part = slots_bytes(pl.slots);
+    const int rc = check_workspace(expand ? with_expanded(part, fp8_shadow_bytes(S, h_len, from)) : part, d_ws, ws_bytes);
+    if (rc != TF_OK) return rc;
+    if (prepare_launch(pool, st) != TF_OK) return TF_E_CUDA;
+    if (expand)
+        return launch_over_expanded(pool, cache, d_pt, max_pages, h_len, from, S, d_ws, ws_bytes, part, st,
                                     [&](tf_kvpool *sh, const int32_t *spt, int maxp) {
                                         return attend_shared(sh, 0, spt, maxp, e, order, n, S, R, H, d_q, scale, d_out,
                                                              d_lse, d_ws, pl, rb, st);

@@ -341,12 +341,6 @@ static int call_checks(const tf_kvpool *p, int32_t cache, const int32_t *d_pt, i
     return TF_OK;
 }
 
-static int ws_check(size_t need, const void *d_ws, size_t ws_bytes) {
-    if (need == 0) return TF_OK;
-    if (!d_ws || (reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0) return TF_E_ARG;
-    return ws_bytes < need ? TF_E_NOMEM : TF_OK;
-}
-
 // Host arithmetic on caller sizes allocates (the plan's unit table), and no exception leaves a C entry.
 template <typename F>
 static int no_throw(F &&f) {
@@ -357,31 +351,29 @@ static int no_throw(F &&f) {
     }
 }
 
-static int blocks_size(const tf_kvpool *p, int32_t S, int32_t R, int32_t H, const int64_t *h_len, int32_t max_blk, size_t *bytes) {
+static int blocks_checks(int32_t S, int32_t R, int32_t H, const int64_t *h_len, int32_t max_blk) {
     const int rc = batch_checks(S, R, H, h_len);
-    if (rc != TF_OK) return rc;
-    if (max_blk < 1) return TF_E_ARG;
-    return no_throw([&] {
-        *bytes = blocks_workspace_bytes(p && is_fp8(p->desc), S, R, H, h_len, max_blk);
-        return TF_OK;
-    });
+    return rc != TF_OK ? rc : max_blk < 1 ? TF_E_ARG : TF_OK;
 }
 
 extern "C" size_t tf_paged_mla_blocks_workspace_bytes(const tf_kvpool *p, int32_t S, int32_t R, int32_t H,
                                                       const int64_t *h_len, int32_t max_blk) {
+    if (blocks_checks(S, R, H, h_len, max_blk) != TF_OK) return 0;
     size_t n = 0;
-    return blocks_size(p, S, R, H, h_len, max_blk, &n) == TF_OK ? n : 0;
+    const int rc = no_throw([&] {
+        n = blocks_workspace_bytes(p && is_fp8(p->desc), S, R, H, h_len, max_blk);
+        return TF_OK;
+    });
+    return rc == TF_OK ? n : 0;
 }
 
 extern "C" int tf_paged_mla_attend_blocks(tf_kvpool *p, int32_t cache, const int32_t *d_pt, int32_t max_pages,
                                           const int64_t *h_len, const int32_t *d_blk, int32_t max_blk, int32_t S,
                                           int32_t R, int32_t H, const void *d_q, float scale, void *d_out,
                                           float *d_lse, void *d_ws, size_t ws_bytes, void *stream) {
-    size_t need = 0;
-    int rc = blocks_size(p, S, R, H, h_len, max_blk, &need);
+    int rc = blocks_checks(S, R, H, h_len, max_blk);
     if (rc == TF_OK) rc = call_checks(p, cache, d_pt, max_pages, h_len, S, d_q, scale, d_out);
     if (rc == TF_OK && !d_blk) rc = TF_E_ARG;
-    if (rc == TF_OK) rc = ws_check(need, d_ws, ws_bytes);
     if (rc != TF_OK) return rc;
     return no_throw([&] {
         return launch_attend_blocks(p, cache, d_pt, max_pages, h_len, d_blk, max_blk, S, R, H, d_q, scale, d_out,
@@ -389,8 +381,8 @@ extern "C" int tf_paged_mla_attend_blocks(tf_kvpool *p, int32_t cache, const int
     });
 }
 
-static int shared_size(const tf_kvpool *p, int32_t S, int32_t R, int32_t H, const int64_t *h_len, const int32_t *h_gsize, int32_t G,
-                       const int64_t *h_prefix, size_t *bytes) {
+static int shared_checks(int32_t S, int32_t R, int32_t H, const int64_t *h_len, const int32_t *h_gsize, int32_t G,
+                         const int64_t *h_prefix) {
     const int rc = batch_checks(S, R, H, h_len);
     if (rc != TF_OK) return rc;
     if (!h_gsize || !h_prefix || G < 1 || G > S) return TF_E_ARG;
@@ -404,14 +396,17 @@ static int shared_size(const tf_kvpool *p, int32_t S, int32_t R, int32_t H, cons
     for (int g = 0, s = 0; g < G; ++g)
         for (int k = 0; k < h_gsize[g]; ++k, ++s)
             if (h_prefix[g] < 0 || h_prefix[g] > h_len[s] - R + 1) return TF_E_RANGE;
-    return no_throw([&] { return shared_workspace_bytes(p && is_fp8(p->desc), S, R, H, h_len, h_gsize, G, h_prefix, bytes); });
+    return TF_OK;
 }
 
 extern "C" size_t tf_paged_mla_shared_workspace_bytes(const tf_kvpool *p, int32_t S, int32_t R, int32_t H,
                                                       const int64_t *h_len, const int32_t *h_gsize, int32_t G,
                                                       const int64_t *h_prefix) {
+    if (shared_checks(S, R, H, h_len, h_gsize, G, h_prefix) != TF_OK) return 0;
     size_t n = 0;
-    return shared_size(p, S, R, H, h_len, h_gsize, G, h_prefix, &n) == TF_OK ? n : 0;
+    const int rc = no_throw(
+        [&] { return shared_workspace_bytes(p && is_fp8(p->desc), S, R, H, h_len, h_gsize, G, h_prefix, &n); });
+    return rc == TF_OK ? n : 0;
 }
 
 extern "C" int tf_paged_mla_attend_shared(tf_kvpool *p, int32_t cache, const int32_t *d_pt, int32_t max_pages,
@@ -419,10 +414,8 @@ extern "C" int tf_paged_mla_attend_shared(tf_kvpool *p, int32_t cache, const int
                                           const int64_t *h_prefix, int32_t S, int32_t R, int32_t H, const void *d_q,
                                           float scale, void *d_out, float *d_lse, void *d_ws, size_t ws_bytes,
                                           void *stream) {
-    size_t need = 0;
-    int rc = shared_size(p, S, R, H, h_len, h_gsize, G, h_prefix, &need);
+    int rc = shared_checks(S, R, H, h_len, h_gsize, G, h_prefix);
     if (rc == TF_OK) rc = call_checks(p, cache, d_pt, max_pages, h_len, S, d_q, scale, d_out);
-    if (rc == TF_OK) rc = ws_check(need, d_ws, ws_bytes);
     if (rc != TF_OK) return rc;
     return no_throw([&] {
         return launch_attend_shared(p, cache, d_pt, max_pages, h_len, h_gsize, G, h_prefix, S, R, H, d_q, scale, d_out,

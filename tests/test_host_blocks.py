@@ -171,7 +171,7 @@ def test_binding_refuses_what_the_library_cannot_see(L):
         lambda: B.tf_block_scores(p, bk, pt, 2, [64, 64, 64], q, 0.1, torch.zeros(2, 4)),
         lambda: B.tf_block_scores(p, bk, pt, 2, [64, 64], q, 0.1, torch.zeros(1, 4)),
         lambda: B.tf_block_scores(p, bk, pt, 2, [64, 640], q, 0.1, torch.zeros(2, 16)[:, :8]),
-        lambda: B.tf_block_scores(p, bk, pt, 2, [64, 64], q, 0.1, torch.zeros(2, 4), w=torch.zeros(2, 16)),
+        lambda: B.tf_block_scores(p, bk, pt, 2, [64, 64], q, 0.1, torch.zeros(2, 4), w=torch.zeros(2, 15)),
         lambda: B.tf_block_scores(p, bk, pt, 2, [64, 64], q, 0.1, torch.zeros(2, 4), nblk=torch.zeros(2)),
         lambda: B.tf_paged_mla_attend_blocks(p, 0, pt, 2, [64, 64], blk.long(), q, 0.1, out, lse),
         lambda: B.tf_paged_mla_attend_blocks(p, 0, pt, 2, [64, 64], blk[:1], q, 0.1, out, lse),
