@@ -216,7 +216,10 @@ struct Items {
     int64_t i, i1;         // next item, end
     int64_t first;         // the pair's first item
     int64_t i0 = 0;        // the block tile's first item
-    int p0 = 0;            // the pair that holds it
+    // the pairs that hold the block tile: f0 .. f0 + nfull - 1 with all their items, the pair before
+    // them with its times [fa, fe) and the one behind them with its times [0, le)
+    int f0 = 0, nfull = 0;
+    int64_t fa = 0, fe = 0, le = 0;
     int pair, s = -1;
     int64_t bt = -1;
     bool fresh = false;    // another block tile than the last item's
@@ -241,8 +244,20 @@ struct Items {
             s = a;
             bt = (i - p.item0[s]) / p.nrt;
             i0 = p.item0[s] + bt * p.nrt;
-            p0 = pair;
+            const int64_t end = i0 + p.nrt;
+            int p0 = pair, p1 = pair;   // they hold its first and its last item
             while (start(p0) > i0) --p0;
+            while (start(p1 + 1) < end) ++p1;
+            f0 = p0;
+            fa = fe = le = 0;
+            const bool cut0 = start(p0) < i0, cut1 = start(p1 + 1) > end;
+            if (cut0) {
+                ++f0;
+                fa = i0 - start(p0);
+                fe = (p1 > p0 ? start(p0 + 1) : end) - start(p0);
+            }
+            if (cut1 && !(cut0 && p1 == p0)) le = end - start(p1);
+            nfull = max(0, (cut1 ? p1 - 1 : p1) - f0 + 1);
         }
         ++i;
         return true;
@@ -250,16 +265,10 @@ struct Items {
     // after next(): the item's row tile
     __device__ __forceinline__ int64_t row_tile(const ScoreParams &p) const {
         if (p.nrt == 1) return 0;
-        const int64_t t = i - 1 - first, end = i0 + p.nrt;
-        int64_t rank = 0;
-        int64_t at = start(p0);
-        for (int q = p0; at < end; ++q) {   // items of pair q in this block tile: times [a, e)
-            const int64_t to = start(q + 1);
-            const int64_t a = (at > i0 ? at : i0) - at, e = (to < end ? to : end) - at;
-            rank += t < a ? 0 : t >= e ? e - a : t - a + (q < pair);
-            at = to;
-        }
-        return rank;
+        const int64_t t = i - 1 - first;   // <= len, so every full pair has t items before time t
+        const int before = (t < len ? pair : (int)min((int64_t)pair, more)) - f0;   // full pairs ahead of this one at time t
+        return t * nfull + max(0, min(before, nfull)) + min(t, le) +
+               (t < fa ? 0 : t >= fe ? fe - fa : t - fa + (f0 - 1 < pair));
     }
     // after next(): the last item of its block tile here
     __device__ __forceinline__ bool last_of_tile(const ScoreParams &p) const { return i >= i1 || i == i0 + p.nrt; }
