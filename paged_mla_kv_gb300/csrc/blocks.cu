@@ -173,7 +173,7 @@ constexpr int TCOLS = 2 * NMAX;
 // Barriers marked L are waited on in the leader (rank 0) only and reached from both CTAs; the
 // others are each CTA's own, and the MMA warp's commits arrive on both.
 struct Ctrl {
-    uint64_t a_full, a_free;                    // L: both CTAs' block keys landed; the tile's products are done
+    uint64_t a_full, a_free;                    // L: both CTAs' block keys are there; the tile's products are done
     uint64_t b_full[STAGES], b_free[STAGES];    // L: both halves of a query box landed; its products are done
     uint64_t d_full[2], d_free[2];              // accumulator computed; L: read by both CTAs' epilogue warps
     uint64_t drain;
@@ -186,8 +186,8 @@ static_assert(ROWS == 64, "positions are shifted by 6");
 static_assert(SMEM_TOTAL <= 232448, "shared memory budget");
 
 struct ScoreParams {
-    CUtensorMap tm_k;   // 3D {576, 8 blocks, pages}, box {64, 8, 1}
     CUtensorMap tm_q;   // 2D {576, S*R*H}, box {64, npad / 2}
+    const char *bkeys;
     const int32_t *pt;
     const float *w;
     float *scores;
@@ -281,14 +281,6 @@ __device__ __forceinline__ void arrive_at(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // TMA into this CTA's shared memory, completing on a barrier of the pair.
-// 64 values from x on of a page's eight block keys: one 1 KB atom of the 128-byte swizzle.
-__device__ __forceinline__ void tma_page_keys(void *dst, const CUtensorMap *tm, uint32_t bar, int x, int page) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(ptx::smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(x), "r"(0), "r"(page)
-        : "memory");
-}
 __device__ __forceinline__ void tma_queries(void *dst, const CUtensorMap *tm, uint32_t bar, int x, int row,
                                             uint64_t policy) {
     asm volatile(
@@ -296,12 +288,6 @@ __device__ __forceinline__ void tma_queries(void *dst, const CUtensorMap *tm, ui
         " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(ptx::smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(x), "r"(row), "l"(policy)
         : "memory");
-}
-// Ask for a box of queries in L2.
-__device__ __forceinline__ void prefetch_queries(const CUtensorMap *tm, int x, int row) {
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(tm)),
-                 "r"(x), "r"(row)
-                 : "memory");
 }
 __device__ __forceinline__ void pair_tmem_alloc(uint32_t *dst, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(ptx::smem_u32(dst)), "r"(ncols)
@@ -367,7 +353,7 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
     ptx::griddep_launch_dependents();
     const uint32_t rank = ptx::cluster_rank();
     if (threadIdx.x == 0) {
-        ptx::mbar_init(&c.a_full, 1);
+        ptx::mbar_init(&c.a_full, 2 * EPI / 32);
         ptx::mbar_init(&c.a_free, 1);
         for (int i = 0; i < STAGES; ++i) {
             ptx::mbar_init(&c.b_full[i], 1);
@@ -392,51 +378,19 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
 
     if (warp == EPI / 32) {
         // ================= TMA =================
-        // Lane 0 waits and loads this CTA's half of each query box; its half of a block tile is
-        // loaded a page a lane (nine one-atom boxes of 8 blocks x 64 values, to where the
-        // 128-byte-swizzled tile has them).  All land on the leader's barriers, which the leader arms
-        // with the bytes of both halves.
-        if (lane == 0) {
-            ptx::prefetch_tmap(&p.tm_k);
-            ptx::prefetch_tmap(&p.tm_q);
-        }
+        // Lane 0 waits and loads this CTA's half of each query box; both land on the leader's barrier,
+        // which the leader arms with the bytes of both.
+        if (lane == 0) ptx::prefetch_tmap(&p.tm_q);
         const uint64_t pol_q = ptx::policy_evict_last();
-        const uint32_t a_bar = leader_addr(&c.a_full);
-        int na = 0;        // block tiles loaded
         int64_t nb = 0;    // query boxes loaded
         bool ok = true;
-        Items it(p), ahead(p);   // ahead: an item further, whose queries are asked for in L2
-        bool more = ahead.next(p);
-        auto row_of = [&](const Items &x) {
-            return (int)(((int64_t)x.s * p.R + x.row_tile(p) * p.rpt) * p.H) + (int)rank * (p.npad / 2);
+        Items it(p);
+        auto row_of = [&]() {
+            return (int)(((int64_t)it.s * p.R + it.row_tile(p) * p.rpt) * p.H) + (int)rank * (p.npad / 2);
         };
-        int qrow = 0, qnext = more ? row_of(ahead) : 0;
-        while (ok && it.next(p)) {
-            qrow = qnext;
-            more = ahead.next(p);
-            if (more) qnext = row_of(ahead);
-            if (it.fresh) {
-                if (na > 0) ok = ptx::mbar_wait_warp(&c.a_free, (na - 1) & 1, abort, p.err, 30);
-                if (!ok) break;
-                // a lane past the stream's pages takes its last one again (no score is made of it); for a
-                // page out of the pool page 0 stands in (the scores are undefined)
-                if (lane < TILE_PAGES) {
-                    const int64_t pages = (p.len[it.s] + kPageRows - 1) / kPageRows;
-                    int64_t lp = it.bt * (2 * TILE_PAGES) + rank * TILE_PAGES + lane;
-                    const bool there = lp < pages;
-                    if (!there) lp = pages - 1;
-                    int id = p.pt ? __ldg(p.pt + (int64_t)it.s * p.max_pages + lp) : it.s * p.max_pages + (int)lp;
-                    if (id < 0 || id >= p.num_pages) {
-                        if (there) ptx::record_error(p.err, TF_E_DEVICE, id);
-                        id = 0;
-                    }
-                    if (lane == 0 && rank == 0) ptx::mbar_arrive_expect_tx(&c.a_full, 2 * TILE_PAGES * PAGE_KEYS);
-                    for (int k = 0; k < KBOX; ++k)
-                        tma_page_keys(smem + SMEM_A + lane * PAGE_KEYS + k * 1024, &p.tm_k, a_bar, k * 64, id);
-                }
-                __syncwarp();
-                ++na;
-            }
+        bool more = it.next(p);
+        int qrow = more ? row_of() : 0;
+        while (ok && more) {
             if (lane == 0) {
                 for (int kb = 0; ok && kb < KBOX; ++kb) {
                     const int64_t n = nb + kb;
@@ -448,16 +402,16 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
                     }
                     if (rank == 0) ptx::mbar_arrive_expect_tx(&c.b_full[st], p.npad * 128);
                     tma_queries(smem + SMEM_B + st * STAGE_BYTES, &p.tm_q, leader_addr(&c.b_full[st]), kb * 64, qrow, pol_q);
-                    if (more) prefetch_queries(&p.tm_q, kb * 64, qnext);
                 }
             }
             nb += KBOX;
+            more = it.next(p);   // worked out while the boxes are on their way
+            if (more) qrow = row_of();
             ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
         }
         // No copy may still be writing shared memory when a CTA exits, nor a commit of the leader's be
         // on its way to a barrier of the peer's: what was loaded last has to be released.
         if (lane == 0) {
-            if (na > 0) ptx::mbar_wait(&c.a_free, (na - 1) & 1, abort, p.err, 32, 1ll << 28);
             for (int k = 0; k < STAGES; ++k)
                 if (nb > k) {
                     const int64_t last = nb - 1 - k;
@@ -465,7 +419,6 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
                 }
             // after a wait that ran out: the copies themselves (all land on the leader's barriers)
             if (*abort && rank == 0) {
-                if (na > 0) ptx::mbar_wait(&c.a_full, (na - 1) & 1, abort, p.err, 32, 1ll << 28);
                 for (int k = 0; k < STAGES; ++k)
                     if (nb > k) {
                         const int64_t last = nb - 1 - k;
@@ -516,12 +469,15 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
         const int tid = (int)threadIdx.x;
         const int half = warp >> 2;
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint64_t pol_k = ptx::policy_evict_last();
         int64_t nd = 0;
         bool ok = true;
         // The weights of an item's columns go to shared memory for all to read; those of the next are
         // fetched while this one's products run (a column a thread).
         Items it(p);
         bool more = it.next(p);
+        bool fresh = false, freshn = more;
+        int na = 0;   // block tiles loaded
         int64_t r0 = 0, r0n = more ? it.row_tile(p) * p.rpt : 0;   // first query row: this item's, the next one's
         int s = 0, sn = it.s;
         int64_t bt = 0, btn = it.bt;
@@ -536,6 +492,38 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
             r0 = r0n;
             s = sn;
             bt = btn;
+            fresh = freshn;
+            if (fresh) {
+                // The block tile's keys, once its predecessor's products are done: two pages a warp, 18
+                // copies of 16 bytes a lane and page into the 128-byte-swizzled tile (as TMA boxes, 144 of
+                // one 1 KB atom, they took 8,300 cycles to issue).  A page past the stream's is left
+                // out (no score is made of it), and so is one out of the pool (its scores are undefined):
+                // the other lanes of the product do not see it.
+                if (na > 0 && !ptx::mbar_wait_warp(&c.a_free, (na - 1) & 1, abort, p.err, 30)) ok = false;
+                const int64_t pages = (p.len[s] + kPageRows - 1) / kPageRows;
+#pragma unroll 1
+                for (int k = 2 * warp; ok && k < 2 * warp + 2; ++k) {
+                    const int64_t lp = bt * (2 * TILE_PAGES) + rank * TILE_PAGES + k;
+                    if (lp >= pages) break;
+                    const int id = p.pt ? __ldg(p.pt + (int64_t)s * p.max_pages + lp) : s * p.max_pages + (int)lp;
+                    if (id < 0 || id >= p.num_pages) {
+                        if (lane == 0) ptx::record_error(p.err, TF_E_DEVICE, id);
+                        continue;
+                    }
+                    const char *src = p.bkeys + (size_t)id * PAGE_KEYS;
+                    uint8_t *dst = smem + SMEM_A + k * PAGE_KEYS;
+#pragma unroll 6
+                    for (int i = 0; i < PAGE_KEYS / 16 / 32; ++i) {
+                        const int x = i * 32 + lane, row = x / (kDk / 8), ch = x % (kDk / 8);   // chunk ch of block `row`
+                        ptx::cp_async16(dst + (ch >> 3) * 1024 + row * 128 + (((ch & 7) ^ row) << 4), src + x * 16, pol_k);
+                    }
+                }
+                ptx::cp_async_wait_all();
+                ptx::fence_proxy_async_smem();   // the tensor cores read them
+                __syncwarp();
+                if (lane == 0) arrive_at(leader_addr(&c.a_full));
+                ++na;
+            }
             // the previous item's weights are read; the warps leave together when a wait ran out
             if (ptx::named_bar_or(1, EPI, !ok || *abort)) break;
             if (p.w) {
@@ -547,6 +535,7 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
                 r0n = it.row_tile(p) * p.rpt;
                 sn = it.s;
                 btn = it.bt;
+                freshn = it.fresh;
                 fetch();
             }
             if (!ptx::mbar_wait_warp(&c.d_full[buf], (uint32_t)(nd / 2) & 1, abort, p.err, 37)) {
@@ -614,6 +603,8 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
             __syncwarp();
             if (lane == 0) arrive_at(leader_addr(&c.d_free[buf]));
         }
+        // the leader's last commit has to have reached this CTA's barrier before it exits
+        if (na > 0) ptx::mbar_wait_warp(&c.a_free, (na - 1) & 1, abort, p.err, 32, 1ll << 28);
         // rows of streams with fewer block tiles than the longest: no block there; and every row's
         // visible blocks
         for (int64_t r = blockIdx.x; r < (int64_t)p.S * p.R; r += gridDim.x) {
@@ -682,12 +673,7 @@ int launch_block_scores(tf_kvpool *pool, const void *d_bkeys, const int32_t *d_p
     thread_local std::unique_ptr<ScoreParams> pp;
     if (!pp) pp.reset(new ScoreParams());
     ScoreParams &p = *pp;
-    {
-        const uint64_t dims[3] = {(uint64_t)kDk, (uint64_t)PER_PAGE, (uint64_t)pool->desc.num_pages};
-        const uint64_t strides[2] = {(uint64_t)kDk * 2, (uint64_t)PAGE_KEYS};
-        const uint32_t box[3] = {64, (uint32_t)PER_PAGE, 1};
-        if (!encode_tmap_bf16(&p.tm_k, const_cast<void *>(d_bkeys), 3, dims, strides, box)) return TF_E_CUDA;
-    }
+    p.bkeys = static_cast<const char *>(d_bkeys);
     p.rpt = std::min(R, std::max(1, NMAX / H));
     // a warp of the epilogue reads 32 columns at a time from its first row on, up to the buffer's end
     auto reach = [&](int nr) { return (nr + 1) / 2 * H + (nr / 2 * H + 31) / 32 * 32; };
