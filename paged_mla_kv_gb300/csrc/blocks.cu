@@ -41,104 +41,196 @@ struct KeysParams {
 __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// One CTA a block: thread (g, c) adds 16-byte chunk c of rows g, g + G, ... in fp32; the G sums of a
-// value are added in order and divided by the rows the block holds, rounded once to bf16.
-// BF16 pages: 72 chunks of 8 values, 4 row groups.  FP8: 32 chunks of 16 codes (each value is
-// bf16(code * scale), as the attention takes it) and 8 rope chunks, 8 row groups.
-template <bool FP8>
-struct KeysShape {
-    static constexpr int C = FP8 ? 40 : 72;
-    static constexpr int G = FP8 ? 8 : 4;
-    static constexpr int T = C * G;
-    static constexpr int V = FP8 ? 16 : 8;   // values a latent chunk
-};
-
-template <bool FP8>
-__global__ void __launch_bounds__(KeysShape<FP8>::T) block_keys_kernel(const __grid_constant__ KeysParams p) {
-    using K = KeysShape<FP8>;
-    __shared__ float part[K::G][kDk];
-    ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
-    const int64_t n = blockIdx.x;
-    int s = 0;
-    for (int a = p.S - 1; s < a;) {   // the stream whose blocks hold number n
+// Numbered block n of the call: its stream and its number there.
+__device__ __forceinline__ int64_t block_of(const KeysParams &p, int64_t n, int &s) {
+    s = 0;
+    for (int a = p.S - 1; s < a;) {   // the last stream whose blocks begin at or before n
         const int mid = (s + a + 1) >> 1;
         if (p.off[mid] <= n) s = mid; else a = mid - 1;
     }
-    const int64_t b = p.first[s] + (n - p.off[s]);
-    const int lp = (int)(b / PER_PAGE), ib = (int)(b % PER_PAGE);
-    const int page = p.pt ? __ldg(p.pt + (int64_t)s * p.max_pages + lp) : s * p.max_pages + lp;
+    return p.first[s] + (n - p.off[s]);
+}
+
+// The block's page and rows; false, recorded, for a page out of the pool.
+__device__ __forceinline__ bool block_rows(const KeysParams &p, int s, int64_t b, int &page, int &rows) {
+    const int lp = (int)(b / PER_PAGE);
+    page = p.pt ? __ldg(p.pt + (int64_t)s * p.max_pages + lp) : s * p.max_pages + lp;
     if (page < 0 || page >= p.num_pages) {
-        if (threadIdx.x == 0) ptx::record_error(p.err, TF_E_DEVICE, page);
-        return;
+        ptx::record_error(p.err, TF_E_DEVICE, page);
+        return false;
     }
     const int64_t left = p.len[s] - b * ROWS;
-    const int rows = left < ROWS ? (int)left : ROWS;
-    const int c = (int)threadIdx.x % K::C, g = (int)threadIdx.x / K::C;
-    const char *pg = p.cache_base + (size_t)page * (FP8 ? kF8PageBytes : kPageBytes);
-    const int row0 = ib * ROWS;
-    constexpr int LC = FP8 ? kLat / 16 : kLat / 8;   // latent chunks
-    const bool rope = c >= LC;
-    const size_t lat_stride = FP8 ? kLat : kLat * 2;
-    const char *src = rope ? pg + (FP8 ? kF8RopeOff : kLatBlockBytes) + (size_t)row0 * (kRope * 2) + (c - LC) * 16
-                           : pg + (size_t)row0 * lat_stride + c * 16;
-    const size_t stride = rope ? (size_t)kRope * 2 : lat_stride;
-    const float *scales = reinterpret_cast<const float *>(pg + kF8ScaleOff) + row0;
-    float acc[K::V];
+    rows = left < ROWS ? (int)left : ROWS;
+    return true;
+}
+
+// Values 2 i, 2 i + 1 of a block's key: the G sums of each, added in order, over the rows, rounded once.
+template <int G>
+__device__ __forceinline__ uint32_t mean_pair(const float (&part)[G][kDk], int i, int rows) {
+    float a = 0.f, d = 0.f;
 #pragma unroll
-    for (int i = 0; i < K::V; ++i) acc[i] = 0.f;
-    constexpr int N = ROWS / K::G;   // rows a thread
+    for (int k = 0; k < G; ++k) {
+        a += part[k][2 * i];
+        d += part[k][2 * i + 1];
+    }
+    return ptx::pack_bf16x2(__fdiv_rn(a, (float)rows), __fdiv_rn(d, (float)rows));
+}
+
+// BF16 pages, one CTA a block: thread (g, c) adds 16-byte chunk c (72 a row) of rows g, g + 4, ... in
+// fp32, eight loads in flight.  Bound by HBM: 301,904 rows take 54.8 us, 0.94 of the measured copy rate.
+constexpr int KC = kDk / 8, KG = 4;
+__global__ void __launch_bounds__(KC *KG) block_keys_kernel(const __grid_constant__ KeysParams p) {
+    __shared__ float part[KG][kDk];
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    int s, page, rows;
+    const int64_t b = block_of(p, blockIdx.x, s);
+    if (!block_rows(p, s, b, page, rows)) return;
+    const int c = (int)threadIdx.x % KC, g = (int)threadIdx.x / KC;
+    const int ib = (int)(b % PER_PAGE), row0 = ib * ROWS;
+    const char *pg = p.cache_base + (size_t)page * kPageBytes;
+    constexpr int LC = kLat / 8;   // latent chunks
+    const bool rope = c >= LC;
+    const size_t stride = rope ? (size_t)kRope * 2 : (size_t)kLat * 2;
+    const char *src = (rope ? pg + kLatBlockBytes + (c - LC) * 16 : pg + c * 16) + (size_t)row0 * stride;
+    float acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
     constexpr int U = 8;             // loads in flight
 #pragma unroll
-    for (int i0 = 0; i0 < N; i0 += U) {
+    for (int i0 = 0; i0 < ROWS / KG; i0 += U) {
         uint4 v[U];
-        float sc[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int r = (i0 + u) * K::G + g;
-            v[u] = make_uint4(0, 0, 0, 0);
-            sc[u] = 0.f;
-            if (r < rows) {
-                v[u] = __ldg(reinterpret_cast<const uint4 *>(src + (size_t)r * stride));
-                if (FP8) sc[u] = __ldg(scales + r);
-            }
+            const int r = (i0 + u) * KG + g;
+            v[u] = r < rows ? __ldg(reinterpret_cast<const uint4 *>(src + (size_t)r * stride)) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-            if (!FP8 || rope) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    acc[2 * k] += lo(w[k]);
-                    acc[2 * k + 1] += hi(w[k]);
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < K::V / 2; ++k) {
-                    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
-                        (__nv_fp8x2_storage_t)((w[k / 2] >> (16 * (k & 1))) & 0xFFFFu), __NV_E4M3);
-                    const float2 f = __half22float2(__half2(hr));
-                    const uint32_t x = ptx::pack_bf16x2(f.x * sc[u], f.y * sc[u]);
-                    acc[2 * k] += lo(x);
-                    acc[2 * k + 1] += hi(x);
-                }
+            for (int k = 0; k < 4; ++k) {
+                acc[2 * k] += lo(w[k]);
+                acc[2 * k + 1] += hi(w[k]);
             }
         }
     }
-    const int v0 = rope ? kLat + (c - LC) * 8 : c * K::V;
 #pragma unroll
-    for (int i = 0; i < K::V; ++i)
-        if (!rope || i < 8) part[g][v0 + i] = acc[i];
+    for (int i = 0; i < 8; ++i) part[g][8 * c + i] = acc[i];
     __syncthreads();
     uint32_t *dst = reinterpret_cast<uint32_t *>(p.bkeys + ((size_t)page * PER_PAGE + ib) * kDk);
-    for (int i = threadIdx.x; i < kDk / 2; i += K::T) {
-        float a = 0.f, d = 0.f;
-#pragma unroll
-        for (int k = 0; k < K::G; ++k) {
-            a += part[k][2 * i];
-            d += part[k][2 * i + 1];
+    for (int i = threadIdx.x; i < kDk / 2; i += KC * KG) dst[i] = mean_pair(part, i, rows);
+}
+
+// FP8 pages: a row's latent value is bf16(code * scale), as the attention takes it, so a value costs
+// about five instructions and the loads of a CTA that also computes leave HBM idle (35 us for
+// 208,000 rows in the form above).  Here a CTA a SM walks the blocks: one warp copies a block's codes
+// (32 KB), rope rows and scales into a ring, and teams of ten warps take the blocks in turn, thread
+// (g, c) of a team chunk c of rows g, g + 8, ... (32 chunks of 16 codes and 8 of 8 rope values a row).
+// One team is latency-bound (43 us).
+constexpr int FC = kLat / 16 + kRope / 8, FG = 8, FT = FC * FG;   // 40 chunks, 8 row groups, 320 threads
+constexpr int FTEAMS = 3;
+constexpr int FSTAGES = 4;
+constexpr int F_ROPE = ROWS * kLat, F_SCALE = F_ROPE + ROWS * kRope * 2, F_STAGE = F_SCALE + ROWS * 4;
+struct KeysFp8Shared {
+    alignas(128) uint8_t ring[FSTAGES][F_STAGE];
+    float part[FTEAMS][FG][kDk];
+    uint64_t full[FSTAGES], empty[FSTAGES];
+    int rows[FSTAGES], dst[FSTAGES];   // rows of the stage's block (0: left out), its key's number
+    int abort;
+};
+__global__ void __launch_bounds__(FTEAMS * FT + 32, 1) block_keys_fp8_kernel(const __grid_constant__ KeysParams p) {
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    KeysFp8Shared &sh = *reinterpret_cast<KeysFp8Shared *>(smem_raw);
+    ptx::griddep_launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < FSTAGES; ++i) {
+            ptx::mbar_init(&sh.full[i], 1);
+            ptx::mbar_init(&sh.empty[i], FT / 32);
         }
-        dst[i] = ptx::pack_bf16x2(__fdiv_rn(a, (float)rows), __fdiv_rn(d, (float)rows));
+        sh.abort = 0;
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+    ptx::griddep_wait();
+    volatile int *abort = &sh.abort;
+    const int64_t total = p.off[p.S];
+    if (threadIdx.x >= FTEAMS * FT) {
+        if (threadIdx.x != FTEAMS * FT) return;
+        int64_t k = 0;
+        for (int64_t n = blockIdx.x; n < total; n += gridDim.x, ++k) {
+            const int st = (int)(k % FSTAGES);
+            int s, page = 0, rows = 0;
+            const int64_t b = block_of(p, n, s);
+            const bool good = block_rows(p, s, b, page, rows);
+            if (k >= FSTAGES && !ptx::mbar_wait(&sh.empty[st], (uint32_t)(k / FSTAGES - 1) & 1, abort, p.err, 40)) break;
+            sh.rows[st] = good ? rows : 0;
+            sh.dst[st] = page * PER_PAGE + (int)(b % PER_PAGE);
+            if (!good) {
+                ptx::mbar_arrive(&sh.full[st]);
+                continue;
+            }
+            const char *pg = p.cache_base + (size_t)page * kF8PageBytes;
+            const int row0 = (int)(b % PER_PAGE) * ROWS;
+            const uint32_t sb = (rows * 4 + 15) / 16 * 16;   // whole 16 bytes of the page's scales
+            ptx::mbar_arrive_expect_tx(&sh.full[st], rows * (kLat + kRope * 2) + sb);
+            ptx::bulk_g2s(sh.ring[st], pg + (size_t)row0 * kLat, rows * kLat, &sh.full[st]);
+            ptx::bulk_g2s(sh.ring[st] + F_ROPE, pg + kF8RopeOff + (size_t)row0 * kRope * 2, rows * kRope * 2, &sh.full[st]);
+            ptx::bulk_g2s(sh.ring[st] + F_SCALE, pg + kF8ScaleOff + (size_t)row0 * 4, sb, &sh.full[st]);
+        }
+        // no copy may still be writing shared memory when the CTA exits
+        for (int64_t j = k > FSTAGES ? k - FSTAGES : 0; j < k; ++j)
+            ptx::mbar_wait(&sh.full[j % FSTAGES], (uint32_t)(j / FSTAGES) & 1, abort, p.err, 41, 1ll << 28);
+        return;
+    }
+    const int team = (int)threadIdx.x / FT, tid = (int)threadIdx.x % FT;
+    const int c = tid % FC, g = tid / FC;
+    const bool rope = c >= kLat / 16;
+    float(&part)[FG][kDk] = sh.part[team];
+    int64_t k = team;
+    bool ok = true;
+    for (int64_t n = blockIdx.x + (int64_t)team * gridDim.x; n < total; n += FTEAMS * (int64_t)gridDim.x, k += FTEAMS) {
+        const int st = (int)(k % FSTAGES);
+        if (!ptx::mbar_wait_warp(&sh.full[st], (uint32_t)(k / FSTAGES) & 1, abort, p.err, 42)) ok = false;
+        // the team's previous sums are read; its warps leave together when a wait ran out
+        if (ptx::named_bar_or(1 + team, FT, !ok || *abort)) return;
+        const int rows = sh.rows[st], dn = sh.dst[st];
+        float2 acc[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = make_float2(0.f, 0.f);
+        if (rope) {
+            for (int r = g; r < rows; r += FG) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(sh.ring[st] + F_ROPE + r * kRope * 2 + (c - kLat / 16) * 16);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[i] = ptx::add2(acc[i], make_float2(lo(w[i]), hi(w[i])));
+            }
+        } else {
+#pragma unroll 4
+            for (int r = g; r < rows; r += FG) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(sh.ring[st] + r * kLat + c * 16);
+                const float sc = reinterpret_cast<const float *>(sh.ring[st] + F_SCALE)[r];
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
+                        (__nv_fp8x2_storage_t)((w[i / 2] >> (16 * (i & 1))) & 0xFFFFu), __NV_E4M3);
+                    const float2 f = ptx::mul2(__half22float2(__half2(hr)), make_float2(sc, sc));
+                    const uint32_t x = ptx::pack_bf16x2(f.x, f.y);
+                    acc[i] = ptx::add2(acc[i], make_float2(lo(x), hi(x)));
+                }
+            }
+        }
+        const int v0 = rope ? kLat + (c - kLat / 16) * 8 : c * 16;
+        float2 *dst = reinterpret_cast<float2 *>(&part[g][v0]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!rope || i < 4) dst[i] = acc[i];
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&sh.empty[st]);
+        ptx::named_bar(1 + team, FT);
+        if (rows > 0 && tid < kDk / 2)
+            reinterpret_cast<uint32_t *>(p.bkeys + (size_t)dn * kDk)[tid] = mean_pair(part, tid, rows);
     }
 }
 
@@ -330,16 +422,6 @@ __device__ __forceinline__ void pair_commit_warp(uint64_t *bar) {
         "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], both;\n\t}" ::"r"(
             ptx::smem_u32(bar))
         : "memory");
-}
-
-// a * b + c on two values at once
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
 }
 
 // C: a divisor of H that the epilogue adds up without asking whether the query row ends (32, 8 or 1;
@@ -565,10 +647,10 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
                         for (int k = j; k < j + C; k += 4) {
                             const float4 wk = p.w ? *reinterpret_cast<const float4 *>(w + n0 + k)
                                                   : make_float4(1.f, 1.f, 1.f, 1.f);
-                            acc[0] = fma2(make_float2(wk.x, wk.y),
+                            acc[0] = ptx::fma2(make_float2(wk.x, wk.y),
                                           make_float2(fmaxf(__uint_as_float(v[k]), 0.f),
                                                       fmaxf(__uint_as_float(v[k + 1]), 0.f)), acc[0]);
-                            acc[1] = fma2(make_float2(wk.z, wk.w),
+                            acc[1] = ptx::fma2(make_float2(wk.z, wk.w),
                                           make_float2(fmaxf(__uint_as_float(v[k + 2]), 0.f),
                                                       fmaxf(__uint_as_float(v[k + 3]), 0.f)), acc[1]);
                         }
@@ -625,6 +707,24 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
 
 }  // namespace blk
 
+// The device's SMs, with every kernel opted in to its shared memory; 0 when that failed.
+static int device_ready() {
+    using namespace blk;
+    static std::once_flag once;
+    static int sms = 0;
+    std::call_once(once, [] {
+        int dev = 0, n = 0;
+        bool ok = cudaFuncSetAttribute(block_keys_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)sizeof(KeysFp8Shared)) == cudaSuccess;
+        for (auto *kern : {block_scores_kernel<32>, block_scores_kernel<8>, block_scores_kernel<1>})
+            ok = ok && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL) == cudaSuccess;
+        if (ok && cudaGetDevice(&dev) == cudaSuccess &&
+            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+            sms = n;
+    });
+    return sms;
+}
+
 int launch_block_keys(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_from,
                       const int64_t *h_len, int S, void *d_bkeys, cudaStream_t st) {
     using namespace blk;
@@ -647,9 +747,11 @@ int launch_block_keys(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_p
     p.off[S] = n;
     if (n == 0) return TF_OK;
     if (n > 0x7FFFFFFF) return TF_E_UNSUPPORTED;
+    if (f8 && device_ready() <= 0) return TF_E_CUDA;
     if (prepare_launch(pool, st) != TF_OK) return TF_E_CUDA;
-    const cudaError_t e = f8 ? launch_pdl(block_keys_kernel<true>, dim3((unsigned)n), dim3(KeysShape<true>::T), 0, st, p)
-                             : launch_pdl(block_keys_kernel<false>, dim3((unsigned)n), dim3(KeysShape<false>::T), 0, st, p);
+    const cudaError_t e = f8 ? launch_pdl(block_keys_fp8_kernel, dim3((unsigned)std::min<int64_t>(n, device_ready())),
+                                          dim3(FTEAMS * FT + 32), sizeof(KeysFp8Shared), st, p)
+                             : launch_pdl(block_keys_kernel, dim3((unsigned)n), dim3(KC * KG), 0, st, p);
     launch_counter()++;
     return e == cudaSuccess ? TF_OK : TF_E_CUDA;
 }
@@ -658,17 +760,7 @@ int launch_block_scores(tf_kvpool *pool, const void *d_bkeys, const int32_t *d_p
                         int S, int R, int H, const void *d_q, const float *d_w, float scale, int sink, int local,
                         float *d_scores, int64_t ld, int32_t *d_nblk, cudaStream_t st) {
     using namespace blk;
-    static std::once_flag once;
-    static int ready_sms = 0;
-    std::call_once(once, [] {
-        int dev = 0, n = 0;
-        bool ok = true;
-        for (auto *kern : {block_scores_kernel<32>, block_scores_kernel<8>, block_scores_kernel<1>})
-            ok = ok && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL) == cudaSuccess;
-        if (ok && cudaGetDevice(&dev) == cudaSuccess &&
-            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
-            ready_sms = n;
-    });
+    const int ready_sms = device_ready();
     if (ready_sms <= 0) return TF_E_CUDA;
     thread_local std::unique_ptr<ScoreParams> pp;
     if (!pp) pp.reset(new ScoreParams());
