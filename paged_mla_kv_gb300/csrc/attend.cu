@@ -511,10 +511,9 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NROPE; ++i) {
-            // BF16: the TMA warp's one arrival with the tile's bytes; FP8: one arrival a pair the
-            // expansion warps finish
-            ptx::mbar_init(&c.tile_full[i], FP8 ? 2 : CP_ROWS ? LOAD_THREADS : 1);
-            ptx::mbar_init(&c.tile_half[i], FP8 ? 2 : CP_ROWS ? LOAD_THREADS : 1);
+            // BF16: the TMA warp's one arrival with the tile's bytes; FP8: one of each expansion warp
+            ptx::mbar_init(&c.tile_full[i], FP8 ? F8_THREADS / 32 : CP_ROWS ? LOAD_THREADS : 1);
+            ptx::mbar_init(&c.tile_half[i], FP8 ? F8_THREADS / 32 : CP_ROWS ? LOAD_THREADS : 1);
             ptx::mbar_init(&c.rope_empty[i], 1);
             ptx::mbar_init(&c.p_full[i], 5);       // four softmax warps and the rescale warps
             ptx::mbar_init(&c.corr_req[i], 4);
@@ -1122,8 +1121,11 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
         // ================= FP8 expansion (warps 11-14): half a tile row a thread =================
         // Box b's 64 codes of row r become bf16(code * scale_r), written 128B-swizzled into BF16
         // box b (16-byte chunk j of the row at j ^ (r & 7)); thread (r, hf) does codes 32hf..+31.
-        // Each finished pair is one arrival on the tile's half barrier (pairs 0-1) or full barrier
-        // (pairs 2-3), after a proxy fence.
+        // Pairs 0-1 are one arrival a warp on the tile's half barrier, pairs 2-3 on its full barrier,
+        // each after a proxy fence.  Where the threads have to wait for one another: the scales lie in
+        // pair slot 1, the codes of pairs 0-1 in slot 2 and those of pairs 2-3 in slot 3, so everyone
+        // has read the scales before slot 1 is written, pairs 0-1 before slot 2 and pair 3 before slot 3.
+        // (With a barrier and a fence a pair the expansion took 3,400 cycles a tile.)
         const int ft = (int)threadIdx.x - THREADS;
         const int r = ft >> 1, hf = ft & 1;
         bool ok = true;
@@ -1134,11 +1136,11 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
             for (int tl = 0; tl < q.nt; ++tl, ++gt) {
                 const int rs = rope_slot(gt);
                 const bool landed = ptx::mbar_wait_warp(&c.f8_full[rs], rope_use(gt) & 1, abort, errp, 16);
+                const float sc = landed ? reinterpret_cast<const float *>(smem + scales_off(gt))[r] : 0.f;
                 if (ptx::named_bar_or(2, F8_THREADS, !landed || *abort)) {
                     ok = false;
                     break;
                 }
-                const float sc = reinterpret_cast<const float *>(smem + scales_off(gt))[r];
                 // one pair a round: {0,1}, {2,3}, {4,5}, {6,7}
 #pragma unroll 1
                 for (int b0 = 0; b0 < 8; b0 += 2) {
@@ -1164,12 +1166,12 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
                                 for (int h = 0; h < 2; ++h) {
                                     const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
                                         (__nv_fp8x2_storage_t)((w4[wi] >> (16 * h)) & 0xFFFFu), __NV_E4M3);
-                                    const float2 f = __half22float2(__half2(hr));
-                                    o[u][k * 8 + wi * 2 + h] = ptx::pack_bf16x2(f.x * sc, f.y * sc);
+                                    const float2 f = ptx::mul2(__half22float2(__half2(hr)), make_float2(sc, sc));
+                                    o[u][k * 8 + wi * 2 + h] = ptx::pack_bf16x2(f.x, f.y);
                                 }
                         }
-                    // boxes 6-7 cover their own codes: every row read before any is overwritten
-                    if (b0 == 6) ptx::named_bar(2, F8_THREADS);
+                    // everyone has read the codes that this round's slot holds
+                    if (b0 >= 4) ptx::named_bar(2, F8_THREADS);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         uint8_t *dst = smem + box_off(gt, b0 + u) + r * 128;
@@ -1180,9 +1182,11 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
                                 make_uint4(o[u][4 * jj], o[u][4 * jj + 1], o[u][4 * jj + 2], o[u][4 * jj + 3]);
                         }
                     }
-                    ptx::fence_proxy_async_smem();
-                    ptx::named_bar(2, F8_THREADS);
-                    if (ft == 0) ptx::mbar_arrive(b0 < 4 ? &c.tile_half[rs] : &c.tile_full[rs]);
+                    if (b0 == 2 || b0 == 6) {
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(b0 == 2 ? &c.tile_half[rs] : &c.tile_full[rs]);
+                    }
                 }
             }
         }
