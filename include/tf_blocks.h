@@ -114,8 +114,8 @@ int tf_paged_mla_attend_blocks(tf_kvpool *pool, int32_t cache, const int32_t *d_
  * The workspace can be larger than that call's (and holds a BF16 copy of the rows of an FP8 pool that
  * many columns read).
  * Errors: as for tf_paged_mla_attend; TF_E_ARG for a null array, a size below 1 or sizes that do not add up;
- * TF_E_RANGE for a prefix outside its bounds; TF_E_UNSUPPORTED if S plus the groups that share passes
- * TF_MAX_STREAMS. */
+ * TF_E_RANGE for a prefix outside its bounds; TF_E_UNSUPPORTED if R * H is not a multiple of 64 and S plus
+ * the groups that share passes TF_MAX_STREAMS. */
 size_t tf_paged_mla_shared_workspace_bytes(const tf_kvpool *pool, int32_t S, int32_t R, int32_t H, const int64_t *h_len,
                                            const int32_t *h_gsize, int32_t G, const int64_t *h_prefix);   /* pool may be NULL: a BF16 pool */
 

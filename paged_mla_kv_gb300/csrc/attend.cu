@@ -177,17 +177,20 @@ static_assert(SMEM_TOTAL <= 232448, "shared memory budget");
 //  - BLOCKS (tf_paged_mla_attend_blocks).  A unit is a query row's group of at most 64 heads and
 //    its tiles are the row's listed 64-row blocks, one TMA tile each, numbered and cut like UNITS
 //    but anywhere: rows choose blocks on their own, so there are no common positions to keep.
-//  - SHARED (tf_paged_mla_attend_shared).  Entries instead of streams: one for each stream's own
-//    rows and one for each group's shared rows, whose columns are the (stream, row, head) columns
-//    of the whole group one after another, so a tile of shared rows is loaded once for 64 of them
-//    whatever stream they belong to.  A column's partials over both are merged.
+//  - SHARED (tf_paged_mla_attend_shared).  Entries instead of streams.  Where a stream's R * H columns
+//    are whole groups of 64, an entry a stream over all its keys, whose shared tiles are read through
+//    the group's first table: the groups' units are cut alike, so its CTAs read them at the same time.
+//    Else one entry for each stream's own rows and one for each group's shared rows, whose columns are
+//    the (stream, row, head) columns of the whole group one after another, so a tile of shared rows is
+//    loaded and multiplied once for 64 of them whatever stream they belong to (16 heads: a quarter of
+//    the products).  A column's partials over both are merged.
 enum { MODE_RANGES = 0, MODE_UNITS = 1, MODE_SPLITS = 2, MODE_SPARSE = 3, MODE_BLOCKS = 4, MODE_SHARED = 5 };
 // the modes whose segments carry their own columns
 __host__ __device__ constexpr bool own_cols(int mode) { return mode == MODE_BLOCKS || mode == MODE_SHARED; }
 
-// One entry per stream, in the caller's order.  SHARED: entry s is stream s's own rows (keys from
-// the shared ones on), entries S and up the groups' shared rows; the fields then hold what
-// SharedEntry names.
+// One entry per stream, in the caller's order.  SHARED: entry s is stream s's rows (from the shared
+// ones on, if those are an entry of their own), entries S and up the groups' shared rows; the fields
+// then hold what SharedEntry names.
 struct StreamPlan {
     int64_t len;
     int64_t toff;     // RANGES: first numbered key tile of the stream
@@ -201,8 +204,10 @@ struct StreamPlan {
 
 // SHARED: the fields of an entry, by the names they have there.
 struct SharedEntry {
-    int64_t len;      // end of the entry's keys
-    int64_t alone;    // 1: its columns have no other entry
+    int32_t len;      // end of the entry's keys
+    int32_t alone;    // 1: its columns have no other entry
+    int32_t ptiles;   // key tiles below this one are read through prow's table
+    int32_t prow;
     int32_t nt;       // key tiles (0: the stream has no rows of its own)
     int32_t tile0;    // first key tile
     int32_t ncols;    // columns
@@ -283,6 +288,7 @@ struct Seg {
     int64_t gcol;           // first of the segment's columns among the batch's S * R * H
     int nc;                 // its columns
     int row;                // the page table's row
+    int ptiles, prow;       // SHARED: tiles below ptiles are read through table row prow
     bool causal;            // SHARED: own rows (shared ones are visible to every column)
     int64_t pos;            // BLOCKS: the query row's position
     const int32_t *list;    // BLOCKS: the segment's part of the row's list
@@ -408,16 +414,22 @@ struct SegIter {
             q.g = (int)(u - e.unit0);
             q.causal = lo < p.S;
             q.row = e.row;
+            q.ptiles = e.ptiles;
+            q.prow = e.prow;
             q.len = e.len;
             q.gcol = (int64_t)e.col0 + q.g * NCOL;
             q.nc = min(NCOL, e.ncols - q.g * NCOL);
             const int64_t te = (x1 >> 32) == u ? (x1 & 0xffffffffll) : e.nt;
             q.nt = (int)(te - t);
             q.kb = ((int64_t)e.tile0 + t) * BK;
-            q.ke = min(e.len, ((int64_t)e.tile0 + te) * BK);
-            // every segment of a CTA can be a partial: unit + CTA numbers them without gaps or
-            // repeats (of two segments the later one has the larger unit, CTA or both)
-            q.slot = e.alone && t == 0 && te == e.nt ? -1 : (int)u + (int)blockIdx.x;
+            q.ke = min((int64_t)e.len, ((int64_t)e.tile0 + te) * BK);
+            // Partials: with entries of shared rows every segment of a CTA can be one, and unit + CTA
+            // numbers them without repeats (of two segments the later one has the larger unit, CTA or
+            // both); else only a CTA's first and last
+            q.slot = e.alone && t == 0 && te == e.nt ? -1
+                     : p.nent > p.S                  ? (int)u + (int)blockIdx.x
+                                                     : 2 * (int)blockIdx.x + (k == 0 ? 0 : 1);
+            ++k;
             x = te == e.nt ? unit_pos(u + 1, 0) : unit_pos(u, te);
             return true;
         }
@@ -768,9 +780,8 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
                 if (si > 0 && !ptx::mbar_wait(&c.q_free, (si - 1) & 1, abort, errp, 15)) break;
                 ptx::mbar_arrive_expect_tx(&c.q_full, Q_SMEM_BOXES * QBOX_BYTES);
                 const int qrow = own_cols(MODE) ? (int)q.gcol : q.s * R_ * H_ + q.g * NCOL;
-                const int trow = seg_row<MODE>(q);
-                // SHARED: the group's other columns read the shared rows too
-                if (MODE == MODE_SHARED) pol_kv = q.causal ? ptx::policy_evict_first() : ptx::policy_evict_last();
+                int trow = seg_row<MODE>(q);
+                const uint64_t pol_first = ptx::policy_evict_first(), pol_last = ptx::policy_evict_last();
                 for (int b = 0; b < Q_SMEM_BOXES; ++b)
                     ptx::tma_load_2d(smem + SMEM_Q + b * QBOX_BYTES, &p.tm_q, &c.q_full, (Q_TMEM_BOXES + b) * 64, qrow,
                                      pol_q);
@@ -817,6 +828,13 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
                         cur_lp = -1;
                     }
                     const int lp = (int)(k0 >> 9), row = (int)(k0 & 511);
+                    if (MODE == MODE_SHARED) {
+                        // the group's other columns read the shared rows too
+                        const bool shared = k0 < (int64_t)q.ptiles * BK;
+                        pol_kv = shared ? pol_last : pol_first;
+                        if (trow != (shared ? q.prow : q.row)) cur_lp = -1;
+                        trow = shared ? q.prow : q.row;
+                    }
                     if (lp != cur_lp) {
                         const int raw = MODE == MODE_BLOCKS ? pg_blk
                                         : windowed          ? trow * max_pages + lp
@@ -1708,15 +1726,20 @@ __device__ __forceinline__ bool combine_unit(const Params &p, CombineUnit &cu) {
 // the group's packed columns), then those over the stream's own.  False: the column was written whole.
 struct CombineColumn {
     int n, n1, first1, first2, col1, col2;
+    int c0;   // no entries of shared rows: the first CTA, whose successors use their first slots (else -1)
     __device__ __forceinline__ size_t place(const Params &, int j, int) const {
+        if (c0 >= 0 && j > 0) return (size_t)(2 * (c0 + j)) * NCOL + col2;
         return j < n1 ? (size_t)(first1 + j) * NCOL + col1 : (size_t)(first2 + j - n1) * NCOL + col2;
     }
 };
 __device__ __forceinline__ bool combine_column(const Params &p, int s, int c, CombineColumn &cc) {
-    // the slots of unit u of an entry: u + the CTAs that hold a piece of it
+    // the slots of unit u of an entry: u + the CTAs that hold a piece of it, or these CTAs' own
+    const bool own_slots = p.nent == p.S;
+    cc.c0 = -1;
     auto pieces = [&](const SharedEntry &e, int64_t u, int &first) {
         const int c0 = range_of(p, unit_pos(u, 0));
-        first = (int)u + c0;
+        first = own_slots ? 2 * c0 + (unit_pos(u, 0) == p.rb[c0] ? 0 : 1) : (int)u + c0;
+        if (own_slots) cc.c0 = c0;
         return range_of(p, unit_pos(u, e.nt - 1)) - c0 + 1;
     };
     cc.n1 = 0;
@@ -1758,9 +1781,9 @@ __global__ void __launch_bounds__(WIDE ? COMBINE_THREADS : COMBINE_COLS * 32) ml
     std::conditional_t<SHARED, CombineColumn, CombineUnit> cu;
     size_t orow;
     if constexpr (SHARED) {
-        const int c = (int)blockIdx.y * NCOL + col;
-        if (c >= p.ncols || !combine_column(p, (int)blockIdx.z, c, cu)) return;   // WIDE: the whole block
-        orow = (size_t)blockIdx.z * p.ncols + c;
+        // blockIdx.x runs over all columns of stream blockIdx.y
+        if (col >= p.ncols || !combine_column(p, (int)blockIdx.y, col, cu)) return;   // WIDE: the whole block
+        orow = (size_t)blockIdx.y * p.ncols + col;
     } else {
         if (!combine_unit(p, cu)) return;
         if (col >= cu.nc) return;   // WIDE: the whole block
@@ -2190,37 +2213,30 @@ inline Plan plan_blocks(int S, int R, int H, const int64_t *h_len, int max_blk, 
     return pl;
 }
 
-// The entries of a shared call: own rows of each stream, then the shared rows of each group that
-// shares any (in whole tiles; the rest of a prefix counts as each stream's own).  order[s]: the
-// entry of stream s's shared rows or -1.  Returns the entries, or -1 when they pass the table.
+// The entries of a shared call (see SHARED).  Shared rows count in whole tiles, the rest of a prefix as
+// each stream's own.  order[s]: the entry of stream s's shared rows or -1.  Returns the entries, or -1
+// when they pass the table.
 inline int shared_entries(int S, int R, int H, const int64_t *h_len, const int32_t *h_gsize, int G,
                           const int64_t *h_prefix, SharedEntry *e, int16_t *order, std::vector<int32_t> *nt) {
     const int ncols = R * H;
     const int groups = (ncols + NCOL - 1) / NCOL;
+    const bool split = ncols % NCOL != 0;   // shared rows are entries of their own
     int n = S, units = 0;
     for (int g = 0, s = 0; g < G; ++g) {
-        const int64_t whole = h_gsize[g] > 1 ? h_prefix[g] / BK * BK : 0;
-        if (whole > 0) {
+        const int first = s;
+        const int32_t whole = h_gsize[g] > 1 ? (int32_t)(h_prefix[g] / BK) : 0;   // tiles
+        const int pe = split && whole > 0 ? n : -1;
+        if (pe >= 0) {
             if (n >= TF_MAX_STREAMS) return -1;
-            e[n].len = whole;
-            e[n].alone = 0;
-            e[n].nt = (int32_t)(whole / BK);
-            e[n].tile0 = 0;
-            e[n].ncols = h_gsize[g] * ncols;
-            e[n].col0 = s * ncols;
-            e[n].row = s;
+            e[n] = SharedEntry{whole * BK, 0, whole, first, whole, 0, h_gsize[g] * ncols, 0, first * ncols, first};
+            ++n;
         }
         for (int k = 0; k < h_gsize[g]; ++k, ++s) {
-            e[s].len = h_len[s];
-            e[s].alone = whole == 0;
-            e[s].tile0 = (int32_t)(whole / BK);
-            e[s].nt = (int32_t)((h_len[s] - whole + BK - 1) / BK);
-            e[s].ncols = ncols;
-            e[s].col0 = s * ncols;
-            e[s].row = s;
-            order[s] = (int16_t)(whole > 0 ? n : -1);
+            const int32_t tile0 = pe >= 0 ? whole : 0;
+            const int32_t tiles = (int32_t)((h_len[s] + BK - 1) / BK);
+            e[s] = SharedEntry{(int32_t)h_len[s], pe < 0, whole, first, tiles - tile0, tile0, ncols, 0, s * ncols, s};
+            order[s] = (int16_t)pe;
         }
-        if (whole > 0) ++n;
     }
     for (int i = 0; i < n; ++i) {
         e[i].unit0 = units;
@@ -2241,7 +2257,7 @@ inline Plan plan_shared(const std::vector<int32_t> &nt, int nshared, int sms, in
     int64_t load = 0;
     pl.nranges = cut_units(nt, UNIT_MIN_TILES, sms, rb, &cut, &load);
     pl.nctas = pl.nranges;
-    pl.slots = cut || nshared > 0 ? nt.size() + (size_t)pl.nctas : 0;
+    pl.slots = nshared > 0 ? nt.size() + (size_t)pl.nctas : cut ? 2 * (size_t)pl.nctas : 0;
     return pl;
 }
 
@@ -2348,17 +2364,15 @@ size_t blocks_workspace_bytes(bool fp8, int S, int R, int H, const int64_t *h_le
 
 // The first page of each stream that is its own to expand: a group's later streams read the shared
 // rows through the first one's table.
-static bool expand_shared(int S, const int32_t *h_gsize, int G, const attn::SharedEntry *e, const int16_t *order, int n,
-                          int32_t *h_from) {
+static bool expand_shared(int S, const int32_t *h_gsize, int G, const attn::SharedEntry *e, int n, int32_t *h_from) {
+    constexpr int kPageTiles = kPageRows / attn::BK;
     int64_t visits = 0, tiles = 0;
-    for (int i = 0; i < n; ++i) {
-        const int64_t units = ((int64_t)e[i].ncols + attn::NCOL - 1) / attn::NCOL;
-        visits += units * e[i].nt;
-        if (e[i].nt > 0) tiles += e[i].nt + kPageRows / attn::BK;   // to whole pages
-    }
+    for (int i = 0; i < n; ++i) visits += ((int64_t)e[i].ncols + attn::NCOL - 1) / attn::NCOL * e[i].nt;
     for (int g = 0, s = 0; g < G; ++g)
-        for (int k = 0; k < h_gsize[g]; ++k, ++s)
-            h_from[s] = k > 0 && order[s] >= 0 ? (int32_t)((int64_t)e[s].tile0 * attn::BK / kPageRows) : 0;
+        for (int k = 0; k < h_gsize[g]; ++k, ++s) {
+            h_from[s] = k > 0 ? e[s].ptiles / kPageTiles : 0;
+            tiles += ((int64_t)e[s].len + kPageRows - 1) / kPageRows * kPageTiles - (int64_t)h_from[s] * kPageTiles;
+        }
     return expand_fp8(visits, tiles);
 }
 
@@ -2372,7 +2386,7 @@ int shared_workspace_bytes(bool fp8, int S, int R, int H, const int64_t *h_len, 
     int64_t rb[attn::MAX_CTAS + 1];
     *bytes = slots_bytes(attn::plan_shared(nt, n - S, device_sms(), rb).slots);
     int32_t from[TF_MAX_STREAMS];
-    if (fp8 && expand_shared(S, h_gsize, G, e, order, n, from))
+    if (fp8 && expand_shared(S, h_gsize, G, e, n, from))
         *bytes = with_expanded(*bytes, fp8_shadow_bytes(S, h_len, from));
     return TF_OK;
 }
@@ -2641,7 +2655,9 @@ static int launch_plan(tf_kvpool *pool, attn::Params &p, const attn::Plan &pl, v
         const int gx = wide ? NCOL : NCOL / COMBINE_COLS;
         // UNITS, BLOCKS: blockIdx.y runs over the range bounds (only cut units merge)
         const bool bounds = pl.mode == MODE_UNITS || pl.mode == MODE_BLOCKS;
-        const dim3 grid = bounds ? dim3(gx, pl.nranges - 1) : dim3(gx, groups, p.S);
+        const dim3 grid = bounds                     ? dim3(gx, pl.nranges - 1)
+                          : pl.mode == MODE_SHARED ? dim3((unsigned)gx * groups, p.S)
+                                                   : dim3(gx, groups, p.S);
         auto *kern = pl.mode == MODE_SHARED ? (wide ? mla_combine_kernel<true, true> : mla_combine_kernel<false, true>)
                                             : (wide ? mla_combine_kernel<true, false> : mla_combine_kernel<false, false>);
         const cudaError_t e = launch_pdl(kern, grid, dim3(wide ? COMBINE_THREADS : COMBINE_COLS * 32), 0, st, p);
@@ -2774,7 +2790,7 @@ int launch_attend_shared(tf_kvpool *pool, int cache, const int32_t *d_pt, int ma
     int64_t rb[MAX_CTAS + 1];
     const Plan pl = plan_shared(nt, n - S, device_sms(), rb);
     int32_t from[TF_MAX_STREAMS];
-    const bool expand = is_fp8(pool->desc) && expand_shared(S, h_gsize, G, e, order, n, from);
+    const bool expand = is_fp8(pool->desc) && expand_shared(S, h_gsize, G, e, n, from);
     const size_t part = slots_bytes(pl.slots);
     const int rc = check_workspace(expand ? with_expanded(part, fp8_shadow_bytes(S, h_len, from)) : part, d_ws, ws_bytes);
     if (rc != TF_OK) return rc;

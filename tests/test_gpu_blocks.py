@@ -437,17 +437,34 @@ def test_two_calls_on_two_streams_at_once():
 
 # ---- streams that share a prefix ---------------------------------------------------------------
 
+class Prefixed(Y.Workload):
+    """Streams whose prefix ends inside a page: the page is each one's own, its first rows are the same."""
+
+    def page_rows(self, cache, s, page):
+        lat, rope = super().page_rows(cache, s, page)
+        first, p = self.extra["prefix"][s]
+        n = p - page * 512
+        if s != first and 0 < n < 512:
+            l0, r0 = super().page_rows(cache, first, page)
+            lat[:n], rope[:n] = l0[:n], r0[:n]
+        return lat, rope
+
+
 def shared_workload(name, seed, groups, R, H):
     """groups: (prefix rows, [own rows...]); pages under a prefix are held by reference."""
+    extra = []
     lens, share, sizes, prefixes, first = [], [], [], [], 0
     for p, own in groups:
         for i, n in enumerate(own):
             lens.append(p + n)
             share.append((first, p // 512) if i else (0, 0))
+            extra.append((first, p))
         sizes.append(len(own))
         prefixes.append(p)
         first += len(own)
     w = Y.custom(name, seed, lens=lens, R=R, H=H, share=share, q_std=1.0, value_std=0.5)
+    w.__class__ = Prefixed
+    w.extra["prefix"] = extra
     return w, sizes, prefixes
 
 
@@ -477,6 +494,8 @@ def check_dense(w, out, lse, fp8=False, rows=None):
     ([(1536, [3, 3])], 3, 128), ([(512, [40, 90, 41])], 40, 5), ([(2560, [1] * 30)], 1, 5),
     ([(512, [100]), (1024, [100])], 1, 64),           # groups of one stream share nothing
     ([(16384, [1, 900, 17])], 1, 64),
+    ([(1000, [300, 90]), (0, [100, 70])], 70, 64),      # chunks of rows behind a prefix that ends inside a page
+    ([(520, [1, 2, 3])], 1, 64), ([(960, [33] * 5), (64, [700])], 4, 16),
     ([(4096, [9, 70, 600]), (2560, [5, 5])], 5, 128)])   # rows that many columns read: FP8 pages are expanded first
 def test_attend_shared(groups, R, H, fp8):
     w, sizes, prefixes = shared_workload("sh", 140 + R + H, groups, R, H)
