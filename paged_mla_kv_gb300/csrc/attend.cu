@@ -1780,17 +1780,19 @@ __global__ void __launch_bounds__(WIDE ? COMBINE_THREADS : COMBINE_COLS * 32) ml
     const int col = WIDE ? (int)blockIdx.x : (int)blockIdx.x * COMBINE_COLS + warp;   // column of the group
     std::conditional_t<SHARED, CombineColumn, CombineUnit> cu;
     size_t orow;
+    bool live;   // WIDE: the same for the whole block
     if constexpr (SHARED) {
         // blockIdx.x runs over all columns of stream blockIdx.y
-        if (col >= p.ncols || !combine_column(p, (int)blockIdx.y, col, cu)) return;   // WIDE: the whole block
+        live = col < p.ncols && combine_column(p, (int)blockIdx.y, col, cu);
         orow = (size_t)blockIdx.y * p.ncols + col;
     } else {
-        if (!combine_unit(p, cu)) return;
-        if (col >= cu.nc) return;   // WIDE: the whole block
+        live = combine_unit(p, cu) && col < cu.nc;
         orow = (size_t)cu.s * p.ncols + cu.col0 + col;
     }
-    // where the partials lie follows from the parameters alone; the wait comes before the first of them
+    // Where the partials lie follows from the parameters alone; the wait comes before the first of
+    // them.  Every block waits: a launch behind this one relies on it for the attention's end too.
     ptx::griddep_wait();
+    if (!live) return;
     const int n = cu.n;
     float4 acc[4];
 #pragma unroll
@@ -2138,8 +2140,12 @@ inline int cut_by_limit(const std::vector<int32_t> &nt, int64_t seg, int64_t lim
 // prefill chunk's 2,048 rows: whole rows would leave 14 a CTA against 13.5); cuts by limit fit few: 64
 // streams of 32 tiles are 128 CTAs of one segment, where even cuts give 152 CTAs two segments each
 // and more partials to merge.
-// *largest: that load, with the combine pass where a unit is cut.
-inline int cut_units(const std::vector<int32_t> &nt, int min_tiles, int sms, int64_t *b, bool *cut, int64_t *largest) {
+// *largest: that load, with the combine pass where a unit is cut.  limit_ties: of equal ones the cuts by
+// limit are taken (listed blocks, which decode reads from HBM: fewer partials; 64 streams of 32 blocks
+// 39.6 us against 42.3), else the even cuts (shared prefixes, bound by the products: eight streams of
+// 64 heads behind 8,192 rows 25 us against 27).
+inline int cut_units(const std::vector<int32_t> &nt, int min_tiles, int sms, bool limit_ties, int64_t *b, bool *cut,
+                     int64_t *largest) {
     const int64_t seg = UNIT_SEG_COST;
     int64_t tiles = 0, most = 0;
     for (int32_t t : nt) {
@@ -2158,7 +2164,7 @@ inline int cut_units(const std::vector<int32_t> &nt, int min_tiles, int sms, int
     *largest = load + (*cut ? combine_cost(nt.size()) : 0);
     // the smallest limit that needs at most sms ranges and cuts nothing below min_tiles
     int64_t lo = std::max<int64_t>(seg + std::min<int64_t>(most, min_tiles), (tiles + sms - 1) / sms + seg);
-    int64_t hi = *largest;
+    int64_t hi = *largest - (limit_ties ? 0 : 1);
     if (lo > hi || cut_by_limit(nt, seg, hi, sms, nullptr, nullptr) > sms) return n;
     while (lo < hi) {
         const int64_t mid = lo + (hi - lo) / 2;
@@ -2167,7 +2173,7 @@ inline int cut_units(const std::vector<int32_t> &nt, int min_tiles, int sms, int
     bool c2 = false;
     cut_by_limit(nt, seg, lo, sms, nullptr, &c2);
     const int64_t cost = lo + (c2 ? combine_cost(nt.size()) : 0);
-    if (cost > *largest) return n;
+    if (cost > *largest - (limit_ties ? 0 : 1)) return n;
     *largest = cost;
     *cut = c2;
     return cut_by_limit(nt, seg, lo, sms, b, nullptr);
@@ -2190,7 +2196,7 @@ inline Plan plan_blocks(int S, int R, int H, const int64_t *h_len, int max_blk, 
     pl.total = (int64_t)nt.size();
     pl.rep = 1;
     int64_t load = 0;
-    pl.nranges = cut_units(nt, UNIT_MIN_TILES, sms, rb, &cut, &load);
+    pl.nranges = cut_units(nt, UNIT_MIN_TILES, sms, true, rb, &cut, &load);
     pl.nctas = pl.nranges;
     pl.slots = cut ? 2 * (size_t)pl.nctas : 0;
     // few units: k CTAs each, one cluster, for the k that ends first
@@ -2255,7 +2261,7 @@ inline Plan plan_shared(const std::vector<int32_t> &nt, int nshared, int sms, in
     pl.total = (int64_t)nt.size();
     pl.rep = 1;
     int64_t load = 0;
-    pl.nranges = cut_units(nt, UNIT_MIN_TILES, sms, rb, &cut, &load);
+    pl.nranges = cut_units(nt, UNIT_MIN_TILES, sms, false, rb, &cut, &load);
     pl.nctas = pl.nranges;
     pl.slots = nshared > 0 ? nt.size() + (size_t)pl.nctas : cut ? 2 * (size_t)pl.nctas : 0;
     return pl;

@@ -582,3 +582,50 @@ def test_attend_shared_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+# ---- pools ---------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_calls_on_a_batch_invariant_pool(fp8):
+    """The plans are the calls' own whatever the pool's flags."""
+    w, sizes, prefixes = shared_workload("inv", 160, [(1024, [30, 200, 513])], 2, 64)
+    out = []
+    for invariant in (False, True):
+        res = Resident(w, fp8=fp8, invariant=invariant)
+        a = run_shared(res, w, sizes, prefixes)
+        b = run_blocks(res, w, random_lists(w, 9, 4))
+        no_device_error(res.pool)
+        out.append([bits(a[0]), bits(b[0]), a[1].cpu().numpy(), b[1].cpu().numpy()])
+    for x, y in zip(*out):
+        assert np.array_equal(x, y)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_pages_past_four_gigabytes(fp8):
+    """A stream whose pages lie anywhere in a pool of 9 GB: the bits of a small pool."""
+    w = Y.custom("far", 161, lens=[1500, 700], R=2, H=16, q_std=1.0, value_std=0.5)
+    got = []
+    for pages in (8, 9_400_000_000 // (B.PAGE_BYTES_FP8 if fp8 else B.PAGE_BYTES_BF16)):
+        res = Resident.__new__(Resident)
+        res.w, res.windowed, res.device, res.max_pages = w, False, "cuda", w.max_pages
+        res.pool = B.KVPool(1, pages, seed=5, fp8=fp8)
+        ids = np.concatenate([res.pool.take(3), res.pool.take(2)])
+        if pages > 8:      # both ends and what is between
+            ids = np.array([pages - 1, 1, pages - 2, pages // 2, pages - 3], np.int32)
+        pt = np.full((2, 3), -1, np.int32)
+        pt[0], pt[1, :2] = ids[:3], ids[3:]
+        res.pt, res.pt_host, res.lens = torch.from_numpy(pt).cuda(), pt, np.asarray(w.lens, np.int64)
+        for s in range(2):
+            res.append_rows(0, s, 0, int(w.lens[s]))
+        bk = torch.zeros((pages, 8, 576), dtype=torch.bfloat16, device="cuda")
+        B.tf_block_keys_update(res.pool, 0, res.pt, 3, [0, 0], w.lens, bk)
+        x, n, cols = run_scores(res, w, bk, res.q())
+        out, lse = run_blocks(res, w, random_lists(w, 6, 2))
+        sh = run_shared(res, w, [1, 1], [512, 0])
+        no_device_error(res.pool)
+        keys = torch.stack([bk[int(pt[s, b // 8]), b % 8] for s in range(2) for b in range(K.blocks_of(int(w.lens[s])))])
+        got.append([bits(keys), x[:, :cols].cpu().numpy(), bits(out), lse.cpu().numpy(), bits(sh[0])])
+        del res, bk
+    for a, b in zip(*got):
+        assert np.array_equal(a, b)
