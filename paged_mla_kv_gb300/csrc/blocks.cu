@@ -77,7 +77,7 @@ __device__ __forceinline__ uint32_t mean_pair(const float (&part)[G][kDk], int i
 }
 
 // BF16 pages, one CTA a block: thread (g, c) adds 16-byte chunk c (72 a row) of rows g, g + 4, ... in
-// fp32, eight loads in flight.  Bound by HBM: 301,904 rows take 54.8 us, 0.94 of the measured copy rate.
+// fp32, eight loads in flight.  Bound by HBM: 297,264 rows take 54.8 us, 0.94 of the measured copy rate.
 constexpr int KC = kDk / 8, KG = 4;
 __global__ void __launch_bounds__(KC *KG) block_keys_kernel(const __grid_constant__ KeysParams p) {
     __shared__ float part[KG][kDk];
