@@ -1485,7 +1485,7 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
                     ptx::named_bar(1, 128);
                     if (threadIdx.x == 0)
                         ptx::bulk_s2g(ws_o + ((size_t)q.slot * NCOL + h2) * kLat, stage + h2 * kLat,
-                                      32 * kLat * sizeof(float));
+                                      min(32, ncols - h2) * kLat * sizeof(float));
                 }
                 if (threadIdx.x == 0) ptx::bulk_s2g_wait();
             } else if (q.slot >= 0) {
