@@ -389,6 +389,11 @@ def _dense(t, dtype, n: int) -> bool:
     return t.dtype is dtype and t.numel() == n and t.is_contiguous()
 
 
+def _table(pt, max_pages: int, S: int, i32) -> bool:
+    """A page table (None: stream s has the pages from s * max_pages on) with a row of max_pages for each stream."""
+    return pt is None or (pt.dtype is i32 and pt.numel() >= S * max_pages and pt.is_contiguous())
+
+
 def _qout(q, out, lse, cols: int, bf16, f32) -> bool:
     """q of 576, out of 512 and lse (or None) of one value for each of `cols` (stream, row, head)."""
     return (_dense(q, bf16, cols * 576) and _dense(out, bf16, cols * 512) and (lse is None or _dense(lse, f32, cols)))
@@ -404,7 +409,8 @@ def tf_block_keys_update(pool: KVPool, cache: int, pt, max_pages: int, start, le
     tensor [pages][8][576]."""
     a, p = _i64(start)
     b, pl = _i64(lens)
-    if not (len(a) == len(b) and _dense(bkeys, _dtypes()[0], pool.num_pages * 4608)):
+    bf16, _, i32 = _dtypes()
+    if not (len(a) == len(b) and _dense(bkeys, bf16, pool.num_pages * 4608) and _table(pt, max_pages, len(b), i32)):
         _refuse("tf_block_keys_update")
     _check(lib().tf_block_keys_update(pool.handle, cache, _ptr(pt), max_pages, p, pl, len(b), bkeys.data_ptr(),
                                       _stream(stream)), "tf_block_keys_update")
@@ -421,7 +427,8 @@ def tf_block_scores(pool: KVPool, bkeys, pt, max_pages: int, lens, q, scale: flo
     ld, one = scores.stride()
     if not (len(a) == S and _dense(q, bf16, S * R * H * 576) and _dense(bkeys, bf16, pool.num_pages * 4608) and
             (w is None or _dense(w, f32, S * R * H)) and (nblk is None or _dense(nblk, i32, S * R)) and
-            scores.dtype is f32 and rows == S * R and (one == 1 or cols == 1) and cols * TF_BLOCK_ROWS >= (max(a) if type(a) is array.array else a.max())):
+            scores.dtype is f32 and rows == S * R and (one == 1 or cols == 1) and _table(pt, max_pages, S, i32) and
+            S > 0 and cols * TF_BLOCK_ROWS >= (max(a) if type(a) is array.array else a.max())):
         _refuse("tf_block_scores")
     _check(lib().tf_block_scores(pool.handle, bkeys.data_ptr(), _ptr(pt), max_pages, p, S, R, H, q.data_ptr(), _ptr(w),
                                  scale, sink, local, scores.data_ptr(), ld, _ptr(nblk), _stream(stream)),
@@ -444,7 +451,8 @@ def tf_paged_mla_attend_blocks(pool: KVPool, cache: int, pt, max_pages: int, len
     bf16, f32, i32 = _dtypes()
     a, p = _i64(lens)
     max_blk = blk.shape[-1]
-    if not (len(a) == S and _qout(q, out, lse, S * R * H, bf16, f32) and _dense(blk, i32, S * R * max_blk)):
+    if not (len(a) == S and _qout(q, out, lse, S * R * H, bf16, f32) and _dense(blk, i32, S * R * max_blk) and
+            _table(pt, max_pages, S, i32)):
         _refuse("tf_paged_mla_attend_blocks")
     _check(lib().tf_paged_mla_attend_blocks(pool.handle, cache, _ptr(pt), max_pages, p, blk.data_ptr(), max_blk, S, R, H,
                                             q.data_ptr(), scale, out.data_ptr(), _ptr(lse), _ptr(ws),
@@ -467,11 +475,12 @@ def tf_paged_mla_attend_shared(pool: KVPool, cache: int, pt, max_pages: int, len
     """group_sizes: streams of each group, in order; prefixes: the rows each group's streams have in common; the rest
     as in tf_paged_mla_attend."""
     S, R, H, _ = q.shape
-    bf16, f32, _ = _dtypes()
+    bf16, f32, i32 = _dtypes()
     a, p = _i64(lens)
     g, pg = _i32(group_sizes)
     f, pf = _i64(prefixes)
-    if not (len(a) == S and len(g) == len(f) and _qout(q, out, lse, S * R * H, bf16, f32)):
+    if not (len(a) == S and len(g) == len(f) and _qout(q, out, lse, S * R * H, bf16, f32) and
+            _table(pt, max_pages, S, i32)):
         _refuse("tf_paged_mla_attend_shared")
     _check(lib().tf_paged_mla_attend_shared(pool.handle, cache, _ptr(pt), max_pages, p, pg, len(g), pf, S, R, H,
                                             q.data_ptr(), scale, out.data_ptr(), _ptr(lse), _ptr(ws),

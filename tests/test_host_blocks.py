@@ -188,6 +188,32 @@ def test_binding_refuses_what_the_library_cannot_see(L):
         assert e.value.code == B.TF_E_ARG, i
 
 
+@pytest.mark.parametrize("pt", [torch.zeros(2, 2, dtype=torch.int64), torch.zeros(1, 2, dtype=torch.int32),
+                                torch.zeros(3, dtype=torch.int32), torch.zeros(2, 4, dtype=torch.int32)[:, :2]],
+                         ids=["int64", "one_row", "short", "strided"])
+def test_binding_refuses_a_table_of_another_form(L, pt):
+    p = _FakePool()
+    bf = dict(dtype=torch.bfloat16)
+    bk, q = torch.zeros(4, 8, 576, **bf), torch.zeros(2, 1, 16, 576, **bf)
+    out, blk = torch.zeros(2, 1, 16, 512, **bf), torch.zeros(2, 1, 4, dtype=torch.int32)
+    for f in (lambda: B.tf_block_keys_update(p, 0, pt, 2, [0, 0], [64, 64], bk),
+              lambda: B.tf_block_scores(p, bk, pt, 2, [64, 64], q, 0.1, torch.zeros(2, 4)),
+              lambda: B.tf_paged_mla_attend_blocks(p, 0, pt, 2, [64, 64], blk, q, 0.1, out),
+              lambda: B.tf_paged_mla_attend_shared(p, 0, pt, 2, [64, 64], [2], [0], q, 0.1, out)):
+        with pytest.raises(B.TFError) as e:
+            f()
+        assert e.value.code == B.TF_E_ARG
+
+
+def test_binding_refuses_no_streams(L):
+    p = _FakePool()
+    bf = dict(dtype=torch.bfloat16)
+    with pytest.raises(B.TFError) as e:
+        B.tf_block_scores(p, torch.zeros(4, 8, 576, **bf), None, 2, [], torch.zeros(0, 1, 16, 576, **bf), 0.1,
+                          torch.zeros(0, 4))
+    assert e.value.code == B.TF_E_ARG
+
+
 def test_header_is_strict_c99(L, tmp_path):
     src = tmp_path / "t.c"
     src.write_text('#include "tf_blocks.h"\nint main(void) { return TF_BLOCK_ROWS - 64; }\n')
