@@ -1571,14 +1571,18 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
             }
 #pragma unroll
             for (int j = 0; j < MAX_MERGE; ++j) M = fmaxf(M, w[j]);
+            // The weight of a partial without a key is 0, whatever the sum: nothing is read there.  A column
+            // whose scores are NaN has the maximum -inf and a sum of NaN, which makes all its weights NaN.
+            bool none[MAX_MERGE];
 #pragma unroll
             for (int j = 0; j < MAX_MERGE; ++j) {
+                none[j] = l[j] == 0.f;
                 w[j] = w[j] == -INFINITY ? 0.f : ptx::ex2(w[j] - M);
                 L = __fmaf_rn(w[j], l[j], L);
             }
-            const float inv = L > 0.f ? 1.f / L : 0.f;
+            const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
-            for (int j = 0; j < MAX_MERGE; ++j) wts[j * NCOL + col] = w[j] * inv;
+            for (int j = 0; j < MAX_MERGE; ++j) wts[j * NCOL + col] = none[j] ? 0.f : w[j] * inv;
             if (lsep && col >= mine * per && col < c1)
                 lsep[(size_t)s * ncols_all + r * H_ + h0 + col] = (M + log2f(L)) * 0.69314718055994531f;
         }
