@@ -61,8 +61,9 @@ int tf_block_keys_update(tf_kvpool *pool, int32_t cache, const int32_t *d_pt, in
  * each block b of 0 .. own:
  *   score[s,r,b] = sum_h w[s,r,h] max(0, scale q[s,r,h] . k_b)        bf16 products, fp32 sums
  * but +inf for b < sink and for b > own - local: the first `sink` blocks and the last `local` ones, the
- * row's own among them, are always chosen first.  (A product that is NaN counts as 0.)  local is at least 1, so no score depends on a row
- * behind the query: every other block is full and lies before the row's own.
+ * row's own among them, are always chosen first.  local is at least 1, so no score depends on a row
+ * behind the query: every other block is full and lies before the row's own.  A NaN in a query, a key or a
+ * weight makes the scores NaN that it enters (tf_topk_blocked ranks those below all others).
  * d_q: bf16 [S][R][H][576], the queries of the attention; d_w: fp32 [S][R][H], or NULL for ones.
  * d_scores: fp32 [S * R][ld], ld a multiple of 4 and at least cols, the blocks of the longest stream.
  *   Columns 0 .. cols - 1 of every row are written (-inf behind the row's own block), the others left.

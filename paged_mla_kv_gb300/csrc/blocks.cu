@@ -642,18 +642,18 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
                 for (int j = 0; j < 32; j += C) {
                     if (n0 + j >= ncols) break;
                     if (C == 1) {
-                        acc[0].x = fmaf(p.w ? w[n0 + j] : 1.f, fmaxf(__uint_as_float(v[j]), 0.f), acc[0].x);
+                        acc[0].x = fmaf(p.w ? w[n0 + j] : 1.f, ptx::relu_nan(__uint_as_float(v[j])), acc[0].x);
                     } else {
 #pragma unroll
                         for (int k = j; k < j + C; k += 4) {
                             const float4 wk = p.w ? *reinterpret_cast<const float4 *>(w + n0 + k)
                                                   : make_float4(1.f, 1.f, 1.f, 1.f);
                             acc[0] = ptx::fma2(make_float2(wk.x, wk.y),
-                                          make_float2(fmaxf(__uint_as_float(v[k]), 0.f),
-                                                      fmaxf(__uint_as_float(v[k + 1]), 0.f)), acc[0]);
+                                               make_float2(ptx::relu_nan(__uint_as_float(v[k])),
+                                                           ptx::relu_nan(__uint_as_float(v[k + 1]))), acc[0]);
                             acc[1] = ptx::fma2(make_float2(wk.z, wk.w),
-                                          make_float2(fmaxf(__uint_as_float(v[k + 2]), 0.f),
-                                                      fmaxf(__uint_as_float(v[k + 3]), 0.f)), acc[1]);
+                                               make_float2(ptx::relu_nan(__uint_as_float(v[k + 2])),
+                                                           ptx::relu_nan(__uint_as_float(v[k + 3]))), acc[1]);
                         }
                     }
                     left -= C;

@@ -469,6 +469,13 @@ __device__ __forceinline__ void transpose_bf16(const float (&v)[32], uint4 (&o)[
     }
 }
 
+// max(x, 0) that leaves a NaN one.
+__device__ __forceinline__ float relu_nan(float x) {
+    float y;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Two fp32 values at once: a * b + c, a * b, a + b, each rounded to nearest.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;

@@ -46,3 +46,48 @@ def test_nan_queries_give_nan(S, H, n, k, fp8):
         lat, rope = rows64(w, s, fp8)
         fine = ~bad[s, 0].numpy()
         check_row(o[s, 0][fine], l[s, 0][fine], qs[s, 0][fine], lat, rope, K.rows_of_list(b[s, 0].tolist(), n - 1), w.scale)
+
+
+@pytest.mark.parametrize("H,weighted", [(64, False), (64, True), (8, True), (20, False), (20, True), (5, True), (1, False)])
+def test_scores_of_nan_and_infinite_keys(H, weighted):
+    """A block whose key was never averaged must not pass for an ordinary one."""
+    lens, R = [5000, 700], 3
+    w = Y.custom("nans", 175, lens=lens, R=R, H=H)
+    res = Resident(w, caches=[])
+    g = torch.Generator(device="cuda").manual_seed(H)
+    bk = torch.randn((res.pool.num_pages, 8, 576), generator=g, device="cuda").bfloat16()
+    q = torch.randn((2, R, H, 576), generator=g, device="cuda").bfloat16()
+    wt = torch.randn((2, R, H), generator=g, device="cuda") if weighted else None
+    nan, inf = float("nan"), float("inf")
+
+    def key(s, b):
+        return bk[int(res.pt_host[s, b // 8]), b % 8]
+
+    key(0, 5)[:] = nan                      # every product
+    key(0, 9)[575] = nan
+    key(1, 2)[0] = nan
+    key(0, 20)[7], key(0, 21)[7] = inf, -inf
+    key(0, 22)[3], key(0, 22)[4] = inf, inf   # inf - inf for some heads
+    q[0, 1, 0, 100] = nan                   # one head of one row: all its scores
+    if weighted:
+        wt[0, 2, H - 1] = inf
+    cols = K.blocks_of(5000)
+    x = torch.zeros((2 * R, -(-cols // 4) * 4), device="cuda")
+    B.tf_block_scores(res.pool, bk, res.pt, res.max_pages, lens, q, w.scale, x, w=wt, sink=1, local=2)
+    no_device_error(res.pool)
+    xs, keys, qs = host(x), host(bk), host(q)
+    with np.errstate(invalid="ignore"):
+        for s, n in enumerate(lens):
+            nb = K.blocks_of(n)
+            k = np.stack([keys[int(res.pt_host[s, b // 8]), b % 8] for b in range(nb)])
+            ws = None if wt is None else host(wt)[s]
+            ref = K.block_scores(qs[s], k, n, ws, w.scale, 1, 2)
+            got = xs[s * R:(s + 1) * R, :nb]
+            assert np.array_equal(np.isnan(got), np.isnan(ref))
+            fin = np.isfinite(ref)
+            odd = ~fin & ~np.isnan(ref)
+            assert np.array_equal(got[odd], ref[odd])
+            mag = np.abs(qs[s]) @ np.abs(k).T
+            mag = (mag if ws is None else mag * np.abs(ws)[..., None]).sum(1)
+            assert np.all(np.abs(got[fin] - ref[fin]) <= (w.scale * (580 + H) * 2.0 ** -23 * mag)[fin])
+    assert np.isnan(xs[0, 5]) and np.isnan(xs[2, 9]) and np.isnan(xs[3, 2]) and np.isnan(xs[1, 1:70]).all()
