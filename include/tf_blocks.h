@@ -87,7 +87,8 @@ int tf_block_scores(tf_kvpool *pool, const void *d_bkeys, const int32_t *d_pt, i
  * An entry of -1 is no block, and a block behind pos has no key to see; a row left without keys gives
  * out 0 and lse -inf.  A block listed twice counts twice.  The order of a list decides only the order of
  * the sums.  An entry below -1 or at and past the stream's last block is recorded as TF_E_DEVICE, and so is
- * a table entry outside the pool; the call's output is then undefined.
+ * a table entry outside the pool that a listed block needs; the call's output is then undefined.  Entries of
+ * pages that no list names are not used.
  * d_blk: int32 [S][R][max_blk]; everything else as in tf_paged_mla_attend, BF16 and FP8 pages alike.  The
  * blocks are dealt out by the default plan whatever the pool's flags: a row's bits may differ (within
  * rounding) between batches and are the same on every call of one batch.  The rows of an FP8 pool that many
@@ -107,7 +108,8 @@ int tf_paged_mla_attend_blocks(tf_kvpool *pool, int32_t cache, const int32_t *d_
  * are the same.  The shared rows, in whole 64-row tiles, are read once for the group, through the first
  * stream's table, and multiplied with the queries of all its streams together; the rest of each stream is
  * read through its own.  That the rows are the same is the caller's word: pages held by reference, or
- * copies of the same bytes.  A group of one stream, or a prefix of 0, shares nothing.
+ * copies of the same bytes.  A group of one stream, or a prefix of 0, shares nothing.  Table
+ * entries of pages of which a stream reads no row of its own are not used, but for the group's first stream.
  * 0 <= h_prefix[g] <= h_len[s] - R + 1 for every stream s of the group: each query row sees all of it.
  * Both arrays have G entries, 1 <= G <= S.  All else as in tf_paged_mla_attend, BF16 and FP8 pages alike;
  * the keys are dealt out by a plan of their own whatever the pool's flags, so bits may differ (within

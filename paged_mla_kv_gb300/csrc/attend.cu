@@ -227,6 +227,8 @@ struct Params {
                                 // BLOCKS: [S][R][max_idx] block numbers of each row
     int32_t max_idx;
     const int32_t *pt;
+    const int32_t *src_pt;      // rows expanded from FP8 pages: the pool's own table (else null), for the
+    int32_t src_max_pages;      // ids of pages that it does not have
     const __nv_bfloat16 *q;     // [S*R*H][576]: the TMEM part of each column group is read from here
     __nv_bfloat16 *out;
     float *lse;
@@ -841,7 +843,8 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
                                                             : __ldg(pt + (int64_t)trow * max_pages + lp);
                         cur_lp = lp;
                         if (raw < 0 || raw >= num_pages) {
-                            ptx::record_error(errp, TF_E_DEVICE, raw);
+                            const int64_t at = (int64_t)trow * p.src_max_pages + lp;
+                            ptx::record_error(errp, TF_E_DEVICE, p.src_pt ? __ldg(p.src_pt + at) : raw);
                             *abort = 1;
                             stop = true;
                             break;
@@ -2607,6 +2610,8 @@ static int fill_params(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_
         if (!encode(&p.tm_q, const_cast<void *>(d_q), 2, dims, strides, box)) return TF_E_CUDA;
     }
     p.pt = d_pt;
+    p.src_pt = pool->src_pt;
+    p.src_max_pages = pool->src_max_pages;
     p.q = static_cast<const __nv_bfloat16 *>(d_q);
     p.out = static_cast<__nv_bfloat16 *>(d_out);
     p.lse = d_lse;

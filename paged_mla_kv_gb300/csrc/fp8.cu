@@ -110,7 +110,6 @@ struct DequantParams {
     const int32_t *pt;       // [S][max_pages] or null (windows)
     char *shadow;            // BF16 pages
     int32_t *shadow_pt;      // [S][maxp]
-    DevErr *err;
     int32_t max_pages, num_pages, S, maxp;
     int64_t len[TF_MAX_STREAMS];
     int32_t off[TF_MAX_STREAMS];  // the shadow page of the stream's logical page 0
@@ -132,12 +131,10 @@ __global__ void __launch_bounds__(kDequantThreads) dequant_kernel(const __grid_c
     if (rem <= 0 || j < p.from[s]) return;
     const int rows = rem < kDequantRows ? (int)rem : kDequantRows;
     const int page = p.pt ? __ldg(p.pt + (int64_t)s * p.max_pages + j) : s * p.max_pages + j;
-    if (page < 0 || page >= p.num_pages) {
-        if (threadIdx.x == 0) ptx::record_error(p.err, TF_E_DEVICE, page);
-        return;
-    }
+    const bool good = page >= 0 && page < p.num_pages;
     const int dpage = p.off[s] + j;
-    if (threadIdx.x == 0 && r0 == 0) p.shadow_pt[(int64_t)s * p.maxp + j] = dpage;
+    if (threadIdx.x == 0 && r0 == 0) p.shadow_pt[(int64_t)s * p.maxp + j] = good ? dpage : -1;
+    if (!good) return;
     const char *src = p.cache_base + (size_t)page * kF8PageBytes;
     char *dst = p.shadow + (size_t)dpage * kPageBytes;
     const float *scales = reinterpret_cast<const float *>(src + kF8ScaleOff) + r0;
@@ -276,13 +273,14 @@ int launch_over_expanded(tf_kvpool *pool, int cache, const int32_t *d_pt, int ma
     sh->err = pool->err;
     sh->err_cleared.store(true);
     sh->prof = false;
+    sh->src_pt = d_pt;
+    sh->src_max_pages = max_pages;
 
     DequantParams p;
     p.cache_base = pool->base + (size_t)cache * pool->desc.num_pages * kF8PageBytes;
     p.pt = d_pt;
     p.shadow = shadow;
     p.shadow_pt = spt;
-    p.err = pool->err;
     p.max_pages = max_pages;
     p.num_pages = pool->desc.num_pages;
     p.S = S;

@@ -71,6 +71,9 @@ struct tf_kvpool {
     // the rows into, set up and launched under shadow_mu (calls from several host threads)
     tf_kvpool *shadow = nullptr;
     std::mutex shadow_mu;
+    // of such a view: the table its rows were expanded through, for the page ids that errors name
+    const int32_t *src_pt = nullptr;
+    int32_t src_max_pages = 0;
     ~tf_kvpool() { delete shadow; }
 };
 
@@ -147,7 +150,8 @@ int launch_state_copy_fp8(tf_kvpool *pool, int cache, const int32_t *d_src, cons
                           cudaStream_t st);
 // Rows expanded to BF16 pages in the workspace, stream s from its page h_from[s] on (null: 0), and the
 // attention that `attend` launches over that view (a pool, its page table and the table's width).  A
-// stream's table entries before h_from[s] are not set.
+// stream's table entries before h_from[s] are not set.  A page outside the pool is not expanded and its
+// entry is -1: it is an error only if the attention comes to read it, as without the expansion.
 size_t fp8_shadow_bytes(int S, const int64_t *h_len, const int32_t *h_from = nullptr);
 int launch_over_expanded(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_len,
                          const int32_t *h_from, int S, void *d_ws, size_t ws_bytes, size_t attend_ws, cudaStream_t st,
