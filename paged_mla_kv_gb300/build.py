@@ -18,7 +18,7 @@ LIB = os.path.join(OUT, "libtf_paged_mla.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["pool.cpp", "copy_kernels.cu", "attend.cu", "attend_noalloc.cu", "topk.cu", "fp8.cu", "blocks.cu"]
-HEADERS = ["tf_internal.h", "ptx.cuh"]
+HEADERS = ["tf_internal.h", "ptx.cuh", "per_device.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -51,6 +51,7 @@
 #include <numeric>
 #include <type_traits>
 
+#include "per_device.h"
 #include "ptx.cuh"
 #include "tf_internal.h"
 
@@ -1892,6 +1893,7 @@ struct Plan {
     int64_t total;
     int nranges, rep, nctas;
     size_t slots;   // workspace slots of partials
+    size_t need = 0;   // BLOCKS: slots that the workspace must hold (slots or more)
     int merge = 0;  // BLOCKS: CTAs a unit, in a cluster that merges (0: a combine pass if there are slots)
 };
 
@@ -2186,7 +2188,8 @@ inline int cut_units(const std::vector<int32_t> &nt, int min_tiles, int sms, boo
     return cut_by_limit(nt, seg, lo, sms, b, nullptr);
 }
 
-// clusters[k]: clusters of k CTAs that the device runs at a time.
+// clusters[k]: clusters of k CTAs that the device runs at a time (never more than sms / k).  Null: none; `need`
+// does not depend on them.
 inline Plan plan_blocks(int S, int R, int H, const int64_t *h_len, int max_blk, int sms, const int *clusters,
                         int64_t *rb) {
     Plan pl;
@@ -2206,12 +2209,17 @@ inline Plan plan_blocks(int S, int R, int H, const int64_t *h_len, int max_blk, 
     pl.nranges = cut_units(nt, UNIT_MIN_TILES, sms, true, rb, &cut, &load);
     pl.nctas = pl.nranges;
     pl.slots = cut ? 2 * (size_t)pl.nctas : 0;
-    // few units: k CTAs each, one cluster, for the k that ends first
+    // few units: k CTAs each, one cluster, for the k that ends first; the workspace holds the partials of
+    // every k that could be taken, so its size does not depend on how many clusters the device runs
     int32_t most = 0;
     for (int32_t t : nt) most = std::max(most, t);
+    pl.need = pl.slots;
+    const int64_t uncut = load;
     for (int k = 2; k <= MAX_MERGE && k <= most; ++k) {
         const int64_t l = (most + k - 1) / k + UNIT_SEG_COST + MERGE_COST;
-        if ((int64_t)nt.size() <= clusters[k] && l < load) {
+        if (l >= uncut || (int64_t)nt.size() > sms / k) continue;
+        pl.need = std::max(pl.need, nt.size() * k);
+        if (clusters && (int64_t)nt.size() <= clusters[k] && l < load) {
             load = l;
             pl.merge = k;
         }
@@ -2334,10 +2342,6 @@ static int device_sms() {
     return n < attn::MAX_CTAS ? n : attn::MAX_CTAS;
 }
 
-// Clusters of k = 0 .. MAX_MERGE attention CTAs that the current device runs at a time (0 for k < 2,
-// and without a device).  One resident CTA a SM in every instance, so one instance is asked.
-static const int *device_clusters();
-
 static size_t slots_bytes(size_t slots) {
     if (slots == 0) return 0;
     const size_t o = slots * attn::slot_bytes();
@@ -2371,7 +2375,7 @@ static bool expand_blocks(int S, int R, int H, const int64_t *h_len, int max_blk
 size_t blocks_workspace_bytes(bool fp8, int S, int R, int H, const int64_t *h_len, int max_blk) {
     int64_t rb[attn::MAX_CTAS + 1];
     const size_t part =
-        slots_bytes(attn::plan_blocks(S, R, H, h_len, max_blk, device_sms(), device_clusters(), rb).slots);
+        slots_bytes(attn::plan_blocks(S, R, H, h_len, max_blk, device_sms(), nullptr, rb).need);
     return fp8 && expand_blocks(S, R, H, h_len, max_blk) ? with_expanded(part, fp8_shadow_bytes(S, h_len)) : part;
 }
 
@@ -2539,33 +2543,37 @@ static int ensure_pool_maps(tf_kvpool *pool) {
     return TF_OK;
 }
 
-// Every instance opted in to its shared memory once, whichever host thread comes first.
+// Every instance opted in to its shared memory on the current device.
 static bool attend_ready() {
     using namespace attn;
-    static std::once_flag attr_once;
-    static bool attr_ok = false;
-    std::call_once(attr_once, [] {
-        attr_ok = true;
+    static PerDevice<bool> ready;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    return ready.get(dev, [](bool &v) {
+        v = true;
         for (auto *kern : {mla_attend_kernel<MODE_RANGES>, mla_attend_kernel<MODE_UNITS>, mla_attend_kernel<MODE_SPLITS>,
                            mla_attend_kernel<MODE_SPARSE>, mla_attend_kernel<MODE_BLOCKS>, mla_attend_kernel<MODE_SHARED>,
                            mla_attend_kernel<MODE_RANGES, true>, mla_attend_kernel<MODE_UNITS, true>,
                            mla_attend_kernel<MODE_SPARSE, true>, mla_attend_kernel<MODE_BLOCKS, true>,
                            mla_attend_kernel<MODE_SHARED, true>})
-            attr_ok = attr_ok && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL) ==
-                                     cudaSuccess;
-    });
-    return attr_ok;
+            v = v && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL) == cudaSuccess;
+        if (!v) cudaGetLastError();
+        return v;
+    }) != nullptr;
 }
 
+// Clusters of k = 0 .. MAX_MERGE attention CTAs that the current device runs at a time (0 for k < 2; all 0
+// when it does not answer).  One resident CTA a SM in every instance, so one instance is asked.
+struct Clusters {
+    int n[attn::MAX_MERGE + 1];
+};
 static const int *device_clusters() {
     using namespace attn;
-    static int n[MAX_MERGE + 1] = {};
-    static std::once_flag once;
-    std::call_once(once, [] {
-        if (!attend_ready()) {
-            cudaGetLastError();
-            return;
-        }
+    static PerDevice<Clusters> clusters;
+    static const Clusters none = {};
+    int dev = 0;
+    if (!attend_ready() || cudaGetDevice(&dev) != cudaSuccess) return none.n;
+    const Clusters *c = clusters.get(dev, [](Clusters &v) {
         for (int k = 2; k <= MAX_MERGE; ++k) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3((unsigned)k);
@@ -2577,13 +2585,15 @@ static const int *device_clusters() {
             a.val.clusterDim.y = a.val.clusterDim.z = 1;
             cfg.attrs = &a;
             cfg.numAttrs = 1;
-            int c = 0;
-            if (cudaOccupancyMaxActiveClusters(&c, mla_attend_kernel<MODE_BLOCKS, true>, &cfg) == cudaSuccess) n[k] = c;
-            else cudaGetLastError();
-            n[k] = std::min(n[k], MAX_CTAS / k);   // the bounds' table
+            if (cudaOccupancyMaxActiveClusters(&v.n[k], mla_attend_kernel<MODE_BLOCKS, true>, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                return false;
+            }
+            v.n[k] = std::min(v.n[k], MAX_CTAS / k);   // the bounds' table
         }
+        return true;
     });
-    return n;
+    return c ? c->n : none.n;
 }
 
 // The parameters every mode takes.  Params is large (tensor maps + the per-stream plan); there is
@@ -2765,7 +2775,7 @@ int launch_attend_blocks(tf_kvpool *pool, int cache, const int32_t *d_pt, int ma
     int64_t rb[MAX_CTAS + 1];
     const Plan pl = plan_blocks(S, R, H, h_len, max_blk, device_sms(), device_clusters(), rb);
     const bool expand = is_fp8(pool->desc) && expand_blocks(S, R, H, h_len, max_blk);
-    const size_t part = slots_bytes(pl.slots);
+    const size_t part = slots_bytes(pl.need);
     const int rc = check_workspace(expand ? with_expanded(part, fp8_shadow_bytes(S, h_len)) : part, d_ws, ws_bytes);
     if (rc != TF_OK) return rc;
     if (prepare_launch(pool, st) != TF_OK) return TF_E_CUDA;

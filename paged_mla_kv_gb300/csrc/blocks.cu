@@ -14,8 +14,8 @@
 
 #include <algorithm>
 #include <memory>
-#include <mutex>
 
+#include "per_device.h"
 #include "ptx.cuh"
 #include "tf_internal.h"
 
@@ -708,22 +708,22 @@ __global__ void __launch_bounds__(THREADS, 1) block_scores_kernel(const __grid_c
 
 }  // namespace blk
 
-// The device's SMs, with every kernel opted in to its shared memory; 0 when that failed.
+// The current device's SMs, with every kernel opted in to its shared memory there; 0 when that failed.
 static int device_ready() {
     using namespace blk;
-    static std::once_flag once;
-    static int sms = 0;
-    std::call_once(once, [] {
-        int dev = 0, n = 0;
+    static PerDevice<int> sms;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    const int *n = sms.get(dev, [&](int &v) {
         bool ok = cudaFuncSetAttribute(block_keys_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)sizeof(KeysFp8Shared)) == cudaSuccess;
         for (auto *kern : {block_scores_kernel<32>, block_scores_kernel<8>, block_scores_kernel<4>, block_scores_kernel<1>})
             ok = ok && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL) == cudaSuccess;
-        if (ok && cudaGetDevice(&dev) == cudaSuccess &&
-            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
-            sms = n;
+        ok = ok && cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
+        if (!ok) cudaGetLastError();
+        return ok;
     });
-    return sms;
+    return n ? *n : 0;
 }
 
 int launch_block_keys(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_from,
@@ -748,9 +748,10 @@ int launch_block_keys(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_p
     p.off[S] = n;
     if (n == 0) return TF_OK;
     if (n > 0x7FFFFFFF) return TF_E_UNSUPPORTED;
-    if (f8 && device_ready() <= 0) return TF_E_CUDA;
+    const int sms = f8 ? device_ready() : 0;
+    if (f8 && sms <= 0) return TF_E_CUDA;
     if (prepare_launch(pool, st) != TF_OK) return TF_E_CUDA;
-    const cudaError_t e = f8 ? launch_pdl(block_keys_fp8_kernel, dim3((unsigned)std::min<int64_t>(n, device_ready())),
+    const cudaError_t e = f8 ? launch_pdl(block_keys_fp8_kernel, dim3((unsigned)std::min<int64_t>(n, sms)),
                                           dim3(FTEAMS * FT + 32), sizeof(KeysFp8Shared), st, p)
                              : launch_pdl(block_keys_kernel, dim3((unsigned)n), dim3(KC * KG), 0, st, p);
     launch_counter()++;

@@ -14,9 +14,9 @@
 // level sorts them (a bitonic network: registers, warp shuffles, then shared memory) and writes
 // columns and values.
 #include <cstdint>
-#include <mutex>
 
 #include "../../include/tf_topk.h"
+#include "per_device.h"
 #include "ptx.cuh"
 #include "tf_internal.h"
 
@@ -643,11 +643,12 @@ inline size_t smem_of(void (*k)(Level)) {
     return kSmemBase;
 }
 
-// Opt every instance in to its dynamic shared memory, once.
+// Opt every instance in to its dynamic shared memory on the current device.
 inline bool attributes_set() {
-    static std::once_flag once;
-    static bool ok = false;
-    std::call_once(once, [] {
+    static PerDevice<bool> set;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    return set.get(dev, [](bool &ok) {
         ok = cudaFuncSetAttribute(topk_level_kernel<true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   (int)kSmemFinal) == cudaSuccess &&
              cudaFuncSetAttribute(topk_level_kernel<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -656,8 +657,9 @@ inline bool attributes_set() {
                                   (int)kSmemBase) == cudaSuccess &&
              cudaFuncSetAttribute(topk_level_kernel<false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   (int)kSmemBase) == cudaSuccess;
-    });
-    return ok;
+        if (!ok) cudaGetLastError();
+        return ok;
+    }) != nullptr;
 }
 
 inline Plan plan_of(int64_t n, int k) {
