@@ -49,7 +49,7 @@ extern "C" {
 #define TF_OK 0
 #define TF_E_ARG (-1)          /* a null pointer, a bad size or a bad flag */
 #define TF_E_RANGE (-2)        /* an id, length or position outside what the pool holds */
-#define TF_E_NOMEM (-3)        /* the pool has too few free pages, or a buffer is too small */
+#define TF_E_NOMEM (-3)        /* the pool has too few free pages, a buffer is too small, or host memory ran out */
 #define TF_E_CUDA (-4)         /* a CUDA runtime or driver call failed */
 #define TF_E_TIMEOUT (-5)      /* a kernel's bounded wait ran out (device error word) */
 #define TF_E_UNSUPPORTED (-6)  /* a shape this library does not handle */

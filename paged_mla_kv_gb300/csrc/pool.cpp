@@ -35,12 +35,28 @@ ProfScope::~ProfScope() {
     if (!a || !b) return;
     cudaEventRecord(b, stream);
     std::lock_guard<std::mutex> g(pool->mu);
-    pool->recs.push_back(ProfRec{kind, a, b});
+    try {
+        pool->recs.push_back(ProfRec{kind, a, b});
+    } catch (...) {   // this launch is not counted
+        cudaEventDestroy(a);
+        cudaEventDestroy(b);
+    }
 }
 
 }  // namespace tf
 
 using namespace tf;
+
+// Plans, page bookkeeping and a host thread's first launch take host memory, and no exception leaves a C
+// entry: what runs out of it returns TF_E_NOMEM.
+template <typename F>
+static int no_throw(F &&f) {
+    try {
+        return f();
+    } catch (...) {
+        return TF_E_NOMEM;
+    }
+}
 
 static bool desc_ok(const tf_kvpool_desc *d) {
     // the poison and state-copy launches put the caches on the grid's y dimension (at most 65,535)
@@ -76,8 +92,15 @@ extern "C" int tf_kvpool_create(const tf_kvpool_desc *d, void *dev_base, size_t 
     p->base = static_cast<char *>(dev_base);
     p->bytes = dev_bytes;
     p->err = reinterpret_cast<DevErr *>(p->base + need - kCtrlBytes);
-    p->refcnt.assign(d->num_pages, 0);
-    p->free_ring.resize(d->num_pages);
+    const int rc = no_throw([&] {
+        p->refcnt.assign(d->num_pages, 0);
+        p->free_ring.resize(d->num_pages);
+        return TF_OK;
+    });
+    if (rc != TF_OK) {
+        delete p;
+        return rc;
+    }
     for (int i = 0; i < d->num_pages; ++i) p->free_ring[i] = i;
     if (d->seed) {  // Fisher-Yates with a seeded mixer
         uint64_t st = d->seed;
@@ -132,24 +155,24 @@ extern "C" int tf_kvpool_ref(tf_kvpool *p, const int32_t *ids, int32_t n) {
 
 extern "C" int tf_kvpool_release(tf_kvpool *p, const int32_t *ids, int32_t n) {
     if (!p || n < 0 || (n > 0 && !ids)) return TF_E_ARG;
-    std::lock_guard<std::mutex> g(p->mu);
-    // check first (a repeated id must hold as many references as it appears)
-    std::vector<int32_t> need;
-    for (int i = 0; i < n; ++i) {
-        if (ids[i] < 0 || ids[i] >= p->desc.num_pages) return TF_E_RANGE;
-        need.push_back(ids[i]);
-    }
-    std::vector<int32_t> cnt(p->refcnt);
-    for (int32_t id : need)
-        if (--cnt[id] < 0) return TF_E_RANGE;
-    const size_t N = p->free_ring.size();
-    for (int32_t id : need) {
-        if (--p->refcnt[id] == 0) {
-            p->free_ring[(p->free_head + p->free_count) % N] = id;
-            p->free_count++;
+    return no_throw([&] {
+        std::lock_guard<std::mutex> g(p->mu);
+        // check first (a repeated id must hold as many references as it appears)
+        for (int i = 0; i < n; ++i)
+            if (ids[i] < 0 || ids[i] >= p->desc.num_pages) return TF_E_RANGE;
+        std::vector<int32_t> cnt(p->refcnt);
+        for (int i = 0; i < n; ++i)
+            if (--cnt[ids[i]] < 0) return TF_E_RANGE;
+        const size_t N = p->free_ring.size();
+        for (int i = 0; i < n; ++i) {
+            const int32_t id = ids[i];
+            if (--p->refcnt[id] == 0) {
+                p->free_ring[(p->free_head + p->free_count) % N] = id;
+                p->free_count++;
+            }
         }
-    }
-    return TF_OK;
+        return TF_OK;
+    });
 }
 
 extern "C" int32_t tf_kvpool_free_pages(const tf_kvpool *p) { return p ? (int32_t)p->free_count : -1; }
@@ -225,10 +248,15 @@ extern "C" size_t tf_paged_mla_workspace_bytes(const tf_kvpool *p, int32_t S, in
     for (int s = 0; s < S; ++s)
         if (h_len[s] < R || h_len[s] > kMaxStreamRows) return 0;
     const bool invariant = p && (p->desc.flags & TF_POOL_BATCH_INVARIANT);
-    const size_t part = attend_workspace_bytes(invariant, S, R, H, h_len);
+    size_t n = 0;
+    const int rc = no_throw([&] {
+        n = attend_workspace_bytes(invariant, S, R, H, h_len);
+        return TF_OK;
+    });
+    if (rc != TF_OK) return 0;
     // FP8 pages on a batch-invariant pool are expanded to bf16 in the workspace first
-    if (p && is_fp8(p->desc) && invariant) return (part + 1023) / 1024 * 1024 + fp8_shadow_bytes(S, h_len);
-    return part;
+    if (p && is_fp8(p->desc) && invariant) return (n + 1023) / 1024 * 1024 + fp8_shadow_bytes(S, h_len);
+    return n;
 }
 
 extern "C" int tf_paged_mla_plan_info(int32_t S, int32_t R, int32_t H, const int64_t *h_len, int32_t sms,
@@ -238,7 +266,8 @@ extern "C" int tf_paged_mla_plan_info(int32_t S, int32_t R, int32_t H, const int
     if ((int64_t)S * R * H > (int64_t)1 << 30) return TF_E_UNSUPPORTED;   // as tf_paged_mla_attend
     for (int s = 0; s < S; ++s)
         if (h_len[s] < R || h_len[s] > kMaxStreamRows) return TF_E_RANGE;
-    return attend_plan_info(S, R, H, h_len, sms, invariant != 0, info, range_bounds, split_keys);
+    return no_throw(
+        [&] { return attend_plan_info(S, R, H, h_len, sms, invariant != 0, info, range_bounds, split_keys); });
 }
 
 extern "C" int tf_paged_mla_attend(tf_kvpool *p, int32_t cache, const int32_t *d_pt, int32_t max_pages,
@@ -258,20 +287,21 @@ extern "C" int tf_paged_mla_attend(tf_kvpool *p, int32_t cache, const int32_t *d
         if (h_len[s] > kMaxStreamRows) return TF_E_UNSUPPORTED;
     if ((reinterpret_cast<uintptr_t>(d_q) & 15u) != 0 || (reinterpret_cast<uintptr_t>(d_out) & 15u) != 0)
         return TF_E_ARG;
-    const bool invariant = (p->desc.flags & TF_POOL_BATCH_INVARIANT) != 0;
-    const size_t part = attend_workspace_bytes(invariant, S, R, H, h_len);
-    const bool expand = is_fp8(p->desc) && invariant;   // else FP8 codes are expanded in the kernel
-    const size_t need = expand ? (part + 1023) / 1024 * 1024 + fp8_shadow_bytes(S, h_len) : part;
-    if (need > 0 && (!d_ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0))
-        return d_ws && ws_bytes < need ? TF_E_NOMEM : TF_E_ARG;
-    if (expand)
-        return launch_attend_fp8(p, cache, d_pt, max_pages, h_len, S, R, H, d_q, scale, d_out, d_lse, d_ws, ws_bytes,
-                                 part, (cudaStream_t)stream);
-    return launch_attend(p, cache, d_pt, max_pages, h_len, S, R, H, d_q, scale, d_out, d_lse, d_ws, ws_bytes,
-                         (cudaStream_t)stream);
+    return no_throw([&] {
+        const bool invariant = (p->desc.flags & TF_POOL_BATCH_INVARIANT) != 0;
+        const size_t part = attend_workspace_bytes(invariant, S, R, H, h_len);
+        const bool expand = is_fp8(p->desc) && invariant;   // else FP8 codes are expanded in the kernel
+        const size_t need = expand ? (part + 1023) / 1024 * 1024 + fp8_shadow_bytes(S, h_len) : part;
+        if (need > 0 && (!d_ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0))
+            return d_ws && ws_bytes < need ? TF_E_NOMEM : TF_E_ARG;
+        if (expand)
+            return launch_attend_fp8(p, cache, d_pt, max_pages, h_len, S, R, H, d_q, scale, d_out, d_lse, d_ws, ws_bytes,
+                                     part, (cudaStream_t)stream);
+        return launch_attend(p, cache, d_pt, max_pages, h_len, S, R, H, d_q, scale, d_out, d_lse, d_ws, ws_bytes,
+                             (cudaStream_t)stream);
+    });
 }
 
-// ---- kept-state copy ----
 // ---- attention over listed rows ----
 static int sparse_checks(const tf_kvpool *p, int32_t S, int32_t H, int32_t max_idx, const int32_t *h_nidx) {
     if (S < 1 || S > TF_MAX_STREAMS || H < 1 || H > TF_MAX_HEADS || max_idx < 1 || !h_nidx) return TF_E_ARG;
@@ -311,8 +341,10 @@ extern "C" int tf_paged_mla_attend_sparse(tf_kvpool *p, int32_t cache, const int
     const size_t need = attend_workspace_bytes(false, S, 1, H, n, true);
     if (need > 0 && (!d_ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0))
         return d_ws && ws_bytes < need ? TF_E_NOMEM : TF_E_ARG;
-    return launch_attend(p, cache, d_pt, max_pages, h_len, S, 1, H, d_q, scale, d_out, d_lse, d_ws, ws_bytes,
-                         (cudaStream_t)stream, d_idx, max_idx, h_nidx);
+    return no_throw([&] {
+        return launch_attend(p, cache, d_pt, max_pages, h_len, S, 1, H, d_q, scale, d_out, d_lse, d_ws, ws_bytes,
+                             (cudaStream_t)stream, d_idx, max_idx, h_nidx);
+    });
 }
 
 // ---- attention over listed blocks, and of streams that share a prefix ----
@@ -339,16 +371,6 @@ static int call_checks(const tf_kvpool *p, int32_t cache, const int32_t *d_pt, i
     if ((reinterpret_cast<uintptr_t>(d_q) & 15u) != 0 || (reinterpret_cast<uintptr_t>(d_out) & 15u) != 0)
         return TF_E_ARG;
     return TF_OK;
-}
-
-// Host arithmetic on caller sizes allocates (the plan's unit table), and no exception leaves a C entry.
-template <typename F>
-static int no_throw(F &&f) {
-    try {
-        return f();
-    } catch (const std::bad_alloc &) {
-        return TF_E_NOMEM;
-    }
 }
 
 static int blocks_checks(int32_t S, int32_t R, int32_t H, const int64_t *h_len, int32_t max_blk) {
@@ -454,10 +476,13 @@ extern "C" int tf_block_scores(tf_kvpool *p, const void *d_bkeys, const int32_t 
     int64_t cols = 0;
     for (int s = 0; s < S; ++s) cols = std::max(cols, (h_len[s] + TF_BLOCK_ROWS - 1) / TF_BLOCK_ROWS);
     if (ld % 4 != 0 || ld < cols) return TF_E_ARG;
-    return launch_block_scores(p, d_bkeys, d_pt, max_pages, h_len, S, R, H, d_q, d_w, scale, sink, local, d_scores, ld,
-                               d_nblk, (cudaStream_t)stream);
+    return no_throw([&] {
+        return launch_block_scores(p, d_bkeys, d_pt, max_pages, h_len, S, R, H, d_q, d_w, scale, sink, local, d_scores,
+                                   ld, d_nblk, (cudaStream_t)stream);
+    });
 }
 
+// ---- kept-state copy ----
 extern "C" int tf_state_copy_rows(tf_kvpool *p, int32_t cache, const int32_t *d_src, const int32_t *d_dst,
                                   int64_t at, void *stream) {
     if (!p || at < 0) return TF_E_ARG;
@@ -501,6 +526,12 @@ extern "C" int tf_profile_read(tf_kvpool *p, int32_t kind, double *total_ms, int
     double tot = 0.0;
     int64_t cnt = 0;
     std::vector<ProfRec> keep;
+    const int rc = no_throw([&] {
+        keep.reserve(p->recs.size());
+        p->spare_events.reserve(p->spare_events.size() + 2 * p->recs.size());
+        return TF_OK;
+    });
+    if (rc != TF_OK) return rc;
     for (auto &r : p->recs) {
         if (r.kind != kind) {
             keep.push_back(r);
