@@ -204,6 +204,7 @@ class KVPool:
             import torch
             memory = torch.empty(self.bytes + 1024, dtype=torch.uint8, device=device or "cuda")
         self.memory = memory
+        self.device = memory.get_device()   # the GPU that holds the pool
         base = memory.data_ptr()
         off = (-base) % 1024
         self.base = base + off
@@ -369,7 +370,8 @@ TF_BLOCK_ROWS = 64
 
 
 # What the library cannot see is refused here: host arrays of another length, tensors of another type,
-# size or layout.  A check is on every call's path, so it asks for as little as it can.
+# size or layout, tensors that do not lie on the pool's GPU.  A check is on every call's path, so it asks
+# for as little as it can.
 _types = None
 
 
@@ -382,7 +384,15 @@ def _dtypes():
 
 
 def _refuse(what: str):
-    raise TFError(TF_E_ARG, what)
+    raise TFError(TF_E_ARG, what + " (an argument's form)")
+
+
+def _elsewhere(what: str):
+    raise TFError(TF_E_ARG, what + " (a tensor that is not on the pool's device)")
+
+
+def _on(dev: int, t) -> bool:
+    return t is None or t.get_device() == dev
 
 
 def _dense(t, dtype, n: int) -> bool:
@@ -412,6 +422,9 @@ def tf_block_keys_update(pool: KVPool, cache: int, pt, max_pages: int, start, le
     bf16, _, i32 = _dtypes()
     if not (len(a) == len(b) and _dense(bkeys, bf16, pool.num_pages * 4608) and _table(pt, max_pages, len(b), i32)):
         _refuse("tf_block_keys_update")
+    dev = pool.device
+    if bkeys.get_device() != dev or not (pt is None or pt.get_device() == dev):
+        _elsewhere("tf_block_keys_update")
     _check(lib().tf_block_keys_update(pool.handle, cache, _ptr(pt), max_pages, p, pl, len(b), bkeys.data_ptr(),
                                       _stream(stream)), "tf_block_keys_update")
 
@@ -430,6 +443,11 @@ def tf_block_scores(pool: KVPool, bkeys, pt, max_pages: int, lens, q, scale: flo
             scores.dtype is f32 and rows == S * R and (one == 1 or cols == 1) and _table(pt, max_pages, S, i32) and
             S > 0 and cols * TF_BLOCK_ROWS >= (max(a) if type(a) is array.array else a.max())):
         _refuse("tf_block_scores")
+    dev = pool.device
+    if not (q.get_device() == dev and bkeys.get_device() == dev and scores.get_device() == dev and
+            (pt is None or pt.get_device() == dev) and (nblk is None or nblk.get_device() == dev) and
+            (w is None or w.get_device() == dev)):
+        _elsewhere("tf_block_scores")
     _check(lib().tf_block_scores(pool.handle, bkeys.data_ptr(), _ptr(pt), max_pages, p, S, R, H, q.data_ptr(), _ptr(w),
                                  scale, sink, local, scores.data_ptr(), ld, _ptr(nblk), _stream(stream)),
            "tf_block_scores")
@@ -454,6 +472,10 @@ def tf_paged_mla_attend_blocks(pool: KVPool, cache: int, pt, max_pages: int, len
     if not (len(a) == S and _qout(q, out, lse, S * R * H, bf16, f32) and _dense(blk, i32, S * R * max_blk) and
             _table(pt, max_pages, S, i32)):
         _refuse("tf_paged_mla_attend_blocks")
+    dev = pool.device
+    if not (q.get_device() == dev and out.get_device() == dev and blk.get_device() == dev and _on(dev, pt) and
+            _on(dev, lse) and _on(dev, ws)):
+        _elsewhere("tf_paged_mla_attend_blocks")
     _check(lib().tf_paged_mla_attend_blocks(pool.handle, cache, _ptr(pt), max_pages, p, blk.data_ptr(), max_blk, S, R, H,
                                             q.data_ptr(), scale, out.data_ptr(), _ptr(lse), _ptr(ws),
                                             0 if ws is None else ws.nbytes, _stream(stream)),
@@ -482,6 +504,9 @@ def tf_paged_mla_attend_shared(pool: KVPool, cache: int, pt, max_pages: int, len
     if not (len(a) == S and len(g) == len(f) and _qout(q, out, lse, S * R * H, bf16, f32) and
             _table(pt, max_pages, S, i32)):
         _refuse("tf_paged_mla_attend_shared")
+    dev = pool.device
+    if not (q.get_device() == dev and out.get_device() == dev and _on(dev, pt) and _on(dev, lse) and _on(dev, ws)):
+        _elsewhere("tf_paged_mla_attend_shared")
     _check(lib().tf_paged_mla_attend_shared(pool.handle, cache, _ptr(pt), max_pages, p, pg, len(g), pf, S, R, H,
                                             q.data_ptr(), scale, out.data_ptr(), _ptr(lse), _ptr(ws),
                                             0 if ws is None else ws.nbytes, _stream(stream)),
