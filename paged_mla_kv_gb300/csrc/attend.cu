@@ -2090,58 +2090,100 @@ constexpr int UNIT_MIN_TILES = 2;
 // more with more columns), or a cluster's merge.  Measured: 64 streams of 32 tiles in clusters of 2 take
 // 37.3 us against 39.6 with a combine pass, 16 units of 16 tiles in clusters of 8 16.3 against 18.0; one
 // stream of 32 tiles takes 16.5 us in a cluster of 8 and 13.5 on 16 CTAs with a combine pass.
-inline int64_t combine_cost(size_t units) { return 4 + std::min<int64_t>(3, (int64_t)units / 16); }
+inline int64_t combine_cost(int64_t units) { return 4 + std::min<int64_t>(3, units / 16); }
 constexpr int64_t MERGE_COST = 4;
 
-// Ranges over units of nt[u] tiles (no tile: no unit), cut anywhere: bound i at weighted position
-// i W / n, a unit's start weighing `seg` tiles (a bound that falls into that weight moves to the
-// unit's start).  Writes b[0..n] as unit_pos values and returns n; *cut: a bound inside a unit.
-inline int cut_evenly(const std::vector<int32_t> &nt, int64_t seg, int min_tiles, int sms, int64_t *b, bool *cut) {
-    const int64_t units = (int64_t)nt.size();
-    int64_t W = 0, tiles = 0;
-    for (int32_t t : nt) tiles += t;
-    W = tiles + seg * units;
-    const int64_t want = (tiles + min_tiles - 1) / min_tiles;
+// Units of a plan, in order: runs of units that have equally many tiles (at least one).  A stream's query
+// rows take few block counts, and a shared call's entry one, so a plan is small whatever the batch.
+struct Units {
+    struct Run {
+        int64_t units, nt;
+    };
+    std::vector<Run> runs;
+    int64_t units = 0, tiles = 0, most = 0;   // in all; the largest unit's tiles
+    void add(int64_t n, int64_t nt) {
+        if (n <= 0) return;
+        if (!runs.empty() && runs.back().nt == nt) runs.back().units += n;
+        else runs.push_back(Run{n, nt});
+        units += n;
+        tiles += n * nt;
+        most = std::max(most, nt);
+    }
+    // f(first unit, units, tiles of each) for every run
+    template <typename F>
+    void each(F &&f) const {
+        int64_t u = 0;
+        for (const Run &r : runs) {
+            f(u, r.units, r.nt);
+            u += r.units;
+        }
+    }
+};
+
+// Ranges over units, cut anywhere: bound i at weighted position i W / n, a unit's start weighing `seg`
+// tiles (a bound that falls into that weight moves to the unit's start).  Writes b[0..n] as unit_pos
+// values and returns n; *cut: a bound inside a unit; *load: the largest range's tiles and segments.
+inline int cut_evenly(const Units &all, int64_t seg, int min_tiles, int sms, int64_t *b, bool *cut, int64_t *load) {
+    const int64_t W = all.tiles + seg * all.units;
+    const int64_t want = (all.tiles + min_tiles - 1) / min_tiles;
     int n = (int)(want < sms ? want : sms);
     if (n < 1) n = 1;
     *cut = false;
+    *load = 0;
     b[0] = 0;
-    int64_t u = 0, w = 0;   // unit u starts at weight w
+    int64_t u = 0, w = 0;   // the run's first unit and its weight
+    size_t r = 0;
     int m = 0;              // bounds written
+    int64_t last = 0;       // weight of the last bound, a cut unit's segment counted again
     for (int i = 1; i < n; ++i) {
         const int64_t tau = i * W / n;
-        while (w + seg + nt[u] <= tau) w += seg + nt[u++];
-        const int64_t t = tau - w - seg;
-        const int64_t x = t > 0 ? unit_pos(u, t) : unit_pos(u, 0);
+        while (w + all.runs[r].units * (seg + all.runs[r].nt) <= tau) {
+            w += all.runs[r].units * (seg + all.runs[r].nt);
+            u += all.runs[r++].units;
+        }
+        const int64_t whole = (tau - w) / (seg + all.runs[r].nt);
+        const int64_t v = u + whole, at = w + whole * (seg + all.runs[r].nt);   // the unit, and its weight
+        const int64_t t = tau - at - seg;
+        const int64_t x = unit_pos(v, t > 0 ? t : 0);
         if (x <= b[m]) continue;   // no empty range
         b[++m] = x;
         *cut |= t > 0;
+        *load = std::max(*load, at + (t > 0 ? seg + t : 0) - last);
+        last = at + (t > 0 ? t : 0);
     }
-    b[++m] = unit_pos(units, 0);
+    b[++m] = unit_pos(all.units, 0);
+    *load = std::max(*load, W - last);
     return m;
 }
 
 // The same with a unit cut only if it does not fit a range, and then into equal parts that are ranges
 // of their own; smaller units share a range, whole, while it holds them.  Ranges hold at most `lim`
 // (tiles + seg a segment).  Returns the ranges, sms + 1 if there are more than sms; b may be null.
-inline int cut_by_limit(const std::vector<int32_t> &nt, int64_t seg, int64_t lim, int sms, int64_t *b, bool *cut) {
+inline int cut_by_limit(const Units &all, int64_t seg, int64_t lim, int sms, int64_t *b, bool *cut) {
     int n = 0;
     int64_t load = 0;   // of the range that is open (0: none)
-    for (int64_t u = 0; u < (int64_t)nt.size(); ++u) {
-        const int64_t t = nt[u];
-        if (load > 0 && load + t + seg <= lim) {
-            load += t + seg;
-            continue;
+    int64_t u = 0;
+    for (const Units::Run &r : all.runs) {
+        const int64_t t = r.nt, k = (t + lim - seg - 1) / (lim - seg);   // parts
+        int64_t left = r.units;
+        if (k == 1 && load > 0) {   // what the open range still holds
+            const int64_t more = std::min(left, (lim - load) / (t + seg));
+            load += more * (t + seg);
+            left -= more;
         }
-        const int64_t k = (t + lim - seg - 1) / (lim - seg);   // parts
-        if (n + k > sms) return sms + 1;
-        for (int64_t i = 0; i < k; ++i)
-            if (b) b[n + i] = unit_pos(u, t * i / k);
-        n += (int)k;
-        if (k > 1 && cut) *cut = true;
-        load = k > 1 ? lim : t + seg;
+        const int64_t per = k == 1 ? lim / (t + seg) : 1;   // units a range
+        const int64_t steps = (left + per - 1) / per;
+        if (steps > sms || n + steps * k > sms) return sms + 1;
+        for (int64_t j = 0; b && j < steps; ++j)
+            for (int64_t i = 0; i < k; ++i) b[n + j * k + i] = unit_pos(u + r.units - left + j * per, t * i / k);
+        if (steps > 0) {
+            n += (int)(steps * k);
+            load = k > 1 ? lim : (left - (steps - 1) * per) * (t + seg);
+            if (k > 1 && cut) *cut = true;
+        }
+        u += r.units;
     }
-    if (b) b[n] = unit_pos((int64_t)nt.size(), 0);
+    if (b) b[n] = unit_pos(all.units, 0);
     return n;
 }
 
@@ -2153,39 +2195,26 @@ inline int cut_by_limit(const std::vector<int32_t> &nt, int64_t seg, int64_t lim
 // limit are taken (listed blocks, which decode reads from HBM: fewer partials; 64 streams of 32 blocks
 // 39.6 us against 42.3), else the even cuts (shared prefixes, bound by the products: eight streams of
 // 64 heads behind 8,192 rows 25 us against 27).
-inline int cut_units(const std::vector<int32_t> &nt, int min_tiles, int sms, bool limit_ties, int64_t *b, bool *cut,
-                     int64_t *largest) {
+inline int cut_units(const Units &all, int min_tiles, int sms, bool limit_ties, int64_t *b, bool *cut, int64_t *largest) {
     const int64_t seg = UNIT_SEG_COST;
-    int64_t tiles = 0, most = 0;
-    for (int32_t t : nt) {
-        tiles += t;
-        most = std::max<int64_t>(most, t);
-    }
-    const int n = cut_evenly(nt, seg, min_tiles, sms, b, cut);
     int64_t load = 0;
-    for (int i = 0; i < n; ++i) {   // tiles and segments of [b[i], b[i + 1])
-        int64_t u = b[i] >> 32, t = b[i] & 0xffffffffll, w = 0;
-        const int64_t ue = b[i + 1] >> 32, te = b[i + 1] & 0xffffffffll;
-        for (; u < ue; ++u, t = 0) w += nt[u] - t + seg;
-        if (te > t) w += te - t + seg;
-        load = std::max(load, w);
-    }
-    *largest = load + (*cut ? combine_cost(nt.size()) : 0);
+    const int n = cut_evenly(all, seg, min_tiles, sms, b, cut, &load);
+    *largest = load + (*cut ? combine_cost(all.units) : 0);
     // the smallest limit that needs at most sms ranges and cuts nothing below min_tiles
-    int64_t lo = std::max<int64_t>(seg + std::min<int64_t>(most, min_tiles), (tiles + sms - 1) / sms + seg);
+    int64_t lo = std::max<int64_t>(seg + std::min<int64_t>(all.most, min_tiles), (all.tiles + sms - 1) / sms + seg);
     int64_t hi = *largest - (limit_ties ? 0 : 1);
-    if (lo > hi || cut_by_limit(nt, seg, hi, sms, nullptr, nullptr) > sms) return n;
+    if (lo > hi || cut_by_limit(all, seg, hi, sms, nullptr, nullptr) > sms) return n;
     while (lo < hi) {
         const int64_t mid = lo + (hi - lo) / 2;
-        if (cut_by_limit(nt, seg, mid, sms, nullptr, nullptr) <= sms) hi = mid; else lo = mid + 1;
+        if (cut_by_limit(all, seg, mid, sms, nullptr, nullptr) <= sms) hi = mid; else lo = mid + 1;
     }
     bool c2 = false;
-    cut_by_limit(nt, seg, lo, sms, nullptr, &c2);
-    const int64_t cost = lo + (c2 ? combine_cost(nt.size()) : 0);
+    cut_by_limit(all, seg, lo, sms, nullptr, &c2);
+    const int64_t cost = lo + (c2 ? combine_cost(all.units) : 0);
     if (cost > *largest - (limit_ties ? 0 : 1)) return n;
     *largest = cost;
     *cut = c2;
-    return cut_by_limit(nt, seg, lo, sms, b, nullptr);
+    return cut_by_limit(all, seg, lo, sms, b, nullptr);
 }
 
 // clusters[k]: clusters of k CTAs that the device runs at a time (never more than sms / k).  Null: none; `need`
@@ -2194,41 +2223,41 @@ inline Plan plan_blocks(int S, int R, int H, const int64_t *h_len, int max_blk, 
                         int64_t *rb) {
     Plan pl;
     const int hg = (H + NCOL - 1) / NCOL;
-    std::vector<int32_t> nt((size_t)S * R * hg);
-    size_t u = 0;
+    Units all;
     for (int s = 0; s < S; ++s)
-        for (int r = 0; r < R; ++r) {
-            const int32_t n = (int32_t)row_blocks(h_len[s] - R + r, max_blk);
-            for (int h = 0; h < hg; ++h) nt[u++] = n;
+        for (int64_t r = 0, e; r < R; r = e) {   // rows [r, e) take equally many blocks
+            const int64_t pos = h_len[s] - R + r, n = row_blocks(pos, max_blk);
+            e = n == max_blk ? R : std::min<int64_t>(R, r + BK - pos % BK);
+            all.add((e - r) * hg, n);
         }
     bool cut = false;
     pl.mode = MODE_BLOCKS;
-    pl.total = (int64_t)nt.size();
+    pl.total = all.units;
     pl.rep = 1;
     int64_t load = 0;
-    pl.nranges = cut_units(nt, UNIT_MIN_TILES, sms, true, rb, &cut, &load);
+    pl.nranges = cut_units(all, UNIT_MIN_TILES, sms, true, rb, &cut, &load);
     pl.nctas = pl.nranges;
     pl.slots = cut ? 2 * (size_t)pl.nctas : 0;
     // few units: k CTAs each, one cluster, for the k that ends first; the workspace holds the partials of
     // every k that could be taken, so its size does not depend on how many clusters the device runs
-    int32_t most = 0;
-    for (int32_t t : nt) most = std::max(most, t);
     pl.need = pl.slots;
     const int64_t uncut = load;
-    for (int k = 2; k <= MAX_MERGE && k <= most; ++k) {
-        const int64_t l = (most + k - 1) / k + UNIT_SEG_COST + MERGE_COST;
-        if (l >= uncut || (int64_t)nt.size() > sms / k) continue;
-        pl.need = std::max(pl.need, nt.size() * k);
-        if (clusters && (int64_t)nt.size() <= clusters[k] && l < load) {
+    for (int k = 2; k <= MAX_MERGE && k <= all.most; ++k) {
+        const int64_t l = (all.most + k - 1) / k + UNIT_SEG_COST + MERGE_COST;
+        if (l >= uncut || all.units > sms / k) continue;
+        pl.need = std::max(pl.need, (size_t)all.units * k);
+        if (clusters && all.units <= clusters[k] && l < load) {
             load = l;
             pl.merge = k;
         }
     }
     if (pl.merge) {
-        for (size_t v = 0; v < nt.size(); ++v)
-            for (int i = 0; i < pl.merge; ++i) rb[v * pl.merge + i] = unit_pos((int64_t)v, (int64_t)nt[v] * i / pl.merge);
-        pl.nranges = pl.nctas = (int)nt.size() * pl.merge;
-        rb[pl.nranges] = unit_pos((int64_t)nt.size(), 0);
+        all.each([&](int64_t u, int64_t units, int64_t nt) {
+            for (int64_t v = u; v < u + units; ++v)
+                for (int i = 0; i < pl.merge; ++i) rb[v * pl.merge + i] = unit_pos(v, nt * i / pl.merge);
+        });
+        pl.nranges = pl.nctas = (int)all.units * pl.merge;
+        rb[pl.nranges] = unit_pos(all.units, 0);
         pl.slots = (size_t)pl.nctas;
     }
     return pl;
@@ -2238,7 +2267,7 @@ inline Plan plan_blocks(int S, int R, int H, const int64_t *h_len, int max_blk, 
 // each stream's own.  order[s]: the entry of stream s's shared rows or -1.  Returns the entries, or -1
 // when they pass the table.
 inline int shared_entries(int S, int R, int H, const int64_t *h_len, const int32_t *h_gsize, int G,
-                          const int64_t *h_prefix, SharedEntry *e, int16_t *order, std::vector<int32_t> *nt) {
+                          const int64_t *h_prefix, SharedEntry *e, int16_t *order, Units *all) {
     const int ncols = R * H;
     const int groups = (ncols + NCOL - 1) / NCOL;
     const bool split = ncols % NCOL != 0;   // shared rows are entries of their own
@@ -2264,21 +2293,21 @@ inline int shared_entries(int S, int R, int H, const int64_t *h_len, const int32
         if (e[i].nt == 0) continue;
         const int k = i < S ? groups : (e[i].ncols + NCOL - 1) / NCOL;
         units += k;
-        if (nt) nt->insert(nt->end(), k, e[i].nt);
+        if (all) all->add(k, e[i].nt);
     }
     return n;
 }
 
-inline Plan plan_shared(const std::vector<int32_t> &nt, int nshared, int sms, int64_t *rb) {
+inline Plan plan_shared(const Units &all, int nshared, int sms, int64_t *rb) {
     Plan pl;
     bool cut = false;
     pl.mode = MODE_SHARED;
-    pl.total = (int64_t)nt.size();
+    pl.total = all.units;
     pl.rep = 1;
     int64_t load = 0;
-    pl.nranges = cut_units(nt, UNIT_MIN_TILES, sms, false, rb, &cut, &load);
+    pl.nranges = cut_units(all, UNIT_MIN_TILES, sms, false, rb, &cut, &load);
     pl.nctas = pl.nranges;
-    pl.slots = nshared > 0 ? nt.size() + (size_t)pl.nctas : cut ? 2 * (size_t)pl.nctas : 0;
+    pl.slots = nshared > 0 ? (size_t)all.units + (size_t)pl.nctas : cut ? 2 * (size_t)pl.nctas : 0;
     return pl;
 }
 
@@ -2397,11 +2426,11 @@ int shared_workspace_bytes(bool fp8, int S, int R, int H, const int64_t *h_len, 
                            const int64_t *h_prefix, size_t *bytes) {
     attn::SharedEntry e[TF_MAX_STREAMS];
     int16_t order[TF_MAX_STREAMS];
-    std::vector<int32_t> nt;
-    const int n = attn::shared_entries(S, R, H, h_len, h_gsize, G, h_prefix, e, order, &nt);
+    attn::Units all;
+    const int n = attn::shared_entries(S, R, H, h_len, h_gsize, G, h_prefix, e, order, &all);
     if (n < 0) return TF_E_UNSUPPORTED;
     int64_t rb[attn::MAX_CTAS + 1];
-    *bytes = slots_bytes(attn::plan_shared(nt, n - S, device_sms(), rb).slots);
+    *bytes = slots_bytes(attn::plan_shared(all, n - S, device_sms(), rb).slots);
     int32_t from[TF_MAX_STREAMS];
     if (fp8 && expand_shared(S, h_gsize, G, e, n, from))
         *bytes = with_expanded(*bytes, fp8_shadow_bytes(S, h_len, from));
@@ -2809,11 +2838,11 @@ int launch_attend_shared(tf_kvpool *pool, int cache, const int32_t *d_pt, int ma
     using namespace attn;
     SharedEntry e[TF_MAX_STREAMS];
     int16_t order[TF_MAX_STREAMS];
-    std::vector<int32_t> nt;
-    const int n = shared_entries(S, R, H, h_len, h_gsize, G, h_prefix, e, order, &nt);
+    Units all;
+    const int n = shared_entries(S, R, H, h_len, h_gsize, G, h_prefix, e, order, &all);
     if (n < 0) return TF_E_UNSUPPORTED;
     int64_t rb[MAX_CTAS + 1];
-    const Plan pl = plan_shared(nt, n - S, device_sms(), rb);
+    const Plan pl = plan_shared(all, n - S, device_sms(), rb);
     int32_t from[TF_MAX_STREAMS];
     const bool expand = is_fp8(pool->desc) && expand_shared(S, h_gsize, G, e, n, from);
     const size_t part = slots_bytes(pl.slots);
