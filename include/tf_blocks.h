@@ -127,6 +127,33 @@ int tf_paged_mla_attend_shared(tf_kvpool *pool, int32_t cache, const int32_t *d_
                                int32_t R, int32_t H, const void *d_q, float scale, void *d_out, float *d_lse, void *d_ws,
                                size_t ws_bytes, void *cuda_stream);
 
+/* ---- the work plans of the two attention calls, for inspection ----
+ * Host arithmetic only, nothing launched.  sms > 0: for a device of that many SMs (at most
+ * TF_PLAN_MAX_RANGES) that runs sms / k clusters of k CTAs at a time; sms <= 0: the current device, as the
+ * calls do (without one: TF_PLAN_MAX_RANGES SMs and no clusters).
+ * A unit is a group of at most 64 columns over its key tiles: of blocks, unit (s * R + r) * ceil(H / 64) + g is
+ * head group g of query row r of stream s, a tile a block; of shared prefixes they are numbered entry by
+ * entry (the streams' own rows, then the groups' shared rows where R * H is not a multiple of 64), an entry
+ * without tiles having none.
+ *   info->ctas   CTAs; CTA i takes the unit tiles from range_bounds[i] up to range_bounds[i + 1], each a unit in
+ *                the upper 32 bits and a tile of it in the lower ones
+ *   info->merge  CTAs of a unit that a cluster merges (0: ranges; what they cut is merged by a second launch)
+ *   info->cut    1 if some bound lies inside a unit
+ *   info->units  units
+ *   info->slots  64-column slots of fp32 partials that the workspace holds
+ * range_bounds: int64 [TF_PLAN_MAX_RANGES + 1], or NULL.
+ * Errors: TF_E_ARG for a null info, and what the calls' workspace sizes refuse. */
+typedef struct {
+    int32_t ctas, merge, cut, pad;
+    int64_t units, slots;
+} tf_unit_plan;
+
+int tf_paged_mla_blocks_plan_info(int32_t S, int32_t R, int32_t H, const int64_t *h_len, int32_t max_blk, int32_t sms,
+                                  tf_unit_plan *info, int64_t *range_bounds);
+
+int tf_paged_mla_shared_plan_info(int32_t S, int32_t R, int32_t H, const int64_t *h_len, const int32_t *h_gsize, int32_t G,
+                                  const int64_t *h_prefix, int32_t sms, tf_unit_plan *info, int64_t *range_bounds);
+
 #ifdef __cplusplus
 }
 #endif

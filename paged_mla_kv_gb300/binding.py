@@ -53,6 +53,11 @@ class tf_attend_plan(ctypes.Structure):
                 ("groups", ctypes.c_int32), ("work", ctypes.c_int64), ("slots", ctypes.c_int64)]
 
 
+class tf_unit_plan(ctypes.Structure):
+    _fields_ = [("ctas", ctypes.c_int32), ("merge", ctypes.c_int32), ("cut", ctypes.c_int32), ("pad", ctypes.c_int32),
+                ("units", ctypes.c_int64), ("slots", ctypes.c_int64)]
+
+
 TF_PLAN_MAX_RANGES = 240
 
 
@@ -99,6 +104,8 @@ _SIGS = {
     "tf_paged_mla_shared_workspace_bytes": (_SZ, [_P, _I32, _I32, _I32, _P, _P, _I32, _P]),
     "tf_paged_mla_attend_shared": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _P, _I32, _P, _I32, _I32, _I32, _P, _F, _P,
                                                   _P, _P, _SZ, _P]),
+    "tf_paged_mla_blocks_plan_info": (ctypes.c_int, [_I32, _I32, _I32, _P, _I32, _I32, _P, _P]),
+    "tf_paged_mla_shared_plan_info": (ctypes.c_int, [_I32, _I32, _I32, _P, _P, _I32, _P, _I32, _P, _P]),
     "tf_profile_enable": (ctypes.c_int, [_P, _I32]),
     "tf_profile_read": (ctypes.c_int, [_P, _I32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_I64)]),
 }
@@ -528,6 +535,37 @@ def tf_paged_mla_plan_info(S: int, R: int, H: int, lens, sms: int = 0, invariant
     out["bounds"] = bounds[:out["nranges"] + 1] if out["mode"] in (0, 1) else None
     out["split_keys"] = splits[:S] if out["mode"] == 2 else None
     return out
+
+
+def _unit_plan(info, bounds) -> dict:
+    out = {f: int(getattr(info, f)) for f, _ in tf_unit_plan._fields_ if f != "pad"}
+    out["bounds"] = bounds[:out["ctas"] + 1]
+    return out
+
+
+def tf_paged_mla_blocks_plan_info(S: int, R: int, H: int, lens, max_blk: int, sms: int = 0) -> dict:
+    """The work plan of tf_paged_mla_attend_blocks for these lengths: ctas, merge (CTAs of a unit that a cluster
+    merges), cut, units, slots, and each CTA's bounds (unit << 32 | tile) as an int64 array."""
+    a, p = _i64(lens)
+    if len(a) != S:
+        _refuse("tf_paged_mla_blocks_plan_info")
+    info, bounds = tf_unit_plan(), np.zeros(TF_PLAN_MAX_RANGES + 1, np.int64)
+    _check(lib().tf_paged_mla_blocks_plan_info(S, R, H, p, int(max_blk), sms, ctypes.byref(info), bounds.ctypes.data),
+           "tf_paged_mla_blocks_plan_info")
+    return _unit_plan(info, bounds)
+
+
+def tf_paged_mla_shared_plan_info(S: int, R: int, H: int, lens, group_sizes, prefixes, sms: int = 0) -> dict:
+    """The same of tf_paged_mla_attend_shared."""
+    a, p = _i64(lens)
+    g, pg = _i32(group_sizes)
+    f, pf = _i64(prefixes)
+    if not (len(a) == S and len(g) == len(f)):
+        _refuse("tf_paged_mla_shared_plan_info")
+    info, bounds = tf_unit_plan(), np.zeros(TF_PLAN_MAX_RANGES + 1, np.int64)
+    _check(lib().tf_paged_mla_shared_plan_info(S, R, H, p, pg, len(g), pf, sms, ctypes.byref(info), bounds.ctypes.data),
+           "tf_paged_mla_shared_plan_info")
+    return _unit_plan(info, bounds)
 
 
 def tf_launch_count() -> int:

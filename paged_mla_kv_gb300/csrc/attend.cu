@@ -2371,6 +2371,8 @@ static int device_sms() {
     return n < attn::MAX_CTAS ? n : attn::MAX_CTAS;
 }
 
+static const int *device_clusters();
+
 static size_t slots_bytes(size_t slots) {
     if (slots == 0) return 0;
     const size_t o = slots * attn::slot_bytes();
@@ -2434,6 +2436,53 @@ int shared_workspace_bytes(bool fp8, int S, int R, int H, const int64_t *h_len, 
     int32_t from[TF_MAX_STREAMS];
     if (fp8 && expand_shared(S, h_gsize, G, e, n, from))
         *bytes = with_expanded(*bytes, fp8_shadow_bytes(S, h_len, from));
+    return TF_OK;
+}
+
+// The SMs of a plan query, and its clusters: the current device's for sms <= 0, else a device's that runs as
+// many as fit its SMs.
+static int query_sms(int sms, int *clusters) {
+    using namespace attn;
+    if (sms <= 0) {
+        std::copy(device_clusters(), device_clusters() + MAX_MERGE + 1, clusters);
+        return device_sms();
+    }
+    sms = std::min(sms, MAX_CTAS);
+    for (int k = 0; k <= MAX_MERGE; ++k) clusters[k] = k < 2 ? 0 : sms / k;
+    return sms;
+}
+
+static void unit_plan_info(const attn::Plan &pl, const int64_t *rb, tf_unit_plan *info, int64_t *range_bounds) {
+    *info = tf_unit_plan{};
+    info->ctas = pl.nctas;
+    info->merge = pl.merge;
+    for (int i = 1; i < pl.nctas; ++i) info->cut |= (rb[i] & 0xffffffffll) != 0;
+    info->units = pl.total;
+    info->slots = (int64_t)std::max(pl.slots, pl.need);
+    if (range_bounds) std::copy(rb, rb + pl.nctas + 1, range_bounds);
+}
+
+int blocks_plan_info(int S, int R, int H, const int64_t *h_len, int max_blk, int sms, tf_unit_plan *info,
+                     int64_t *range_bounds) {
+    int clusters[attn::MAX_MERGE + 1];
+    sms = query_sms(sms, clusters);
+    int64_t rb[attn::MAX_CTAS + 1];
+    const attn::Plan pl = attn::plan_blocks(S, R, H, h_len, max_blk, sms, clusters, rb);
+    unit_plan_info(pl, rb, info, range_bounds);
+    return TF_OK;
+}
+
+int shared_plan_info(int S, int R, int H, const int64_t *h_len, const int32_t *h_gsize, int G, const int64_t *h_prefix,
+                     int sms, tf_unit_plan *info, int64_t *range_bounds) {
+    attn::SharedEntry e[TF_MAX_STREAMS];
+    int16_t order[TF_MAX_STREAMS];
+    attn::Units all;
+    const int n = attn::shared_entries(S, R, H, h_len, h_gsize, G, h_prefix, e, order, &all);
+    if (n < 0) return TF_E_UNSUPPORTED;
+    sms = sms <= 0 ? device_sms() : std::min(sms, attn::MAX_CTAS);
+    int64_t rb[attn::MAX_CTAS + 1];
+    const attn::Plan pl = attn::plan_shared(all, n - S, sms, rb);
+    unit_plan_info(pl, rb, info, range_bounds);
     return TF_OK;
 }
 

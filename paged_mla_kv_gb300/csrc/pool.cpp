@@ -389,6 +389,14 @@ extern "C" size_t tf_paged_mla_blocks_workspace_bytes(const tf_kvpool *p, int32_
     return rc == TF_OK ? n : 0;
 }
 
+extern "C" int tf_paged_mla_blocks_plan_info(int32_t S, int32_t R, int32_t H, const int64_t *h_len, int32_t max_blk,
+                                             int32_t sms, tf_unit_plan *info, int64_t *range_bounds) {
+    if (!info) return TF_E_ARG;
+    const int rc = blocks_checks(S, R, H, h_len, max_blk);
+    if (rc != TF_OK) return rc;
+    return no_throw([&] { return blocks_plan_info(S, R, H, h_len, max_blk, sms, info, range_bounds); });
+}
+
 extern "C" int tf_paged_mla_attend_blocks(tf_kvpool *p, int32_t cache, const int32_t *d_pt, int32_t max_pages,
                                           const int64_t *h_len, const int32_t *d_blk, int32_t max_blk, int32_t S,
                                           int32_t R, int32_t H, const void *d_q, float scale, void *d_out,
@@ -429,6 +437,16 @@ extern "C" size_t tf_paged_mla_shared_workspace_bytes(const tf_kvpool *p, int32_
     const int rc = no_throw(
         [&] { return shared_workspace_bytes(p && is_fp8(p->desc), S, R, H, h_len, h_gsize, G, h_prefix, &n); });
     return rc == TF_OK ? n : 0;
+}
+
+extern "C" int tf_paged_mla_shared_plan_info(int32_t S, int32_t R, int32_t H, const int64_t *h_len,
+                                             const int32_t *h_gsize, int32_t G, const int64_t *h_prefix, int32_t sms,
+                                             tf_unit_plan *info, int64_t *range_bounds) {
+    if (!info) return TF_E_ARG;
+    const int rc = shared_checks(S, R, H, h_len, h_gsize, G, h_prefix);
+    if (rc != TF_OK) return rc;
+    return no_throw(
+        [&] { return shared_plan_info(S, R, H, h_len, h_gsize, G, h_prefix, sms, info, range_bounds); });
 }
 
 extern "C" int tf_paged_mla_attend_shared(tf_kvpool *p, int32_t cache, const int32_t *d_pt, int32_t max_pages,

@@ -173,6 +173,10 @@ size_t blocks_workspace_bytes(bool fp8, int S, int R, int H, const int64_t *h_le
 int launch_attend_blocks(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_len,
                          const int32_t *d_blk, int max_blk, int S, int R, int H, const void *d_q, float scale,
                          void *d_out, float *d_lse, void *d_ws, size_t ws_bytes, cudaStream_t st);
+int blocks_plan_info(int S, int R, int H, const int64_t *h_len, int max_blk, int sms, tf_unit_plan *info,
+                     int64_t *range_bounds);
+int shared_plan_info(int S, int R, int H, const int64_t *h_len, const int32_t *h_gsize, int G, const int64_t *h_prefix,
+                     int sms, tf_unit_plan *info, int64_t *range_bounds);
 // Both launchers refuse a workspace that is null, unaligned or too small before they launch anything.
 // TF_E_UNSUPPORTED: too many streams and sharing groups for one launch.
 int shared_workspace_bytes(bool fp8, int S, int R, int H, const int64_t *h_len, const int32_t *h_gsize, int G,
