@@ -344,7 +344,7 @@ int64_t tf_launch_count(void);
 /* With on != 0, every launch made for this pool is bracketed by CUDA events on
  * its stream.  tf_profile_read synchronises on them and returns, for kernel
  * kind `kind` (0 append, 1 attention main pass, 2 split combine, 3 state copy,
- * 4 poison fill), the summed milliseconds and the launch count since the last
+ * 4 poison fill, 5 block keys, 6 block scores), the summed milliseconds and the launch count since the last
  * read, then forgets them. */
 int tf_profile_enable(tf_kvpool *pool, int32_t on);
 int tf_profile_read(tf_kvpool *pool, int32_t kind, double *total_ms, int64_t *launches);

@@ -751,6 +751,7 @@ int launch_block_keys(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_p
     const int sms = f8 ? device_ready() : 0;
     if (f8 && sms <= 0) return TF_E_CUDA;
     if (prepare_launch(pool, st) != TF_OK) return TF_E_CUDA;
+    ProfScope prof(pool, kProfBlockKeys, st);
     const cudaError_t e = f8 ? launch_pdl(block_keys_fp8_kernel, dim3((unsigned)std::min<int64_t>(n, sms)),
                                           dim3(FTEAMS * FT + 32), sizeof(KeysFp8Shared), st, p)
                              : launch_pdl(block_keys_kernel, dim3((unsigned)n), dim3(KC * KG), 0, st, p);
@@ -810,6 +811,7 @@ int launch_block_scores(tf_kvpool *pool, const void *d_bkeys, const int32_t *d_p
                  : H % 8 == 0 ? block_scores_kernel<8>
                  : H % 4 == 0 ? block_scores_kernel<4>
                               : block_scores_kernel<1>;
+    ProfScope prof(pool, kProfBlockScores, st);
     const cudaError_t e = launch_pdl_pairs(kern, dim3((unsigned)ctas), dim3(THREADS), SMEM_TOTAL, st, p);
     launch_counter()++;
     return e == cudaSuccess ? TF_OK : TF_E_CUDA;

@@ -41,7 +41,10 @@ struct DevErr {
     int64_t detail; // offending page id or wait site
 };
 
-enum ProfKind { kProfAppend = 0, kProfAttend = 1, kProfCombine = 2, kProfCopy = 3, kProfPoison = 4, kProfKinds = 5 };
+enum ProfKind {
+    kProfAppend = 0, kProfAttend = 1, kProfCombine = 2, kProfCopy = 3, kProfPoison = 4, kProfBlockKeys = 5,
+    kProfBlockScores = 6, kProfKinds = 7
+};
 
 struct ProfRec {
     int kind;
