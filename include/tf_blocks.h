@@ -46,6 +46,9 @@ extern "C" {
  * [h_from[s], h_len[s]), from all its rows up to h_len[s].  After an append of n rows at pos that is
  * h_from = pos, h_len = pos + n.  h_from[s] == h_len[s] leaves the stream's keys alone.  Keys of no
  * other block are read or written.
+ * Keys do not move with rows: pages that tf_state_copy_rows filled, and pages of a pool that came with its
+ * rows, hold whatever keys their last owner left until an update from h_from = 0 (or a copy of the source
+ * pages' keys, for whole pages).
  * d_pt / max_pages as in tf_paged_append.  d_bkeys: 16-byte aligned.  A table entry outside the pool is
  * recorded as TF_E_DEVICE and its blocks are skipped.
  * Errors: TF_E_ARG for a null pointer, S outside [1, TF_MAX_STREAMS], max_pages < 1 or an unaligned

@@ -290,6 +290,8 @@ int tf_paged_mla_attend_static(tf_kvpool *pool, int32_t cache, const int32_t *d_
  * pages d_src_pages[0 .. ceil(at/512)) to the pages d_dst_pages[same], row for
  * row.  Rows at and past `at` of the last page are neither read nor written.
  * Page ids outside the pool are recorded as TF_E_DEVICE and skipped.  Bit-exact.
+ * Block keys (tf_blocks.h) lie beside the pool and are not copied: after a copy the
+ * stream's blocks are averaged again, tf_block_keys_update from row 0.
  * TF_E_ARG for a null pool, at < 0, or null tables with at > 0; TF_E_RANGE for a
  * cache >= num_caches or at > num_pages * 512.  at == 0 launches nothing. */
 int tf_state_copy_rows(tf_kvpool *pool, int32_t cache, const int32_t *d_src_pages,
