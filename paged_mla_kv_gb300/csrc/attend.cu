@@ -2191,18 +2191,18 @@ inline int cut_by_limit(const Units &all, int64_t seg, int64_t lim, int sms, int
 // prefill chunk's 2,048 rows: whole rows would leave 14 a CTA against 13.5); cuts by limit fit few: 64
 // streams of 32 tiles are 128 CTAs of one segment, where even cuts give 152 CTAs two segments each
 // and more partials to merge.
-// *largest: that load, with the combine pass where a unit is cut.  limit_ties: of equal ones the cuts by
-// limit are taken (listed blocks, which decode reads from HBM: fewer partials; 64 streams of 32 blocks
-// 39.6 us against 42.3), else the even cuts (shared prefixes, bound by the products: eight streams of
-// 64 heads behind 8,192 rows 25 us against 27).
-inline int cut_units(const Units &all, int min_tiles, int sms, bool limit_ties, int64_t *b, bool *cut, int64_t *largest) {
+// *largest: that load, with the combine pass where a unit is cut.  Of equal ones the cuts by limit are taken,
+// which leave fewer partials: over the shapes where both loads are equal (1 to 256 streams, 1 to 4 rows, 16 to
+// 128 heads) even cuts took 1.3% longer for shared prefixes of 2,048 to 131,072 rows (443 shapes, from 4% less
+// to 18% more) and 3.3% for 8 to 256 listed blocks (24 shapes, 1% less to 10% more).
+inline int cut_units(const Units &all, int min_tiles, int sms, int64_t *b, bool *cut, int64_t *largest) {
     const int64_t seg = UNIT_SEG_COST;
     int64_t load = 0;
     const int n = cut_evenly(all, seg, min_tiles, sms, b, cut, &load);
     *largest = load + (*cut ? combine_cost(all.units) : 0);
     // the smallest limit that needs at most sms ranges and cuts nothing below min_tiles
     int64_t lo = std::max<int64_t>(seg + std::min<int64_t>(all.most, min_tiles), (all.tiles + sms - 1) / sms + seg);
-    int64_t hi = *largest - (limit_ties ? 0 : 1);
+    int64_t hi = *largest;
     if (lo > hi || cut_by_limit(all, seg, hi, sms, nullptr, nullptr) > sms) return n;
     while (lo < hi) {
         const int64_t mid = lo + (hi - lo) / 2;
@@ -2211,7 +2211,7 @@ inline int cut_units(const Units &all, int min_tiles, int sms, bool limit_ties, 
     bool c2 = false;
     cut_by_limit(all, seg, lo, sms, nullptr, &c2);
     const int64_t cost = lo + (c2 ? combine_cost(all.units) : 0);
-    if (cost > *largest - (limit_ties ? 0 : 1)) return n;
+    if (cost > *largest) return n;
     *largest = cost;
     *cut = c2;
     return cut_by_limit(all, seg, lo, sms, b, nullptr);
@@ -2235,7 +2235,7 @@ inline Plan plan_blocks(int S, int R, int H, const int64_t *h_len, int max_blk, 
     pl.total = all.units;
     pl.rep = 1;
     int64_t load = 0;
-    pl.nranges = cut_units(all, UNIT_MIN_TILES, sms, true, rb, &cut, &load);
+    pl.nranges = cut_units(all, UNIT_MIN_TILES, sms, rb, &cut, &load);
     pl.nctas = pl.nranges;
     pl.slots = cut ? 2 * (size_t)pl.nctas : 0;
     // few units: k CTAs each, one cluster, for the k that ends first; the workspace holds the partials of
@@ -2305,7 +2305,7 @@ inline Plan plan_shared(const Units &all, int nshared, int sms, int64_t *rb) {
     pl.total = all.units;
     pl.rep = 1;
     int64_t load = 0;
-    pl.nranges = cut_units(all, UNIT_MIN_TILES, sms, false, rb, &cut, &load);
+    pl.nranges = cut_units(all, UNIT_MIN_TILES, sms, rb, &cut, &load);
     pl.nctas = pl.nranges;
     pl.slots = nshared > 0 ? (size_t)all.units + (size_t)pl.nctas : cut ? 2 * (size_t)pl.nctas : 0;
     return pl;

@@ -110,6 +110,12 @@ def test_shared_prefix_plans(seed):
         assert not p["merge"]
 
 
+def test_of_equal_loads_the_one_with_fewer_partials():
+    """24 streams behind 4,096 shared rows: 19 tiles a CTA on 144 CTAs or on 152."""
+    lens = [4104 + 100 * (s * 618 % 1000) // 1000 for s in range(24)]
+    assert B.tf_paged_mla_shared_plan_info(24, 1, 64, lens, [24], [4096], 152)["ctas"] == 144
+
+
 def test_plans_size_the_workspace():
     for S, R, H, n, k in ((64, 1, 64, 32768, 32), (1, 2048, 64, 102048, 32), (1, 1, 16, 2048, 8), (3, 2, 96, 5000, 20), (1, 1, 16, 64, 8)):
         slots = B.tf_paged_mla_blocks_plan_info(S, R, H, [n] * S, k)["slots"]
