@@ -108,11 +108,14 @@ int tf_paged_mla_attend_blocks(tf_kvpool *pool, int32_t cache, const int32_t *d_
 /* ---- attention of streams that share a prefix ----
  * What tf_paged_mla_attend computes, for a batch in which streams with the same first rows follow one
  * another: group g is the next h_gsize[g] streams (the sizes add up to S), whose rows 0 .. h_prefix[g] - 1
- * are the same.  The shared rows, in whole 64-row tiles, are read once for the group, through the first
- * stream's table, and multiplied with the queries of all its streams together; the rest of each stream is
- * read through its own.  That the rows are the same is the caller's word: pages held by reference, or
- * copies of the same bytes.  A group of one stream, or a prefix of 0, shares nothing.  Table
- * entries of pages of which a stream reads no row of its own are not used, but for the group's first stream.
+ * are the same.  The shared rows, in whole 64-row tiles, are read through the first stream's table, the rest
+ * of each stream through its own.  Where R * H is not a multiple of 64 the columns (stream, row, head) of a
+ * group are packed, and a shared tile is loaded and multiplied once for 64 of them, whatever stream they
+ * belong to (16 heads: a quarter of the work).  Where it is, a stream's columns fill their products by
+ * themselves: the work is tf_paged_mla_attend's, and the tiles that the streams share meet in L2.  That the
+ * rows are the same is the caller's word: pages held by reference, or copies of the same bytes.  A group of
+ * one stream, or a prefix of 0, shares nothing.  Table entries of pages of which a stream reads no row of its
+ * own are not used, but for the group's first stream.
  * 0 <= h_prefix[g] <= h_len[s] - R + 1 for every stream s of the group: each query row sees all of it.
  * Both arrays have G entries, 1 <= G <= S.  All else as in tf_paged_mla_attend, BF16 and FP8 pages alike;
  * the keys are dealt out by a plan of their own whatever the pool's flags, so bits may differ (within

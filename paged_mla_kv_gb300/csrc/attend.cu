@@ -180,7 +180,9 @@ static_assert(SMEM_TOTAL <= 232448, "shared memory budget");
 //    but anywhere: rows choose blocks on their own, so there are no common positions to keep.
 //  - SHARED (tf_paged_mla_attend_shared).  Entries instead of streams.  Where a stream's R * H columns
 //    are whole groups of 64, an entry a stream over all its keys, whose shared tiles are read through
-//    the group's first table: the groups' units are cut alike, so its CTAs read them at the same time.
+//    the group's first table.  Each unit loads and multiplies them itself; the units' cuts are their own,
+//    but all CTAs walk the same rows within a short time and L2 serves the later ones (8 streams of 64
+//    heads behind 131,072 rows read 159 MB of DRAM for 153 MB held).
 //    Else one entry for each stream's own rows and one for each group's shared rows, whose columns are
 //    the (stream, row, head) columns of the whole group one after another, so a tile of shared rows is
 //    loaded and multiplied once for 64 of them whatever stream they belong to (16 heads: a quarter of
@@ -1355,7 +1357,10 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&c.corr_req[rs]);
                 // P rows as bf16, 128B-swizzled K-major, into the tile's rope slot (QK^T has read
-                // the rope box: S is complete): keys 8j.. of row r in 16-byte chunk j ^ (r & 7)
+                // the rope box: S is complete): keys 8j.. of row r in 16-byte chunk j ^ (r & 7).
+                // bf16 because an MMA's operands have one type, and the rows are bf16: a weight is off
+                // by at most 2^-8 of itself, the outputs by 0.0020 (rms, relative) where weights in fp32
+                // leave 0.0017, their own rounding.  The sums l take the weights in fp32.
                 uint8_t *pb = smem + SMEM_ROPE + rs * BOX_BYTES;
                 uint8_t *p0 = pb + r0 * 128 + 2 * kq;
                 uint8_t *p1 = pb + r1 * 128 + 2 * kq;
@@ -2082,8 +2087,8 @@ inline Plan plan_of(int S, int R, int H, const int64_t *h_len, int sms, bool inv
 }
 
 // What a CTA pays for a segment beyond its tiles, in tiles (queries, the pipeline's refill, the
-// epilogue), from a trace of the kernel: 8,000 cycles of 2,600-cycle tiles.  A CTA's load is its tiles
-// plus this for each segment.
+// epilogue), from a trace of the kernel: 6,000 to 8,500 cycles, of 2,660-cycle tiles.  On FP8 pages it is
+// two of the 4,200-cycle tiles; the one weight serves both.
 constexpr int64_t UNIT_SEG_COST = 3;
 constexpr int UNIT_MIN_TILES = 2;
 // What merging cut units takes, in tiles: a combine pass (5 to 9 us from the last CTA's end to its own,
@@ -2386,7 +2391,7 @@ size_t attend_workspace_bytes(bool invariant, int S, int R, int H, const int64_t
 
 // FP8 pages whose rows many column groups read are expanded to BF16 pages in the workspace first:
 // `visits` key tiles are taken in all (one column group each) and `tiles` tiles are held.  A tile of codes
-// takes a CTA 4,090 cycles, one of bf16 rows 2,660, which is 5 ns a visit over all SMs; expanding a
+// takes a CTA about 4,200 cycles, one of bf16 rows 2,660, which is 5 ns a visit over all SMs; expanding a
 // tile moves 115 KB, 21 ns, and its launch 4 us.  Measured with and without: 131,072 shared rows and 4
 // column groups 147 / 139 us, 6 groups 178 / 195, 16 groups 381 / 500; 8,192 rows and 8 groups
 // 36 / 32, 16 groups 47 / 49; 2,048 rows over 32 blocks of 102,048 rows 717 / 997.
