@@ -87,8 +87,8 @@ int tf_block_scores(tf_kvpool *pool, const void *d_bkeys, const int32_t *d_pt, i
  * other entries are not read.
  *   s_j = scale * (q[s][r][h][0:512] . C_j + q[s][r][h][512:576] . Kr_j)
  *   out[s][r][h][:] = sum_j softmax(s)_j * C_j;  lse[s][r][h] = log sum_j exp(s_j).
- * An entry of -1 is no block, and a block behind pos has no key to see; a row left without keys gives
- * out 0 and lse -inf.  A block listed twice counts twice.  The order of a list decides only the order of
+ * An entry of -1 is no block, and a block behind pos has no key to see; what rows behind pos hold, NaN
+ * included, does not reach the outputs; a row left without keys gives out 0 and lse -inf.  A block listed twice counts twice.  The order of a list decides only the order of
  * the sums.  An entry below -1 or at and past the stream's last block is recorded as TF_E_DEVICE, and so is
  * a table entry outside the pool that a listed block needs; the call's output is then undefined.  Entries of
  * pages that no list names are not used.
@@ -117,7 +117,8 @@ int tf_paged_mla_attend_blocks(tf_kvpool *pool, int32_t cache, const int32_t *d_
  * one stream, or a prefix of 0, shares nothing.  Table entries of pages of which a stream reads no row of its
  * own are not used, but for the group's first stream.
  * 0 <= h_prefix[g] <= h_len[s] - R + 1 for every stream s of the group: each query row sees all of it.
- * Both arrays have G entries, 1 <= G <= S.  All else as in tf_paged_mla_attend, BF16 and FP8 pages alike;
+ * Both arrays have G entries, 1 <= G <= S.  All else as in tf_paged_mla_attend, BF16 and FP8 pages alike (a
+ * NaN among a stream's last R rows reaches all R outputs: their columns share the products);
  * the keys are dealt out by a plan of their own whatever the pool's flags, so bits may differ (within
  * rounding) from tf_paged_mla_attend and between batches, and are the same on every call of one batch.
  * The workspace can be larger than that call's (and holds a BF16 copy of the rows of an FP8 pool that

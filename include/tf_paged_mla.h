@@ -220,7 +220,8 @@ int tf_paged_append(tf_kvpool *pool, int32_t cache, const int32_t *d_pt, int32_t
  * d_ws: caller workspace of at least tf_paged_mla_workspace_bytes(pool, ...) bytes,
  * 256-byte aligned, used for the split partials (fp32); it may be NULL only when
  * that size is 0.  Rows past h_len[s] are never read into the result (they may
- * hold NaN).  Limits: 1 <= S <= TF_MAX_STREAMS, 1 <= H <= TF_MAX_HEADS, scale a
+ * hold NaN); a NaN among a stream's last R rows reaches the outputs of all R query
+ * rows (their columns share the products).  Limits: 1 <= S <= TF_MAX_STREAMS, 1 <= H <= TF_MAX_HEADS, scale a
  * finite number > 0, d_q and d_out 16-byte aligned (TF_E_ARG otherwise); h_len[s] <=
  * INT32_MAX (TF_E_UNSUPPORTED otherwise, and a workspace size of 0).  TF_E_RANGE for a
  * cache outside the pool, a length below R or past the table, or a NULL table wider than

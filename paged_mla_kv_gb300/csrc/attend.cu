@@ -828,7 +828,7 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
                             stop = true;
                             break;
                         }
-                        // -1: no block.  Any tile will do (QK^T's issuer zeroes all its rows).
+                        // -1: no block.  Any tile will do (the softmax zeroes all its rows).
                         k0 = bc < 0 ? 0 : (int64_t)bc * BK;
                         cur_lp = -1;
                     }
@@ -927,14 +927,14 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
             // the tile's S buffer has been read out (by the softmax of tile tq - 2)
             if (tq >= 2 && !ptx::mbar_wait_warp(&c.s_free[tq & 1], ((tq - 2) >> 1) & 1, abort, errp, 4)) return false;
             // rows past the stream's end may hold NaN poison: zero them in latent boxes [b0, b1) and
-            // the rope box, so that P = 0 times V stays 0 in the PV contraction
+            // the rope box, so that P = 0 times V stays 0 in the PV contraction (BLOCKS: the softmax does)
             auto zero_box = [&](int b) {
-                const int valid = MODE == MODE_BLOCKS && rem < 0 ? 0 : (int)rem;
+                const int valid = (int)rem;
                 uint4 *bx = reinterpret_cast<uint4 *>(smem + box_off(tq, b));
                 for (int k = lane; k < (BK - valid) * 8; k += 32) bx[valid * 8 + k] = make_uint4(0, 0, 0, 0);
             };
             auto zero_tail = [&](int b0, int b1, bool rope) {
-                if (rem >= BK) return;
+                if (MODE == MODE_BLOCKS || rem >= BK) return;
                 if (rope) zero_box(8);
                 for (int b = b0; b < b1; ++b) zero_box(b);
                 ptx::fence_proxy_async_smem();
@@ -1012,17 +1012,7 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
             if (qk_role) {
                 ok = ptx::mbar_wait_warp(&c.q_full, si & 1, abort, errp, 2) &&
                      ptx::mbar_wait_warp(&c.q_tmem_full, si & 1, abort, errp, 2);
-                int bn = MODE == MODE_BLOCKS ? __ldg(q.list) : 0;   // the next tile's block
-                for (int tl = 0; ok && tl < q.nt; ++tl) {
-                    int64_t rem;
-                    if (MODE == MODE_BLOCKS) {
-                        rem = bn < 0 ? 0 : q.len - (int64_t)bn * BK;
-                        bn = tl + 1 < q.nt ? __ldg(q.list + tl + 1) : 0;
-                    } else {
-                        rem = q.len - (q.kb + (int64_t)tl * BK);
-                    }
-                    ok = qk_tile(gt + tl, tl, q, rem);
-                }
+                for (int tl = 0; ok && tl < q.nt; ++tl) ok = qk_tile(gt + tl, tl, q, q.len - (q.kb + (int64_t)tl * BK));
             } else {
                 for (int tl = 0; ok && tl < q.nt; ++tl) ok = pv_tile(gt + tl, tl, idesc_pv);
             }
@@ -1368,6 +1358,19 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
                 for (int j = 0; j < 8; ++j) {
                     *reinterpret_cast<uint32_t *>(p0 + ((j ^ (r0 & 7)) << 4)) = pk0[j];
                     *reinterpret_cast<uint32_t *>(p1 + ((j ^ (r1 & 7)) << 4)) = pk1[j];
+                }
+                if (MODE == MODE_BLOCKS) {
+                    // Rows that the unit's query row does not see (past the stream's end, behind the query,
+                    // all of no block) may hold anything: zero them, two latent boxes a warp, so that P = 0
+                    // times V stays 0.  QK^T has read the tile, and PV waits for p_full.  (With the QK^T issuer
+                    // zeroing them ahead of its products 2,048 rows over 32 blocks took 698 us, here 645.)
+                    const int64_t lim = q.pos + 1 - k0;
+                    const int seen = lim < 0 ? 0 : lim > BK ? BK : (int)lim;
+                    if (seen < BK)
+                        for (int b = 2 * q4; b < 2 * q4 + 2; ++b) {
+                            uint4 *bx = reinterpret_cast<uint4 *>(smem + box_off(t, b));
+                            for (int k = seen * 8 + lane; k < BK * 8; k += 32) bx[k] = make_uint4(0, 0, 0, 0);
+                        }
                 }
                 ptx::fence_proxy_async_smem();
                 __syncwarp();

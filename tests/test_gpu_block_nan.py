@@ -91,3 +91,34 @@ def test_scores_of_nan_and_infinite_keys(H, weighted):
             mag = (mag if ws is None else mag * np.abs(ws)[..., None]).sum(1)
             assert np.all(np.abs(got[fin] - ref[fin]) <= (w.scale * (580 + H) * 2.0 ** -23 * mag)[fin])
     assert np.isnan(xs[0, 5]) and np.isnan(xs[2, 9]) and np.isnan(xs[3, 2]) and np.isnan(xs[1, 1:70]).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n,R,H,k", [(200, 4, 16, 4), (1000, 3, 64, 16), (1500, 130, 16, 8), (20000, 2, 64, 300), (1300, 70, 64, 21)])
+def test_rows_behind_a_query_may_be_nan(n, R, H, k, fp8):
+    """A query attends the rows up to its own.  What the rows behind it hold, in its own block or in listed ones that
+    begin behind it, does not reach its output."""
+    w = Y.custom("behind", 176 + R, lens=[n, n - 3], R=R, H=H, q_std=1.0, value_std=0.5)
+    res = Resident(w, fp8=fp8)
+    g = np.random.default_rng(R)
+    blk = random_lists(w, k, k, holes=False)
+    own = torch.tensor([[(int(L) - R + r) // 64 for r in range(R)] for L in w.lens], dtype=torch.int32, device="cuda")
+    last = torch.tensor([[(int(L) - 1) // 64] for L in w.lens], dtype=torch.int32, device="cuda")
+    seen = torch.clamp_max(own + 1, k)                        # the entries that are read
+    place = torch.from_numpy(g.permutation(k)).cuda()
+    pick = place[None, None].expand(2, R, k) < seen[..., None]
+    first = torch.where(pick, place[None, None].expand(2, R, k), k).amin(-1, keepdim=True).long()
+    blk.scatter_(2, first, own[..., None])                    # each row lists its own block
+    if k > 2:
+        blk[..., 0] = torch.where((own != last) & (first[..., 0] != 0), last.expand(2, R), blk[..., 0])   # and some the last one
+    good = run_blocks(res, w, blk)
+    no_device_error(res.pool)
+    bad = R // 2                                              # the rows behind query row `bad` - 1 are NaN
+    for s in range(2):
+        lat = torch.full((1, R - bad, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
+        rope = torch.full((1, R - bad, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+        B.tf_paged_append(res.pool, 0, res.stream_pt(s), res.max_pages, [int(w.lens[s]) - R + bad], lat, rope)
+    out, lse = run_blocks(res, w, blk)
+    no_device_error(res.pool)
+    assert torch.equal(out[:, :bad], good[0][:, :bad]) and torch.equal(lse[:, :bad], good[1][:, :bad])
+    assert torch.isnan(out[:, bad:]).any(-1).all()            # the others see their own row
