@@ -2090,8 +2090,8 @@ inline Plan plan_of(int S, int R, int H, const int64_t *h_len, int sms, bool inv
 }
 
 // What a CTA pays for a segment beyond its tiles, in tiles (queries, the pipeline's refill, the
-// epilogue), from a trace of the kernel: 6,000 to 8,500 cycles, of 2,660-cycle tiles.  On FP8 pages it is
-// two of the 4,200-cycle tiles; the one weight serves both.
+// epilogue), from a trace of the kernel: about 9,000 cycles, of 2,410-cycle tiles (listed blocks) or 4,200
+// (FP8 pages).  Over 50 shapes of both calls on both kinds of pages 4 and 5 took 0.1 to 0.2% longer than 3.
 constexpr int64_t UNIT_SEG_COST = 3;
 constexpr int UNIT_MIN_TILES = 2;
 // What merging cut units takes, in tiles: a combine pass (5 to 9 us from the last CTA's end to its own,
@@ -2394,7 +2394,7 @@ size_t attend_workspace_bytes(bool invariant, int S, int R, int H, const int64_t
 
 // FP8 pages whose rows many column groups read are expanded to BF16 pages in the workspace first:
 // `visits` key tiles are taken in all (one column group each) and `tiles` tiles are held.  A tile of codes
-// takes a CTA about 4,200 cycles, one of bf16 rows 2,660, which is 5 ns a visit over all SMs; expanding a
+// takes a CTA about 4,200 cycles, one of bf16 rows 2,400 to 2,660, which is 5 to 6 ns a visit over all SMs; expanding a
 // tile moves 115 KB, 21 ns, and its launch 4 us.  Measured with and without: 131,072 shared rows and 4
 // column groups 147 / 139 us, 6 groups 178 / 195, 16 groups 381 / 500; 8,192 rows and 8 groups
 // 36 / 32, 16 groups 47 / 49; 2,048 rows over 32 blocks of 102,048 rows 717 / 997.
