@@ -230,8 +230,6 @@ struct Params {
                                 // BLOCKS: [S][R][max_idx] block numbers of each row
     int32_t max_idx;
     const int32_t *pt;
-    const int32_t *src_pt;      // rows expanded from FP8 pages: the pool's own table (else null), for the
-    int32_t src_max_pages;      // ids of pages that it does not have
     const __nv_bfloat16 *q;     // [S*R*H][576]: the TMEM part of each column group is read from here
     __nv_bfloat16 *out;
     float *lse;
@@ -255,6 +253,8 @@ struct Params {
     };
     int16_t order[TF_MAX_STREAMS];   // SPLITS: launch order (streams with longer splits first);
                                      // SHARED: the stream's entry of shared rows, or -1
+    const int32_t *src_pt;      // rows expanded from FP8 pages: the pool's own table (else null), for the
+    int32_t src_max_pages;      // ids of pages that it does not have
 };
 
 // BLOCKS: blocks a query row at position pos takes from its list: no more than it can see
@@ -484,6 +484,13 @@ __device__ __forceinline__ void store_column(const Params &p, size_t orow, int l
         o2[1] = __floats2bfloat162_rn(acc[i].z * inv, acc[i].w * inv);
     }
     if (lane == 0 && p.lse) p.lse[orow] = (M + log2f(L)) * 0.69314718055994531f;
+}
+
+// A table entry outside the pool; rows expanded from FP8 pages are named by the pool's own table.  Not
+// inlined, and not in the modes that never take expanded rows: in the TMA producer's loop these few
+// instructions cost a dense prompt chunk 1.2%, shared prefixes 0.5 to 0.9%.
+__device__ __noinline__ void record_bad_page(const Params &p, int row, int lp, int raw) {
+    ptx::record_error(p.err, TF_E_DEVICE, p.src_pt ? __ldg(p.src_pt + (int64_t)row * p.src_max_pages + lp) : raw);
 }
 
 #define ALLW(x) __all_sync(0xffffffffu, (x))
@@ -846,8 +853,8 @@ __global__ void __launch_bounds__(kernel_threads<MODE, FP8>(), 1) mla_attend_ker
                                                             : __ldg(pt + (int64_t)trow * max_pages + lp);
                         cur_lp = lp;
                         if (raw < 0 || raw >= num_pages) {
-                            const int64_t at = (int64_t)trow * p.src_max_pages + lp;
-                            ptx::record_error(errp, TF_E_DEVICE, p.src_pt ? __ldg(p.src_pt + at) : raw);
+                            if (MODE == MODE_SPLITS || own_cols(MODE)) record_bad_page(p, trow, lp, raw);
+                            else ptx::record_error(errp, TF_E_DEVICE, raw);
                             *abort = 1;
                             stop = true;
                             break;
