@@ -2403,8 +2403,9 @@ size_t attend_workspace_bytes(bool invariant, int S, int R, int H, const int64_t
 // `visits` key tiles are taken in all (one column group each) and `tiles` tiles are held.  A tile of codes
 // takes a CTA about 4,200 cycles, one of bf16 rows 2,400 to 2,660, which is 5 to 6 ns a visit over all SMs; expanding a
 // tile moves 115 KB, 21 ns, and its launch 4 us.  Measured with and without: 131,072 shared rows and 4
-// column groups 147 / 139 us, 6 groups 178 / 195, 16 groups 381 / 500; 8,192 rows and 8 groups
-// 36 / 32, 16 groups 47 / 49; 2,048 rows over 32 blocks of 102,048 rows 717 / 997.
+// column groups 138 / 140 us, 6 groups 179 / 199, 16 groups 362 / 480; 8,192 rows and 8 groups 33 to
+// 35 / 36, 16 groups 46 / 52; 2,048 rows over 32 blocks of 102,048 rows 681 / 963, 16 rows over 64
+// blocks of 4,096 rows 37 / 38, 64 rows over 32 blocks of 8,192 rows 41 / 51.
 static bool expand_fp8(int64_t visits, int64_t tiles) { return visits >= 5 * tiles + 800; }
 
 static size_t with_expanded(size_t part, size_t shadow) { return (part + 1023) / 1024 * 1024 + shadow; }
