@@ -77,20 +77,18 @@ def whole_job_rate(units_per_rank: float, world: int, slowest_ms: float) -> floa
 # the SHA-256 of the kernel's source the capture was taken on: once the kernel changes, the
 # counters no longer describe it and "traffic" is reported null until it is re-captured.
 NCU_TRAFFIC = {
-    # attention on source 7d9fa675422c97da, one launch each: `--metrics dram__bytes_read.sum,
+    # attention on source 0522530be1c351cc, one launch each: `--metrics dram__bytes_read.sum,
     # dram__bytes_write.sum,gpu__time_duration.sum --cache-control none` (L2 as the back-to-back
     # steps leave it); the prefill chunk with ncu's default cache flush; profiles/mla_attend_*.md.
-    # e00360dc80e0534f differs from it only in how many columns a CTA's last cut partial stages (those PV
-    # computed, in 32-column steps): all 64 for every workload below, so the same bytes move.
-    "e00360dc80e0534f": {"decode_batch": 370_056_704 + 2_340_864,
-                         "long_window": 1_207_117_312 + 827_392,
-                         "sparse_decode": 155_352_064 + 22_679_040,
-                         "fp8_decode": 216_005_888 + 17_167_104,
-                         "prefill_100k": 20_034_719_744 + 158_304_512},
+    "0522530be1c351cc": {"decode_batch": 370_369_536 + 2_493_696,
+                         "long_window": 1_206_660_864 + 561_408,
+                         "sparse_decode": 155_503_104 + 22_721_792,
+                         "fp8_decode": 216_298_240 + 17_138_432,
+                         "prefill_100k": 23_847_287_808 + 159_604_224},
     # top-k: both launches of one call (first level 811.1 + 8.6 MB, merge 58.8 + 0.2 MB), taken
-    # on source 4e5c0b41cdefdfb7; 689a485f4717fede differs from it in comments and host-side argument
-    # checks only (the cubins built without line info hash the same)
-    "689a485f4717fede": {"topk_prefill": 811_079_680 + 8_606_208 + 58_786_560 + 240_640},
+    # on source 4e5c0b41cdefdfb7; b8717a4a29ea8e95 differs from it in comments, host-side argument
+    # checks and the opt-in only (the cubins built without line info hash the same)
+    "b8717a4a29ea8e95": {"topk_prefill": 811_079_680 + 8_606_208 + 58_786_560 + 240_640},
 }
 
 
