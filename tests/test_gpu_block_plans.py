@@ -50,7 +50,7 @@ def test_clusters_of_two(S, H, fp8):
 
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("S,H,k,merge", [
-    (3, 96, 3, 3), (12, 96, 7, 4), (14, 128, 8, 4), (8, 96, 10, 5), (12, 96, 14, 5), (5, 16, 5, 5), (6, 96, 6, 6), (5, 96, 7, 7),
+    (3, 96, 3, 3), (12, 96, 7, 4), (14, 128, 8, 4), (8, 96, 10, 5), (8, 128, 9, 5), (5, 16, 5, 5), (6, 96, 6, 6), (5, 96, 7, 7),
     (1, 100, 7, 7), (1, 16, 8, 8), (4, 96, 8, 8), (2, 128, 8, 8)])
 def test_larger_clusters(S, H, k, merge, fp8):
     lens = [64 * k + 100 + 37 * s for s in range(S)]
