@@ -26,7 +26,8 @@ PAGE_BYTES_BF16 = 589824
 PAGE_BYTES_FP8 = 329728    # 512 x 512 E4M3 codes, 512 fp32 scales, 512 x 64 bf16 rope
 ERR_NAMES = {0: "TF_OK", -1: "TF_E_ARG", -2: "TF_E_RANGE", -3: "TF_E_NOMEM", -4: "TF_E_CUDA",
              -5: "TF_E_TIMEOUT", -6: "TF_E_UNSUPPORTED", -7: "TF_E_DEVICE"}
-PROF_APPEND, PROF_ATTEND, PROF_COMBINE, PROF_COPY, PROF_POISON, PROF_BLOCK_KEYS, PROF_BLOCK_SCORES = range(7)
+PROF_APPEND, PROF_ATTEND, PROF_COMBINE, PROF_COPY, PROF_POISON, PROF_BLOCK_KEYS, PROF_BLOCK_SCORES, \
+    PROF_READ, PROF_PROMPT = range(9)
 
 
 class TFError(RuntimeError):
@@ -56,6 +57,32 @@ class tf_attend_plan(ctypes.Structure):
 class tf_unit_plan(ctypes.Structure):
     _fields_ = [("ctas", ctypes.c_int32), ("merge", ctypes.c_int32), ("cut", ctypes.c_int32), ("pad", ctypes.c_int32),
                 ("units", ctypes.c_int64), ("slots", ctypes.c_int64)]
+
+
+TF_ROPE_INTERLEAVED, TF_ROPE_HALF = 0, 1
+TF_ROPE_PLAIN, TF_ROPE_LINEAR, TF_ROPE_YARN = 0, 1, 2
+TF_ROPE_MAX_DIM = 256
+
+
+class tf_rope_desc(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original", ctypes.c_double), ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("amplitude", ctypes.c_double)]
+
+
+class tf_rope(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("made", ctypes.c_uint32), ("turn", ctypes.c_uint64 * (TF_ROPE_MAX_DIM // 2))]
+
+
+class tf_heads(ctypes.Structure):
+    _fields_ = [("d_p", ctypes.c_void_p), ("row", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class tf_prompt_plan(ctypes.Structure):
+    _fields_ = [("items", ctypes.c_int64), ("slots", ctypes.c_int64), ("rows", ctypes.c_int32),
+                ("splits", ctypes.c_int32)]
 
 
 TF_PLAN_MAX_RANGES = 240
@@ -106,6 +133,14 @@ _SIGS = {
                                                   _P, _P, _SZ, _P]),
     "tf_paged_mla_blocks_plan_info": (ctypes.c_int, [_I32, _I32, _I32, _P, _I32, _I32, _P, _P]),
     "tf_paged_mla_shared_plan_info": (ctypes.c_int, [_I32, _I32, _I32, _P, _P, _I32, _P, _I32, _P, _P]),
+    "tf_rope_make": (ctypes.c_int, [_P, _P]),
+    "tf_rope_apply": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _P, _I64, _I64, _P, _I64, _I64, _P]),
+    "tf_paged_append_rope": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _P, _I32, _P, _I64, _P, _F, _P, _P]),
+    "tf_paged_read": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _P, _I32, _P, _I64, _P, _I64, _P]),
+    "tf_prompt_workspace_bytes": (_SZ, [_P, _P, _I32, _I32, _I32, _I32, _I32, _I32]),
+    "tf_prompt_attend": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _I64, _P, _F, _I32, _P, _P,
+                                        _P, _SZ, _P]),
+    "tf_prompt_plan_info": (ctypes.c_int, [_P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _P]),
     "tf_profile_enable": (ctypes.c_int, [_P, _I32]),
     "tf_profile_read": (ctypes.c_int, [_P, _I32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_I64)]),
 }
@@ -566,6 +601,150 @@ def tf_paged_mla_shared_plan_info(S: int, R: int, H: int, lens, group_sizes, pre
     _check(lib().tf_paged_mla_shared_plan_info(S, R, H, p, pg, len(g), pf, sms, ctypes.byref(info), bounds.ctypes.data),
            "tf_paged_mla_shared_plan_info")
     return _unit_plan(info, bounds)
+
+
+# ---- the prompt path (include/tf_prompt.h) ----
+
+def tf_rope_make(dim: int, layout: int = TF_ROPE_INTERLEAVED, base: float = 10000.0, scaling: int = TF_ROPE_PLAIN,
+                 factor: float = 1.0, original: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                 amplitude: float = 0.0) -> tf_rope:
+    """The table of rotary frequencies that tf_rope_apply and tf_paged_append_rope take; made once, kept by the caller."""
+    out = tf_rope()
+    desc = tf_rope_desc(dim, layout, scaling, 0, base, factor, original, beta_fast, beta_slow, amplitude)
+    _check(lib().tf_rope_make(ctypes.byref(desc), ctypes.byref(out)), "tf_rope_make")
+    return out
+
+
+def _sum(a) -> int:
+    """The rows of a packed call."""
+    return sum(a) if type(a) is array.array else int(a.sum())
+
+
+def _rows_form(t, n: int, width: int, bf16) -> bool:
+    """bf16 [n][width], each row's values side by side."""
+    return t.dtype is bf16 and t.dim() == 2 and t.shape[0] == n and t.shape[1] == width and t.stride(1) == 1
+
+
+def _heads_form(t, n: int, heads: int, width: int, bf16) -> bool:
+    """bf16 [n][heads][width], each head's values side by side."""
+    return t.dtype is bf16 and t.dim() == 3 and tuple(t.shape) == (n, heads, width) and t.stride(2) == 1
+
+
+def _row_stride(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _strides(t):
+    """(row, head) of [rows][heads][width]; of a single row or head any that is allowed."""
+    row, head, _ = t.stride()
+    n, heads, width = t.shape
+    return row if n > 1 else heads * width, head if heads > 1 else width
+
+
+def tf_rope_apply(rope: tf_rope, pos, n, x, y=None, stream=None) -> None:
+    """x: bf16 CUDA tensor [rows][H][rope.dim], the values to turn (a slice of a head's values, for instance); y: the
+    same shape, or None: in place.  n[s] rows of stream s, packed, the first of them at position pos[s]."""
+    y = x if y is None else y
+    a, p = _i64(pos)
+    b, pn = _i64(n)
+    bf16 = _dtypes()[0]
+    rows, H = int(x.shape[0]), int(x.shape[1])
+    if not (len(a) == len(b) and _sum(b) == rows and _heads_form(x, rows, H, rope.dim, bf16) and
+            _heads_form(y, rows, H, rope.dim, bf16)):
+        _refuse("tf_rope_apply")
+    if not (x.is_cuda and y.get_device() == x.get_device()):
+        raise TFError(TF_E_ARG, "tf_rope_apply (tensors that are not on one GPU)")
+    xr, xh = _strides(x)
+    yr, yh = _strides(y)
+    _check(lib().tf_rope_apply(ctypes.addressof(rope), p, pn, len(b), H, x.data_ptr(), xr, xh, y.data_ptr(), yr, yh,
+                               _stream(stream)), "tf_rope_apply")
+
+
+def tf_paged_append_rope(pool: KVPool, cache: int, pt, max_pages: int, pos, n, rows, gain=None, eps: float = 1e-6,
+                         rope: tf_rope | None = None, stream=None) -> None:
+    """rows: bf16 CUDA tensor [sum of n][576], 512 latent and 64 rope values, n[s] rows of stream s from its row pos[s]
+    on; gain: bf16 [512], the latent's RMS norm (None: none); rope: a table of dim 64 (None: the key as it is)."""
+    a, p = _i64(pos)
+    b, pn = _i64(n)
+    bf16, _, i32 = _dtypes()
+    if not (len(a) == len(b) and _rows_form(rows, _sum(b), 576, bf16) and (gain is None or _dense(gain, bf16, 512)) and
+            _table(pt, max_pages, len(b), i32)):
+        _refuse("tf_paged_append_rope")
+    dev = pool.device
+    if not (rows.get_device() == dev and _on(dev, gain) and _on(dev, pt)):
+        _elsewhere("tf_paged_append_rope")
+    _check(lib().tf_paged_append_rope(pool.handle, cache, _ptr(pt), max_pages, p, pn, len(b), rows.data_ptr(),
+                                      _row_stride(rows), _ptr(gain), eps, None if rope is None else ctypes.addressof(rope),
+                                      _stream(stream)), "tf_paged_append_rope")
+
+
+def tf_paged_read(pool: KVPool, cache: int, pt, max_pages: int, start, n, latent=None, rope=None, stream=None) -> None:
+    """latent: bf16 CUDA tensor [sum of n][512], rope: bf16 [sum of n][64] (either may be None): rows start[s] ..
+    start[s] + n[s] - 1 of every stream s, packed."""
+    a, p = _i64(start)
+    b, pn = _i64(n)
+    bf16, _, i32 = _dtypes()
+    rows = _sum(b)
+    if not (len(a) == len(b) and (latent is None or _rows_form(latent, rows, 512, bf16)) and
+            (rope is None or _rows_form(rope, rows, 64, bf16)) and _table(pt, max_pages, len(b), i32)):
+        _refuse("tf_paged_read")
+    dev = pool.device
+    if not (_on(dev, latent) and _on(dev, rope) and _on(dev, pt)):
+        _elsewhere("tf_paged_read")
+    _check(lib().tf_paged_read(pool.handle, cache, _ptr(pt), max_pages, p, pn, len(b), _ptr(latent),
+                               0 if latent is None else _row_stride(latent), _ptr(rope), 0 if rope is None else _row_stride(rope),
+                               _stream(stream)), "tf_paged_read")
+
+
+def tf_prompt_workspace_bytes(nq, nk, H: int, Hkv: int, dqk: int, dv: int, causal: bool = True) -> int:
+    a, p = _i64(nq)
+    b, pk = _i64(nk)
+    if len(a) != len(b):
+        _refuse("tf_prompt_workspace_bytes")
+    return int(lib().tf_prompt_workspace_bytes(p, pk, len(a), H, Hkv, dqk, dv, 1 if causal else 0))
+
+
+def _heads(t) -> tf_heads:
+    row, head = _strides(t)
+    return tf_heads(t.data_ptr(), row, head)
+
+
+def tf_prompt_attend(pool: KVPool, nq, nk, q, k, v, scale: float, out, lse=None, kr=None, causal: bool = True, ws=None,
+                     stream=None) -> None:
+    """q: bf16 CUDA tensor [sum of nq][H][dqk]; k: bf16 [sum of nk][Hkv][dqk] (dqk - 64 with kr: bf16 [sum of nk][64], the
+    last 64 values of every head's keys); v: bf16 [sum of nk][Hkv][dv]; out: bf16 [sum of nq][H][dv]; lse: fp32 [sum of
+    nq][H] or None; ws: uint8 workspace.  Rows and heads may be strided."""
+    a, p = _i64(nq)
+    b, pk = _i64(nk)
+    bf16, f32, _ = _dtypes()
+    rows, H, dqk = q.shape
+    keys, Hkv, dv = v.shape
+    if not (len(a) == len(b) and _sum(a) == rows and _sum(b) == keys and _heads_form(q, rows, H, dqk, bf16) and
+            _heads_form(k, keys, Hkv, dqk - (0 if kr is None else 64), bf16) and _heads_form(v, keys, Hkv, dv, bf16) and
+            _heads_form(out, rows, H, dv, bf16) and (kr is None or _rows_form(kr, keys, 64, bf16)) and
+            (lse is None or _dense(lse, f32, rows * H))):
+        _refuse("tf_prompt_attend")
+    dev = pool.device
+    if not (q.get_device() == dev and k.get_device() == dev and v.get_device() == dev and out.get_device() == dev and
+            _on(dev, kr) and _on(dev, lse) and _on(dev, ws)):
+        _elsewhere("tf_prompt_attend")
+    hq, hk, hv, ho = _heads(q), _heads(k), _heads(v), _heads(out)
+    _check(lib().tf_prompt_attend(pool.handle, p, pk, len(a), H, Hkv, dqk, dv, ctypes.addressof(hq), ctypes.addressof(hk),
+                                  _ptr(kr), 0 if kr is None else _row_stride(kr), ctypes.addressof(hv), scale,
+                                  1 if causal else 0, ctypes.addressof(ho), _ptr(lse), _ptr(ws),
+                                  0 if ws is None else ws.nbytes, _stream(stream)), "tf_prompt_attend")
+
+
+def tf_prompt_plan_info(nq, nk, H: int, Hkv: int, dqk: int, dv: int, causal: bool = True, sms: int = 0) -> dict:
+    """The work plan of tf_prompt_attend (host arithmetic, nothing launched): items, rows, splits, slots."""
+    a, p = _i64(nq)
+    b, pk = _i64(nk)
+    if len(a) != len(b):
+        _refuse("tf_prompt_plan_info")
+    info = tf_prompt_plan()
+    _check(lib().tf_prompt_plan_info(p, pk, len(a), H, Hkv, dqk, dv, 1 if causal else 0, sms, ctypes.addressof(info)),
+           "tf_prompt_plan_info")
+    return {f: int(getattr(info, f)) for f, _ in tf_prompt_plan._fields_}
 
 
 def tf_launch_count() -> int:

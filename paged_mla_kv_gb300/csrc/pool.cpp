@@ -47,17 +47,6 @@ ProfScope::~ProfScope() {
 
 using namespace tf;
 
-// Plans, page bookkeeping and a host thread's first launch take host memory, and no exception leaves a C
-// entry: what runs out of it returns TF_E_NOMEM.
-template <typename F>
-static int no_throw(F &&f) {
-    try {
-        return f();
-    } catch (...) {
-        return TF_E_NOMEM;
-    }
-}
-
 static bool desc_ok(const tf_kvpool_desc *d) {
     // the poison and state-copy launches put the caches on the grid's y dimension (at most 65,535)
     return d && d->num_caches >= 1 && d->num_caches <= 65535 && d->num_pages >= 1 && d->page_rows == kPageRows &&

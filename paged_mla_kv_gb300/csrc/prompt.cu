@@ -1,0 +1,911 @@
+// Attention of packed prompts whose heads have keys and values of their own (include/tf_prompt.h): the form
+// of the attention that a layer uses where the projected keys cost less than the absorbed ones (2 (192 + 128)
+// operations a query, key and head against 2 (576 + 512)).
+//
+//   S = Q K^T            [128 query rows x 128 keys], tcgen05, accumulated in TMEM
+//   P = 2^(c S - m)      c = scale log2(e); the running maximum m moves only when a row passes it by 2^8
+//   O = O + P V          P in TMEM (over S), V as it lies (MN-major)
+//   out = O / l, lse = (m + log2 l) ln 2
+//
+// A query tile is 128 rows: tokens times the H / Hkv heads that share a key head, so that the keys of a
+// single token's heads are read once.  A work item is a key head and a block of one or two such tiles over a
+// range of 128-key tiles; two softmax warpgroups keep a tile each.  With two query tiles each takes one of
+// them, over the same keys; with one, they take every other key tile of it and join what they have at the end.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <climits>
+#include <memory>
+
+#include "per_device.h"
+#include "ptx.cuh"
+#include "tf_internal.h"
+
+namespace tf {
+
+namespace prm {
+
+constexpr int BM = 128;              // rows of a query tile
+constexpr int BN = 128;              // keys of a tile
+constexpr int BOX = 64;              // values of a box's row: 128 bytes, one swizzle atom
+constexpr int VH = 64;               // keys of a half of a value tile
+constexpr int THREADS = 384;         // two softmax warpgroups, and one with the MMA warp and the TMA warp
+// Registers a thread: 168 at launch, of which the third warpgroup gives 80 to the others (2 * 208 + 88 = 3 * 168).
+constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 88;
+static_assert(2 * REGS_SOFTMAX + REGS_OTHER <= 3 * 168, "a split above the launch's total would wait forever");
+constexpr int MMA_WARP = 8, TMA_WARP = 9;
+constexpr int MAX_SMS = TF_PLAN_MAX_RANGES;
+
+// Shared memory (bytes): the two query tiles, KS key tiles, VS halves of value tiles; 224 KB in each form.
+template <int DQK, int DV>
+struct Lay {
+    static constexpr int QB = DQK / BOX, VB = DV / BOX;
+    static constexpr int Q_TILE = BM * DQK * 2, K_TILE = BN * DQK * 2, V_HALF = VH * DV * 2;
+    static constexpr int KS = DQK == 192 ? 2 : DQK == 128 ? 3 : 6;
+    static constexpr int VS = (229376 - 2 * Q_TILE - KS * K_TILE) / V_HALF;
+    static constexpr int OFF_K = 2 * Q_TILE, OFF_V = OFF_K + KS * K_TILE, BYTES = OFF_V + VS * V_HALF;
+    static_assert(BYTES == 229376 && VS >= 2, "fills the 224 KB");
+};
+
+struct Ctl {
+    uint64_t q_full, q_free;
+    uint64_t k_full[6], k_free[6];
+    uint64_t v_full[12], v_free[12];
+    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t join_full, join_free;   // 32 columns of warpgroup 1's sums
+    uint64_t next_full[2], next_free[2];
+    uint64_t drain;
+    alignas(16) uint4 next[2];       // the answer to "another item?"
+    float2 ml[BM];                   // warpgroup 1's (m, l) of each row, for the join
+    uint32_t tmem;
+    int abort;
+};
+constexpr int SMEM = 229376 + 1024 + (int)((sizeof(Ctl) + 127) / 128 * 128);
+static_assert(SMEM <= 232448, "227 KB");
+
+// Streams in the order of their work, the longest first.
+struct Params {
+    CUtensorMap q, k, kr, v;
+    uint16_t *out;
+    float *lse;
+    float *part;                     // [slots][BM][DV], then (m, l) [slots][BM]
+    DevErr *err;
+    int64_t out_row, out_head, slots;
+    float scale_log2, thr;           // c; 8 / c
+    int32_t S, H, Hkv, G, tpt, causal, has_kr;   // tpt: tokens of a query tile
+    int32_t item0[TF_MAX_STREAMS];   // first item
+    int32_t qoff[TF_MAX_STREAMS], nq[TF_MAX_STREAMS], koff[TF_MAX_STREAMS], nk[TF_MAX_STREAMS];
+    int32_t chunk[TF_MAX_STREAMS];   // key tiles of a split
+    int32_t slot0[TF_MAX_STREAMS];   // first slot of a stream whose keys are split, or -1
+    int16_t nsp[TF_MAX_STREAMS];     // splits
+    int16_t hg[TF_MAX_STREAMS];      // key heads side by side
+};
+
+__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// What an item is.  Items of a stream: groups of hg key heads; in a group blocks from the last (the longest of a
+// causal prompt) to the first, in a block its splits, in a split the group's heads.  The heads of a group read
+// keys that fit L2 together, and blocks of one head share them there.
+struct Item {
+    int st, h, blk, sp;      // stream (in Params order), key head, block, split
+    int tok0, ntok;          // first token in the stream, tokens
+    bool pair;               // two query tiles
+    int c0;                  // first key tile
+    int n0, n1;              // key tiles of each warpgroup
+    int slot;                // slot of query tile 0, or -1
+
+    __device__ __forceinline__ int n(int w) const { return w ? n1 : n0; }
+
+    __device__ __forceinline__ void decode(const Params &p, int i) {
+        st = 0;
+        for (int a = p.S - 1; st < a;) {
+            const int mid = (st + a + 1) >> 1;
+            if (p.item0[mid] <= i) st = mid; else a = mid - 1;
+        }
+        const int nq = p.nq[st], nsp = p.nsp[st], hg = p.hg[st];
+        const int blocks = ceil_div(nq, 2 * p.tpt);
+        int x = i - p.item0[st];
+        const int per = blocks * nsp * hg, g = x / per;
+        x -= g * per;
+        const int heads = min(hg, p.Hkv - g * hg);
+        const int b = x / (nsp * heads);
+        x -= b * nsp * heads;
+        sp = x / heads;
+        h = g * hg + x - sp * heads;
+        blk = blocks - 1 - b;
+        tok0 = blk * 2 * p.tpt;
+        ntok = min(nq - tok0, 2 * p.tpt);
+        pair = ntok > p.tpt;
+        c0 = sp * p.chunk[st];
+        const int t0 = tiles(p, min(ntok, p.tpt)), t1 = tiles(p, ntok);
+        const int end = c0 + p.chunk[st];
+        if (pair) {
+            n0 = max(0, min(end, t0) - c0);
+            n1 = max(0, min(end, t1) - c0);
+        } else {
+            const int m = max(0, min(end, t0) - c0);
+            n0 = (m + 1) / 2;
+            n1 = m / 2;
+        }
+        slot = p.slot0[st] < 0 ? -1 : p.slot0[st] + ((h * blocks + blk) * nsp + sp) * 2;
+    }
+    // Keys that the first `t` tokens of the block see at most.
+    __device__ __forceinline__ int seen(const Params &p, int t) const {
+        const int nk = p.nk[st];
+        if (!p.causal) return nk;
+        return max(0, min(nk, nk - p.nq[st] + tok0 + t));
+    }
+    __device__ __forceinline__ int tiles(const Params &p, int t) const { return ceil_div(seen(p, t), BN); }
+    // Key tile of warpgroup w's step j.
+    __device__ __forceinline__ int key_tile(int w, int j) const { return pair ? c0 + j : c0 + 2 * j + w; }
+    // Keys of that tile that any row of warpgroup w's query tile sees, rounded up to the 16 of a product step.
+    __device__ __forceinline__ int steps(const Params &p, int w, int kt) const {
+        const int t = pair ? (w ? ntok : p.tpt) : ntok;
+        return min(BN / 16, ceil_div(seen(p, t) - kt * BN, 16));
+    }
+};
+
+// ---- the next item: a CTA that has not been launched yet is taken over (cluster launch control) ----
+__device__ __forceinline__ void ask_next(uint4 *dst, uint64_t *bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     ptx::smem_u32(dst)),
+                 "r"(ptx::smem_u32(bar))
+                 : "memory");
+}
+// Its index, or -1 when there is none left.
+__device__ __forceinline__ int read_next(const uint4 *src) {
+    uint64_t a, b;
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(ptx::smem_u32(src)) : "memory");
+    int r;
+    asm volatile(
+        "{\n\t.reg .b128 x;\n\t.reg .pred c;\n\t"
+        "mov.b128 x, {%1, %2};\n\t"
+        "mov.u32 %0, -1;\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 c, x;\n\t"
+        "@c clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, x;\n\t}"
+        : "=r"(r)
+        : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, uint64_t *bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(ptx::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(ptx::smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+// `n` (1 to 4) products of 16 keys: P from TMEM (8 columns a step), V MN-major (two 1 KB groups of 8 keys a step).
+__device__ __forceinline__ void pv_warp(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, int n) {
+#pragma unroll 1
+    for (int i = 0; i < n; ++i, a += 8, b += 2048 >> 4, acc = 1) ptx::mma_bf16_ts_warp(d, a, b, idesc, acc);
+}
+
+// ptx::mbar_wait_warp without the call to its polling loop: a call would hold the registers around it to
+// what the whole kernel was launched with.  Bounded in the same way.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort, DevErr *err, int site,
+                                     long long limit = 1ll << 31) {
+    bool done = ptx::mbar_try_wait(bar, parity);
+    if (!done) {
+        const long long t0 = clock64();
+        for (uint32_t spins = 1; !(done = ptx::mbar_try_wait(bar, parity)); ++spins) {
+            if ((spins & 255u) != 0) continue;
+            if (*abort) break;
+            if (clock64() - t0 > limit) {
+                ptx::record_error(err, TF_E_TIMEOUT, site);
+                *abort = 1;
+                break;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, done);
+}
+
+// What every role walks: the items of this CTA.
+struct Walk {
+    int i, count;   // the item, how many came before
+    __device__ __forceinline__ Walk() : i((int)blockIdx.x), count(0) {}
+    // The item after this one; false at the end or after a timeout.  `who` frees the answer.
+    __device__ __forceinline__ bool next(Ctl &c, const Params &p, bool who) {
+        const int b = count & 1;
+        if (!wait(&c.next_full[b], (uint32_t)(count >> 1) & 1, &c.abort, p.err, 50)) return false;
+        i = read_next(&c.next[b]);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (who) ptx::mbar_arrive(&c.next_free[b]);
+        ++count;
+        return i >= 0;
+    }
+};
+
+template <int DQK, int DV>
+__global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constant__ Params p) {
+    using L = Lay<DQK, DV>;
+    extern __shared__ uint8_t raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    Ctl &c = *reinterpret_cast<Ctl *>(smem + L::BYTES);
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = (int)threadIdx.x & 31;
+
+    ptx::griddep_launch_dependents();
+    if (threadIdx.x == 0) {
+        c.abort = 0;
+        ptx::mbar_init(&c.q_full, 1);
+        ptx::mbar_init(&c.q_free, 5);   // the last product with the queries, warpgroup 0's warps
+        for (int i = 0; i < L::KS; ++i) ptx::mbar_init(&c.k_full[i], 1), ptx::mbar_init(&c.k_free[i], 1);
+        for (int i = 0; i < L::VS; ++i) ptx::mbar_init(&c.v_full[i], 1), ptx::mbar_init(&c.v_free[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&c.s_full[i], 1);
+            ptx::mbar_init(&c.p_full[i], 4);
+            ptx::mbar_init(&c.o_full[i], 1);
+            ptx::mbar_init(&c.next_full[i], 1);
+            ptx::mbar_init(&c.next_free[i], 10);
+        }
+        ptx::mbar_init(&c.join_full, 4);
+        ptx::mbar_init(&c.join_free, 4);
+        ptx::mbar_init(&c.drain, 1);
+        ptx::fence_mbar_init();
+    }
+    if (warp == MMA_WARP) {
+        ptx::tmem_alloc(&c.tmem, 512);
+        ptx::tmem_relinquish();
+    }
+    if (warp == TMA_WARP && lane == 0) {
+        ptx::prefetch_tmap(&p.q);
+        ptx::prefetch_tmap(&p.k);
+        ptx::prefetch_tmap(&p.v);
+        if (p.has_kr) ptx::prefetch_tmap(&p.kr);
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = c.tmem;
+    ptx::griddep_wait();
+
+    if (warp == TMA_WARP) {
+        // ================= TMA, and the question for the next item =================
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+        uint32_t nk = 0, nv = 0;   // key tiles and halves of value tiles so far
+        int asked = 0;
+        bool ok = true;
+        Walk it;
+        int nq = 0;
+        do {
+            Item x;
+            x.decode(p, it.i);
+            // the next item, while this one runs
+            {
+                const int b = it.count & 1;
+                if (it.count >= 2 && !wait(&c.next_free[b], (uint32_t)(it.count / 2 - 1) & 1, &c.abort, p.err, 51)) break;
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(&c.next_full[b], 16);
+                    ask_next(&c.next[b], &c.next_full[b]);
+                }
+                ++asked;
+                __syncwarp();
+            }
+            const int row = p.koff[x.st];
+            if (x.n0 + x.n1 > 0) {
+                if (nq > 0 && !wait(&c.q_free, (uint32_t)(nq - 1) & 1, &c.abort, p.err, 52)) break;
+                if (lane == 0) {
+                    const int tiles = x.pair ? 2 : 1;
+                    ptx::mbar_arrive_expect_tx(&c.q_full, (uint32_t)(tiles * L::QB * p.tpt * p.G * 128));
+                    for (int w = 0; w < tiles; ++w)
+                        for (int b = 0; b < L::QB; ++b)
+                            tma_load_3d(smem + w * L::Q_TILE + b * (BM * 128), &p.q, &c.q_full, b * BOX, x.h * p.G,
+                                        p.qoff[x.st] + x.tok0 + w * p.tpt);
+                }
+                ++nq;
+                __syncwarp();
+            }
+            auto load_k = [&](int kt) {
+                const int st = (int)(nk % L::KS);
+                const uint32_t use = nk / L::KS;
+                if (use > 0 && !wait(&c.k_free[st], (uint32_t)(use - 1) & 1, &c.abort, p.err, 53)) return false;
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(&c.k_full[st], L::K_TILE);
+                    uint8_t *dst = smem + L::OFF_K + st * L::K_TILE;
+                    for (int b = 0; b < L::QB; ++b) {
+                        const bool shared = p.has_kr && b == L::QB - 1;
+                        tma_load_3d(dst + b * (BN * 128), shared ? &p.kr : &p.k, &c.k_full[st], shared ? 0 : b * BOX,
+                                    shared ? 0 : x.h, row + kt * BN);
+                    }
+                }
+                ++nk;
+                __syncwarp();
+                return true;
+            };
+            auto load_v = [&](int kt) {
+                for (int half = 0; half < 2; ++half, ++nv) {
+                    const int st = (int)(nv % L::VS);
+                    const uint32_t use = nv / L::VS;
+                    if (use > 0 && !wait(&c.v_free[st], (uint32_t)(use - 1) & 1, &c.abort, p.err, 54)) return false;
+                    if (lane == 0) {
+                        ptx::mbar_arrive_expect_tx(&c.v_full[st], L::V_HALF);
+                        uint8_t *dst = smem + L::OFF_V + st * L::V_HALF;
+                        for (int b = 0; b < L::VB; ++b)
+                            tma_load_3d(dst + b * (VH * 128), &p.v, &c.v_full[st], b * BOX, x.h, row + kt * BN + half * VH);
+                    }
+                    __syncwarp();
+                }
+                return true;
+            };
+            // in the order in which the MMA warp takes them
+            if (x.pair) {
+                if (x.n1 > 0) ok = load_k(x.key_tile(1, 0));
+                for (int j = 0; ok && j < x.n1; ++j) {
+                    ok = load_v(x.key_tile(1, j));
+                    if (ok && j + 1 < x.n1) ok = load_k(x.key_tile(1, j + 1));
+                }
+            } else {
+                for (int w = 0; ok && w < 2; ++w)
+                    if (x.n(w) > 0) ok = load_k(x.key_tile(w, 0));
+                for (int j = 0; ok && j < x.n0; ++j)
+                    for (int w = 0; ok && w < 2; ++w) {
+                        if (j < x.n(w)) ok = load_v(x.key_tile(w, j));
+                        if (ok && j + 1 < x.n(w)) ok = load_k(x.key_tile(w, j + 1));
+                    }
+            }
+            if (!ok) break;
+        } while (it.next(c, p, lane == 0));
+        // no copy may still be on its way into this CTA's shared memory when it ends
+        constexpr long long LIMIT = 1ll << 28;
+        if (asked > 0) wait(&c.next_full[(asked - 1) & 1], (uint32_t)((asked - 1) >> 1) & 1, &c.abort, p.err, 55, LIMIT);
+        if (nq > 0) wait(&c.q_full, (uint32_t)(nq - 1) & 1, &c.abort, p.err, 55, LIMIT);
+        for (uint32_t n = nk > L::KS ? nk - L::KS : 0; n < nk; ++n)
+            wait(&c.k_full[n % L::KS], (n / L::KS) & 1, &c.abort, p.err, 55, LIMIT);
+        for (uint32_t n = nv > L::VS ? nv - L::VS : 0; n < nv; ++n)
+            wait(&c.v_full[n % L::VS], (n / L::VS) & 1, &c.abort, p.err, 55, LIMIT);
+        __syncwarp();
+    } else if (warp == MMA_WARP) {
+        // ================= MMA =================
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+        const uint64_t dq = ptx::sdesc_sw128(ptx::smem_u32(smem), 16, 1024);
+        const uint64_t dk = ptx::sdesc_sw128(ptx::smem_u32(smem + L::OFF_K), 16, 1024);
+        const uint64_t dv = ptx::sdesc_sw128(ptx::smem_u32(smem + L::OFF_V), VH * 128, 1024);
+        constexpr uint32_t IQK = ptx::idesc_bf16_f32(BM, BN, false, false);
+        constexpr uint32_t IPV = ptx::idesc_bf16_f32(BM, DV, false, true);
+        uint32_t nk = 0, nv = 0;
+        uint32_t np0 = 0, np1 = 0;   // softmax tiles of each warpgroup so far
+        int nq = 0;
+        bool ok = true;
+        Walk it;
+        do {
+            Item x;
+            x.decode(p, it.i);
+            if (x.n0 + x.n1 == 0) continue;
+            if (!wait(&c.q_full, (uint32_t)nq & 1, &c.abort, p.err, 60)) break;
+            ++nq;
+            // Key tile number k of the item: with two query tiles step k of both, else step k / 2 of k % 2.
+            auto qk = [&](int w, int j) {
+                const uint32_t k = nk + (x.pair ? j : 2 * j + w);
+                const int st = (int)(k % L::KS);
+                const bool first = !x.pair || w == 0 || j >= x.n0;
+                if (first && !wait(&c.k_full[st], (uint32_t)(k / L::KS) & 1, &c.abort, p.err, 61)) return false;
+                ptx::tc_fence_after();
+                const uint64_t a = dq + (uint64_t)(((x.pair ? w : 0) * L::Q_TILE) >> 4);
+                const uint64_t b = dk + (uint64_t)((st * L::K_TILE) >> 4);
+#pragma unroll 1
+                for (int i = 0; i < L::QB; ++i)
+                    ptx::mma4_bf16_ss_warp(tmem + w * BN, a + (uint64_t)((i * BM * 128) >> 4), b + (uint64_t)((i * BN * 128) >> 4),
+                                           IQK, i == 0);
+                ptx::mma_commit_warp(&c.s_full[w]);
+                if (!x.pair || w == 1) ptx::mma_commit_warp(&c.k_free[st]);
+                return true;
+            };
+            auto pv = [&](int w, int j) {
+                if (!wait(&c.p_full[w], (w ? np1 : np0) & 1, &c.abort, p.err, 62)) return false;
+                if (w) ++np1; else ++np0;
+                const uint32_t k = nv + 2 * (x.pair ? j : 2 * j + w);
+                const int steps = x.steps(p, w, x.key_tile(w, j));
+                const bool first = !x.pair || w == 0 || j >= x.n0;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    const int st = (int)((k + half) % L::VS);
+                    if (first && !wait(&c.v_full[st], (uint32_t)((k + half) / L::VS) & 1, &c.abort, p.err, 63)) return false;
+                    ptx::tc_fence_after();
+                    pv_warp(tmem + 2 * BN + w * DV, tmem + w * BN + half * 32, dv + (uint64_t)((st * L::V_HALF) >> 4), IPV,
+                            j > 0 || half > 0, min(4, steps - 4 * half));
+                    if (!x.pair || w == 1) ptx::mma_commit_warp(&c.v_free[st]);
+                }
+                if (j == x.n(w) - 1) ptx::mma_commit_warp(&c.o_full[w]);
+                return true;
+            };
+            for (int w = 0; ok && w < 2; ++w)
+                if (x.n(w) > 0) ok = qk(w, 0);
+            const int steps = max(x.n0, x.n1);
+            if (ok && steps == 1) ptx::mma_commit_warp(&c.q_free);
+#pragma unroll 1
+            for (int j = 0; ok && j < steps; ++j)
+#pragma unroll 1
+                for (int w = 0; ok && w < 2; ++w) {
+                    if (j >= x.n(w)) continue;
+                    ok = pv(w, j);
+                    if (ok && j + 1 < x.n(w)) ok = qk(w, j + 1);
+                    // the last product with the queries: warpgroup 1's when both have as many steps
+                    if (ok && j + 2 == steps && w == (x.n1 == steps)) ptx::mma_commit_warp(&c.q_free);
+                }
+            if (!ok) break;
+            nk += x.pair ? x.n1 : x.n0 + x.n1;
+            nv += 2 * (x.pair ? x.n1 : x.n0 + x.n1);
+        } while (it.next(c, p, lane == 0));
+        // no product may still run when TMEM is freed
+        ptx::mma_commit_warp(&c.drain);
+        wait(&c.drain, 0, &c.abort, p.err, 64, 1ll << 29);
+        __syncwarp();
+    } else if (warp < 8) {
+        // ================= softmax, and the output: a query row a thread =================
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
+        const int w = warp >> 2;
+        const int row = (int)threadIdx.x & (BM - 1);
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + w * BN + lanes, to = tmem + 2 * BN + w * DV + lanes;
+        const float cl = p.scale_log2;
+        const int rt = row / p.G, rh = row - rt * p.G;   // the row's token in the tile, and its head
+        uint32_t ns = 0, nv = 0;
+        int no = 0, nj = 0;   // outputs, joined pieces so far
+        bool ok = true;
+        Walk it;
+        do {
+            Item x;
+            x.decode(p, it.i);
+            const int n = x.n(w);
+            const int tok = x.tok0 + (x.pair ? w * p.tpt : 0) + rt;
+            const bool live = rt < p.tpt && tok < x.tok0 + x.ntok;
+            // keys that the row sees; rows of no token take whatever comes, and a warp of them nothing at all
+            const int vis = live ? x.seen(p, tok - x.tok0 + 1) : INT_MAX;
+            const bool idle = __all_sync(0xffffffffu, !live);
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; ok && j < n; ++j, ++ns) {
+                const int kt = x.key_tile(w, j);
+                const int limit = vis - kt * BN;   // columns of this tile that the row sees
+                if (!wait(&c.s_full[w], (uint32_t)ns & 1, &c.abort, p.err, 70)) {
+                    ok = false;
+                    break;
+                }
+                // rows of the value tile behind the stream's last key: whatever they hold, 0 times it has to be 0
+                const int tail = p.nk[x.st] - kt * BN;
+                if (tail < BN && (tail & 15)) {
+                    const uint32_t k = nv + 2 * (x.pair ? j : 2 * j + w) + (tail >= VH);
+                    const int st = (int)(k % L::VS);
+                    if (!wait(&c.v_full[st], (uint32_t)(k / L::VS) & 1, &c.abort, p.err, 71)) {
+                        ok = false;
+                        break;
+                    }
+                    const int r0 = tail & (VH - 1), r1 = (r0 + 15) & ~15;
+                    uint8_t *dst = smem + L::OFF_V + st * L::V_HALF;
+                    for (int i = row; i < (r1 - r0) * 8 * L::VB; i += BM) {   // 16-byte chunks, whatever their order in a row
+                        const int b = i / ((r1 - r0) * 8), y = i - b * (r1 - r0) * 8;
+                        *reinterpret_cast<uint4 *>(dst + b * (VH * 128) + (r0 + y / 8) * 128 + (y % 8) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    ptx::fence_proxy_async_smem();
+                }
+                if (idle) {
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&c.p_full[w]);
+                    continue;
+                }
+                ptx::tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) ptx::tmem_ld32(ts + 32 * q, s[q]);
+                ptx::tmem_ld_wait();
+                if (__any_sync(0xffffffffu, limit < BN)) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (q * 32 + i >= limit) s[q][i] = 0xFF800000u;
+                }
+                float mx[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    mx[q] = __uint_as_float(s[q][0]);
+#pragma unroll
+                    for (int i = 1; i < 32; ++i) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][i]));
+                }
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                // the maximum moves only by more than 2^8: P stays far below bf16's largest value
+                const bool move = top > m + p.thr || (m == -INFINITY && top > m);
+                if (__any_sync(0xffffffffu, move)) {
+                    float f = 1.f;
+                    if (move) {
+                        f = m == -INFINITY ? 0.f : ptx::ex2((m - top) * cl);
+                        m = top;
+                        l *= f;
+                    }
+                    if (j > 0) {   // O up to the tile before: its products are done, S of this one came after them
+#pragma unroll 1
+                        for (int q = 0; q < DV; q += 32) {
+                            uint32_t o[32];
+                            ptx::tmem_ld32(to + q, o);
+                            ptx::tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            ptx::tmem_st32(to + q, o);
+                        }
+                    }
+                }
+                const float mc = m == -INFINITY ? 0.f : m * cl;
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int q = 0; q < 4; q += 2) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const uint32_t (&v)[32] = s[q + i / 16];
+                        const float2 t = ptx::fma2(make_float2(__uint_as_float(v[2 * i % 32]), __uint_as_float(v[2 * i % 32 + 1])),
+                                                   make_float2(cl, cl), make_float2(-mc, -mc));
+                        const float2 e = make_float2(ptx::ex2(t.x), ptx::ex2(t.y));
+                        sum[i & 1] = ptx::add2(sum[i & 1], e);
+                        pk[i] = ptx::pack_bf16x2(e.x, e.y);
+                    }
+                    ptx::tmem_st32(ts + 16 * q, pk);
+                }
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&c.p_full[w]);
+            }
+            if (ok && n > 0) {
+                ok = wait(&c.o_full[w], (uint32_t)no & 1, &c.abort, p.err, 72);
+                ++no;
+                ptx::tc_fence_after();
+            }
+            if (!ok) break;
+            nv += 2 * (x.pair ? x.n1 : x.n0 + x.n1);
+            // One query tile: warpgroup 1's sums join warpgroup 0's, 32 columns at a time through the room of
+            // query tile 1 (row by row: warp i of one with warp i of the other).
+            const bool join = !x.pair && x.n1 > 0;
+            float f0 = 1.f, f1 = 0.f;
+            float *xch = reinterpret_cast<float *>(smem + L::Q_TILE);   // [32][BM]
+            const bool writes = live && (x.pair || w == 0);
+            const bool direct = x.slot < 0;
+            float inv = direct ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+            const int64_t orow = (int64_t)p.qoff[x.st] + tok;
+            const int head = x.h * p.G + rh;
+            uint16_t *out = p.out + orow * p.out_row + head * p.out_head;
+            const int64_t slot = (int64_t)x.slot + (x.pair ? w : 0);
+            float *part = p.part + (slot * BM + row) * DV;
+#pragma unroll 1
+            for (int q = 0; q < DV; q += 32) {
+                uint32_t o[32];
+                if (n > 0) {
+                    ptx::tmem_ld32(to + q, o);
+                    ptx::tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = 0u;
+                }
+                if (join && w == 1) {
+                    if (nj > 0 && !wait(&c.join_free, (uint32_t)(nj - 1) & 1, &c.abort, p.err, 73)) {
+                        ok = false;
+                        break;
+                    }
+                    if (q == 0) c.ml[row] = make_float2(m, l);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) xch[i * BM + row] = __uint_as_float(o[i]);
+                    ptx::fence_proxy_async_smem();   // queries are copied here next
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&c.join_full);
+                    ++nj;
+                } else if (join) {
+                    if (!wait(&c.join_full, (uint32_t)nj & 1, &c.abort, p.err, 74)) {
+                        ok = false;
+                        break;
+                    }
+                    ++nj;
+                    if (q == 0) {
+                        const float2 other = c.ml[row];
+                        const float top = fmaxf(m, other.x);
+                        f0 = m == -INFINITY ? 0.f : ptx::ex2((m - top) * cl);
+                        f1 = other.x == -INFINITY ? 0.f : ptx::ex2((other.x - top) * cl);
+                        l = l * f0 + other.y * f1;
+                        m = top;
+                        if (direct) inv = l == 0.f ? 0.f : 1.f / l;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f0 + xch[i * BM + row] * f1);
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&c.join_free);
+                }
+                if (writes && direct) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            v[k] = ptx::pack_bf16x2(__uint_as_float(o[i + 2 * k]) * inv, __uint_as_float(o[i + 2 * k + 1]) * inv);
+                        *reinterpret_cast<uint4 *>(out + q + i) = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                } else if (writes) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<uint4 *>(part + q + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                }
+            }
+            if (!ok) break;
+            if (writes) {
+                if (!direct)
+                    reinterpret_cast<float2 *>(p.part + p.slots * BM * DV)[slot * BM + row] = make_float2(m, l);
+                else if (p.lse)
+                    p.lse[orow * p.H + head] = l == 0.f ? -INFINITY : (m * cl + log2f(l)) * 0.69314718055994531f;
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            // query tile 1's room is free again (the queries themselves: the MMA warp's arrival)
+            if (w == 0 && lane == 0 && x.n0 + x.n1 > 0) {
+                ptx::fence_proxy_async_smem();
+                ptx::mbar_arrive(&c.q_free);
+            }
+        } while (it.next(c, p, lane == 0));
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == MMA_WARP) ptx::tmem_dealloc(tmem, 512);
+}
+
+// The splits of one row joined in order: a warp a row, DV / 32 values a lane.
+template <int DV>
+__global__ void __launch_bounds__(128) prompt_combine_kernel(const __grid_constant__ Params p) {
+    ptx::griddep_launch_dependents();
+    const int lane = (int)threadIdx.x & 31;
+    const int st = (int)blockIdx.y;
+    if (p.slot0[st] < 0) return;
+    const int64_t i = (int64_t)blockIdx.x * 4 + ((int)threadIdx.x >> 5);   // (token, head), heads inner
+    const int nq = p.nq[st], nsp = p.nsp[st];
+    if (i >= (int64_t)nq * p.H) return;
+    const int tok = (int)(i / p.H), head = (int)(i - (int64_t)tok * p.H);
+    const int h = head / p.G, rh = head - h * p.G;
+    const int blocks = ceil_div(nq, 2 * p.tpt), blk = tok / (2 * p.tpt), in = tok - blk * 2 * p.tpt;
+    const int tile = in / p.tpt, row = (in - tile * p.tpt) * p.G + rh;
+    const int64_t slot = (int64_t)p.slot0[st] + (int64_t)(h * blocks + blk) * nsp * 2 + tile;
+    const float2 *ml = reinterpret_cast<const float2 *>(p.part + p.slots * BM * DV);
+    ptx::griddep_wait();
+    float m = -INFINITY;
+    for (int s = lane; s < nsp; s += 32) m = fmaxf(m, ml[(slot + 2 * s) * BM + row].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float cl = p.scale_log2;
+    constexpr int V = DV / 32;
+    float acc[V], l = 0.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < nsp; ++s) {
+        const float2 t = ml[(slot + 2 * s) * BM + row];
+        const float f = t.x == -INFINITY ? 0.f : ptx::ex2((t.x - m) * cl);
+        l = fmaf(t.y, f, l);
+        const float *src = p.part + ((slot + 2 * s) * BM + row) * DV + lane * V;
+        float v[V];
+        if (V == 4) {
+            const float4 u = *reinterpret_cast<const float4 *>(src);
+            v[0] = u.x, v[1] = u.y, v[2 % V] = u.z, v[3 % V] = u.w;
+        } else {
+            const float2 u = *reinterpret_cast<const float2 *>(src);
+            v[0] = u.x, v[1] = u.y;
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] = fmaf(v[k], f, acc[k]);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t orow = (int64_t)p.qoff[st] + tok;
+    uint16_t *out = p.out + orow * p.out_row + head * p.out_head + lane * V;
+    if (V == 4) {
+        *reinterpret_cast<uint2 *>(out) = make_uint2(ptx::pack_bf16x2(acc[0] * inv, acc[1] * inv),
+                                                     ptx::pack_bf16x2(acc[2 % V] * inv, acc[3 % V] * inv));
+    } else {
+        *reinterpret_cast<uint32_t *>(out) = ptx::pack_bf16x2(acc[0] * inv, acc[1] * inv);
+    }
+    if (lane == 0 && p.lse) p.lse[orow * p.H + head] = l == 0.f ? -INFINITY : (m * cl + log2f(l)) * 0.69314718055994531f;
+}
+
+// ---- the plan ----
+// Fills in what depends on the lengths.  Streams' keys are split where there are fewer items than SMs to
+// take them.
+struct Plan {
+    int64_t items = 0, slots = 0;
+    int splits = 1;
+};
+
+static int plan(Params &p, const int64_t *h_nq, const int64_t *h_nk, int S, int H, int Hkv, int dqk, int dv, int causal,
+                int sms, Plan *out) {
+    const int G = H / Hkv, tpt = BM / G;
+    p.H = H;
+    p.Hkv = Hkv;
+    p.G = G;
+    p.tpt = tpt;
+    p.causal = causal;
+    // streams with rows, the most key tiles first
+    struct Str {
+        int64_t tiles, blocks;
+        int32_t qoff, koff, nq, nk;
+    };
+    Str e[TF_MAX_STREAMS];
+    int n = 0;
+    int64_t q = 0, k = 0, items = 0, most = 1;
+    for (int s = 0; s < S; ++s) {
+        if (h_nq[s] > 0) {
+            const int64_t blocks = (h_nq[s] + 2 * tpt - 1) / (2 * tpt), tiles = (h_nk[s] + BN - 1) / BN;
+            e[n++] = {tiles, blocks, (int32_t)q, (int32_t)k, (int32_t)h_nq[s], (int32_t)h_nk[s]};
+            items += blocks * Hkv;
+            most = std::max(most, tiles);
+        }
+        q += h_nq[s];
+        k += h_nk[s];
+    }
+    std::stable_sort(e, e + n, [](const Str &a, const Str &b) { return a.tiles > b.tiles; });
+    // A split of `chunk` key tiles: items are then at most that long.  The chunk with the smallest estimate of
+    // the time (in key tiles): the larger of the mean load and the longest item, an item's start and end taken
+    // as START tiles, and the join's launch.
+    constexpr int64_t START = 2, JOIN = 3;
+    int64_t chunk = most;
+    if (items < sms) {
+        double best = 1e30;
+        for (int64_t c = most; c >= 1; c = c > 16 ? c - c / 8 : c - 1) {
+            int64_t cnt = 0, load = 0;
+            for (int i = 0; i < n; ++i) {
+                const int64_t sp = std::max<int64_t>(1, (e[i].tiles + c - 1) / c);
+                cnt += e[i].blocks * Hkv * sp;
+                load += e[i].blocks * Hkv * (e[i].tiles + sp * START);
+            }
+            const int64_t waves = (cnt + sms - 1) / sms;
+            const double t = std::max<double>((double)load / sms, (double)std::min<int64_t>(waves, 2) * (std::min(c, most) + START)) +
+                             (c < most ? JOIN : 0);
+            if (t < best) {
+                best = t;
+                chunk = c;
+            }
+            if (cnt > 4 * (int64_t)sms) break;
+        }
+    }
+    out->items = 0;
+    out->slots = 0;
+    out->splits = 1;
+    // heads side by side: as many as keep their keys and values within a quarter of L2
+    for (int i = 0; i < n; ++i) {
+        const int64_t sp = std::max<int64_t>(1, (e[i].tiles + chunk - 1) / chunk);
+        if (sp > INT16_MAX) return TF_E_UNSUPPORTED;
+        const int64_t bytes = std::max<int64_t>(1, (int64_t)e[i].nk * (dqk + dv) * 2);
+        p.item0[i] = (int32_t)out->items;
+        p.qoff[i] = e[i].qoff;
+        p.nq[i] = e[i].nq;
+        p.koff[i] = e[i].koff;
+        p.nk[i] = e[i].nk;
+        p.nsp[i] = (int16_t)sp;
+        p.chunk[i] = (int32_t)(sp > 1 ? chunk : std::max<int64_t>(1, e[i].tiles));
+        p.hg[i] = (int16_t)std::max<int64_t>(1, std::min<int64_t>(Hkv, (32 << 20) / bytes));
+        p.slot0[i] = sp > 1 ? (int32_t)out->slots : -1;
+        const int64_t cnt = e[i].blocks * Hkv * sp;
+        if (sp > 1) out->slots += cnt * 2;
+        out->items += cnt;
+        out->splits = std::max(out->splits, (int)sp);
+        if (out->items > INT32_MAX / 2 || out->slots > INT32_MAX / 2) return TF_E_UNSUPPORTED;
+    }
+    p.S = n;
+    p.slots = out->slots;
+    return TF_OK;
+}
+
+static size_t ws_bytes_of(const Plan &pl, int dv) {
+    return ((size_t)pl.slots * BM * (dv * 4 + 8) + 255) / 256 * 256;
+}
+
+}  // namespace prm
+
+// The current device's SMs, or an upper bound when no device answers.
+static int prompt_sms() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        return prm::MAX_SMS;
+    }
+    return std::min(n, prm::MAX_SMS);
+}
+
+// The parameter block of this host thread's next launch (a launch copies it).
+static prm::Params &prompt_params() {
+    thread_local std::unique_ptr<prm::Params> pp;
+    if (!pp) pp.reset(new prm::Params());
+    return *pp;
+}
+
+int prompt_plan(const int64_t *h_nq, const int64_t *h_nk, int S, int H, int Hkv, int dqk, int dv, int causal, int sms,
+                tf_prompt_plan *info, size_t *bytes) {
+    prm::Plan pl;
+    if (sms <= 0) sms = prompt_sms();
+    const int rc = prm::plan(prompt_params(), h_nq, h_nk, S, H, Hkv, dqk, dv, causal, std::min(sms, prm::MAX_SMS), &pl);
+    if (rc != TF_OK) return rc;
+    if (info) {
+        info->items = pl.items;
+        info->slots = pl.slots;
+        info->rows = 2 * (prm::BM / (H / Hkv)) * (H / Hkv);
+        info->splits = pl.splits;
+    }
+    if (bytes) *bytes = prm::ws_bytes_of(pl, dv);
+    return TF_OK;
+}
+
+int launch_prompt_attend(tf_kvpool *pool, const int64_t *h_nq, const int64_t *h_nk, int S, int H, int Hkv, int dqk, int dv,
+                         const tf_heads *q, const tf_heads *k, const void *d_kr, int64_t kr_row, const tf_heads *v,
+                         float scale, int causal, const tf_heads *out, float *d_lse, void *d_ws, size_t ws_bytes,
+                         cudaStream_t st) {
+    using namespace prm;
+    Params &p = prompt_params();
+    Plan pl;
+    const int sms = prompt_sms();
+    const int rc = plan(p, h_nq, h_nk, S, H, Hkv, dqk, dv, causal, sms, &pl);
+    if (rc != TF_OK) return rc;
+    const size_t need = ws_bytes_of(pl, dv);
+    if (need > 0 && (!d_ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0))
+        return d_ws && ws_bytes < need ? TF_E_NOMEM : TF_E_ARG;
+    if (pl.items == 0) return TF_OK;
+
+    using Kern = void (*)(const Params);
+    const Kern kern = dqk == 192 ? prompt_kernel<192, 128> : dqk == 128 ? prompt_kernel<128, 128> : prompt_kernel<64, 64>;
+    static PerDevice<int> ready;   // opted in to the shared memory
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return TF_E_CUDA;
+    if (!ready.get(dev, [&](int &one) {
+            one = 1;
+            bool ok = true;
+            for (const Kern f : {prompt_kernel<192, 128>, prompt_kernel<128, 128>, prompt_kernel<64, 64>})
+                ok = ok && cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) == cudaSuccess;
+            if (!ok) cudaGetLastError();
+            return ok;
+        }))
+        return TF_E_CUDA;
+
+    int64_t rows = 0, keys = 0;
+    for (int s = 0; s < S; ++s) rows += h_nq[s], keys += h_nk[s];
+    auto map = [&](CUtensorMap *tm, const void *d_p, int64_t row, int64_t head, int values, int heads, int64_t n, uint32_t box_h,
+                   uint32_t box_n) {
+        const uint64_t dims[3] = {(uint64_t)values, (uint64_t)heads, (uint64_t)n};
+        // the stride of a single head is never used
+        const uint64_t strides[2] = {(uint64_t)(heads > 1 ? head : values) * 2, (uint64_t)row * 2};
+        const uint32_t box[3] = {BOX, box_h, box_n};
+        return encode_tmap_bf16(tm, const_cast<void *>(d_p), 3, dims, strides, box);
+    };
+    if (!map(&p.q, q->d_p, q->row, q->head, dqk, H, rows, (uint32_t)p.G, (uint32_t)p.tpt)) return TF_E_CUDA;
+    p.has_kr = d_kr != nullptr;
+    if (keys > 0) {
+        if (!map(&p.k, k->d_p, k->row, k->head, dqk - (d_kr ? 64 : 0), Hkv, keys, 1, BN)) return TF_E_CUDA;
+        if (!map(&p.v, v->d_p, v->row, v->head, dv, Hkv, keys, 1, VH)) return TF_E_CUDA;
+        if (!d_kr) p.kr = p.k;
+        else if (!map(&p.kr, d_kr, kr_row, 64, 64, 1, keys, 1, BN)) return TF_E_CUDA;
+    } else {
+        p.k = p.kr = p.v = p.q;   // nothing is loaded through them
+    }
+    p.out = static_cast<uint16_t *>(out->d_p);
+    p.out_row = out->row;
+    p.out_head = out->head;
+    p.lse = d_lse;
+    p.part = static_cast<float *>(d_ws);
+    p.err = pool->err;
+    p.scale_log2 = scale * 1.44269504088896341f;
+    p.thr = 8.0f / p.scale_log2;
+    if (prepare_launch(pool, st) != TF_OK) return TF_E_CUDA;
+    {
+        ProfScope prof(pool, kProfPrompt, st);
+        const cudaError_t e = launch_pdl(kern, dim3((unsigned)pl.items), dim3(THREADS), SMEM, st, p);
+        launch_counter()++;
+        if (e != cudaSuccess) return TF_E_CUDA;
+    }
+    if (pl.slots == 0) return TF_OK;
+    int64_t most = 0;
+    for (int i = 0; i < p.S; ++i)
+        if (p.slot0[i] >= 0) most = std::max<int64_t>(most, p.nq[i]);
+    ProfScope prof(pool, kProfCombine, st);
+    auto *join = dv == 128 ? prompt_combine_kernel<128> : prompt_combine_kernel<64>;
+    const cudaError_t e = launch_pdl(join, dim3((unsigned)((most * H + 3) / 4), (unsigned)p.S), dim3(128), 0, st, p);
+    launch_counter()++;
+    return e == cudaSuccess ? TF_OK : TF_E_CUDA;
+}
+
+}  // namespace tf

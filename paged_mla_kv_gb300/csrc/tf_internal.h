@@ -13,6 +13,7 @@
 
 #include "../../include/tf_blocks.h"
 #include "../../include/tf_paged_mla.h"
+#include "../../include/tf_prompt.h"
 
 namespace tf {
 
@@ -43,7 +44,7 @@ struct DevErr {
 
 enum ProfKind {
     kProfAppend = 0, kProfAttend = 1, kProfCombine = 2, kProfCopy = 3, kProfPoison = 4, kProfBlockKeys = 5,
-    kProfBlockScores = 6, kProfKinds = 7
+    kProfBlockScores = 6, kProfRead = 7, kProfPrompt = 8, kProfKinds = 9
 };
 
 struct ProfRec {
@@ -83,6 +84,17 @@ struct tf_kvpool {
 namespace tf {
 
 std::atomic<int64_t> &launch_counter();
+
+// Plans, page bookkeeping and a host thread's first launch take host memory, and no exception leaves a C
+// entry: what runs out of it returns TF_E_NOMEM.
+template <typename F>
+inline int no_throw(F &&f) {
+    try {
+        return f();
+    } catch (...) {
+        return TF_E_NOMEM;
+    }
+}
 
 // Called before every launch.  The first launch on a pool zeroes the device error word and
 // waits for it, under the pool's lock, so no launch from any host thread or stream can run
@@ -193,6 +205,22 @@ int launch_block_keys(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_p
 int launch_block_scores(tf_kvpool *pool, const void *d_bkeys, const int32_t *d_pt, int max_pages, const int64_t *h_len,
                         int S, int R, int H, const void *d_q, const float *d_w, float scale, int sink, int local,
                         float *d_scores, int64_t ld, int32_t *d_nblk, cudaStream_t st);
+
+// The prompt path (rows.cu, prompt.cu).  Arguments are already validated, but for the workspace.
+int launch_rope(const tf_rope *rope, const int64_t *h_pos, const int64_t *h_n, int S, int H, const void *d_x, int64_t x_row,
+                int64_t x_head, void *d_y, int64_t y_row, int64_t y_head, cudaStream_t st);
+int launch_append_rope(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_pos,
+                       const int64_t *h_n, int S, const void *d_rows, int64_t row_stride, const void *d_gain, float eps,
+                       const tf_rope *rope, cudaStream_t st);
+int launch_paged_read(tf_kvpool *pool, int cache, const int32_t *d_pt, int max_pages, const int64_t *h_from,
+                      const int64_t *h_n, int S, void *d_latent, int64_t lat_stride, void *d_rope, int64_t rope_stride,
+                      cudaStream_t st);
+int prompt_plan(const int64_t *h_nq, const int64_t *h_nk, int S, int H, int Hkv, int dqk, int dv, int causal, int sms,
+                tf_prompt_plan *info, size_t *bytes);
+int launch_prompt_attend(tf_kvpool *pool, const int64_t *h_nq, const int64_t *h_nk, int S, int H, int Hkv, int dqk, int dv,
+                         const tf_heads *q, const tf_heads *k, const void *d_kr, int64_t kr_row, const tf_heads *v,
+                         float scale, int causal, const tf_heads *out, float *d_lse, void *d_ws, size_t ws_bytes,
+                         cudaStream_t st);
 
 // The driver's tensor-map encoder (attend.cu); null without a driver.
 bool encode_tmap_bf16(CUtensorMap *tm, void *base, int rank, const uint64_t *dims, const uint64_t *strides,
