@@ -29,11 +29,11 @@ constexpr int BM = 128;              // rows of a query tile
 constexpr int BN = 128;              // keys of a tile
 constexpr int BOX = 64;              // values of a box's row: 128 bytes, one swizzle atom
 constexpr int VH = 64;               // keys of a half of a value tile
-constexpr int THREADS = 384;         // two softmax warpgroups, and one with the MMA warp and the TMA warp
+constexpr int THREADS = 384;         // two softmax warpgroups, and one with a MMA warp for each of them and the TMA warp
 // Registers a thread: 168 at launch, of which the third warpgroup gives 80 to the others (2 * 208 + 88 = 3 * 168).
 constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 88;
 static_assert(2 * REGS_SOFTMAX + REGS_OTHER <= 3 * 168, "a split above the launch's total would wait forever");
-constexpr int MMA_WARP = 8, TMA_WARP = 9;
+constexpr int MMA_WARP = 8, TMA_WARP = 10;
 constexpr int MAX_SMS = TF_PLAN_MAX_RANGES;
 
 // Shared memory (bytes): the two query tiles, KS key tiles, VS halves of value tiles; 224 KB in each form.
@@ -51,7 +51,7 @@ struct Ctl {
     uint64_t q_full, q_free;
     uint64_t k_full[6], k_free[6];
     uint64_t v_full[12], v_free[12];
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2], p_full[2][2], o_full[2];   // P comes in halves of 64 keys
     uint64_t join_full, join_free;   // 32 columns of warpgroup 1's sums
     uint64_t next_full[2], next_free[2];
     uint64_t drain;
@@ -73,6 +73,7 @@ struct Params {
     int64_t out_row, out_head, slots;
     float scale_log2, thr;           // c; 8 / c
     int32_t S, H, Hkv, G, tpt, causal, has_kr;   // tpt: tokens of a query tile
+    int32_t more;                    // more items than SMs
     int32_t item0[TF_MAX_STREAMS];   // first item
     int32_t qoff[TF_MAX_STREAMS], nq[TF_MAX_STREAMS], koff[TF_MAX_STREAMS], nk[TF_MAX_STREAMS];
     int32_t chunk[TF_MAX_STREAMS];   // key tiles of a split
@@ -176,8 +177,23 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, ui
         : "memory");
 }
 
-// `n` (1 to 4) products of 16 keys: P from TMEM (8 columns a step), V MN-major (two 1 KB groups of 8 keys a step).
+// `n` (0 to 4) products of 16 keys: P from TMEM (8 columns a step), V MN-major (two 1 KB groups of 8 keys a step).
 __device__ __forceinline__ void pv_warp(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, int n) {
+    if (n == 4) {   // one block: a loop around single products issues them at half the pace of the tensor cores
+        asm volatile(
+            "{\n\t.reg .pred e, p;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+            "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+            "add.u64 b1, %2, 128;\n\tadd.u64 b2, %2, 256;\n\tadd.u64 b3, %2, 384;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, 1;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, 1;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, 1;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+        return;
+    }
 #pragma unroll 1
     for (int i = 0; i < n; ++i, a += 8, b += 2048 >> 4, acc = 1) ptx::mma_bf16_ts_warp(d, a, b, idesc, acc);
 }
@@ -208,9 +224,10 @@ struct Walk {
     __device__ __forceinline__ Walk() : i((int)blockIdx.x), count(0) {}
     // The item after this one; false at the end or after a timeout.  `who` frees the answer.
     __device__ __forceinline__ bool next(Ctl &c, const Params &p, bool who) {
+        if (!p.more) return false;
         const int b = count & 1;
         if (!wait(&c.next_full[b], (uint32_t)(count >> 1) & 1, &c.abort, p.err, 50)) return false;
-        i = read_next(&c.next[b]);
+        i = __shfl_sync(0xffffffffu, read_next(&c.next[b]), 0);
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (who) ptx::mbar_arrive(&c.next_free[b]);
@@ -231,19 +248,20 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
     if (threadIdx.x == 0) {
         c.abort = 0;
         ptx::mbar_init(&c.q_full, 1);
-        ptx::mbar_init(&c.q_free, 5);   // the last product with the queries, warpgroup 0's warps
-        for (int i = 0; i < L::KS; ++i) ptx::mbar_init(&c.k_full[i], 1), ptx::mbar_init(&c.k_free[i], 1);
-        for (int i = 0; i < L::VS; ++i) ptx::mbar_init(&c.v_full[i], 1), ptx::mbar_init(&c.v_free[i], 1);
+        ptx::mbar_init(&c.q_free, 6);   // both MMA warps' last product with the queries, warpgroup 0's warps
+        for (int i = 0; i < L::KS; ++i) ptx::mbar_init(&c.k_full[i], 1), ptx::mbar_init(&c.k_free[i], 2);
+        for (int i = 0; i < L::VS; ++i) ptx::mbar_init(&c.v_full[i], 1), ptx::mbar_init(&c.v_free[i], 2);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&c.s_full[i], 1);
-            ptx::mbar_init(&c.p_full[i], 4);
+            ptx::mbar_init(&c.p_full[i][0], 4);
+            ptx::mbar_init(&c.p_full[i][1], 4);
             ptx::mbar_init(&c.o_full[i], 1);
             ptx::mbar_init(&c.next_full[i], 1);
-            ptx::mbar_init(&c.next_free[i], 10);
+            ptx::mbar_init(&c.next_free[i], 11);
         }
         ptx::mbar_init(&c.join_full, 4);
         ptx::mbar_init(&c.join_free, 4);
-        ptx::mbar_init(&c.drain, 1);
+        ptx::mbar_init(&c.drain, 2);
         ptx::fence_mbar_init();
     }
     if (warp == MMA_WARP) {
@@ -259,7 +277,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = c.tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, c.tmem, 0);
     ptx::griddep_wait();
 
     if (warp == TMA_WARP) {
@@ -273,17 +291,20 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
         do {
             Item x;
             x.decode(p, it.i);
-            // the next item, while this one runs
-            {
+            // The next item is asked for when this one's last tiles are copied.  Asked for at an item's start it is
+            // taken from an SM that has none yet, or runs behind an item that others would have ended before.
+            auto ask = [&]() {
+                if (!p.more) return true;
                 const int b = it.count & 1;
-                if (it.count >= 2 && !wait(&c.next_free[b], (uint32_t)(it.count / 2 - 1) & 1, &c.abort, p.err, 51)) break;
+                if (it.count >= 2 && !wait(&c.next_free[b], (uint32_t)(it.count / 2 - 1) & 1, &c.abort, p.err, 51)) return false;
                 if (lane == 0) {
                     ptx::mbar_arrive_expect_tx(&c.next_full[b], 16);
                     ask_next(&c.next[b], &c.next_full[b]);
                 }
                 ++asked;
                 __syncwarp();
-            }
+                return true;
+            };
             const int row = p.koff[x.st];
             if (x.n0 + x.n1 > 0) {
                 if (nq > 0 && !wait(&c.q_free, (uint32_t)(nq - 1) & 1, &c.abort, p.err, 52)) break;
@@ -330,11 +351,13 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                 }
                 return true;
             };
+            if (x.n0 + x.n1 == 0) ok = ask();
             // in the order in which the MMA warp takes them
             if (x.pair) {
                 if (x.n1 > 0) ok = load_k(x.key_tile(1, 0));
                 for (int j = 0; ok && j < x.n1; ++j) {
-                    ok = load_v(x.key_tile(1, j));
+                    if (j == x.n1 - 1) ok = ask();
+                    if (ok) ok = load_v(x.key_tile(1, j));
                     if (ok && j + 1 < x.n1) ok = load_k(x.key_tile(1, j + 1));
                 }
             } else {
@@ -342,6 +365,8 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                     if (x.n(w) > 0) ok = load_k(x.key_tile(w, 0));
                 for (int j = 0; ok && j < x.n0; ++j)
                     for (int w = 0; ok && w < 2; ++w) {
+                        if (j == x.n0 - 1 && w == 0) ok = ask();
+                        if (!ok) break;
                         if (j < x.n(w)) ok = load_v(x.key_tile(w, j));
                         if (ok && j + 1 < x.n(w)) ok = load_k(x.key_tile(w, j + 1));
                     }
@@ -357,16 +382,18 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
         for (uint32_t n = nv > L::VS ? nv - L::VS : 0; n < nv; ++n)
             wait(&c.v_full[n % L::VS], (n / L::VS) & 1, &c.abort, p.err, 55, LIMIT);
         __syncwarp();
-    } else if (warp == MMA_WARP) {
-        // ================= MMA =================
+    } else if (warp >= MMA_WARP && warp < TMA_WARP) {
+        // ================= MMA: a warp for each softmax warpgroup, so that neither waits behind the other =================
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+        const int w = warp - MMA_WARP;
         const uint64_t dq = ptx::sdesc_sw128(ptx::smem_u32(smem), 16, 1024);
         const uint64_t dk = ptx::sdesc_sw128(ptx::smem_u32(smem + L::OFF_K), 16, 1024);
         const uint64_t dv = ptx::sdesc_sw128(ptx::smem_u32(smem + L::OFF_V), VH * 128, 1024);
         constexpr uint32_t IQK = ptx::idesc_bf16_f32(BM, BN, false, false);
         constexpr uint32_t IPV = ptx::idesc_bf16_f32(BM, DV, false, true);
-        uint32_t nk = 0, nv = 0;
-        uint32_t np0 = 0, np1 = 0;   // softmax tiles of each warpgroup so far
+        const uint32_t ts = tmem + w * BN, to = tmem + 2 * BN + w * DV;
+        uint32_t nk = 0, nv = 0;   // key tiles, halves of value tiles
+        uint32_t np = 0;           // softmax tiles of this warpgroup
         int nq = 0;
         bool ok = true;
         Walk it;
@@ -374,64 +401,87 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
             Item x;
             x.decode(p, it.i);
             if (x.n0 + x.n1 == 0) continue;
+            const int n = x.n(w);
             if (!wait(&c.q_full, (uint32_t)nq & 1, &c.abort, p.err, 60)) break;
             ++nq;
-            // Key tile number k of the item: with two query tiles step k of both, else step k / 2 of k % 2.
-            auto qk = [&](int w, int j) {
-                const uint32_t k = nk + (x.pair ? j : 2 * j + w);
-                const int st = (int)(k % L::KS);
-                const bool first = !x.pair || w == 0 || j >= x.n0;
-                if (first && !wait(&c.k_full[st], (uint32_t)(k / L::KS) & 1, &c.abort, p.err, 61)) return false;
+            // Both warps go through every tile in the order in which they are copied, and wait for and free those
+            // of the other one too: a parity tells a phase from the one before it only.
+            auto qk = [&](bool mine, int j) {
+                const int st = (int)(nk % L::KS);
+                if (!wait(&c.k_full[st], (nk / L::KS) & 1, &c.abort, p.err, 61)) return false;
+                ++nk;
+                if (!mine) {
+                    if (lane == 0) ptx::mbar_arrive(&c.k_free[st]);
+                    return true;
+                }
                 ptx::tc_fence_after();
                 const uint64_t a = dq + (uint64_t)(((x.pair ? w : 0) * L::Q_TILE) >> 4);
                 const uint64_t b = dk + (uint64_t)((st * L::K_TILE) >> 4);
-#pragma unroll 1
+#pragma unroll
                 for (int i = 0; i < L::QB; ++i)
-                    ptx::mma4_bf16_ss_warp(tmem + w * BN, a + (uint64_t)((i * BM * 128) >> 4), b + (uint64_t)((i * BN * 128) >> 4),
-                                           IQK, i == 0);
+                    ptx::mma4_bf16_ss_warp(ts, a + (uint64_t)((i * BM * 128) >> 4), b + (uint64_t)((i * BN * 128) >> 4), IQK, i == 0);
                 ptx::mma_commit_warp(&c.s_full[w]);
-                if (!x.pair || w == 1) ptx::mma_commit_warp(&c.k_free[st]);
+                ptx::mma_commit_warp(&c.k_free[st]);
+                if (j == n - 1) ptx::mma_commit_warp(&c.q_free);
                 return true;
             };
-            auto pv = [&](int w, int j) {
-                if (!wait(&c.p_full[w], (w ? np1 : np0) & 1, &c.abort, p.err, 62)) return false;
-                if (w) ++np1; else ++np0;
-                const uint32_t k = nv + 2 * (x.pair ? j : 2 * j + w);
-                const int steps = x.steps(p, w, x.key_tile(w, j));
-                const bool first = !x.pair || w == 0 || j >= x.n0;
-#pragma unroll 1
+            auto pv = [&](bool mine, int j) {
+                const int kt = x.key_tile(w, j);
+                const int steps = x.steps(p, w, kt), tail = p.nk[x.st] - kt * BN;
+#pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    const int st = (int)((k + half) % L::VS);
-                    if (first && !wait(&c.v_full[st], (uint32_t)((k + half) / L::VS) & 1, &c.abort, p.err, 63)) return false;
+                    const int st = (int)(nv % L::VS);
+                    if (!wait(&c.v_full[st], (nv / L::VS) & 1, &c.abort, p.err, 63)) return false;
+                    ++nv;
+                    if (!mine) {
+                        if (lane == 0) ptx::mbar_arrive(&c.v_free[st]);
+                        continue;
+                    }
+                    const int r0 = tail - half * VH;
+                    if (r0 > 0 && r0 < VH && (r0 & 15)) {
+                        // Rows behind the stream's last key, up to the 16 of a product's step: whatever they hold, 0
+                        // times it has to be 0.  (16-byte chunks, whatever their order in a row.)
+                        const int chunks = (16 - (r0 & 15)) * 8;
+                        uint8_t *dst = smem + L::OFF_V + st * L::V_HALF + r0 * 128;
+                        for (int i = lane; i < chunks * L::VB; i += 32)
+                            *reinterpret_cast<uint4 *>(dst + i / chunks * (VH * 128) + i % chunks * 16) = make_uint4(0, 0, 0, 0);
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (!wait(&c.p_full[w][half], np & 1, &c.abort, p.err, 62)) return false;
                     ptx::tc_fence_after();
-                    pv_warp(tmem + 2 * BN + w * DV, tmem + w * BN + half * 32, dv + (uint64_t)((st * L::V_HALF) >> 4), IPV,
-                            j > 0 || half > 0, min(4, steps - 4 * half));
-                    if (!x.pair || w == 1) ptx::mma_commit_warp(&c.v_free[st]);
+                    pv_warp(to, ts + half * 32, dv + (uint64_t)((st * L::V_HALF) >> 4), IPV, j > 0 || half > 0,
+                            max(0, min(4, steps - 4 * half)));
+                    ptx::mma_commit_warp(&c.v_free[st]);
                 }
-                if (j == x.n(w) - 1) ptx::mma_commit_warp(&c.o_full[w]);
+                if (mine) {
+                    ++np;
+                    if (j == n - 1) ptx::mma_commit_warp(&c.o_full[w]);
+                }
                 return true;
             };
-            for (int w = 0; ok && w < 2; ++w)
-                if (x.n(w) > 0) ok = qk(w, 0);
-            const int steps = max(x.n0, x.n1);
-            if (ok && steps == 1) ptx::mma_commit_warp(&c.q_free);
+            if (n == 0 && lane == 0) ptx::mbar_arrive(&c.q_free);
+            if (x.pair) {
+                ok = qk(n > 0, 0);
 #pragma unroll 1
-            for (int j = 0; ok && j < steps; ++j)
-#pragma unroll 1
-                for (int w = 0; ok && w < 2; ++w) {
-                    if (j >= x.n(w)) continue;
-                    ok = pv(w, j);
-                    if (ok && j + 1 < x.n(w)) ok = qk(w, j + 1);
-                    // the last product with the queries: warpgroup 1's when both have as many steps
-                    if (ok && j + 2 == steps && w == (x.n1 == steps)) ptx::mma_commit_warp(&c.q_free);
+                for (int j = 0; ok && j < x.n1; ++j) {
+                    ok = pv(j < n, j);
+                    if (ok && j + 1 < x.n1) ok = qk(j + 1 < n, j + 1);
                 }
+            } else {
+#pragma unroll 1
+                for (int j = -1; ok && j < x.n0; ++j)
+#pragma unroll 1
+                    for (int o = 0; ok && o < 2; ++o) {   // warpgroup o's tiles
+                        if (j >= 0 && j < x.n(o)) ok = pv(o == w, j);
+                        if (ok && j + 1 < x.n(o)) ok = qk(o == w, j + 1);
+                    }
+            }
             if (!ok) break;
-            nk += x.pair ? x.n1 : x.n0 + x.n1;
-            nv += 2 * (x.pair ? x.n1 : x.n0 + x.n1);
         } while (it.next(c, p, lane == 0));
         // no product may still run when TMEM is freed
         ptx::mma_commit_warp(&c.drain);
-        wait(&c.drain, 0, &c.abort, p.err, 64, 1ll << 29);
+        if (warp == MMA_WARP) wait(&c.drain, 0, &c.abort, p.err, 64, 1ll << 29);
         __syncwarp();
     } else if (warp < 8) {
         // ================= softmax, and the output: a query row a thread =================
@@ -442,7 +492,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
         const uint32_t ts = tmem + w * BN + lanes, to = tmem + 2 * BN + w * DV + lanes;
         const float cl = p.scale_log2;
         const int rt = row / p.G, rh = row - rt * p.G;   // the row's token in the tile, and its head
-        uint32_t ns = 0, nv = 0;
+        uint32_t ns = 0;
         int no = 0, nj = 0;   // outputs, joined pieces so far
         bool ok = true;
         Walk it;
@@ -463,26 +513,8 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                     ok = false;
                     break;
                 }
-                // rows of the value tile behind the stream's last key: whatever they hold, 0 times it has to be 0
-                const int tail = p.nk[x.st] - kt * BN;
-                if (tail < BN && (tail & 15)) {
-                    const uint32_t k = nv + 2 * (x.pair ? j : 2 * j + w) + (tail >= VH);
-                    const int st = (int)(k % L::VS);
-                    if (!wait(&c.v_full[st], (uint32_t)(k / L::VS) & 1, &c.abort, p.err, 71)) {
-                        ok = false;
-                        break;
-                    }
-                    const int r0 = tail & (VH - 1), r1 = (r0 + 15) & ~15;
-                    uint8_t *dst = smem + L::OFF_V + st * L::V_HALF;
-                    for (int i = row; i < (r1 - r0) * 8 * L::VB; i += BM) {   // 16-byte chunks, whatever their order in a row
-                        const int b = i / ((r1 - r0) * 8), y = i - b * (r1 - r0) * 8;
-                        *reinterpret_cast<uint4 *>(dst + b * (VH * 128) + (r0 + y / 8) * 128 + (y % 8) * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    ptx::fence_proxy_async_smem();
-                }
                 if (idle) {
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&c.p_full[w]);
+                    if (lane < 2) ptx::mbar_arrive(&c.p_full[w][lane]);
                     continue;
                 }
                 ptx::tc_fence_after();
@@ -541,12 +573,12 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                         pk[i] = ptx::pack_bf16x2(e.x, e.y);
                     }
                     ptx::tmem_st32(ts + 16 * q, pk);
+                    ptx::tmem_st_wait();   // with it what the maximum's move changed in O
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&c.p_full[w][q / 2]);
                 }
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                ptx::tmem_st_wait();
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&c.p_full[w]);
             }
             if (ok && n > 0) {
                 ok = wait(&c.o_full[w], (uint32_t)no & 1, &c.abort, p.err, 72);
@@ -554,7 +586,6 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                 ptx::tc_fence_after();
             }
             if (!ok) break;
-            nv += 2 * (x.pair ? x.n1 : x.n0 + x.n1);
             // One query tile: warpgroup 1's sums join warpgroup 0's, 32 columns at a time through the room of
             // query tile 1 (row by row: warp i of one with warp i of the other).
             const bool join = !x.pair && x.n1 > 0;
@@ -728,41 +759,43 @@ static int plan(Params &p, const int64_t *h_nq, const int64_t *h_nk, int S, int 
     };
     Str e[TF_MAX_STREAMS];
     int n = 0;
-    int64_t q = 0, k = 0, items = 0, most = 1;
+    int64_t q = 0, k = 0, most = 1;
     for (int s = 0; s < S; ++s) {
         if (h_nq[s] > 0) {
             const int64_t blocks = (h_nq[s] + 2 * tpt - 1) / (2 * tpt), tiles = (h_nk[s] + BN - 1) / BN;
             e[n++] = {tiles, blocks, (int32_t)q, (int32_t)k, (int32_t)h_nq[s], (int32_t)h_nk[s]};
-            items += blocks * Hkv;
             most = std::max(most, tiles);
         }
         q += h_nq[s];
         k += h_nk[s];
     }
     std::stable_sort(e, e + n, [](const Str &a, const Str &b) { return a.tiles > b.tiles; });
-    // A split of `chunk` key tiles: items are then at most that long.  The chunk with the smallest estimate of
-    // the time (in key tiles): the larger of the mean load and the longest item, an item's start and end taken
-    // as START tiles, and the join's launch.
-    constexpr int64_t START = 2, JOIN = 3;
+    // Splits of `chunk` key tiles.  The chunk with the smallest estimate of the time, in key tiles: one wave takes
+    // the longest item; more of them the mean load and half of the longest item among the last ones, for what they
+    // leave uneven.  An item's start and end count as START tiles, a split's partial sums as PART more, and the
+    // launch that joins them as JOIN.
+    constexpr int64_t START = 2, PART = 2, JOIN = 3;
     int64_t chunk = most;
-    if (items < sms) {
-        double best = 1e30;
-        for (int64_t c = most; c >= 1; c = c > 16 ? c - c / 8 : c - 1) {
-            int64_t cnt = 0, load = 0;
-            for (int i = 0; i < n; ++i) {
-                const int64_t sp = std::max<int64_t>(1, (e[i].tiles + c - 1) / c);
-                cnt += e[i].blocks * Hkv * sp;
-                load += e[i].blocks * Hkv * (e[i].tiles + sp * START);
-            }
-            const int64_t waves = (cnt + sms - 1) / sms;
-            const double t = std::max<double>((double)load / sms, (double)std::min<int64_t>(waves, 2) * (std::min(c, most) + START)) +
-                             (c < most ? JOIN : 0);
-            if (t < best) {
-                best = t;
-                chunk = c;
-            }
-            if (cnt > 4 * (int64_t)sms) break;
+    double best = 1e300;
+    for (int64_t c = most; c >= 1; c = c > 16 ? c - c / 8 : c - 1) {
+        int64_t cnt = 0, load = 0, longest = 0, tail = 0;
+        bool split = false;
+        for (int i = n - 1; i >= 0; --i) {
+            const int64_t sp = std::max<int64_t>(1, (e[i].tiles + c - 1) / c), each = std::min(e[i].tiles, c) + START + (sp > 1 ? PART : 0);
+            if (cnt < sms) tail = std::max(tail, each);
+            longest = std::max(longest, each);
+            cnt += e[i].blocks * Hkv * sp;
+            // a causal prompt's blocks see half of its own keys on average
+            const int64_t own = causal ? std::min<int64_t>(e[i].tiles, (e[i].nq + BN - 1) / BN) : 0;
+            load += e[i].blocks * Hkv * (2 * e[i].tiles - own) / 2 + e[i].blocks * Hkv * sp * (START + (sp > 1 ? PART : 0));
+            split = split || sp > 1;
         }
+        const double t = (cnt <= sms ? (double)longest : std::max((double)longest, (double)load / sms + 0.5 * tail)) + (split ? JOIN : 0);
+        if (t < best) {
+            best = t;
+            chunk = c;
+        }
+        if (cnt > 32 * (int64_t)sms) break;
     }
     out->items = 0;
     out->slots = 0;
@@ -789,6 +822,7 @@ static int plan(Params &p, const int64_t *h_nq, const int64_t *h_nk, int S, int 
     }
     p.S = n;
     p.slots = out->slots;
+    p.more = out->items > sms;
     return TF_OK;
 }
 

@@ -69,8 +69,8 @@ struct RopeParams {
 // A unit is what a thread turns at once: 8 neighbouring values (interleaved: 4 pairs), or 8 values and the 8
 // that lie half the part further (8 pairs).  A thread keeps its unit's place in the row (head and pairs) and
 // takes the rows r, r + lanes, ... of its block, IT of them with all loads in flight; the block's angles are made
-// once for all heads and wait in shared memory (64 heads share 32 sines a row).  18,887 rows of 64 heads, 64 of
-// 192 values each (319 MB moved): TIME_ROPE.
+// once for all heads and wait in shared memory (64 heads share 32 sines a row).  19,480 rows of 64 heads, 64 of
+// 192 values each (319 MB moved): 53.9 us, 0.87 of the measured copy rate.
 template <bool HALF, int IT>
 __global__ void __launch_bounds__(RT) rope_kernel(const __grid_constant__ RopeParams p) {
     __shared__ float2 tab[RTAB];
