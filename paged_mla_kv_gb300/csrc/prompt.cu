@@ -34,25 +34,44 @@ constexpr int THREADS = 384;         // two softmax warpgroups, and one with a M
 constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 88;
 static_assert(2 * REGS_SOFTMAX + REGS_OTHER <= 3 * 168, "a split above the launch's total would wait forever");
 constexpr int MMA_WARP = 8, TMA_WARP = 10;
+constexpr int MAX_UNITS = 24;
 constexpr int MAX_SMS = TF_PLAN_MAX_RANGES;
 
-// Shared memory (bytes): the two query tiles, KS key tiles, VS halves of value tiles; 224 KB in each form.
+// Shared memory (bytes): the two query tiles, then a ring of units the size of half a value tile (64 keys), in
+// which key tiles (KU units) and halves of value tiles follow one another in the order of their use; 224 KB in each
+// form.  One ring for both holds a step more than two: at 192 wide, 8 units of 16 KB against 5 a step.
 template <int DQK, int DV>
 struct Lay {
     static constexpr int QB = DQK / BOX, VB = DV / BOX;
-    static constexpr int Q_TILE = BM * DQK * 2, K_TILE = BN * DQK * 2, V_HALF = VH * DV * 2;
-    static constexpr int KS = DQK == 192 ? 2 : DQK == 128 ? 3 : 6;
-    static constexpr int VS = (229376 - 2 * Q_TILE - KS * K_TILE) / V_HALF;
-    static constexpr int OFF_K = 2 * Q_TILE, OFF_V = OFF_K + KS * K_TILE, BYTES = OFF_V + VS * V_HALF;
-    static_assert(BYTES == 229376 && VS >= 2, "fills the 224 KB");
+    static constexpr int Q_TILE = BM * DQK * 2, K_TILE = BN * DQK * 2, UNIT = VH * DV * 2;
+    static constexpr int KU = K_TILE / UNIT, BU = BN * 128 / UNIT;   // units of a key tile, of one of its boxes
+    static constexpr int OFF_R = 2 * Q_TILE, BYTES = 229376, U = (BYTES - OFF_R) / UNIT;
+    // a box does not wrap: it starts on a multiple of its own size, as keys and pairs of value halves do
+    static_assert(U * UNIT + OFF_R == BYTES && U <= MAX_UNITS && K_TILE % UNIT == 0 && U % BU == 0 && 2 % BU == 0, "the ring's form");
+};
+
+// A place in the ring: group (a key tile or half of a value tile) number `g` modulo U, its phase, its first unit.
+template <int U>
+struct Ring {
+    int g = 0, u = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void step(int units) {
+        if (++g == U) {
+            g = 0;
+            phase ^= 1;
+        }
+        u += units;
+        if (u >= U) u -= U;
+    }
 };
 
 struct Ctl {
-    uint64_t q_full, q_free;
-    uint64_t k_full[6], k_free[6];
-    uint64_t v_full[12], v_free[12];
+    uint64_t q_full[2], q_free[2];
+    uint64_t full[MAX_UNITS], free[MAX_UNITS];     // of the ring's groups
     uint64_t s_full[2], p_full[2][2], o_full[2];   // P comes in halves of 64 keys
+    uint64_t turn[2];                // of the MMA warps
     uint64_t join_full, join_free;   // 32 columns of warpgroup 1's sums
+    uint64_t join_done;              // an item's sums are joined: query tile 1's room is free
     uint64_t next_full[2], next_free[2];
     uint64_t drain;
     alignas(16) uint4 next[2];       // the answer to "another item?"
@@ -247,20 +266,21 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
     ptx::griddep_launch_dependents();
     if (threadIdx.x == 0) {
         c.abort = 0;
-        ptx::mbar_init(&c.q_full, 1);
-        ptx::mbar_init(&c.q_free, 6);   // both MMA warps' last product with the queries, warpgroup 0's warps
-        for (int i = 0; i < L::KS; ++i) ptx::mbar_init(&c.k_full[i], 1), ptx::mbar_init(&c.k_free[i], 2);
-        for (int i = 0; i < L::VS; ++i) ptx::mbar_init(&c.v_full[i], 1), ptx::mbar_init(&c.v_free[i], 2);
+        for (int i = 0; i < L::U; ++i) ptx::mbar_init(&c.full[i], 1), ptx::mbar_init(&c.free[i], 2);
         for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&c.q_full[i], 1);
+            ptx::mbar_init(&c.q_free[i], 2);
             ptx::mbar_init(&c.s_full[i], 1);
             ptx::mbar_init(&c.p_full[i][0], 4);
             ptx::mbar_init(&c.p_full[i][1], 4);
             ptx::mbar_init(&c.o_full[i], 1);
+            ptx::mbar_init(&c.turn[i], 1);
             ptx::mbar_init(&c.next_full[i], 1);
             ptx::mbar_init(&c.next_free[i], 11);
         }
         ptx::mbar_init(&c.join_full, 4);
         ptx::mbar_init(&c.join_free, 4);
+        ptx::mbar_init(&c.join_done, 4);
         ptx::mbar_init(&c.drain, 2);
         ptx::fence_mbar_init();
     }
@@ -283,11 +303,13 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
     if (warp == TMA_WARP) {
         // ================= TMA, and the question for the next item =================
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
-        uint32_t nk = 0, nv = 0;   // key tiles and halves of value tiles so far
-        int asked = 0;
-        bool ok = true;
+        Ring<L::U> head, tail;     // the next group, the oldest that is not known to be free
+        int room = L::U;           // free units
+        uint32_t keys = 0;         // which groups are key tiles
+        uint32_t groups = 0;       // so far, up to U
+        int asked = 0, nq[2] = {0, 0}, nj = 0;   // questions, uses of each query tile, joined items
+        bool ok = true, joined = false;
         Walk it;
-        int nq = 0;
         do {
             Item x;
             x.decode(p, it.i);
@@ -306,95 +328,115 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                 return true;
             };
             const int row = p.koff[x.st];
-            if (x.n0 + x.n1 > 0) {
-                if (nq > 0 && !wait(&c.q_free, (uint32_t)(nq - 1) & 1, &c.abort, p.err, 52)) break;
-                if (lane == 0) {
-                    const int tiles = x.pair ? 2 : 1;
-                    ptx::mbar_arrive_expect_tx(&c.q_full, (uint32_t)(tiles * L::QB * p.tpt * p.G * 128));
-                    for (int w = 0; w < tiles; ++w)
-                        for (int b = 0; b < L::QB; ++b)
-                            tma_load_3d(smem + w * L::Q_TILE + b * (BM * 128), &p.q, &c.q_full, b * BOX, x.h * p.G,
-                                        p.qoff[x.st] + x.tok0 + w * p.tpt);
+            // The next group's barrier, once there is room for it.
+            auto group = [&](int units, bool is_keys) -> uint64_t * {
+                for (; room < units; tail.step(0)) {
+                    if (!wait(&c.free[tail.g], tail.phase, &c.abort, p.err, 53)) return nullptr;
+                    room += (keys >> tail.g & 1) ? L::KU : 1;
                 }
-                ++nq;
-                __syncwarp();
-            }
+                room -= units;
+                keys = (keys & ~(1u << head.g)) | (uint32_t)is_keys << head.g;
+                if (groups < L::U) ++groups;
+                return &c.full[head.g];
+            };
             auto load_k = [&](int kt) {
-                const int st = (int)(nk % L::KS);
-                const uint32_t use = nk / L::KS;
-                if (use > 0 && !wait(&c.k_free[st], (uint32_t)(use - 1) & 1, &c.abort, p.err, 53)) return false;
+                uint64_t *bar = group(L::KU, true);
+                if (!bar) return false;
                 if (lane == 0) {
-                    ptx::mbar_arrive_expect_tx(&c.k_full[st], L::K_TILE);
-                    uint8_t *dst = smem + L::OFF_K + st * L::K_TILE;
+                    ptx::mbar_arrive_expect_tx(bar, L::K_TILE);
+                    int u = head.u;
                     for (int b = 0; b < L::QB; ++b) {
                         const bool shared = p.has_kr && b == L::QB - 1;
-                        tma_load_3d(dst + b * (BN * 128), shared ? &p.kr : &p.k, &c.k_full[st], shared ? 0 : b * BOX,
-                                    shared ? 0 : x.h, row + kt * BN);
+                        tma_load_3d(smem + L::OFF_R + u * L::UNIT, shared ? &p.kr : &p.k, bar, shared ? 0 : b * BOX, shared ? 0 : x.h,
+                                    row + kt * BN);
+                        u = u + L::BU == L::U ? 0 : u + L::BU;
                     }
                 }
-                ++nk;
+                head.step(L::KU);
                 __syncwarp();
                 return true;
             };
             auto load_v = [&](int kt) {
-                for (int half = 0; half < 2; ++half, ++nv) {
-                    const int st = (int)(nv % L::VS);
-                    const uint32_t use = nv / L::VS;
-                    if (use > 0 && !wait(&c.v_free[st], (uint32_t)(use - 1) & 1, &c.abort, p.err, 54)) return false;
+                for (int half = 0; half < 2; ++half) {
+                    uint64_t *bar = group(1, false);
+                    if (!bar) return false;
                     if (lane == 0) {
-                        ptx::mbar_arrive_expect_tx(&c.v_full[st], L::V_HALF);
-                        uint8_t *dst = smem + L::OFF_V + st * L::V_HALF;
+                        ptx::mbar_arrive_expect_tx(bar, L::UNIT);
                         for (int b = 0; b < L::VB; ++b)
-                            tma_load_3d(dst + b * (VH * 128), &p.v, &c.v_full[st], b * BOX, x.h, row + kt * BN + half * VH);
+                            tma_load_3d(smem + L::OFF_R + head.u * L::UNIT + b * (VH * 128), &p.v, bar, b * BOX, x.h,
+                                        row + kt * BN + half * VH);
                     }
+                    head.step(1);
                     __syncwarp();
                 }
                 return true;
             };
+            auto load_q = [&]() {
+                // query tile 1's room also served the join of the item before
+                if (joined && !wait(&c.join_done, (uint32_t)(nj - 1) & 1, &c.abort, p.err, 56)) return false;
+                for (int w = 0; w < (x.pair ? 2 : 1); ++w, __syncwarp()) {
+                    if (nq[w] > 0 && !wait(&c.q_free[w], (uint32_t)(nq[w] - 1) & 1, &c.abort, p.err, 52)) return false;
+                    ++nq[w];
+                    if (lane != 0) continue;
+                    ptx::mbar_arrive_expect_tx(&c.q_full[w], (uint32_t)(L::QB * p.tpt * p.G * 128));
+                    for (int b = 0; b < L::QB; ++b)
+                        tma_load_3d(smem + w * L::Q_TILE + b * (BM * 128), &p.q, &c.q_full[w], b * BOX, x.h * p.G,
+                                    p.qoff[x.st] + x.tok0 + w * p.tpt);
+                }
+                joined = !x.pair && x.n1 > 0;
+                nj += joined;
+                return true;
+            };
             if (x.n0 + x.n1 == 0) ok = ask();
-            // in the order in which the MMA warp takes them
+            // In the order in which the MMA warps take them; an item's first keys come before its queries, whose room
+            // is free only when the products of the item before are done.
             if (x.pair) {
-                if (x.n1 > 0) ok = load_k(x.key_tile(1, 0));
+                if (x.n1 > 0) ok = load_k(x.key_tile(1, 0)) && load_q();
                 for (int j = 0; ok && j < x.n1; ++j) {
                     if (j == x.n1 - 1) ok = ask();
                     if (ok) ok = load_v(x.key_tile(1, j));
                     if (ok && j + 1 < x.n1) ok = load_k(x.key_tile(1, j + 1));
                 }
             } else {
-                for (int w = 0; ok && w < 2; ++w)
+                for (int w = 0; ok && w < 2; ++w) {
                     if (x.n(w) > 0) ok = load_k(x.key_tile(w, 0));
-                for (int j = 0; ok && j < x.n0; ++j)
+                    if (ok && w == 0 && x.n0 > 0) ok = load_q();
+                }
+                for (int j = 0; ok && j < x.n0; ++j) {
+                    if (j == x.n0 - 1) ok = ask();
                     for (int w = 0; ok && w < 2; ++w) {
-                        if (j == x.n0 - 1 && w == 0) ok = ask();
-                        if (!ok) break;
                         if (j < x.n(w)) ok = load_v(x.key_tile(w, j));
                         if (ok && j + 1 < x.n(w)) ok = load_k(x.key_tile(w, j + 1));
                     }
+                }
             }
             if (!ok) break;
         } while (it.next(c, p, lane == 0));
         // no copy may still be on its way into this CTA's shared memory when it ends
         constexpr long long LIMIT = 1ll << 28;
         if (asked > 0) wait(&c.next_full[(asked - 1) & 1], (uint32_t)((asked - 1) >> 1) & 1, &c.abort, p.err, 55, LIMIT);
-        if (nq > 0) wait(&c.q_full, (uint32_t)(nq - 1) & 1, &c.abort, p.err, 55, LIMIT);
-        for (uint32_t n = nk > L::KS ? nk - L::KS : 0; n < nk; ++n)
-            wait(&c.k_full[n % L::KS], (n / L::KS) & 1, &c.abort, p.err, 55, LIMIT);
-        for (uint32_t n = nv > L::VS ? nv - L::VS : 0; n < nv; ++n)
-            wait(&c.v_full[n % L::VS], (n / L::VS) & 1, &c.abort, p.err, 55, LIMIT);
+        for (int w = 0; w < 2; ++w)
+            if (nq[w] > 0) wait(&c.q_full[w], (uint32_t)(nq[w] - 1) & 1, &c.abort, p.err, 55, LIMIT);
+        for (; groups > 0; --groups) {   // from the last one back
+            if (head.g == 0) head.phase ^= 1;
+            head.g = head.g == 0 ? L::U - 1 : head.g - 1;
+            wait(&c.full[head.g], head.phase, &c.abort, p.err, 55, LIMIT);
+        }
         __syncwarp();
     } else if (warp >= MMA_WARP && warp < TMA_WARP) {
         // ================= MMA: a warp for each softmax warpgroup, so that neither waits behind the other =================
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
         const int w = warp - MMA_WARP;
         const uint64_t dq = ptx::sdesc_sw128(ptx::smem_u32(smem), 16, 1024);
-        const uint64_t dk = ptx::sdesc_sw128(ptx::smem_u32(smem + L::OFF_K), 16, 1024);
-        const uint64_t dv = ptx::sdesc_sw128(ptx::smem_u32(smem + L::OFF_V), VH * 128, 1024);
+        const uint64_t dk = ptx::sdesc_sw128(ptx::smem_u32(smem + L::OFF_R), 16, 1024);
+        const uint64_t dv = ptx::sdesc_sw128(ptx::smem_u32(smem + L::OFF_R), VH * 128, 1024);
         constexpr uint32_t IQK = ptx::idesc_bf16_f32(BM, BN, false, false);
         constexpr uint32_t IPV = ptx::idesc_bf16_f32(BM, DV, false, true);
         const uint32_t ts = tmem + w * BN, to = tmem + 2 * BN + w * DV;
-        uint32_t nk = 0, nv = 0;   // key tiles, halves of value tiles
+        Ring<L::U> r;
         uint32_t np = 0;           // softmax tiles of this warpgroup
-        int nq = 0;
+        uint32_t nt = 0;           // turns
+        uint32_t nq0 = 0, nq1 = 0; // uses of the query tiles
         bool ok = true;
         Walk it;
         do {
@@ -402,80 +444,101 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
             x.decode(p, it.i);
             if (x.n0 + x.n1 == 0) continue;
             const int n = x.n(w);
-            if (!wait(&c.q_full, (uint32_t)nq & 1, &c.abort, p.err, 60)) break;
-            ++nq;
+            const int qt = x.pair ? w : 0;   // the query tile
+            if (!wait(&c.q_full[qt], (qt ? nq1 : nq0) & 1, &c.abort, p.err, 60)) break;
+            ++nq0;
+            nq1 += x.pair;
+            // A query tile is free once both warps say so, or its only one twice.
+            auto free_q = [&]() {
+                ptx::mma_commit_warp(&c.q_free[qt]);
+                if (x.pair) ptx::mma_commit_warp(&c.q_free[qt]);
+            };
             // Both warps go through every tile in the order in which they are copied, and wait for and free those
             // of the other one too: a parity tells a phase from the one before it only.
-            auto qk = [&](bool mine, int j) {
-                const int st = (int)(nk % L::KS);
-                if (!wait(&c.k_full[st], (nk / L::KS) & 1, &c.abort, p.err, 61)) return false;
-                ++nk;
-                if (!mine) {
-                    if (lane == 0) ptx::mbar_arrive(&c.k_free[st]);
-                    return true;
-                }
-                ptx::tc_fence_after();
-                const uint64_t a = dq + (uint64_t)(((x.pair ? w : 0) * L::Q_TILE) >> 4);
-                const uint64_t b = dk + (uint64_t)((st * L::K_TILE) >> 4);
-#pragma unroll
-                for (int i = 0; i < L::QB; ++i)
-                    ptx::mma4_bf16_ss_warp(ts, a + (uint64_t)((i * BM * 128) >> 4), b + (uint64_t)((i * BN * 128) >> 4), IQK, i == 0);
-                ptx::mma_commit_warp(&c.s_full[w]);
-                ptx::mma_commit_warp(&c.k_free[st]);
-                if (j == n - 1) ptx::mma_commit_warp(&c.q_free);
+            auto skip = [&](int units) {
+                if (!wait(&c.full[r.g], r.phase, &c.abort, p.err, 61)) return false;
+                if (lane == 0) ptx::mbar_arrive(&c.free[r.g]);
+                r.step(units);
                 return true;
             };
-            auto pv = [&](bool mine, int j) {
-                const int kt = x.key_tile(w, j);
-                const int steps = x.steps(p, w, kt), tail = p.nk[x.st] - kt * BN;
+            // Round j of this warp: the product with the values of step j (`pv`), that with the keys of step j + 1 (`qk`).
+            // All but the first half of the values' product is issued in turns.  Products of two warps that are issued side
+            // by side run interleaved: both end late, both softmaxes then run together, and the tensor cores idle
+            // meanwhile (4,500 cycles a step of two 192-wide tiles; in turns ROUND).
+            auto round = [&](int j, bool pv, bool qk) {
+                int steps = 0, keys_u = 0, vals_u = 0;
+                uint64_t *keys_free = nullptr, *vals_free = nullptr;
+                if (pv) {
+                    const int kt = x.key_tile(w, j);
+                    steps = x.steps(p, w, kt);
+                    const int tail = p.nk[x.st] - kt * BN;
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int st = (int)(nv % L::VS);
-                    if (!wait(&c.v_full[st], (nv / L::VS) & 1, &c.abort, p.err, 63)) return false;
-                    ++nv;
-                    if (!mine) {
-                        if (lane == 0) ptx::mbar_arrive(&c.v_free[st]);
-                        continue;
+                    for (int half = 0; half < 2; ++half, r.step(1)) {
+                        if (!wait(&c.full[r.g], r.phase, &c.abort, p.err, 63)) return false;
+                        vals_u = r.u;
+                        vals_free = &c.free[r.g];
+                        const int r0 = tail - half * VH;
+                        if (r0 > 0 && r0 < VH && (r0 & 15)) {
+                            // Rows behind the stream's last key, up to the 16 of a product's step: whatever they hold, 0
+                            // times it has to be 0.  (16-byte chunks, whatever their order in a row.)
+                            const int chunks = (16 - (r0 & 15)) * 8;
+                            uint8_t *dst = smem + L::OFF_R + vals_u * L::UNIT + r0 * 128;
+                            for (int i = lane; i < chunks * L::VB; i += 32)
+                                *reinterpret_cast<uint4 *>(dst + i / chunks * (VH * 128) + i % chunks * 16) = make_uint4(0, 0, 0, 0);
+                            ptx::fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                        if (!wait(&c.p_full[w][half], np & 1, &c.abort, p.err, 62)) return false;
+                        if (half == 0) {
+                            ptx::tc_fence_after();
+                            pv_warp(to, ts, dv + (uint64_t)((vals_u * L::UNIT) >> 4), IPV, j > 0, min(4, steps));
+                            ptx::mma_commit_warp(vals_free);
+                        }
                     }
-                    const int r0 = tail - half * VH;
-                    if (r0 > 0 && r0 < VH && (r0 & 15)) {
-                        // Rows behind the stream's last key, up to the 16 of a product's step: whatever they hold, 0
-                        // times it has to be 0.  (16-byte chunks, whatever their order in a row.)
-                        const int chunks = (16 - (r0 & 15)) * 8;
-                        uint8_t *dst = smem + L::OFF_V + st * L::V_HALF + r0 * 128;
-                        for (int i = lane; i < chunks * L::VB; i += 32)
-                            *reinterpret_cast<uint4 *>(dst + i / chunks * (VH * 128) + i % chunks * 16) = make_uint4(0, 0, 0, 0);
-                        ptx::fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                    if (!wait(&c.p_full[w][half], np & 1, &c.abort, p.err, 62)) return false;
-                    ptx::tc_fence_after();
-                    pv_warp(to, ts + half * 32, dv + (uint64_t)((st * L::V_HALF) >> 4), IPV, j > 0 || half > 0,
-                            max(0, min(4, steps - 4 * half)));
-                    ptx::mma_commit_warp(&c.v_free[st]);
-                }
-                if (mine) {
                     ++np;
+                }
+                if (qk) {
+                    if (!wait(&c.full[r.g], r.phase, &c.abort, p.err, 61)) return false;
+                    keys_u = r.u;
+                    keys_free = &c.free[r.g];
+                    r.step(L::KU);
+                }
+                if ((w == 1 || nt > 0) && !wait(&c.turn[w], (nt - (w == 0)) & 1, &c.abort, p.err, 65)) return false;
+                ++nt;
+                ptx::tc_fence_after();
+                if (pv) {
+                    pv_warp(to, ts + 32, dv + (uint64_t)((vals_u * L::UNIT) >> 4), IPV, 1, max(0, steps - 4));
+                    ptx::mma_commit_warp(vals_free);
                     if (j == n - 1) ptx::mma_commit_warp(&c.o_full[w]);
                 }
+                if (qk) {
+                    const uint64_t a = dq + (uint64_t)((qt * L::Q_TILE) >> 4);
+                    int u = keys_u;
+#pragma unroll
+                    for (int i = 0; i < L::QB; ++i) {
+                        ptx::mma4_bf16_ss_warp(ts, a + (uint64_t)((i * BM * 128) >> 4), dk + (uint64_t)((u * L::UNIT) >> 4), IQK, i == 0);
+                        u = u + L::BU == L::U ? 0 : u + L::BU;
+                    }
+                    ptx::mma_commit_warp(&c.s_full[w]);
+                    ptx::mma_commit_warp(keys_free);
+                    if (j + 1 == n - 1) free_q();
+                }
+                if (lane == 0) ptx::mbar_arrive(&c.turn[1 - w]);
                 return true;
             };
-            if (n == 0 && lane == 0) ptx::mbar_arrive(&c.q_free);
-            if (x.pair) {
-                ok = qk(n > 0, 0);
+            if (n == 0) free_q();
+            const int rounds = max(x.n0, x.n1);
 #pragma unroll 1
-                for (int j = 0; ok && j < x.n1; ++j) {
-                    ok = pv(j < n, j);
-                    if (ok && j + 1 < x.n1) ok = qk(j + 1 < n, j + 1);
-                }
-            } else {
-#pragma unroll 1
-                for (int j = -1; ok && j < x.n0; ++j)
-#pragma unroll 1
-                    for (int o = 0; ok && o < 2; ++o) {   // warpgroup o's tiles
-                        if (j >= 0 && j < x.n(o)) ok = pv(o == w, j);
-                        if (ok && j + 1 < x.n(o)) ok = qk(o == w, j + 1);
-                    }
+            for (int j = -1; ok && j < rounds; ++j) {
+                // the other warp's tiles before (1) or after (0) the own ones; with two query tiles those that only it takes
+                auto others = [&]() {
+                    const int o = x.n(1 - w);
+                    if (j >= 0 && j < o && (!x.pair || j >= n)) ok = skip(1) && skip(1);
+                    if (ok && j + 1 < o && (!x.pair || j + 1 >= n)) ok = skip(L::KU);
+                };
+                if (w == 1) others();
+                if (ok) ok = round(j, j >= 0 && j < n, j + 1 < n);
+                if (ok && w == 0) others();
             }
             if (!ok) break;
         } while (it.next(c, p, lane == 0));
@@ -665,10 +728,9 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
             }
             ptx::tc_fence_before();
             __syncwarp();
-            // query tile 1's room is free again (the queries themselves: the MMA warp's arrival)
-            if (w == 0 && lane == 0 && x.n0 + x.n1 > 0) {
+            if (join && w == 0 && lane == 0) {   // query tile 1's room is free again
                 ptx::fence_proxy_async_smem();
-                ptx::mbar_arrive(&c.q_free);
+                ptx::mbar_arrive(&c.join_done);
             }
         } while (it.next(c, p, lane == 0));
     } else {
