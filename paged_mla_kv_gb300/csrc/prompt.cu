@@ -217,32 +217,38 @@ __device__ __forceinline__ void pv_warp(uint32_t d, uint32_t a, uint64_t b, uint
     for (int i = 0; i < n; ++i, a += 8, b += 2048 >> 4, acc = 1) ptx::mma_bf16_ts_warp(d, a, b, idesc, acc);
 }
 
-// ptx::mbar_wait_warp without the call to its polling loop: a call would hold the registers around it to
-// what the whole kernel was launched with.  Bounded in the same way.
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort, DevErr *err, int site,
-                                     long long limit = 1ll << 31) {
-    // the first look without a time to sleep: 38 cycles against 70 where the phase is complete
+// One look at a barrier.  Without a time to sleep it costs 38 cycles where the phase is complete, with one 70.
+__device__ __forceinline__ bool look(uint64_t *bar, uint32_t parity) {
     uint32_t seen;
     asm volatile(
         "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(seen)
         : "r"(ptx::smem_u32(bar)), "r"(parity)
         : "memory");
-    if (__all_sync(0xffffffffu, seen)) return true;
-    bool done = seen != 0;
-    {
-        const long long t0 = clock64();
-        for (uint32_t spins = 1; !done && !(done = ptx::mbar_try_wait(bar, parity)); ++spins) {
-            if ((spins & 255u) != 0) continue;
-            if (*abort) break;
-            if (clock64() - t0 > limit) {
-                ptx::record_error(err, TF_E_TIMEOUT, site);
-                *abort = 1;
-                break;
-            }
-        }
+    return __all_sync(0xffffffffu, seen);
+}
+
+// Whether a wait that began at t0 is to be given up: past its limit (recorded), or as another role gave up.
+__device__ __forceinline__ bool expired(long long t0, long long limit, volatile int *abort, DevErr *err, int site) {
+    bool stop = *abort != 0;
+    if (!stop && clock64() - t0 > limit) {
+        ptx::record_error(err, TF_E_TIMEOUT, site);
+        *abort = 1;
+        stop = true;
     }
-    return __all_sync(0xffffffffu, done);
+    return __any_sync(0xffffffffu, stop);
+}
+
+// ptx::mbar_wait_warp without the call to its polling loop: a call would hold the registers around it to
+// what the whole kernel was launched with.  Bounded in the same way.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort, DevErr *err, int site,
+                                     long long limit = 1ll << 31) {
+    if (look(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (uint32_t spins = 1;; ++spins) {
+        if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+        if ((spins & 255u) == 0 && expired(t0, limit, abort, err, site)) return false;
+    }
 }
 
 // What every role walks: the items of this CTA.
@@ -475,6 +481,10 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
             auto round = [&](int j, bool pv, bool qk) {
                 int steps = 0, keys_u = 0, vals_u = 0;
                 uint64_t *keys_free = nullptr, *vals_free = nullptr;
+                const uint32_t my_turn = (nt - (w == 0)) & 1;
+                bool turn = w == 0 && nt == 0, landed = false;
+                Ring<L::U> next = r;   // the keys'
+                if (pv) next.step(2);
                 if (pv) {
                     const int kt = x.key_tile(w, j);
                     steps = x.steps(p, w, kt);
@@ -492,7 +502,13 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                         ptx::fence_proxy_async_smem();
                         __syncwarp();
                     }
-                    if (!wait(&c.p_full[w][0], np & 1, &c.abort, p.err, 62)) return false;
+                    // P's first half; meanwhile a look at what the rest of the round waits for
+                    const long long t0 = clock64();
+                    for (uint32_t spins = 1; !look(&c.p_full[w][0], np & 1); ++spins) {
+                        if (qk && !landed) landed = look(&c.full[next.g], next.phase);
+                        if (!turn) turn = look(&c.turn[w], my_turn);
+                        if ((spins & 4095u) == 0 && expired(t0, 1ll << 31, &c.abort, p.err, 62)) return false;
+                    }
                     ptx::tc_fence_after();
                     pv_warp(to, ts, dv + (uint64_t)((r.u * L::UNIT) >> 4), IPV, j > 0, min(4, steps));
                     vals_u = r.u + 1 == L::U ? 0 : r.u + 1;
@@ -501,12 +517,12 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                 }
                 // What the turn's products wait for, P's second half last: it is what comes last.
                 if (qk) {
-                    if (!wait(&c.full[r.g], r.phase, &c.abort, p.err, 61)) return false;
+                    if (!landed && !wait(&c.full[r.g], r.phase, &c.abort, p.err, 61)) return false;
                     keys_u = r.u;
                     keys_free = &c.free[r.g];
                     r.step(L::KU);
                 }
-                if ((w == 1 || nt > 0) && !wait(&c.turn[w], (nt - (w == 0)) & 1, &c.abort, p.err, 65)) return false;
+                if (!turn && !wait(&c.turn[w], my_turn, &c.abort, p.err, 65)) return false;
                 ++nt;
                 if (pv && !wait(&c.p_full[w][1], np++ & 1, &c.abort, p.err, 62)) return false;
                 ptx::tc_fence_after();
