@@ -65,23 +65,6 @@ struct Ring {
     }
 };
 
-struct Ctl {
-    uint64_t q_full[2], q_free[2];
-    uint64_t full[MAX_UNITS], free[MAX_UNITS];     // of the ring's groups
-    uint64_t s_full[2], p_full[2][2], o_full[2];   // P comes in halves of 64 keys
-    uint64_t turn[2];                // of the MMA warps
-    uint64_t join_full, join_free;   // 32 columns of warpgroup 1's sums
-    uint64_t join_done;              // an item's sums are joined: query tile 1's room is free
-    uint64_t next_full[2], next_free[2];
-    uint64_t drain;
-    alignas(16) uint4 next[2];       // the answer to "another item?"
-    float2 ml[BM];                   // warpgroup 1's (m, l) of each row, for the join
-    uint32_t tmem;
-    int abort;
-};
-constexpr int SMEM = 229376 + 1024 + (int)((sizeof(Ctl) + 127) / 128 * 128);
-static_assert(SMEM <= 232448, "227 KB");
-
 // Streams in the order of their work, the longest first.
 struct Params {
     CUtensorMap q, k, kr, v;
@@ -106,18 +89,23 @@ __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; 
 // What an item is.  Items of a stream: groups of hg key heads; in a group blocks from the last (the longest of a
 // causal prompt) to the first, in a block its splits, in a split the group's heads.  The heads of a group read
 // keys that fit L2 together, and blocks of one head share them there.
-struct Item {
-    int st, h, blk, sp;      // stream (in Params order), key head, block, split
+struct alignas(16) Item {
+    int h;                   // key head
     int tok0, ntok;          // first token in the stream, tokens
-    bool pair;               // two query tiles
+    int qrow, krow;          // rows of that token and of the stream's first key
+    int nk, lag;             // the stream's keys; those before its first query row's own
     int c0;                  // first key tile
-    int n0, n1;              // key tiles of each warpgroup
+    int n0, n1;              // key tiles of each warpgroup; n0 < 0: no item
     int slot;                // slot of query tile 0, or -1
+    int pair;                // two query tiles
 
-    __device__ __forceinline__ int n(int w) const { return w ? n1 : n0; }
-
+    // Item i (-1: none).  Divisions and a search: the TMA warp does it ahead of time and the others read the result.
     __device__ __forceinline__ void decode(const Params &p, int i) {
-        st = 0;
+        if (i < 0) {
+            n0 = n1 = -1;
+            return;
+        }
+        int st = 0;
         for (int a = p.S - 1; st < a;) {
             const int mid = (st + a + 1) >> 1;
             if (p.item0[mid] <= i) st = mid; else a = mid - 1;
@@ -130,40 +118,58 @@ struct Item {
         const int heads = min(hg, p.Hkv - g * hg);
         const int b = x / (nsp * heads);
         x -= b * nsp * heads;
-        sp = x / heads;
+        const int sp = x / heads, blk = blocks - 1 - b;
         h = g * hg + x - sp * heads;
-        blk = blocks - 1 - b;
         tok0 = blk * 2 * p.tpt;
         ntok = min(nq - tok0, 2 * p.tpt);
+        qrow = p.qoff[st] + tok0;
+        krow = p.koff[st];
+        nk = p.nk[st];
+        lag = nk - nq;
         pair = ntok > p.tpt;
         c0 = sp * p.chunk[st];
-        const int t0 = tiles(p, min(ntok, p.tpt)), t1 = tiles(p, ntok);
         const int end = c0 + p.chunk[st];
+        n0 = max(0, min(end, ceil_div(seen(p, min(ntok, p.tpt)), BN)) - c0);
         if (pair) {
-            n0 = max(0, min(end, t0) - c0);
-            n1 = max(0, min(end, t1) - c0);
+            n1 = max(0, min(end, ceil_div(seen(p, ntok), BN)) - c0);
         } else {
-            const int m = max(0, min(end, t0) - c0);
-            n0 = (m + 1) / 2;
-            n1 = m / 2;
+            n1 = n0 / 2;
+            n0 -= n1;
         }
         slot = p.slot0[st] < 0 ? -1 : p.slot0[st] + ((h * blocks + blk) * nsp + sp) * 2;
     }
+    __device__ __forceinline__ int n(int w) const { return w ? n1 : n0; }
     // Keys that the first `t` tokens of the block see at most.
     __device__ __forceinline__ int seen(const Params &p, int t) const {
-        const int nk = p.nk[st];
-        if (!p.causal) return nk;
-        return max(0, min(nk, nk - p.nq[st] + tok0 + t));
+        return p.causal ? max(0, min(nk, lag + tok0 + t)) : nk;
     }
-    __device__ __forceinline__ int tiles(const Params &p, int t) const { return ceil_div(seen(p, t), BN); }
     // Key tile of warpgroup w's step j.
     __device__ __forceinline__ int key_tile(int w, int j) const { return pair ? c0 + j : c0 + 2 * j + w; }
     // Keys of that tile that any row of warpgroup w's query tile sees, rounded up to the 16 of a product step.
     __device__ __forceinline__ int steps(const Params &p, int w, int kt) const {
-        const int t = pair ? (w ? ntok : p.tpt) : ntok;
+        const int t = pair && w == 0 ? p.tpt : ntok;
         return min(BN / 16, ceil_div(seen(p, t) - kt * BN, 16));
     }
 };
+
+struct Ctl {
+    uint64_t q_full[2], q_free[2];
+    uint64_t full[MAX_UNITS], free[MAX_UNITS];     // of the ring's groups
+    uint64_t s_full[2], p_full[2][2], o_full[2];   // P comes in halves of 64 keys
+    uint64_t turn[2];                // of the MMA warps
+    uint64_t join_full, join_free;   // 32 columns of warpgroup 1's sums
+    uint64_t join_done;              // an item's sums are joined: query tile 1's room is free
+    uint64_t answer;                 // to the question for another item
+    uint64_t item_full[2], item_free[2];
+    uint64_t drain;
+    alignas(16) uint4 next;          // the answer
+    Item item[2];
+    float2 ml[BM];                   // warpgroup 1's (m, l) of each row, for the join
+    uint32_t tmem;
+    int abort;
+};
+constexpr int SMEM = 229376 + 1024 + (int)((sizeof(Ctl) + 127) / 128 * 128);
+static_assert(SMEM <= 232448, "227 KB");
 
 // ---- the next item: a CTA that has not been launched yet is taken over (cluster launch control) ----
 __device__ __forceinline__ void ask_next(uint4 *dst, uint64_t *bar) {
@@ -251,21 +257,24 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
     }
 }
 
-// What every role walks: the items of this CTA.
+// The items of this CTA, as the roles that do not find them read them.
 struct Walk {
-    int i, count;   // the item, how many came before
-    __device__ __forceinline__ Walk() : i((int)blockIdx.x), count(0) {}
-    // The item after this one; false at the end or after a timeout.  `who` frees the answer.
-    __device__ __forceinline__ bool next(Ctl &c, const Params &p, bool who) {
-        if (!p.more) return false;
+    uint32_t count = 0;
+    // The next item; false at the end or after a timeout.
+    __device__ __forceinline__ bool next(Ctl &c, const Params &p, Item &x, int lane) {
         const int b = count & 1;
-        if (!wait(&c.next_full[b], (uint32_t)(count >> 1) & 1, &c.abort, p.err, 50)) return false;
-        i = __shfl_sync(0xffffffffu, read_next(&c.next[b]), 0);
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (who) ptx::mbar_arrive(&c.next_free[b]);
+        if (!wait(&c.item_full[b], (count >> 1) & 1, &c.abort, p.err, 50)) return false;
+        // through a shuffle, so that the compiler knows the values to be the same in all lanes: loops and descriptors
+        // that hang on them then stay in uniform registers (8,192 rows of 64 heads
+        // over 8 key heads: 768 us without it, 652 with)
+        const int *src = reinterpret_cast<const int *>(&c.item[b]);
+        int *dst = reinterpret_cast<int *>(&x);
+        const int mine = src[min(lane, (int)(sizeof(Item) / 4) - 1)];
+#pragma unroll
+        for (int k = 0; k < (int)(sizeof(Item) / 4); ++k) dst[k] = __shfl_sync(0xffffffffu, mine, k);
+        if (lane == 0) ptx::mbar_arrive(&c.item_free[b]);
         ++count;
-        return i >= 0;
+        return x.n0 >= 0;
     }
 };
 
@@ -289,12 +298,13 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
             ptx::mbar_init(&c.p_full[i][1], 4);
             ptx::mbar_init(&c.o_full[i], 1);
             ptx::mbar_init(&c.turn[i], 1);
-            ptx::mbar_init(&c.next_full[i], 1);
-            ptx::mbar_init(&c.next_free[i], 11);
+            ptx::mbar_init(&c.item_full[i], 1);
+            ptx::mbar_init(&c.item_free[i], 10);
         }
         ptx::mbar_init(&c.join_full, 4);
         ptx::mbar_init(&c.join_free, 4);
         ptx::mbar_init(&c.join_done, 4);
+        ptx::mbar_init(&c.answer, 1);
         ptx::mbar_init(&c.drain, 2);
         ptx::fence_mbar_init();
     }
@@ -323,25 +333,27 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
         uint32_t groups = 0;       // so far, up to U
         int asked = 0, nq[2] = {0, 0}, nj = 0;   // questions, uses of each query tile, joined items
         bool ok = true, joined = false;
-        Walk it;
-        do {
+        int i = (int)blockIdx.x;
+        for (uint32_t count = 0;; ++count) {
             Item x;
-            x.decode(p, it.i);
+            x.decode(p, i);
+            if (count >= 2 && !wait(&c.item_free[count & 1], (count / 2 - 1) & 1, &c.abort, p.err, 51)) break;
+            if (lane == 0) {
+                c.item[count & 1] = x;
+                ptx::mbar_arrive(&c.item_full[count & 1]);
+            }
+            if (i < 0) break;
             // The next item is asked for when this one's last tiles are copied.  Asked for at an item's start it is
             // taken from an SM that has none yet, or runs behind an item that others would have ended before.
             auto ask = [&]() {
-                if (!p.more) return true;
-                const int b = it.count & 1;
-                if (it.count >= 2 && !wait(&c.next_free[b], (uint32_t)(it.count / 2 - 1) & 1, &c.abort, p.err, 51)) return false;
-                if (lane == 0) {
-                    ptx::mbar_arrive_expect_tx(&c.next_full[b], 16);
-                    ask_next(&c.next[b], &c.next_full[b]);
+                if (p.more && lane == 0) {
+                    ptx::fence_proxy_async_smem();   // the answer before has been read
+                    ptx::mbar_arrive_expect_tx(&c.answer, 16);
+                    ask_next(&c.next, &c.answer);
                 }
-                ++asked;
+                asked += p.more;
                 __syncwarp();
-                return true;
             };
-            const int row = p.koff[x.st];
             // The next group's barrier, once there is room for it.
             auto group = [&](int units, bool is_keys) -> uint64_t * {
                 for (; room < units; tail.step(0)) {
@@ -362,7 +374,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                     for (int b = 0; b < L::QB; ++b) {
                         const bool shared = p.has_kr && b == L::QB - 1;
                         tma_load_3d(smem + L::OFF_R + u * L::UNIT, shared ? &p.kr : &p.k, bar, shared ? 0 : b * BOX, shared ? 0 : x.h,
-                                    row + kt * BN);
+                                    x.krow + kt * BN);
                         u = u + L::BU == L::U ? 0 : u + L::BU;
                     }
                 }
@@ -377,7 +389,8 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                     ptx::mbar_arrive_expect_tx(bar, 2 * L::UNIT);
                     for (int half = 0, u = head.u; half < 2; ++half, u = u + 1 == L::U ? 0 : u + 1)
                         for (int b = 0; b < L::VB; ++b)
-                            tma_load_3d(smem + L::OFF_R + u * L::UNIT + b * (VH * 128), &p.v, bar, b * BOX, x.h, row + kt * BN + half * VH);
+                            tma_load_3d(smem + L::OFF_R + u * L::UNIT + b * (VH * 128), &p.v, bar, b * BOX, x.h,
+                                        x.krow + kt * BN + half * VH);
                 }
                 head.step(2);
                 __syncwarp();
@@ -393,20 +406,20 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                     ptx::mbar_arrive_expect_tx(&c.q_full[w], (uint32_t)(L::QB * p.tpt * p.G * 128));
                     for (int b = 0; b < L::QB; ++b)
                         tma_load_3d(smem + w * L::Q_TILE + b * (BM * 128), &p.q, &c.q_full[w], b * BOX, x.h * p.G,
-                                    p.qoff[x.st] + x.tok0 + w * p.tpt);
+                                    x.qrow + w * p.tpt);
                 }
                 joined = !x.pair && x.n1 > 0;
                 nj += joined;
                 return true;
             };
-            if (x.n0 + x.n1 == 0) ok = ask();
+            if (x.n0 + x.n1 == 0) ask();
             // In the order in which the MMA warps take them; an item's first keys come before its queries, whose room
             // is free only when the products of the item before are done.
             if (x.pair) {
                 if (x.n1 > 0) ok = load_k(x.key_tile(1, 0)) && load_q();
                 for (int j = 0; ok && j < x.n1; ++j) {
-                    if (j == x.n1 - 1) ok = ask();
-                    if (ok) ok = load_v(x.key_tile(1, j));
+                    if (j == x.n1 - 1) ask();
+                    ok = load_v(x.key_tile(1, j));
                     if (ok && j + 1 < x.n1) ok = load_k(x.key_tile(1, j + 1));
                 }
             } else {
@@ -415,7 +428,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                     if (ok && w == 0 && x.n0 > 0) ok = load_q();
                 }
                 for (int j = 0; ok && j < x.n0; ++j) {
-                    if (j == x.n0 - 1) ok = ask();
+                    if (j == x.n0 - 1) ask();
                     for (int w = 0; ok && w < 2; ++w) {
                         if (j < x.n(w)) ok = load_v(x.key_tile(w, j));
                         if (ok && j + 1 < x.n(w)) ok = load_k(x.key_tile(w, j + 1));
@@ -423,10 +436,15 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                 }
             }
             if (!ok) break;
-        } while (it.next(c, p, lane == 0));
+            i = -1;
+            if (p.more) {
+                if (!wait(&c.answer, (uint32_t)(asked - 1) & 1, &c.abort, p.err, 57)) break;
+                i = __shfl_sync(0xffffffffu, read_next(&c.next), 0);
+            }
+        }
         // no copy may still be on its way into this CTA's shared memory when it ends
         constexpr long long LIMIT = 1ll << 28;
-        if (asked > 0) wait(&c.next_full[(asked - 1) & 1], (uint32_t)((asked - 1) >> 1) & 1, &c.abort, p.err, 55, LIMIT);
+        if (asked > 0) wait(&c.answer, (uint32_t)(asked - 1) & 1, &c.abort, p.err, 55, LIMIT);
         for (int w = 0; w < 2; ++w)
             if (nq[w] > 0) wait(&c.q_full[w], (uint32_t)(nq[w] - 1) & 1, &c.abort, p.err, 55, LIMIT);
         for (; groups > 0; --groups) {   // from the last one back
@@ -451,12 +469,11 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
         uint32_t nq0 = 0, nq1 = 0; // uses of the query tiles
         bool ok = true;
         Walk it;
-        do {
-            Item x;
-            x.decode(p, it.i);
+        Item x;
+        while (it.next(c, p, x, lane)) {
             if (x.n0 + x.n1 == 0) continue;
             const int n = __shfl_sync(0xffffffffu, x.n(w), 0), o = __shfl_sync(0xffffffffu, x.n(1 - w), 0);
-            const bool pair = __shfl_sync(0xffffffffu, (int)x.pair, 0);
+            const bool pair = __shfl_sync(0xffffffffu, x.pair, 0);
             const int qt = pair ? w : 0;   // the query tile
             if (!wait(&c.q_full[qt], (qt ? nq1 : nq0) & 1, &c.abort, p.err, 60)) break;
             ++nq0;
@@ -489,7 +506,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                     const int kt = x.key_tile(w, j);
                     steps = x.steps(p, w, kt);
                     if (!wait(&c.full[r.g], r.phase, &c.abort, p.err, 63)) return false;
-                    const int tail = p.nk[x.st] - kt * BN;
+                    const int tail = x.nk - kt * BN;
                     if (tail < BN && (tail & 15)) {
                         // Rows behind the stream's last key, up to the 16 of a product's step: whatever they hold, 0
                         // times it has to be 0.  (16-byte chunks, whatever their order in a row.)
@@ -560,7 +577,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                 if (ok && w == 0) others();
             }
             if (!ok) break;
-        } while (it.next(c, p, lane == 0));
+        }
         // no product may still run when TMEM is freed
         ptx::mma_commit_warp(&c.drain);
         if (warp == MMA_WARP) wait(&c.drain, 0, &c.abort, p.err, 64, 1ll << 29);
@@ -578,9 +595,8 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
         int no = 0, nj = 0;   // outputs, joined pieces so far
         bool ok = true;
         Walk it;
-        do {
-            Item x;
-            x.decode(p, it.i);
+        Item x;
+        while (it.next(c, p, x, lane)) {
             const int n = x.n(w);
             const int tok = x.tok0 + (x.pair ? w * p.tpt : 0) + rt;
             const bool live = rt < p.tpt && tok < x.tok0 + x.ntok;
@@ -676,7 +692,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
             const bool writes = live && (x.pair || w == 0);
             const bool direct = x.slot < 0;
             float inv = direct ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-            const int64_t orow = (int64_t)p.qoff[x.st] + tok;
+            const int64_t orow = (int64_t)x.qrow + (tok - x.tok0);
             const int head = x.h * p.G + rh;
             uint16_t *out = p.out + orow * p.out_row + head * p.out_head;
             const int64_t slot = (int64_t)x.slot + (x.pair ? w : 0);
@@ -751,7 +767,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                 ptx::fence_proxy_async_smem();
                 ptx::mbar_arrive(&c.join_done);
             }
-        } while (it.next(c, p, lane == 0));
+        }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
     }
