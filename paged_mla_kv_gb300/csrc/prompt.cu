@@ -16,6 +16,7 @@
 #include <algorithm>
 #include <climits>
 #include <memory>
+#include <type_traits>
 
 #include "per_device.h"
 #include "ptx.cuh"
@@ -29,11 +30,12 @@ constexpr int BM = 128;              // rows of a query tile
 constexpr int BN = 128;              // keys of a tile
 constexpr int BOX = 64;              // values of a box's row: 128 bytes, one swizzle atom
 constexpr int VH = 64;               // keys of a half of a value tile
-constexpr int THREADS = 384;         // two softmax warpgroups, and one with a MMA warp for each of them and the TMA warp
-// Registers a thread: 168 at launch, of which the third warpgroup gives 80 to the others (2 * 208 + 88 = 3 * 168).
-constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 88;
-static_assert(2 * REGS_SOFTMAX + REGS_OTHER <= 3 * 168, "a split above the launch's total would wait forever");
-constexpr int MMA_WARP = 8, TMA_WARP = 10;
+// Warps: two softmax warpgroups, one for the outputs, a MMA warp for each softmax warpgroup, the TMA warp.
+constexpr int THREADS = 512;
+constexpr int OUT_WARP = 8, MMA_WARP = 12, TMA_WARP = 14;
+// Registers a thread: 128 at launch, of which the softmax takes more and the others less.
+constexpr int REGS_SOFTMAX = 200, REGS_OUT = 56, REGS_OTHER = 56;
+static_assert(2 * REGS_SOFTMAX + REGS_OUT + REGS_OTHER <= 4 * 128, "a split above the launch's total would wait forever");
 constexpr int MAX_UNITS = 24;
 constexpr int MAX_SMS = TF_PLAN_MAX_RANGES;
 
@@ -76,6 +78,7 @@ struct Params {
     float scale_log2, thr;           // c; 8 / c
     int32_t S, H, Hkv, G, tpt, causal, has_kr;   // tpt: tokens of a query tile
     int32_t more;                    // more items than SMs
+    int32_t out32;                   // output rows lie on 32 bytes
     int32_t item0[TF_MAX_STREAMS];   // first item
     int32_t qoff[TF_MAX_STREAMS], nq[TF_MAX_STREAMS], koff[TF_MAX_STREAMS], nk[TF_MAX_STREAMS];
     int32_t chunk[TF_MAX_STREAMS];   // key tiles of a split
@@ -157,18 +160,18 @@ struct Ctl {
     uint64_t full[MAX_UNITS], free[MAX_UNITS];     // of the ring's groups
     uint64_t s_full[2], p_full[2][2], o_full[2];   // P comes in halves of 64 keys
     uint64_t turn[2];                // of the MMA warps
-    uint64_t join_full, join_free;   // 32 columns of warpgroup 1's sums
-    uint64_t join_done;              // an item's sums are joined: query tile 1's room is free
+    uint64_t ml_full[2], ml_free[2]; // the rows' maxima and sums
+    uint64_t o_free[2];              // the sums have been read
     uint64_t answer;                 // to the question for another item
     uint64_t item_full[2], item_free[2];
     uint64_t drain;
     alignas(16) uint4 next;          // the answer
     Item item[2];
-    float2 ml[BM];                   // warpgroup 1's (m, l) of each row, for the join
+    float2 ml[2][BM];                // (m, l) of each row
     uint32_t tmem;
     int abort;
 };
-constexpr int SMEM = 229376 + 1024 + (int)((sizeof(Ctl) + 127) / 128 * 128);
+constexpr int SMEM = 229376 + (int)((sizeof(Ctl) + 127) / 128 * 128);
 static_assert(SMEM <= 232448, "227 KB");
 
 // ---- the next item: a CTA that has not been launched yet is taken over (cluster launch control) ----
@@ -257,6 +260,23 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
     }
 }
 
+// 16 columns of a warp's 32 lanes of TMEM, a lane a thread.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// 32 bytes at once, 32-byte aligned.
+__device__ __forceinline__ void store32(void *dst, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // The items of this CTA, as the roles that do not find them read them.
 struct Walk {
     uint32_t count = 0;
@@ -281,8 +301,7 @@ struct Walk {
 template <int DQK, int DV>
 __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constant__ Params p) {
     using L = Lay<DQK, DV>;
-    extern __shared__ uint8_t raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];   // swizzle atoms lie on 1 KB
     Ctl &c = *reinterpret_cast<Ctl *>(smem + L::BYTES);
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = (int)threadIdx.x & 31;
 
@@ -298,12 +317,12 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
             ptx::mbar_init(&c.p_full[i][1], 4);
             ptx::mbar_init(&c.o_full[i], 1);
             ptx::mbar_init(&c.turn[i], 1);
+            ptx::mbar_init(&c.ml_full[i], 4);
+            ptx::mbar_init(&c.ml_free[i], 4);
+            ptx::mbar_init(&c.o_free[i], 4);
             ptx::mbar_init(&c.item_full[i], 1);
-            ptx::mbar_init(&c.item_free[i], 10);
+            ptx::mbar_init(&c.item_free[i], 14);
         }
-        ptx::mbar_init(&c.join_full, 4);
-        ptx::mbar_init(&c.join_free, 4);
-        ptx::mbar_init(&c.join_done, 4);
         ptx::mbar_init(&c.answer, 1);
         ptx::mbar_init(&c.drain, 2);
         ptx::fence_mbar_init();
@@ -331,8 +350,8 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
         int room = L::U;           // free units
         uint32_t keys = 0;         // which groups are key tiles
         uint32_t groups = 0;       // so far, up to U
-        int asked = 0, nq[2] = {0, 0}, nj = 0;   // questions, uses of each query tile, joined items
-        bool ok = true, joined = false;
+        int asked = 0, nq[2] = {0, 0};   // questions, uses of each query tile
+        bool ok = true;
         int i = (int)blockIdx.x;
         for (uint32_t count = 0;; ++count) {
             Item x;
@@ -396,37 +415,29 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                 __syncwarp();
                 return true;
             };
-            auto load_q = [&]() {
-                // query tile 1's room also served the join of the item before
-                if (joined && !wait(&c.join_done, (uint32_t)(nj - 1) & 1, &c.abort, p.err, 56)) return false;
-                for (int w = 0; w < (x.pair ? 2 : 1); ++w, __syncwarp()) {
-                    if (nq[w] > 0 && !wait(&c.q_free[w], (uint32_t)(nq[w] - 1) & 1, &c.abort, p.err, 52)) return false;
-                    ++nq[w];
-                    if (lane != 0) continue;
+            auto load_q = [&](int w) {
+                if (nq[w] > 0 && !wait(&c.q_free[w], (uint32_t)(nq[w] - 1) & 1, &c.abort, p.err, 52)) return false;
+                ++nq[w];
+                if (lane == 0) {
                     ptx::mbar_arrive_expect_tx(&c.q_full[w], (uint32_t)(L::QB * p.tpt * p.G * 128));
                     for (int b = 0; b < L::QB; ++b)
-                        tma_load_3d(smem + w * L::Q_TILE + b * (BM * 128), &p.q, &c.q_full[w], b * BOX, x.h * p.G,
-                                    x.qrow + w * p.tpt);
+                        tma_load_3d(smem + w * L::Q_TILE + b * (BM * 128), &p.q, &c.q_full[w], b * BOX, x.h * p.G, x.qrow + w * p.tpt);
                 }
-                joined = !x.pair && x.n1 > 0;
-                nj += joined;
+                __syncwarp();
                 return true;
             };
             if (x.n0 + x.n1 == 0) ask();
-            // In the order in which the MMA warps take them; an item's first keys come before its queries, whose room
-            // is free only when the products of the item before are done.
+            // in the order in which the MMA warps take them
             if (x.pair) {
-                if (x.n1 > 0) ok = load_k(x.key_tile(1, 0)) && load_q();
+                if (x.n1 > 0) ok = load_q(0) && load_k(x.key_tile(1, 0)) && load_q(1);
                 for (int j = 0; ok && j < x.n1; ++j) {
                     if (j == x.n1 - 1) ask();
                     ok = load_v(x.key_tile(1, j));
                     if (ok && j + 1 < x.n1) ok = load_k(x.key_tile(1, j + 1));
                 }
             } else {
-                for (int w = 0; ok && w < 2; ++w) {
-                    if (x.n(w) > 0) ok = load_k(x.key_tile(w, 0));
-                    if (ok && w == 0 && x.n0 > 0) ok = load_q();
-                }
+                if (x.n0 > 0) ok = load_q(0) && load_k(x.key_tile(0, 0));
+                if (ok && x.n1 > 0) ok = load_k(x.key_tile(1, 0));
                 for (int j = 0; ok && j < x.n0; ++j) {
                     if (j == x.n0 - 1) ask();
                     for (int w = 0; ok && w < 2; ++w) {
@@ -453,7 +464,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
             wait(&c.full[head.g], head.phase, &c.abort, p.err, 55, LIMIT);
         }
         __syncwarp();
-    } else if (warp >= MMA_WARP && warp < TMA_WARP) {
+    } else if (warp == MMA_WARP || warp == MMA_WARP + 1) {
         // ================= MMA: a warp for each softmax warpgroup, so that neither waits behind the other =================
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
         const int w = warp - MMA_WARP;
@@ -466,6 +477,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
         Ring<L::U> r;
         uint32_t np = 0;           // softmax tiles of this warpgroup
         uint32_t nt = 0;           // turns
+        uint32_t no = 0;           // outputs
         uint32_t nq0 = 0, nq1 = 0; // uses of the query tiles
         bool ok = true;
         Walk it;
@@ -478,121 +490,148 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
             if (!wait(&c.q_full[qt], (qt ? nq1 : nq0) & 1, &c.abort, p.err, 60)) break;
             ++nq0;
             nq1 += pair;
+            const int rounds = max(n, o);
             // A query tile is free once both warps say so, or its only one twice.
             auto free_q = [&]() {
                 ptx::mma_commit_warp(&c.q_free[qt]);
                 if (pair) ptx::mma_commit_warp(&c.q_free[qt]);
             };
-            // Both warps go through every tile in the order in which they are copied, and wait for and free those
-            // of the other one too: a parity tells a phase from the one before it only.
-            auto skip = [&](int units) {
-                if (!wait(&c.full[r.g], r.phase, &c.abort, p.err, 61)) return false;
-                if (lane == 0) ptx::mbar_arrive(&c.free[r.g]);
-                r.step(units);
-                return true;
+            // A group of the ring is free once both warps say so; one that only this warp takes, once it says so twice.
+            auto free_group = [&](uint64_t *bar, int j) {
+                ptx::mma_commit_warp(bar);
+                if (!pair || j >= o) ptx::mma_commit_warp(bar);
             };
             // Round j of this warp: the product with the values of step j (`pv`), that with the keys of step j + 1 (`qk`).
             // All but the first half of the values' product is issued in turns.  Products of two warps that are issued side
             // by side run interleaved: both end late, both softmaxes then run together, and the tensor cores idle
-            // meanwhile (4,500 cycles a step of two 192-wide tiles; in turns ROUND).
-            auto round = [&](int j, bool pv, bool qk) {
-                int steps = 0, keys_u = 0, vals_u = 0;
-                uint64_t *keys_free = nullptr, *vals_free = nullptr;
+            // meanwhile (2,048 rows behind 16,384, 192 wide: 375 us, in turns 330).  The last round, without keys, needs no
+            // turn: the other warp's next item does not wait for it.
+            // A barrier's parity tells a phase only from the one before it, so a group must not be waited for while an
+            // older use of its barrier is still on its way.  This warp steps over groups that only the other one takes;
+            // but a turn is given after the waits for the keys of its round, so that at most the last values and keys (three
+            // groups) are not known to have landed, and a barrier comes back after 8 groups or more.  An item's first
+            // keys are waited for behind the turn for the same reason.
+            // A warp's first round (no values yet), the ones with both, and its last (no keys any more) are compiled on
+            // their own: the middle ones are the loop that has to keep up, and all their tiles are whole.
+            auto round = [&](int j, auto has_pv, auto has_qk) {
+                constexpr bool pv = decltype(has_pv)::value, qk = decltype(has_qk)::value;
                 const uint32_t my_turn = (nt - (w == 0)) & 1;
                 bool turn = w == 0 && nt == 0, landed = false;
-                Ring<L::U> next = r;   // the keys'
-                if (pv) next.step(2);
+                const Ring<L::U> vals = r;
+                int steps = BN / 16;
                 if (pv) {
-                    const int kt = x.key_tile(w, j);
-                    steps = x.steps(p, w, kt);
                     if (!wait(&c.full[r.g], r.phase, &c.abort, p.err, 63)) return false;
-                    const int tail = x.nk - kt * BN;
-                    if (tail < BN && (tail & 15)) {
-                        // Rows behind the stream's last key, up to the 16 of a product's step: whatever they hold, 0
-                        // times it has to be 0.  (16-byte chunks, whatever their order in a row.)
-                        int u = r.u + (tail >= VH);
-                        if (u >= L::U) u -= L::U;
-                        const int chunks = (16 - (tail & 15)) * 8;
-                        uint8_t *dst = smem + L::OFF_R + u * L::UNIT + (tail & (VH - 1)) * 128;
-                        for (int i = lane; i < chunks * L::VB; i += 32)
-                            *reinterpret_cast<uint4 *>(dst + i / chunks * (VH * 128) + i % chunks * 16) = make_uint4(0, 0, 0, 0);
-                        ptx::fence_proxy_async_smem();
-                        __syncwarp();
+                    r.step(2);
+                    if (!qk) {
+                        const int kt = x.key_tile(w, j), tail = x.nk - kt * BN;
+                        steps = x.steps(p, w, kt);
+                        if (tail < BN && (tail & 15)) {
+                            // Rows behind the stream's last key, up to the 16 of a product's step: whatever they hold, 0
+                            // times it has to be 0.  (16-byte chunks, whatever their order in a row.)
+                            int u = vals.u + (tail >= VH);
+                            if (u >= L::U) u -= L::U;
+                            const int chunks = (16 - (tail & 15)) * 8;
+                            uint8_t *dst = smem + L::OFF_R + u * L::UNIT + (tail & (VH - 1)) * 128;
+                            for (int i = lane; i < chunks * L::VB; i += 32)
+                                *reinterpret_cast<uint4 *>(dst + i / chunks * (VH * 128) + i % chunks * 16) = make_uint4(0, 0, 0, 0);
+                            ptx::fence_proxy_async_smem();
+                            __syncwarp();
+                        }
                     }
                     // P's first half; meanwhile a look at what the rest of the round waits for
                     const long long t0 = clock64();
                     for (uint32_t spins = 1; !look(&c.p_full[w][0], np & 1); ++spins) {
-                        if (qk && !landed) landed = look(&c.full[next.g], next.phase);
-                        if (!turn) turn = look(&c.turn[w], my_turn);
+                        if (qk && !landed) landed = look(&c.full[r.g], r.phase);
+                        if (qk && !turn) turn = look(&c.turn[w], my_turn);
                         if ((spins & 4095u) == 0 && expired(t0, 1ll << 31, &c.abort, p.err, 62)) return false;
                     }
+                    // the item before's sums are read out
+                    if (j == 0 && no > 0 && !wait(&c.o_free[w], (no - 1) & 1, &c.abort, p.err, 66)) return false;
                     ptx::tc_fence_after();
-                    pv_warp(to, ts, dv + (uint64_t)((r.u * L::UNIT) >> 4), IPV, j > 0, min(4, steps));
-                    vals_u = r.u + 1 == L::U ? 0 : r.u + 1;
-                    vals_free = &c.free[r.g];
-                    r.step(2);
+                    pv_warp(to, ts, dv + (uint64_t)((vals.u * L::UNIT) >> 4), IPV, j > 0, qk ? 4 : min(4, steps));
                 }
                 // What the turn's products wait for, P's second half last: it is what comes last.
+                const Ring<L::U> keys = r;
                 if (qk) {
+                    if (!pv && !turn && !wait(&c.turn[w], my_turn, &c.abort, p.err, 65)) return false;
                     if (!landed && !wait(&c.full[r.g], r.phase, &c.abort, p.err, 61)) return false;
-                    keys_u = r.u;
-                    keys_free = &c.free[r.g];
                     r.step(L::KU);
+                    if (pv && !turn && !wait(&c.turn[w], my_turn, &c.abort, p.err, 65)) return false;
+                    ++nt;
                 }
-                if (!turn && !wait(&c.turn[w], my_turn, &c.abort, p.err, 65)) return false;
-                ++nt;
-                if (pv && !wait(&c.p_full[w][1], np++ & 1, &c.abort, p.err, 62)) return false;
-                ptx::tc_fence_after();
                 if (pv) {
-                    pv_warp(to, ts + 32, dv + (uint64_t)((vals_u * L::UNIT) >> 4), IPV, 1, max(0, steps - 4));
-                    ptx::mma_commit_warp(vals_free);
-                    if (j == n - 1) ptx::mma_commit_warp(&c.o_full[w]);
+                    if (!wait(&c.p_full[w][1], np++ & 1, &c.abort, p.err, 62)) return false;
+                    ptx::tc_fence_after();
+                    const int u = vals.u + 1 == L::U ? 0 : vals.u + 1;
+                    pv_warp(to, ts + 32, dv + (uint64_t)((u * L::UNIT) >> 4), IPV, 1, qk ? 4 : max(0, steps - 4));
+                    free_group(&c.free[vals.g], j);
+                    if (!qk) ptx::mma_commit_warp(&c.o_full[w]);
                 }
                 if (qk) {
+                    if (!pv) ptx::tc_fence_after();
                     const uint64_t a = dq + (uint64_t)((qt * L::Q_TILE) >> 4);
-                    int u = keys_u;
+                    int u = keys.u;
 #pragma unroll
                     for (int i = 0; i < L::QB; ++i) {
                         ptx::mma4_bf16_ss_warp(ts, a + (uint64_t)((i * BM * 128) >> 4), dk + (uint64_t)((u * L::UNIT) >> 4), IQK, i == 0);
                         u = u + L::BU == L::U ? 0 : u + L::BU;
                     }
                     ptx::mma_commit_warp(&c.s_full[w]);
-                    ptx::mma_commit_warp(keys_free);
-                    if (j + 1 == n - 1) free_q();
+                    free_group(&c.free[keys.g], j + 1);
+                    if (lane == 0) ptx::mbar_arrive(&c.turn[1 - w]);
                 }
+                return true;
+            };
+            // A turn of a round in which this warp has no keys.
+            auto pass = [&]() {
+                if (!(w == 0 && nt == 0) && !wait(&c.turn[w], (nt - (w == 0)) & 1, &c.abort, p.err, 65)) return false;
+                ++nt;
                 if (lane == 0) ptx::mbar_arrive(&c.turn[1 - w]);
                 return true;
             };
-            if (n == 0) free_q();
-            const int rounds = max(n, o);
+            constexpr std::true_type yes{};
+            constexpr std::false_type none{};
+            // The groups that only the other warp takes lie before the own ones of a round (1) or behind them (0); with two
+            // query tiles they are those that this one has no step for.
+            auto others = [&](int j) {
+                if (j >= 0 && j < o && (!pair || j >= n)) r.step(2);
+                if (j + 1 < o && (!pair || j + 1 >= n)) r.step(L::KU);
+            };
+            if (w == 1) others(-1);
+            ok = n > 0 ? round(-1, none, yes) : pass();
+            if (w == 0) others(-1);
 #pragma unroll 1
-            for (int j = -1; ok && j < rounds; ++j) {
-                // the other warp's tiles before (1) or after (0) the own ones; with two query tiles those that only it takes
-                auto others = [&]() {
-                    if (j >= 0 && j < o && (!pair || j >= n)) ok = skip(2);
-                    if (ok && j + 1 < o && (!pair || j + 1 >= n)) ok = skip(L::KU);
-                };
-                if (w == 1) others();
-                if (ok) ok = round(j, j >= 0 && j < n, j + 1 < n);
-                if (ok && w == 0) others();
+            for (int j = 0; ok && j + 1 < n; ++j) {
+                if (!pair && w == 1) others(j);
+                ok = round(j, yes, yes);
+                if (!pair && w == 0) others(j);
+            }
+            free_q();
+#pragma unroll 1
+            for (int j = max(0, n - 1); ok && j < rounds; ++j) {
+                if (w == 1) others(j);
+                if (j < n) ok = round(j, yes, none);
+                if (ok && j + 1 < rounds) ok = pass();
+                if (w == 0) others(j);
             }
             if (!ok) break;
+            no += n > 0;
         }
         // no product may still run when TMEM is freed
         ptx::mma_commit_warp(&c.drain);
         if (warp == MMA_WARP) wait(&c.drain, 0, &c.abort, p.err, 64, 1ll << 29);
         __syncwarp();
-    } else if (warp < 8) {
-        // ================= softmax, and the output: a query row a thread =================
+    } else if (warp < OUT_WARP) {
+        // ================= softmax: a query row a thread =================
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
         const int w = warp >> 2;
         const int row = (int)threadIdx.x & (BM - 1);
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + w * BN + lanes, to = tmem + 2 * BN + w * DV + lanes;
         const float cl = p.scale_log2;
-        const int rt = row / p.G, rh = row - rt * p.G;   // the row's token in the tile, and its head
+        const int rt = row / p.G;   // the row's token in the tile
         uint32_t ns = 0;
-        int no = 0, nj = 0;   // outputs, joined pieces so far
+        uint32_t nml = 0;   // items with keys
         bool ok = true;
         Walk it;
         Item x;
@@ -679,94 +718,116 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
             if (ok && n > 0) {
-                ok = wait(&c.o_full[w], (uint32_t)no & 1, &c.abort, p.err, 72);
-                ++no;
+                if (nml > 0) ok = wait(&c.ml_free[w], (nml - 1) & 1, &c.abort, p.err, 71);
+                ++nml;
+                c.ml[w][row] = make_float2(m, l);
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&c.ml_full[w]);
+            }
+            if (!ok) break;
+        }
+    } else if (warp < MMA_WARP) {
+        // ================= outputs: a query row a thread, beside the next item's softmax =================
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OUT));
+        const int row = (int)threadIdx.x & (BM - 1);
+        const uint32_t to = tmem + 2 * BN + ((uint32_t)((warp & 3) * 32) << 16);
+        const float cl = p.scale_log2;
+        const int rt = row / p.G, rh = row - rt * p.G;   // the row's token in the tile, and its head
+        uint32_t no0 = 0, no1 = 0;                       // outputs of each warpgroup
+        bool ok = true;
+        Walk it;
+        Item x;
+        while (it.next(c, p, x, lane)) {
+            const bool join = !x.pair && x.n1 > 0;   // one query tile: the two warpgroups' sums are joined
+            // A warpgroup's maxima and sums, and its O after its last product.
+            auto ready = [&](int w, float &m, float &l) {
+                m = -INFINITY;
+                l = 0.f;
+                if (x.n(w) == 0) return true;
+                const uint32_t k = w ? no1++ : no0++;
+                if (!wait(&c.ml_full[w], k & 1, &c.abort, p.err, 72)) return false;
+                const float2 t = c.ml[w][row];
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&c.ml_free[w]);
+                m = t.x;
+                l = t.y;
+                if (!wait(&c.o_full[w], k & 1, &c.abort, p.err, 73)) return false;
                 ptx::tc_fence_after();
-            }
-            if (!ok) break;
-            // One query tile: warpgroup 1's sums join warpgroup 0's, 32 columns at a time through the room of
-            // query tile 1 (row by row: warp i of one with warp i of the other).
-            const bool join = !x.pair && x.n1 > 0;
-            float f0 = 1.f, f1 = 0.f;
-            float *xch = reinterpret_cast<float *>(smem + L::Q_TILE);   // [32][BM]
-            const bool writes = live && (x.pair || w == 0);
-            const bool direct = x.slot < 0;
-            float inv = direct ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-            const int64_t orow = (int64_t)x.qrow + (tok - x.tok0);
-            const int head = x.h * p.G + rh;
-            uint16_t *out = p.out + orow * p.out_row + head * p.out_head;
-            const int64_t slot = (int64_t)x.slot + (x.pair ? w : 0);
-            float *part = p.part + (slot * BM + row) * DV;
+                return true;
+            };
 #pragma unroll 1
-            for (int q = 0; q < DV; q += 32) {
-                uint32_t o[32];
-                if (n > 0) {
-                    ptx::tmem_ld32(to + q, o);
-                    ptx::tmem_ld_wait();
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = 0u;
+            for (int w = 0; w < (x.pair ? 2 : 1); ++w) {
+                float m, l, f0 = 1.f, f1 = 0.f;
+                ok = ready(w, m, l);
+                if (ok && join) {
+                    float m1, l1;
+                    ok = ready(1, m1, l1);
+                    const float top = fmaxf(m, m1);
+                    f0 = m == -INFINITY ? 0.f : ptx::ex2((m - top) * cl);
+                    f1 = m1 == -INFINITY ? 0.f : ptx::ex2((m1 - top) * cl);
+                    l = l * f0 + l1 * f1;
+                    m = top;
                 }
-                if (join && w == 1) {
-                    if (nj > 0 && !wait(&c.join_free, (uint32_t)(nj - 1) & 1, &c.abort, p.err, 73)) {
-                        ok = false;
-                        break;
-                    }
-                    if (q == 0) c.ml[row] = make_float2(m, l);
+                if (!ok) break;
+                const int t = rt + (x.pair ? w * p.tpt : 0);   // the row's token in the block
+                const bool live = rt < p.tpt && t < x.ntok;
+                const int head = x.h * p.G + rh;
+                const int64_t orow = (int64_t)x.qrow + t;
+                if (x.slot < 0) f0 *= l == 0.f ? 0.f : 1.f / l, f1 *= l == 0.f ? 0.f : 1.f / l;
+                uint16_t *out = p.out + orow * p.out_row + head * p.out_head;
+                const int64_t slot = (int64_t)x.slot + w;
+                float *part = p.part + (slot * BM + row) * DV;
+#pragma unroll 1
+                for (int q = 0; q < DV; q += 16) {
+                    uint32_t o[16];
+                    if (x.n(w) > 0) {
+                        tmem_ld16(to + w * DV + q, o);
+                        ptx::tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) xch[i * BM + row] = __uint_as_float(o[i]);
-                    ptx::fence_proxy_async_smem();   // queries are copied here next
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&c.join_full);
-                    ++nj;
-                } else if (join) {
-                    if (!wait(&c.join_full, (uint32_t)nj & 1, &c.abort, p.err, 74)) {
-                        ok = false;
-                        break;
-                    }
-                    ++nj;
-                    if (q == 0) {
-                        const float2 other = c.ml[row];
-                        const float top = fmaxf(m, other.x);
-                        f0 = m == -INFINITY ? 0.f : ptx::ex2((m - top) * cl);
-                        f1 = other.x == -INFINITY ? 0.f : ptx::ex2((other.x - top) * cl);
-                        l = l * f0 + other.y * f1;
-                        m = top;
-                        if (direct) inv = l == 0.f ? 0.f : 1.f / l;
-                    }
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f0);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f0 + xch[i * BM + row] * f1);
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&c.join_free);
+                        for (int i = 0; i < 16; ++i) o[i] = 0u;
+                    }
+                    if (join) {
+                        uint32_t u[16];
+                        tmem_ld16(to + DV + q, u);
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(fmaf(__uint_as_float(u[i]), f1, __uint_as_float(o[i])));
+                    }
+                    if (!live) continue;
+                    if (x.slot < 0) {
+                        uint32_t v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = ptx::pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+                        if (p.out32) {
+                            store32(out + q, v);
+                        } else {
+                            *reinterpret_cast<uint4 *>(out + q) = make_uint4(v[0], v[1], v[2], v[3]);
+                            *reinterpret_cast<uint4 *>(out + q + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; i += 8) {
+                            uint32_t v[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) v[k] = o[i + k];
+                            store32(part + q + i, v);
+                        }
+                    }
                 }
-                if (writes && direct) {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        uint32_t v[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            v[k] = ptx::pack_bf16x2(__uint_as_float(o[i + 2 * k]) * inv, __uint_as_float(o[i + 2 * k + 1]) * inv);
-                        *reinterpret_cast<uint4 *>(out + q + i) = make_uint4(v[0], v[1], v[2], v[3]);
-                    }
-                } else if (writes) {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        *reinterpret_cast<uint4 *>(part + q + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane < 2 && (lane == w || join) && x.n(lane) > 0) ptx::mbar_arrive(&c.o_free[lane]);
+                if (live) {
+                    if (x.slot >= 0)
+                        reinterpret_cast<float2 *>(p.part + p.slots * BM * DV)[slot * BM + row] = make_float2(m, l);
+                    else if (p.lse)
+                        p.lse[orow * p.H + head] = l == 0.f ? -INFINITY : (m * cl + log2f(l)) * 0.69314718055994531f;
                 }
             }
             if (!ok) break;
-            if (writes) {
-                if (!direct)
-                    reinterpret_cast<float2 *>(p.part + p.slots * BM * DV)[slot * BM + row] = make_float2(m, l);
-                else if (p.lse)
-                    p.lse[orow * p.H + head] = l == 0.f ? -INFINITY : (m * cl + log2f(l)) * 0.69314718055994531f;
-            }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (join && w == 0 && lane == 0) {   // query tile 1's room is free again
-                ptx::fence_proxy_async_smem();
-                ptx::mbar_arrive(&c.join_done);
-            }
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
@@ -1016,6 +1077,7 @@ int launch_prompt_attend(tf_kvpool *pool, const int64_t *h_nq, const int64_t *h_
     p.out = static_cast<uint16_t *>(out->d_p);
     p.out_row = out->row;
     p.out_head = out->head;
+    p.out32 = ((reinterpret_cast<uintptr_t>(out->d_p) | (uintptr_t)out->row * 2 | (H > 1 ? (uintptr_t)out->head * 2 : 0)) & 31) == 0;
     p.lse = d_lse;
     p.part = static_cast<float *>(d_ws);
     p.err = pool->err;
