@@ -30,11 +30,11 @@ constexpr int BM = 128;              // rows of a query tile
 constexpr int BN = 128;              // keys of a tile
 constexpr int BOX = 64;              // values of a box's row: 128 bytes, one swizzle atom
 constexpr int VH = 64;               // keys of a half of a value tile
-// Warps: two softmax warpgroups, one for the outputs, a MMA warp for each softmax warpgroup, the TMA warp.
+// Warps: two softmax warpgroups, one for the outputs, the MMA warp, the TMA warp, and one that finds the next item.
 constexpr int THREADS = 512;
-constexpr int OUT_WARP = 8, MMA_WARP = 12, TMA_WARP = 14;
+constexpr int OUT_WARP = 8, MMA_WARP = 12, TMA_WARP = 13, ITEM_WARP = 14;
 // Registers a thread: 128 at launch, of which the softmax takes more and the others less.
-constexpr int REGS_SOFTMAX = 200, REGS_OUT = 56, REGS_OTHER = 56;
+constexpr int REGS_SOFTMAX = 192, REGS_OUT = 64, REGS_OTHER = 64;
 static_assert(2 * REGS_SOFTMAX + REGS_OUT + REGS_OTHER <= 4 * 128, "a split above the launch's total would wait forever");
 constexpr int MAX_UNITS = 24;
 constexpr int MAX_SMS = TF_PLAN_MAX_RANGES;
@@ -159,10 +159,9 @@ struct Ctl {
     uint64_t q_full[2], q_free[2];
     uint64_t full[MAX_UNITS], free[MAX_UNITS];     // of the ring's groups
     uint64_t s_full[2], p_full[2][2], o_full[2];   // P comes in halves of 64 keys
-    uint64_t turn[2];                // of the MMA warps
     uint64_t ml_full[2], ml_free[2]; // the rows' maxima and sums
     uint64_t o_free[2];              // the sums have been read
-    uint64_t answer;                 // to the question for another item
+    uint64_t ask, answer;            // the question for another item
     uint64_t item_full[2], item_free[2];
     uint64_t drain;
     alignas(16) uint4 next;          // the answer
@@ -270,11 +269,28 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "r"(taddr));
 }
 
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
 // 32 bytes at once, 32-byte aligned.
 __device__ __forceinline__ void store32(void *dst, const uint32_t (&v)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
                  "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
+}
+
+// The same without sleeping, for the warp that the tensor cores wait for.
+__device__ __forceinline__ bool spin(uint64_t *bar, uint32_t parity, volatile int *abort, DevErr *err, int site) {
+    const long long t0 = clock64();
+    for (uint32_t spins = 1; !look(bar, parity); ++spins)
+        if ((spins & 4095u) == 0 && expired(t0, 1ll << 31, abort, err, site)) return false;
+    return true;
 }
 
 // The items of this CTA, as the roles that do not find them read them.
@@ -308,23 +324,23 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
     ptx::griddep_launch_dependents();
     if (threadIdx.x == 0) {
         c.abort = 0;
-        for (int i = 0; i < L::U; ++i) ptx::mbar_init(&c.full[i], 1), ptx::mbar_init(&c.free[i], 2);
+        for (int i = 0; i < L::U; ++i) ptx::mbar_init(&c.full[i], 1), ptx::mbar_init(&c.free[i], 1);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&c.q_full[i], 1);
-            ptx::mbar_init(&c.q_free[i], 2);
+            ptx::mbar_init(&c.q_free[i], 1);
             ptx::mbar_init(&c.s_full[i], 1);
             ptx::mbar_init(&c.p_full[i][0], 4);
             ptx::mbar_init(&c.p_full[i][1], 4);
             ptx::mbar_init(&c.o_full[i], 1);
-            ptx::mbar_init(&c.turn[i], 1);
             ptx::mbar_init(&c.ml_full[i], 4);
             ptx::mbar_init(&c.ml_free[i], 4);
             ptx::mbar_init(&c.o_free[i], 4);
             ptx::mbar_init(&c.item_full[i], 1);
             ptx::mbar_init(&c.item_free[i], 14);
         }
+        ptx::mbar_init(&c.ask, 1);
         ptx::mbar_init(&c.answer, 1);
-        ptx::mbar_init(&c.drain, 2);
+        ptx::mbar_init(&c.drain, 1);
         ptx::fence_mbar_init();
     }
     if (warp == MMA_WARP) {
@@ -350,28 +366,15 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
         int room = L::U;           // free units
         uint32_t keys = 0;         // which groups are key tiles
         uint32_t groups = 0;       // so far, up to U
-        int asked = 0, nq[2] = {0, 0};   // questions, uses of each query tile
+        int nq[2] = {0, 0};        // uses of each query tile
         bool ok = true;
-        int i = (int)blockIdx.x;
-        for (uint32_t count = 0;; ++count) {
-            Item x;
-            x.decode(p, i);
-            if (count >= 2 && !wait(&c.item_free[count & 1], (count / 2 - 1) & 1, &c.abort, p.err, 51)) break;
-            if (lane == 0) {
-                c.item[count & 1] = x;
-                ptx::mbar_arrive(&c.item_full[count & 1]);
-            }
-            if (i < 0) break;
-            // The next item is asked for when this one's last tiles are copied.  Asked for at an item's start it is
-            // taken from an SM that has none yet, or runs behind an item that others would have ended before.
+        Walk it;
+        Item x;
+        while (it.next(c, p, x, lane)) {
+            // The next item is asked for shortly before this one's last tiles are copied.  Asked for at an item's start it
+            // is taken from an SM that has none yet, or waits behind an item while others end.
             auto ask = [&]() {
-                if (p.more && lane == 0) {
-                    ptx::fence_proxy_async_smem();   // the answer before has been read
-                    ptx::mbar_arrive_expect_tx(&c.answer, 16);
-                    ask_next(&c.next, &c.answer);
-                }
-                asked += p.more;
-                __syncwarp();
+                if (p.more && lane == 0) ptx::mbar_arrive(&c.ask);
             };
             // The next group's barrier, once there is room for it.
             auto group = [&](int units, bool is_keys) -> uint64_t * {
@@ -431,7 +434,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
             if (x.pair) {
                 if (x.n1 > 0) ok = load_q(0) && load_k(x.key_tile(1, 0)) && load_q(1);
                 for (int j = 0; ok && j < x.n1; ++j) {
-                    if (j == x.n1 - 1) ask();
+                    if (j == max(0, x.n1 - 2)) ask();
                     ok = load_v(x.key_tile(1, j));
                     if (ok && j + 1 < x.n1) ok = load_k(x.key_tile(1, j + 1));
                 }
@@ -439,7 +442,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                 if (x.n0 > 0) ok = load_q(0) && load_k(x.key_tile(0, 0));
                 if (ok && x.n1 > 0) ok = load_k(x.key_tile(1, 0));
                 for (int j = 0; ok && j < x.n0; ++j) {
-                    if (j == x.n0 - 1) ask();
+                    if (j == max(0, x.n0 - 2)) ask();
                     for (int w = 0; ok && w < 2; ++w) {
                         if (j < x.n(w)) ok = load_v(x.key_tile(w, j));
                         if (ok && j + 1 < x.n(w)) ok = load_k(x.key_tile(w, j + 1));
@@ -447,15 +450,9 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                 }
             }
             if (!ok) break;
-            i = -1;
-            if (p.more) {
-                if (!wait(&c.answer, (uint32_t)(asked - 1) & 1, &c.abort, p.err, 57)) break;
-                i = __shfl_sync(0xffffffffu, read_next(&c.next), 0);
-            }
         }
         // no copy may still be on its way into this CTA's shared memory when it ends
         constexpr long long LIMIT = 1ll << 28;
-        if (asked > 0) wait(&c.answer, (uint32_t)(asked - 1) & 1, &c.abort, p.err, 55, LIMIT);
         for (int w = 0; w < 2; ++w)
             if (nq[w] > 0) wait(&c.q_full[w], (uint32_t)(nq[w] - 1) & 1, &c.abort, p.err, 55, LIMIT);
         for (; groups > 0; --groups) {   // from the last one back
@@ -464,163 +461,120 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
             wait(&c.full[head.g], head.phase, &c.abort, p.err, 55, LIMIT);
         }
         __syncwarp();
-    } else if (warp == MMA_WARP || warp == MMA_WARP + 1) {
-        // ================= MMA: a warp for each softmax warpgroup, so that neither waits behind the other =================
+    } else if (warp == MMA_WARP) {
+        // ================= MMA =================
+        // One warp for both warpgroups, first one's values and next keys, then the other's: in that order the tensor cores work
+        // for one while the other's softmax runs.  (Two warps, each at its own pace, came to run side by side: both products
+        // interleaved, both ended late, both softmaxes together, the tensor cores idle meanwhile.)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
-        const int w = warp - MMA_WARP;
         const uint64_t dq = ptx::sdesc_sw128(ptx::smem_u32(smem), 16, 1024);
         const uint64_t dk = ptx::sdesc_sw128(ptx::smem_u32(smem + L::OFF_R), 16, 1024);
         const uint64_t dv = ptx::sdesc_sw128(ptx::smem_u32(smem + L::OFF_R), VH * 128, 1024);
         constexpr uint32_t IQK = ptx::idesc_bf16_f32(BM, BN, false, false);
         constexpr uint32_t IPV = ptx::idesc_bf16_f32(BM, DV, false, true);
-        const uint32_t ts = tmem + w * BN, to = tmem + 2 * BN + w * DV;
         Ring<L::U> r;
-        uint32_t np = 0;           // softmax tiles of this warpgroup
-        uint32_t nt = 0;           // turns
-        uint32_t no = 0;           // outputs
-        uint32_t nq0 = 0, nq1 = 0; // uses of the query tiles
+        uint32_t np0 = 0, np1 = 0;   // softmax tiles of each warpgroup
+        uint32_t no0 = 0, no1 = 0;   // outputs
+        uint32_t nq0 = 0, nq1 = 0;   // uses of the query tiles
         bool ok = true;
         Walk it;
         Item x;
         while (it.next(c, p, x, lane)) {
-            if (x.n0 + x.n1 == 0) continue;
-            const int n = __shfl_sync(0xffffffffu, x.n(w), 0), o = __shfl_sync(0xffffffffu, x.n(1 - w), 0);
-            const bool pair = __shfl_sync(0xffffffffu, x.pair, 0);
-            const int qt = pair ? w : 0;   // the query tile
-            if (!wait(&c.q_full[qt], (qt ? nq1 : nq0) & 1, &c.abort, p.err, 60)) break;
-            ++nq0;
-            nq1 += pair;
-            const int rounds = max(n, o);
-            // A query tile is free once both warps say so, or its only one twice.
-            auto free_q = [&]() {
-                ptx::mma_commit_warp(&c.q_free[qt]);
-                if (pair) ptx::mma_commit_warp(&c.q_free[qt]);
-            };
-            // A group of the ring is free once both warps say so; one that only this warp takes, once it says so twice.
-            auto free_group = [&](uint64_t *bar, int j) {
-                ptx::mma_commit_warp(bar);
-                if (!pair || j >= o) ptx::mma_commit_warp(bar);
-            };
-            // Round j of this warp: the product with the values of step j (`pv`), that with the keys of step j + 1 (`qk`).
-            // All but the first half of the values' product is issued in turns.  Products of two warps that are issued side
-            // by side run interleaved: both end late, both softmaxes then run together, and the tensor cores idle
-            // meanwhile (2,048 rows behind 16,384, 192 wide: 375 us, in turns 330).  The last round, without keys, needs no
-            // turn: the other warp's next item does not wait for it.
-            // A barrier's parity tells a phase only from the one before it, so a group must not be waited for while an
-            // older use of its barrier is still on its way.  This warp steps over groups that only the other one takes;
-            // but a turn is given after the waits for the keys of its round, so that at most the last values and keys (three
-            // groups) are not known to have landed, and a barrier comes back after 8 groups or more.  An item's first
-            // keys are waited for behind the turn for the same reason.
-            // A warp's first round (no values yet), the ones with both, and its last (no keys any more) are compiled on
-            // their own: the middle ones are the loop that has to keep up, and all their tiles are whole.
-            auto round = [&](int j, auto has_pv, auto has_qk) {
-                constexpr bool pv = decltype(has_pv)::value, qk = decltype(has_qk)::value;
-                const uint32_t my_turn = (nt - (w == 0)) & 1;
-                bool turn = w == 0 && nt == 0, landed = false;
-                const Ring<L::U> vals = r;
-                int steps = BN / 16;
-                if (pv) {
-                    if (!wait(&c.full[r.g], r.phase, &c.abort, p.err, 63)) return false;
-                    r.step(2);
-                    if (!qk) {
-                        const int kt = x.key_tile(w, j), tail = x.nk - kt * BN;
-                        steps = x.steps(p, w, kt);
-                        if (tail < BN && (tail & 15)) {
-                            // Rows behind the stream's last key, up to the 16 of a product's step: whatever they hold, 0
-                            // times it has to be 0.  (16-byte chunks, whatever their order in a row.)
-                            int u = vals.u + (tail >= VH);
-                            if (u >= L::U) u -= L::U;
-                            const int chunks = (16 - (tail & 15)) * 8;
-                            uint8_t *dst = smem + L::OFF_R + u * L::UNIT + (tail & (VH - 1)) * 128;
-                            for (int i = lane; i < chunks * L::VB; i += 32)
-                                *reinterpret_cast<uint4 *>(dst + i / chunks * (VH * 128) + i % chunks * 16) = make_uint4(0, 0, 0, 0);
-                            ptx::fence_proxy_async_smem();
-                            __syncwarp();
-                        }
-                    }
-                    // P's first half; meanwhile a look at what the rest of the round waits for
-                    const long long t0 = clock64();
-                    for (uint32_t spins = 1; !look(&c.p_full[w][0], np & 1); ++spins) {
-                        if (qk && !landed) landed = look(&c.full[r.g], r.phase);
-                        if (qk && !turn) turn = look(&c.turn[w], my_turn);
-                        if ((spins & 4095u) == 0 && expired(t0, 1ll << 31, &c.abort, p.err, 62)) return false;
-                    }
-                    // the item before's sums are read out
-                    if (j == 0 && no > 0 && !wait(&c.o_free[w], (no - 1) & 1, &c.abort, p.err, 66)) return false;
-                    ptx::tc_fence_after();
-                    pv_warp(to, ts, dv + (uint64_t)((vals.u * L::UNIT) >> 4), IPV, j > 0, qk ? 4 : min(4, steps));
-                }
-                // What the turn's products wait for, P's second half last: it is what comes last.
-                const Ring<L::U> keys = r;
-                if (qk) {
-                    if (!pv && !turn && !wait(&c.turn[w], my_turn, &c.abort, p.err, 65)) return false;
-                    if (!landed && !wait(&c.full[r.g], r.phase, &c.abort, p.err, 61)) return false;
+            const int n0 = x.n0, n1 = x.n1;
+            if (n0 + n1 == 0) continue;
+            const bool pair = x.pair;
+            Ring<L::U> keys, vals;
+            // Scores of warpgroup w's step j.  With two query tiles both warpgroups use a tile's keys, and the first to come
+            // takes them from the ring; so with the values.
+            auto qk = [&](int w, int j) {
+                if (w == 0 || !pair || j >= n0) {
+                    if (!spin(&c.full[r.g], r.phase, &c.abort, p.err, 61)) return false;
+                    keys = r;
                     r.step(L::KU);
-                    if (pv && !turn && !wait(&c.turn[w], my_turn, &c.abort, p.err, 65)) return false;
-                    ++nt;
                 }
-                if (pv) {
-                    if (!wait(&c.p_full[w][1], np++ & 1, &c.abort, p.err, 62)) return false;
-                    ptx::tc_fence_after();
-                    const int u = vals.u + 1 == L::U ? 0 : vals.u + 1;
-                    pv_warp(to, ts + 32, dv + (uint64_t)((u * L::UNIT) >> 4), IPV, 1, qk ? 4 : max(0, steps - 4));
-                    free_group(&c.free[vals.g], j);
-                    if (!qk) ptx::mma_commit_warp(&c.o_full[w]);
-                }
-                if (qk) {
-                    if (!pv) ptx::tc_fence_after();
-                    const uint64_t a = dq + (uint64_t)((qt * L::Q_TILE) >> 4);
-                    int u = keys.u;
+                ptx::tc_fence_after();
+                const uint64_t a = dq + (uint64_t)(((pair ? w : 0) * L::Q_TILE) >> 4);
+                int u = keys.u;
 #pragma unroll
-                    for (int i = 0; i < L::QB; ++i) {
-                        ptx::mma4_bf16_ss_warp(ts, a + (uint64_t)((i * BM * 128) >> 4), dk + (uint64_t)((u * L::UNIT) >> 4), IQK, i == 0);
-                        u = u + L::BU == L::U ? 0 : u + L::BU;
-                    }
-                    ptx::mma_commit_warp(&c.s_full[w]);
-                    free_group(&c.free[keys.g], j + 1);
-                    if (lane == 0) ptx::mbar_arrive(&c.turn[1 - w]);
+                for (int i = 0; i < L::QB; ++i) {
+                    ptx::mma4_bf16_ss_warp(tmem + w * BN, a + (uint64_t)((i * BM * 128) >> 4), dk + (uint64_t)((u * L::UNIT) >> 4), IQK, i == 0);
+                    u = u + L::BU == L::U ? 0 : u + L::BU;
                 }
+                ptx::mma_commit_warp(&c.s_full[w]);
+                if (w == 1 || !pair) ptx::mma_commit_warp(&c.free[keys.g]);
+                // the last product with a query tile
+                if (pair ? j + 1 == (w ? n1 : n0) : w == (n1 == n0) && j + 1 == n0) ptx::mma_commit_warp(&c.q_free[pair ? w : 0]);
                 return true;
             };
-            // A turn of a round in which this warp has no keys.
-            auto pass = [&]() {
-                if (!(w == 0 && nt == 0) && !wait(&c.turn[w], (nt - (w == 0)) & 1, &c.abort, p.err, 65)) return false;
-                ++nt;
-                if (lane == 0) ptx::mbar_arrive(&c.turn[1 - w]);
+            // The product of step j's P and values.  `whole`: not the warpgroup's last step, all keys count.
+            auto pv = [&](int w, int j, auto is_whole) {
+                constexpr bool whole = decltype(is_whole)::value;
+                if (w == 0 || !pair || j >= n0) {
+                    if (!spin(&c.full[r.g], r.phase, &c.abort, p.err, 63)) return false;
+                    vals = r;
+                    r.step(2);
+                }
+                int steps = BN / 16;
+                if (!whole) {
+                    const int kt = x.key_tile(w, j), tail = x.nk - kt * BN;
+                    steps = x.steps(p, w, kt);
+                    if (tail < BN && (tail & 15)) {
+                        // Rows behind the stream's last key, up to the 16 of a product's step: whatever they hold, 0
+                        // times it has to be 0.  (16-byte chunks, whatever their order in a row.)
+                        int u = vals.u + (tail >= VH);
+                        if (u >= L::U) u -= L::U;
+                        const int chunks = (16 - (tail & 15)) * 8;
+                        uint8_t *dst = smem + L::OFF_R + u * L::UNIT + (tail & (VH - 1)) * 128;
+                        for (int i = lane; i < chunks * L::VB; i += 32)
+                            *reinterpret_cast<uint4 *>(dst + i / chunks * (VH * 128) + i % chunks * 16) = make_uint4(0, 0, 0, 0);
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                }
+                const uint32_t np = w ? np1 : np0, no = w ? no1 : no0;
+                if (!spin(&c.p_full[w][0], np & 1, &c.abort, p.err, 62)) return false;
+                // the sums of the item before are read out
+                if (j == 0 && no > 0 && !wait(&c.o_free[w], (no - 1) & 1, &c.abort, p.err, 66)) return false;
+                ptx::tc_fence_after();
+                const uint32_t ts = tmem + w * BN, to = tmem + 2 * BN + w * DV;
+                pv_warp(to, ts, dv + (uint64_t)((vals.u * L::UNIT) >> 4), IPV, j > 0, whole ? 4 : min(4, steps));
+                if (!spin(&c.p_full[w][1], np & 1, &c.abort, p.err, 62)) return false;
+                ptx::tc_fence_after();
+                const int u = vals.u + 1 == L::U ? 0 : vals.u + 1;
+                pv_warp(to, ts + 32, dv + (uint64_t)((u * L::UNIT) >> 4), IPV, 1, whole ? 4 : max(0, steps - 4));
+                if (w == 1 || !pair) ptx::mma_commit_warp(&c.free[vals.g]);
+                if (!whole) ptx::mma_commit_warp(&c.o_full[w]);
+                if (w) ++np1; else ++np0;
                 return true;
             };
             constexpr std::true_type yes{};
             constexpr std::false_type none{};
-            // The groups that only the other warp takes lie before the own ones of a round (1) or behind them (0); with two
-            // query tiles they are those that this one has no step for.
-            auto others = [&](int j) {
-                if (j >= 0 && j < o && (!pair || j >= n)) r.step(2);
-                if (j + 1 < o && (!pair || j + 1 >= n)) r.step(L::KU);
-            };
-            if (w == 1) others(-1);
-            ok = n > 0 ? round(-1, none, yes) : pass();
-            if (w == 0) others(-1);
+            ok = wait(&c.q_full[0], nq0++ & 1, &c.abort, p.err, 60);
+            if (ok && n0 > 0) ok = qk(0, 0);
+            if (pair && n0 == 0) ptx::mma_commit_warp(&c.q_free[0]);
+            if (ok && pair) ok = wait(&c.q_full[1], nq1++ & 1, &c.abort, p.err, 60);
+            if (ok && n1 > 0) ok = qk(1, 0);
+            // steps that neither warpgroup ends with
+            int j = 0;
 #pragma unroll 1
-            for (int j = 0; ok && j + 1 < n; ++j) {
-                if (!pair && w == 1) others(j);
-                ok = round(j, yes, yes);
-                if (!pair && w == 0) others(j);
-            }
-            free_q();
+            for (; ok && j + 1 < min(n0, n1); ++j)
 #pragma unroll 1
-            for (int j = max(0, n - 1); ok && j < rounds; ++j) {
-                if (w == 1) others(j);
-                if (j < n) ok = round(j, yes, none);
-                if (ok && j + 1 < rounds) ok = pass();
-                if (w == 0) others(j);
-            }
+                for (int w = 0; ok && w < 2; ++w) ok = pv(w, j, yes) && qk(w, j + 1);
+#pragma unroll 1
+            for (; ok && j < max(n0, n1); ++j)
+#pragma unroll 1
+                for (int w = 0; ok && w < 2; ++w) {
+                    const int n = w ? n1 : n0;
+                    if (j + 1 < n) ok = pv(w, j, yes) && qk(w, j + 1);
+                    else if (j < n) ok = pv(w, j, none);
+                }
             if (!ok) break;
-            no += n > 0;
+            no0 += n0 > 0;
+            no1 += n1 > 0;
         }
         // no product may still run when TMEM is freed
         ptx::mma_commit_warp(&c.drain);
-        if (warp == MMA_WARP) wait(&c.drain, 0, &c.abort, p.err, 64, 1ll << 29);
-        __syncwarp();
+        wait(&c.drain, 0, &c.abort, p.err, 64, 1ll << 29);
     } else if (warp < OUT_WARP) {
         // ================= softmax: a query row a thread =================
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
@@ -655,17 +609,26 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                     continue;
                 }
                 ptx::tc_fence_after();
+                if (__any_sync(0xffffffffu, limit < BN)) {
+                    // Hidden columns become -inf where they lie, 16 at a time: a small loop, as it runs once or twice an item
+                    // and has to be fetched each time (128 selects in a row on the loaded scores: 2,000 cycles).
+#pragma unroll 1
+                    for (int k = 0; k < BN; k += 16) {
+                        if (__all_sync(0xffffffffu, limit >= k + 16)) continue;
+                        uint32_t v[16];
+                        tmem_ld16(ts + k, v);
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (k + i >= limit) v[i] = 0xFF800000u;
+                        tmem_st16(ts + k, v);
+                    }
+                    ptx::tmem_st_wait();
+                }
                 uint32_t s[4][32];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) ptx::tmem_ld32(ts + 32 * q, s[q]);
                 ptx::tmem_ld_wait();
-                if (__any_sync(0xffffffffu, limit < BN)) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (q * 32 + i >= limit) s[q][i] = 0xFF800000u;
-                }
                 float mx[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -829,6 +792,35 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
             }
             if (!ok) break;
         }
+    } else if (warp == ITEM_WARP) {
+        // ================= the next item =================
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+        int asked = 0;
+        int i = (int)blockIdx.x;
+        for (uint32_t count = 0;; ++count) {
+            Item x;
+            x.decode(p, i);
+            if (count >= 2 && !wait(&c.item_free[count & 1], (count / 2 - 1) & 1, &c.abort, p.err, 51)) break;
+            if (lane == 0) {
+                c.item[count & 1] = x;
+                ptx::mbar_arrive(&c.item_full[count & 1]);
+            }
+            if (i < 0) break;
+            i = -1;
+            if (!p.more) continue;
+            if (!wait(&c.ask, count & 1, &c.abort, p.err, 56)) break;
+            if (lane == 0) {
+                ptx::fence_proxy_async_smem();   // the answer before has been read
+                ptx::mbar_arrive_expect_tx(&c.answer, 16);
+                ask_next(&c.next, &c.answer);
+            }
+            ++asked;
+            __syncwarp();
+            if (!wait(&c.answer, count & 1, &c.abort, p.err, 57)) break;
+            i = __shfl_sync(0xffffffffu, read_next(&c.next), 0);
+        }
+        // no answer may still be on its way into this CTA's shared memory when it ends
+        if (asked > 0) wait(&c.answer, (uint32_t)(asked - 1) & 1, &c.abort, p.err, 55, 1ll << 28);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
     }
