@@ -478,37 +478,66 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
         uint32_t nq0 = 0, nq1 = 0;   // uses of the query tiles
         bool ok = true;
         Walk it;
-        Item x;
-        while (it.next(c, p, x, lane)) {
+        Item x, y;
+        Ring<L::U> keys, vals;
+        bool early = false, known = false;   // the next item (y) is known, its first scores are made
+        // Scores of warpgroup w from the keys at `k`; `last`: the query tile's last product.
+        auto scores = [&](int w, const Ring<L::U> &k, bool pair, bool last) {
+            ptx::tc_fence_after();
+            const uint64_t a = dq + (uint64_t)(((pair ? w : 0) * L::Q_TILE) >> 4);
+            int u = k.u;
+#pragma unroll
+            for (int i = 0; i < L::QB; ++i) {
+                ptx::mma4_bf16_ss_warp(tmem + w * BN, a + (uint64_t)((i * BM * 128) >> 4), dk + (uint64_t)((u * L::UNIT) >> 4), IQK, i == 0);
+                u = u + L::BU == L::U ? 0 : u + L::BU;
+            }
+            ptx::mma_commit_warp(&c.s_full[w]);
+            if (w == 1 || !pair) ptx::mma_commit_warp(&c.free[k.g]);
+            if (last) ptx::mma_commit_warp(&c.q_free[pair ? w : 0]);
+        };
+        for (;;) {
+            if (!known && !it.next(c, p, y, lane)) break;
+            x = y;
+            known = false;
             const int n0 = x.n0, n1 = x.n1;
+            if (n0 < 0) break;
             if (n0 + n1 == 0) continue;
             const bool pair = x.pair;
-            Ring<L::U> keys, vals;
-            // Scores of warpgroup w's step j.  With two query tiles both warpgroups use a tile's keys, and the first to come
-            // takes them from the ring; so with the values.
+            // With two query tiles both warpgroups use a tile's keys, and the first to come takes them from the ring; so with
+            // the values.
             auto qk = [&](int w, int j) {
                 if (w == 0 || !pair || j >= n0) {
                     if (!spin(&c.full[r.g], r.phase, &c.abort, p.err, 61)) return false;
                     keys = r;
                     r.step(L::KU);
                 }
-                ptx::tc_fence_after();
-                const uint64_t a = dq + (uint64_t)(((pair ? w : 0) * L::Q_TILE) >> 4);
-                int u = keys.u;
-#pragma unroll
-                for (int i = 0; i < L::QB; ++i) {
-                    ptx::mma4_bf16_ss_warp(tmem + w * BN, a + (uint64_t)((i * BM * 128) >> 4), dk + (uint64_t)((u * L::UNIT) >> 4), IQK, i == 0);
-                    u = u + L::BU == L::U ? 0 : u + L::BU;
-                }
-                ptx::mma_commit_warp(&c.s_full[w]);
-                if (w == 1 || !pair) ptx::mma_commit_warp(&c.free[keys.g]);
-                // the last product with a query tile
-                if (pair ? j + 1 == (w ? n1 : n0) : w == (n1 == n0) && j + 1 == n0) ptx::mma_commit_warp(&c.q_free[pair ? w : 0]);
+                scores(w, keys, pair, pair ? j + 1 == (w ? n1 : n0) : w == (n1 == n0) && j + 1 == n0);
                 return true;
             };
+            // Once warpgroup 0 has had its last product, while warpgroup 1 still works: the first scores of the next item,
+            // if all that they need is there.  Without them the tensor cores wait through the last softmax.
+            auto start_next = [&](int left_j) {
+                if (early) return;
+                if (!known) {
+                    if (!look(&c.item_full[it.count & 1], (it.count >> 1) & 1)) return;
+                    it.next(c, p, y, lane);
+                    known = true;
+                }
+                if (y.n0 <= 0 || !look(&c.q_full[0], nq0 & 1)) return;
+                Ring<L::U> at = r;     // behind what this item still takes
+                if (pair) {
+                    for (int j = left_j + 1; j < n1; ++j) {
+                        at.step(L::KU);
+                        at.step(2);
+                    }
+                }
+                if (!look(&c.full[at.g], at.phase)) return;
+                scores(0, at, y.pair, y.pair ? y.n0 == 1 : y.n0 == 1 && y.n1 == 0);
+                early = true;
+            };
             // The product of step j's P and values.  `whole`: not the warpgroup's last step, all keys count.
-            auto pv = [&](int w, int j, auto is_whole) {
-                constexpr bool whole = decltype(is_whole)::value;
+            auto pv = [&](int w, int j, auto is_whole, auto is_alone) {
+                constexpr bool whole = decltype(is_whole)::value, alone = decltype(is_alone)::value;
                 if (w == 0 || !pair || j >= n0) {
                     if (!spin(&c.full[r.g], r.phase, &c.abort, p.err, 63)) return false;
                     vals = r;
@@ -532,7 +561,15 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                     }
                 }
                 const uint32_t np = w ? np1 : np0, no = w ? no1 : no0;
-                if (!spin(&c.p_full[w][0], np & 1, &c.abort, p.err, 62)) return false;
+                if (alone) {   // warpgroup 0 has ended
+                    const long long t0 = clock64();
+                    for (uint32_t spins = 1; !look(&c.p_full[w][0], np & 1); ++spins) {
+                        start_next(j);
+                        if ((spins & 1023u) == 0 && expired(t0, 1ll << 31, &c.abort, p.err, 62)) return false;
+                    }
+                } else if (!spin(&c.p_full[w][0], np & 1, &c.abort, p.err, 62)) {
+                    return false;
+                }
                 // the sums of the item before are read out
                 if (j == 0 && no > 0 && !wait(&c.o_free[w], (no - 1) & 1, &c.abort, p.err, 66)) return false;
                 ptx::tc_fence_after();
@@ -549,9 +586,16 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
             };
             constexpr std::true_type yes{};
             constexpr std::false_type none{};
-            ok = wait(&c.q_full[0], nq0++ & 1, &c.abort, p.err, 60);
-            if (ok && n0 > 0) ok = qk(0, 0);
-            if (pair && n0 == 0) ptx::mma_commit_warp(&c.q_free[0]);
+            if (early) {
+                keys = r;
+                r.step(L::KU);
+                early = false;
+            } else {
+                ok = wait(&c.q_full[0], nq0 & 1, &c.abort, p.err, 60);
+                if (ok && n0 > 0) ok = qk(0, 0);
+                if (pair && n0 == 0) ptx::mma_commit_warp(&c.q_free[0]);
+            }
+            ++nq0;
             if (ok && pair) ok = wait(&c.q_full[1], nq1++ & 1, &c.abort, p.err, 60);
             if (ok && n1 > 0) ok = qk(1, 0);
             // steps that neither warpgroup ends with
@@ -559,15 +603,16 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
 #pragma unroll 1
             for (; ok && j + 1 < min(n0, n1); ++j)
 #pragma unroll 1
-                for (int w = 0; ok && w < 2; ++w) ok = pv(w, j, yes) && qk(w, j + 1);
+                for (int w = 0; ok && w < 2; ++w) ok = pv(w, j, yes, none) && qk(w, j + 1);
+            // the rest: warpgroup 0's last steps, then warpgroup 1's
 #pragma unroll 1
-            for (; ok && j < max(n0, n1); ++j)
+            for (; ok && j < n0; ++j) {
+                ok = j + 1 < n0 ? pv(0, j, yes, none) && qk(0, j + 1) : pv(0, j, none, none);
+                if (ok && j + 1 < n0 && j < n1) ok = pv(1, j, none, none);
+                if (j + 1 == n0) break;
+            }
 #pragma unroll 1
-                for (int w = 0; ok && w < 2; ++w) {
-                    const int n = w ? n1 : n0;
-                    if (j + 1 < n) ok = pv(w, j, yes) && qk(w, j + 1);
-                    else if (j < n) ok = pv(w, j, none);
-                }
+            for (; ok && j < n1; ++j) ok = j + 1 < n1 ? pv(1, j, yes, yes) && qk(1, j + 1) : pv(1, j, none, yes);
             if (!ok) break;
             no0 += n0 > 0;
             no1 += n1 > 0;
@@ -950,7 +995,6 @@ static int plan(Params &p, const int64_t *h_nq, const int64_t *h_nk, int S, int 
     out->items = 0;
     out->slots = 0;
     out->splits = 1;
-    // heads side by side: as many as keep their keys and values within a quarter of L2
     for (int i = 0; i < n; ++i) {
         const int64_t sp = std::max<int64_t>(1, (e[i].tiles + chunk - 1) / chunk);
         if (sp > INT16_MAX) return TF_E_UNSUPPORTED;
@@ -962,7 +1006,9 @@ static int plan(Params &p, const int64_t *h_nq, const int64_t *h_nk, int S, int 
         p.nk[i] = e[i].nk;
         p.nsp[i] = (int16_t)sp;
         p.chunk[i] = (int32_t)(sp > 1 ? chunk : std::max<int64_t>(1, e[i].tiles));
-        p.hg[i] = (int16_t)std::max<int64_t>(1, std::min<int64_t>(Hkv, (32 << 20) / bytes));
+// All heads side by side where their keys and values fit L2 together: the longest blocks of all come first then,
+        // and the last items are short.  Else as many as take a quarter of it.
+        p.hg[i] = (int16_t)(bytes * Hkv <= (96 << 20) ? Hkv : std::max<int64_t>(1, (32 << 20) / bytes));
         p.slot0[i] = sp > 1 ? (int32_t)out->slots : -1;
         const int64_t cnt = e[i].blocks * Hkv * sp;
         if (sp > 1) out->slots += cnt * 2;
