@@ -620,25 +620,20 @@ def _sum(a) -> int:
     return sum(a) if type(a) is array.array else int(a.sum())
 
 
-def _rows_form(t, n: int, width: int, bf16) -> bool:
-    """bf16 [n][width], each row's values side by side."""
-    return t.dtype is bf16 and t.dim() == 2 and t.shape[0] == n and t.shape[1] == width and t.stride(1) == 1
+def _row_stride(t, n: int, width: int, bf16, what: str) -> int:
+    """The row stride of bf16 [n][width] with each row's values side by side (of a single row any that is allowed)."""
+    row, one = t.stride()
+    if not (t.dtype is bf16 and t.shape == (n, width) and one == 1):
+        _refuse(what)
+    return row if n > 1 else width
 
 
-def _heads_form(t, n: int, heads: int, width: int, bf16) -> bool:
-    """bf16 [n][heads][width], each head's values side by side."""
-    return t.dtype is bf16 and t.dim() == 3 and tuple(t.shape) == (n, heads, width) and t.stride(2) == 1
-
-
-def _row_stride(t) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _strides(t):
-    """(row, head) of [rows][heads][width]; of a single row or head any that is allowed."""
-    row, head, _ = t.stride()
-    n, heads, width = t.shape
-    return row if n > 1 else heads * width, head if heads > 1 else width
+def _strides(t, shape, bf16, what: str):
+    """(row, head) strides of bf16 [rows][heads][width] with each head's values side by side."""
+    row, head, one = t.stride()
+    if not (t.dtype is bf16 and t.shape == shape and one == 1):
+        _refuse(what)
+    return row if shape[0] > 1 else shape[1] * shape[2], head if shape[1] > 1 else shape[2]
 
 
 def tf_rope_apply(rope: tf_rope, pos, n, x, y=None, stream=None) -> None:
@@ -648,14 +643,14 @@ def tf_rope_apply(rope: tf_rope, pos, n, x, y=None, stream=None) -> None:
     a, p = _i64(pos)
     b, pn = _i64(n)
     bf16 = _dtypes()[0]
-    rows, H = int(x.shape[0]), int(x.shape[1])
-    if not (len(a) == len(b) and _sum(b) == rows and _heads_form(x, rows, H, rope.dim, bf16) and
-            _heads_form(y, rows, H, rope.dim, bf16)):
+    rows, H, dim = shape = x.shape
+    if not (len(a) == len(b) and _sum(b) == rows and dim == rope.dim):
         _refuse("tf_rope_apply")
-    if not (x.is_cuda and y.get_device() == x.get_device()):
+    xr, xh = _strides(x, shape, bf16, "tf_rope_apply")
+    yr, yh = (xr, xh) if y is x else _strides(y, shape, bf16, "tf_rope_apply")
+    dev = x.get_device()
+    if dev < 0 or y.get_device() != dev:
         raise TFError(TF_E_ARG, "tf_rope_apply (tensors that are not on one GPU)")
-    xr, xh = _strides(x)
-    yr, yh = _strides(y)
     _check(lib().tf_rope_apply(ctypes.addressof(rope), p, pn, len(b), H, x.data_ptr(), xr, xh, y.data_ptr(), yr, yh,
                                _stream(stream)), "tf_rope_apply")
 
@@ -667,14 +662,14 @@ def tf_paged_append_rope(pool: KVPool, cache: int, pt, max_pages: int, pos, n, r
     a, p = _i64(pos)
     b, pn = _i64(n)
     bf16, _, i32 = _dtypes()
-    if not (len(a) == len(b) and _rows_form(rows, _sum(b), 576, bf16) and (gain is None or _dense(gain, bf16, 512)) and
-            _table(pt, max_pages, len(b), i32)):
+    row = _row_stride(rows, _sum(b), 576, bf16, "tf_paged_append_rope")
+    if not (len(a) == len(b) and (gain is None or _dense(gain, bf16, 512)) and _table(pt, max_pages, len(b), i32)):
         _refuse("tf_paged_append_rope")
     dev = pool.device
     if not (rows.get_device() == dev and _on(dev, gain) and _on(dev, pt)):
         _elsewhere("tf_paged_append_rope")
     _check(lib().tf_paged_append_rope(pool.handle, cache, _ptr(pt), max_pages, p, pn, len(b), rows.data_ptr(),
-                                      _row_stride(rows), _ptr(gain), eps, None if rope is None else ctypes.addressof(rope),
+                                      row, _ptr(gain), eps, None if rope is None else ctypes.addressof(rope),
                                       _stream(stream)), "tf_paged_append_rope")
 
 
@@ -685,15 +680,15 @@ def tf_paged_read(pool: KVPool, cache: int, pt, max_pages: int, start, n, latent
     b, pn = _i64(n)
     bf16, _, i32 = _dtypes()
     rows = _sum(b)
-    if not (len(a) == len(b) and (latent is None or _rows_form(latent, rows, 512, bf16)) and
-            (rope is None or _rows_form(rope, rows, 64, bf16)) and _table(pt, max_pages, len(b), i32)):
+    lat_row = 0 if latent is None else _row_stride(latent, rows, 512, bf16, "tf_paged_read")
+    rope_row = 0 if rope is None else _row_stride(rope, rows, 64, bf16, "tf_paged_read")
+    if not (len(a) == len(b) and _table(pt, max_pages, len(b), i32)):
         _refuse("tf_paged_read")
     dev = pool.device
     if not (_on(dev, latent) and _on(dev, rope) and _on(dev, pt)):
         _elsewhere("tf_paged_read")
     _check(lib().tf_paged_read(pool.handle, cache, _ptr(pt), max_pages, p, pn, len(b), _ptr(latent),
-                               0 if latent is None else _row_stride(latent), _ptr(rope), 0 if rope is None else _row_stride(rope),
-                               _stream(stream)), "tf_paged_read")
+                               lat_row, _ptr(rope), rope_row, _stream(stream)), "tf_paged_read")
 
 
 def tf_prompt_workspace_bytes(nq, nk, H: int, Hkv: int, dqk: int, dv: int, causal: bool = True) -> int:
@@ -702,11 +697,6 @@ def tf_prompt_workspace_bytes(nq, nk, H: int, Hkv: int, dqk: int, dv: int, causa
     if len(a) != len(b):
         _refuse("tf_prompt_workspace_bytes")
     return int(lib().tf_prompt_workspace_bytes(p, pk, len(a), H, Hkv, dqk, dv, 1 if causal else 0))
-
-
-def _heads(t) -> tf_heads:
-    row, head = _strides(t)
-    return tf_heads(t.data_ptr(), row, head)
 
 
 def tf_prompt_attend(pool: KVPool, nq, nk, q, k, v, scale: float, out, lse=None, kr=None, causal: bool = True, ws=None,
@@ -719,20 +709,24 @@ def tf_prompt_attend(pool: KVPool, nq, nk, q, k, v, scale: float, out, lse=None,
     bf16, f32, _ = _dtypes()
     rows, H, dqk = q.shape
     keys, Hkv, dv = v.shape
-    if not (len(a) == len(b) and _sum(a) == rows and _sum(b) == keys and _heads_form(q, rows, H, dqk, bf16) and
-            _heads_form(k, keys, Hkv, dqk - (0 if kr is None else 64), bf16) and _heads_form(v, keys, Hkv, dv, bf16) and
-            _heads_form(out, rows, H, dv, bf16) and (kr is None or _rows_form(kr, keys, 64, bf16)) and
-            (lse is None or _dense(lse, f32, rows * H))):
-        _refuse("tf_prompt_attend")
+    what = "tf_prompt_attend"
+    if not (len(a) == len(b) and _sum(a) == rows and _sum(b) == keys and (lse is None or _dense(lse, f32, rows * H))):
+        _refuse(what)
+    qr, qh = _strides(q, (rows, H, dqk), bf16, what)
+    kr_, kh = _strides(k, (keys, Hkv, dqk if kr is None else dqk - 64), bf16, what)
+    vr, vh = _strides(v, (keys, Hkv, dv), bf16, what)
+    outr, outh = _strides(out, (rows, H, dv), bf16, what)
+    rope_row = 0 if kr is None else _row_stride(kr, keys, 64, bf16, what)
     dev = pool.device
     if not (q.get_device() == dev and k.get_device() == dev and v.get_device() == dev and out.get_device() == dev and
             _on(dev, kr) and _on(dev, lse) and _on(dev, ws)):
-        _elsewhere("tf_prompt_attend")
-    hq, hk, hv, ho = _heads(q), _heads(k), _heads(v), _heads(out)
-    _check(lib().tf_prompt_attend(pool.handle, p, pk, len(a), H, Hkv, dqk, dv, ctypes.addressof(hq), ctypes.addressof(hk),
-                                  _ptr(kr), 0 if kr is None else _row_stride(kr), ctypes.addressof(hv), scale,
-                                  1 if causal else 0, ctypes.addressof(ho), _ptr(lse), _ptr(ws),
-                                  0 if ws is None else ws.nbytes, _stream(stream)), "tf_prompt_attend")
+        _elsewhere(what)
+    # four tf_heads one after another (24 bytes each)
+    heads = array.array("q", (q.data_ptr(), qr, qh, k.data_ptr(), kr_, kh, v.data_ptr(), vr, vh, out.data_ptr(), outr, outh))
+    h = heads.buffer_info()[0]
+    _check(lib().tf_prompt_attend(pool.handle, p, pk, len(a), H, Hkv, dqk, dv, h, h + 24, _ptr(kr), rope_row, h + 48, scale,
+                                  1 if causal else 0, h + 72, _ptr(lse), _ptr(ws), 0 if ws is None else ws.nbytes,
+                                  _stream(stream)), what)
 
 
 def tf_prompt_plan_info(nq, nk, H: int, Hkv: int, dqk: int, dv: int, causal: bool = True, sms: int = 0) -> dict:

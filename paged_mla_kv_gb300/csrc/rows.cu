@@ -171,23 +171,21 @@ __global__ void __launch_bounds__(256) append_rope_kernel(const __grid_constant_
     if (row >= p.rows.n) return;
     const int s = stream_of(p.rows, row);
     const int pos = p.rows.base[s] + row;
-    const float2 cs = p.rotate ? turn_of(p.turn[lane], pos, p.amplitude) : make_float2(1.f, 0.f);
-    ptx::griddep_wait();
-    const int page = page_of(p.pt, p.max_pages, p.num_pages, s, pos, p.err, lane == 0);
-    if (page < 0) return;
-    const int r = pos & (kPageRows - 1);
     const uint16_t *src = p.x + row * p.x_row;
     const int ca = FP8 ? 2 * lane : lane, cb = FP8 ? 2 * lane + 1 : lane + 32;   // 16-byte chunks
+    ptx::griddep_wait();
+    // the row is on its way while the page is looked up and the angle made
     const uint4 a = __ldg(reinterpret_cast<const uint4 *>(src) + ca), b = __ldg(reinterpret_cast<const uint4 *>(src) + cb);
-    float k0, k1;   // the rope pair
-    if (HALF) {
-        k0 = lo(__ldg(src + kLat + lane));
-        k1 = lo(__ldg(src + kLat + kRope / 2 + lane));
-    } else {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(src + kLat) + lane);
-        k0 = lo(w);
-        k1 = hi(w);
-    }
+    uint32_t kw;   // the rope pair
+    if (HALF)
+        kw = __ldg(src + kLat + lane) | (uint32_t)__ldg(src + kLat + kRope / 2 + lane) << 16;
+    else
+        kw = __ldg(reinterpret_cast<const uint32_t *>(src + kLat) + lane);
+    const int page = page_of(p.pt, p.max_pages, p.num_pages, s, pos, p.err, lane == 0);
+    const float2 cs = p.rotate ? turn_of(p.turn[lane], pos, p.amplitude) : make_float2(1.f, 0.f);
+    if (page < 0) return;
+    const int r = pos & (kPageRows - 1);
+    float k0 = lo(kw), k1 = hi(kw);
     uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     float x[16];
 #pragma unroll
