@@ -141,8 +141,8 @@ int tf_paged_read(tf_kvpool *pool, int32_t cache, const int32_t *d_pt, int32_t m
  * keys are split.  Not to be shared by calls that may run at the same time.
  * pool: its device error word takes what a kernel records (a wait that ran out); its pages are not read.
  * Errors: TF_E_ARG for a null pointer (k, v and kr may be NULL without keys; q and out without rows), S outside [1, TF_MAX_STREAMS],
- * H outside [1, TF_MAX_HEADS], Hkv that does not divide H, negative counts, a scale that is not a finite number > 0,
- * a causal other than 0 or 1, a pointer that is not 16-byte aligned or a stride that is not a multiple of 8 values, below 1 or
+ * H outside [1, TF_MAX_HEADS], Hkv that does not divide H, negative counts, a scale that is not a number > 0
+ * (below 2^127), a causal other than 0 or 1, a pointer that is not 16-byte aligned or a stride that is not a multiple of 8 values, below 1 or
  * above 2^36 (out's strides may be any multiple of 8; so may the head stride of a single head), an unaligned or missing workspace; TF_E_NOMEM for
  * one that is too small; TF_E_UNSUPPORTED for other dqk and dv, with d_kr a dqk of 64, or more than 2^31 - 1 rows, keys or tiles of work. */
 typedef struct {

@@ -39,8 +39,8 @@ extern "C" int tf_rope_make(const tf_rope_desc *d, tf_rope *out) {
             const double r = std::fmin(1.0, std::fmax(0.0, (i - lo) / std::fmax(hi - lo, 0.001)));
             f = f * (1.0 - r) + f / factor * r;
         }
-        // f <= 1 radian, so less than a sixth of 2^64 (exactly: a double times a power of two)
-        out->turn[i] = (uint64_t)std::llround(std::ldexp(f / (2.0 * pi), 63)) * 2u;
+        // f <= 1 radian, a sixth of a turn: below 2^62
+        out->turn[i] = (uint64_t)std::llround(std::ldexp(f / (2.0 * pi), 64));
     }
     for (int i = d->dim / 2; i < TF_ROPE_MAX_DIM / 2; ++i) out->turn[i] = 0;
     out->dim = d->dim;
@@ -167,7 +167,7 @@ extern "C" int tf_prompt_attend(tf_kvpool *p, const int64_t *h_nq, const int64_t
                                 int32_t dqk, int32_t dv, const tf_heads *q, const tf_heads *k, const void *d_kr,
                                 int64_t kr_row, const tf_heads *v, float scale, int32_t causal, const tf_heads *out,
                                 float *d_lse, void *d_ws, size_t ws_bytes, void *stream) {
-    if (!p || !q || !k || !v || !out || !(scale > 0.0f) || !std::isfinite(scale)) return TF_E_ARG;
+    if (!p || !q || !k || !v || !out || !(scale > 0.0f) || !std::isfinite(2.0f * scale)) return TF_E_ARG;
     int64_t rows = 0, keys = 0;
     const int rc = prompt_checks(h_nq, h_nk, S, H, Hkv, dqk, dv, causal, &rows, &keys);
     if (rc != TF_OK) return rc;

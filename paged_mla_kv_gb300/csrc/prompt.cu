@@ -971,7 +971,7 @@ static int plan(Params &p, const int64_t *h_nq, const int64_t *h_nk, int S, int 
     // launch that joins them as JOIN.
     constexpr int64_t START = 2, PART = 2, JOIN = 3;
     int64_t chunk = most;
-    double best = 1e300;
+    double best = 1e300, whole = 0;
     for (int64_t c = most; c >= 1; c = c > 16 ? c - c / 8 : c - 1) {
         int64_t cnt = 0, load = 0, longest = 0, tail = 0;
         bool split = false;
@@ -990,7 +990,9 @@ static int plan(Params &p, const int64_t *h_nq, const int64_t *h_nk, int S, int 
             best = t;
             chunk = c;
         }
-        if (cnt > 32 * (int64_t)sms) break;
+        // shorter splits only add work: near the unsplit load there is nothing to gain
+        if (c == most) whole = (double)load / sms;
+        if (best <= 1.03 * whole || cnt > 32 * (int64_t)sms) break;
     }
     out->items = 0;
     out->slots = 0;
@@ -1069,28 +1071,26 @@ int launch_prompt_attend(tf_kvpool *pool, const int64_t *h_nq, const int64_t *h_
     using namespace prm;
     Params &p = prompt_params();
     Plan pl;
-    const int sms = prompt_sms();
-    const int rc = plan(p, h_nq, h_nk, S, H, Hkv, dqk, dv, causal, sms, &pl);
+    using Kern = void (*)(const Params);
+    const Kern kern = dqk == 192 ? prompt_kernel<192, 128> : dqk == 128 ? prompt_kernel<128, 128> : prompt_kernel<64, 64>;
+    static PerDevice<int> ready;   // SMs, once the kernels are opted in to their shared memory
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) cudaGetLastError(), dev = -1;
+    const int *sms = ready.get(dev, [&](int &n) {
+        n = prompt_sms();
+        bool ok = true;
+        for (const Kern f : {prompt_kernel<192, 128>, prompt_kernel<128, 128>, prompt_kernel<64, 64>})
+            ok = ok && cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) == cudaSuccess;
+        if (!ok) cudaGetLastError();
+        return ok;
+    });
+    const int rc = plan(p, h_nq, h_nk, S, H, Hkv, dqk, dv, causal, sms ? *sms : prompt_sms(), &pl);
     if (rc != TF_OK) return rc;
     const size_t need = ws_bytes_of(pl, dv);
     if (need > 0 && (!d_ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0))
         return d_ws && ws_bytes < need ? TF_E_NOMEM : TF_E_ARG;
     if (pl.items == 0) return TF_OK;
-
-    using Kern = void (*)(const Params);
-    const Kern kern = dqk == 192 ? prompt_kernel<192, 128> : dqk == 128 ? prompt_kernel<128, 128> : prompt_kernel<64, 64>;
-    static PerDevice<int> ready;   // opted in to the shared memory
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return TF_E_CUDA;
-    if (!ready.get(dev, [&](int &one) {
-            one = 1;
-            bool ok = true;
-            for (const Kern f : {prompt_kernel<192, 128>, prompt_kernel<128, 128>, prompt_kernel<64, 64>})
-                ok = ok && cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) == cudaSuccess;
-            if (!ok) cudaGetLastError();
-            return ok;
-        }))
-        return TF_E_CUDA;
+    if (!sms) return TF_E_CUDA;
 
     int64_t rows = 0, keys = 0;
     for (int s = 0; s < S; ++s) rows += h_nq[s], keys += h_nk[s];

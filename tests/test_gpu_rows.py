@@ -1,10 +1,11 @@
 """GPU parity of rotary positions, the append of a projection's rows and the rows back from the pages, against the
 fp64 definitions, through the C-ABI.
 
-Tolerances.  u = 2^-8 is half a bf16 step (relative), f = 2^-24 half an fp32 step.  An angle is a signed 32-bit
-fraction of a turn, cut to fp32: off by at most (2^-32 + 2^-25 + 2^-22) turns, the last for the double's rounding of the
-frequency at positions below 2^31; sines and cosines of it are good to 2^-22, so a turned pair is off by at most
-A (|a| + |b|) (2 pi 2^-21.6 + 2^-22 + 4 f) < 2^-18.5 A (|a| + |b|), and by its rounding u |ref|.
+Tolerances.  u = 2^-8 is half a bf16 step (relative), f = 2^-24 half an fp32 step.  An angle is off by 0.16 2^-21 turns
+at most for the frequency (three double roundings, times a position below 2^31 and at most 0.16 turns a position), by
+2^-25 + 2^-32 turns as a fraction cut to fp32, and by two roundings of at most pi on its way into the sine: 1.03e-6
+radians.  The hardware's sine and cosine add 2^-21.19 = 4.2e-7, the products and sums 4 f = 2.4e-7: a turned pair is off by less
+than 1.7e-6 < 2^-18.5 = 2.7e-6 times A (|a| + |b|), and by its rounding u |ref|.
 A norm's factor is off by (512 + 8) f relative (a sum of squares in any order), so a latent value by 2^-14 + u.
 """
 import numpy as np
