@@ -347,7 +347,8 @@ int64_t tf_launch_count(void);
 /* With on != 0, every launch made for this pool is bracketed by CUDA events on
  * its stream.  tf_profile_read synchronises on them and returns, for kernel
  * kind `kind` (0 append, 1 attention main pass, 2 split combine, 3 state copy,
- * 4 poison fill, 5 block keys, 6 block scores, 7 rows read, 8 prompt attention), the summed milliseconds and the launch count since the last
+ * 4 poison fill, 5 block keys, 6 block scores; the prompt path's append, attention, its join and the rows
+ * read back count under 0, 1, 2 and 3), the summed milliseconds and the launch count since the last
  * read, then forgets them. */
 int tf_profile_enable(tf_kvpool *pool, int32_t on);
 int tf_profile_read(tf_kvpool *pool, int32_t kind, double *total_ms, int64_t *launches);

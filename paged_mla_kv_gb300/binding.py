@@ -26,8 +26,7 @@ PAGE_BYTES_BF16 = 589824
 PAGE_BYTES_FP8 = 329728    # 512 x 512 E4M3 codes, 512 fp32 scales, 512 x 64 bf16 rope
 ERR_NAMES = {0: "TF_OK", -1: "TF_E_ARG", -2: "TF_E_RANGE", -3: "TF_E_NOMEM", -4: "TF_E_CUDA",
              -5: "TF_E_TIMEOUT", -6: "TF_E_UNSUPPORTED", -7: "TF_E_DEVICE"}
-PROF_APPEND, PROF_ATTEND, PROF_COMBINE, PROF_COPY, PROF_POISON, PROF_BLOCK_KEYS, PROF_BLOCK_SCORES, \
-    PROF_READ, PROF_PROMPT = range(9)
+PROF_APPEND, PROF_ATTEND, PROF_COMBINE, PROF_COPY, PROF_POISON, PROF_BLOCK_KEYS, PROF_BLOCK_SCORES = range(7)
 
 
 class TFError(RuntimeError):

@@ -1123,7 +1123,7 @@ int launch_prompt_attend(tf_kvpool *pool, const int64_t *h_nq, const int64_t *h_
     p.thr = 8.0f / p.scale_log2;
     if (prepare_launch(pool, st) != TF_OK) return TF_E_CUDA;
     {
-        ProfScope prof(pool, kProfPrompt, st);
+        ProfScope prof(pool, kProfAttend, st);
         const cudaError_t e = launch_pdl(kern, dim3((unsigned)pl.items), dim3(THREADS), SMEM, st, p);
         launch_counter()++;
         if (e != cudaSuccess) return TF_E_CUDA;

@@ -44,7 +44,7 @@ struct DevErr {
 
 enum ProfKind {
     kProfAppend = 0, kProfAttend = 1, kProfCombine = 2, kProfCopy = 3, kProfPoison = 4, kProfBlockKeys = 5,
-    kProfBlockScores = 6, kProfRead = 7, kProfPrompt = 8, kProfKinds = 9
+    kProfBlockScores = 6, kProfKinds = 7
 };
 
 struct ProfRec {

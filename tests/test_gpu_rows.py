@@ -388,6 +388,28 @@ def test_launch_timing_covers_the_calls(fp8):
     out = torch.empty_like(q)
     n = B.tf_prompt_workspace_bytes([300], [300], 2, 2, 64, 64)
     B.tf_prompt_attend(pool, [300], [300], q, k, v, 0.125, out, ws=torch.empty(n, dtype=torch.uint8, device="cuda") if n else None)
-    for kind in (B.PROF_APPEND, B.PROF_READ, B.PROF_PROMPT):
+    for kind in (B.PROF_APPEND, B.PROF_COPY, B.PROF_ATTEND):
         ms, count = pool.profile_read(kind)
         assert count == 1 and 0 < ms < 50
+
+
+def test_codes_equal_the_appends_at_every_magnitude():
+    """FP8 codes and scales, bit for bit tf_paged_append's (whose quotients are IEEE divisions): rows from the smallest
+    bf16 values to the largest, random bits, ties and mixed magnitudes."""
+    g = torch.Generator(device="cuda").manual_seed(70)
+    rows = []
+    for e in range(-133, 128, 3):
+        rows.append(torch.randn((4, 576), generator=g, device="cuda").double() * 2.0 ** e)
+    rows.append(torch.randn((300, 576), generator=g, device="cuda").double() * 2.0 ** torch.randint(-60, 60, (300, 576), generator=g, device="cuda").double())
+    ties = torch.arange(576, device="cuda").double() / 16          # quotients half way between codes
+    rows.append(torch.stack([ties * 448 / ties[:512].max(), ties, ties * 3, -ties * 7]))
+    x = torch.cat(rows).clamp(-3.3e38, 3.3e38).bfloat16()
+    x = torch.cat([x, torch.randint(0, 0x7F80, (500, 576), generator=g, device="cuda").to(torch.int16).view(torch.bfloat16)])
+    n = x.shape[0]
+    a, b = (B.KVPool(1, 8, poison=True, fp8=True) for _ in range(2))
+    (pa, mp), (pb, _) = tables(a, [n]), tables(b, [n])
+    B.tf_paged_append(a, 0, pa, mp, [0], x[:, :512].contiguous().view(1, n, 512), x[:, 512:].contiguous().view(1, n, 64))
+    B.tf_paged_append_rope(b, 0, pb, mp, [0], [n], x)
+    no_device_error(b)
+    k = -(-n // 512)
+    assert torch.equal(a.bytes_view()[:, :k], b.bytes_view()[:, :k])
