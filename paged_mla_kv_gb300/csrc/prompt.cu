@@ -87,7 +87,7 @@ struct Params {
     int16_t hg[TF_MAX_STREAMS];      // key heads side by side
 };
 
-__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+__host__ __device__ inline int ceil_div(int a, int b) { return (int)(((unsigned)a + b - 1) / b); }   // 0 <= a <= INT_MAX
 
 // What an item is.  Items of a stream: groups of hg key heads; in a group blocks from the last (the longest of a
 // causal prompt) to the first, in a block its splits, in a split the group's heads.  The heads of a group read
@@ -1008,7 +1008,7 @@ static int plan(Params &p, const int64_t *h_nq, const int64_t *h_nk, int S, int 
         p.nk[i] = e[i].nk;
         p.nsp[i] = (int16_t)sp;
         p.chunk[i] = (int32_t)(sp > 1 ? chunk : std::max<int64_t>(1, e[i].tiles));
-// All heads side by side where their keys and values fit L2 together: the longest blocks of all come first then,
+        // All heads side by side where their keys and values fit L2 together: the longest blocks of all come first then,
         // and the last items are short.  Else as many as take a quarter of it.
         p.hg[i] = (int16_t)(bytes * Hkv <= (96 << 20) ? Hkv : std::max<int64_t>(1, (32 << 20) / bytes));
         p.slot0[i] = sp > 1 ? (int32_t)out->slots : -1;
