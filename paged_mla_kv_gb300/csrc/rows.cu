@@ -37,7 +37,7 @@ __device__ __forceinline__ int stream_of(const Packed &k, int row) {
 
 // (cos, sin) of a pair's angle at a position, times the amplitude.  The angle lies within half a turn, where the
 // hardware's sine and cosine are off by 2^-21 at most, a 4,000th of the rounding to bf16 that follows (sincospif
-// instead: appending 297,264 rows takes 121 us against 112).
+// instead: turning 297,264 rows of one head takes 22.7 us against 20.1, appending them to FP8 pages 109 against 106).
 __device__ __forceinline__ float2 turn_of(uint64_t turn, int pos, float amplitude) {
     const int32_t frac = (int32_t)(uint32_t)((turn * (uint64_t)(uint32_t)pos) >> 32);
     const float angle = (float)frac * (3.14159265358979f * 0x1p-31f);
@@ -88,11 +88,22 @@ __global__ void __launch_bounds__(RT) rope_kernel(const __grid_constant__ RopePa
     const int tpr = p.threads_per_row, lanes = RT / tpr, pairs = p.dim / 2;
     const int row0 = (int)blockIdx.x * lanes * IT;
     const int nrows = min(p.rows.n - row0, lanes * IT);
-    {   // a thread makes one pair's angles, of every (RT / pairs)-th row
+    {   // a thread makes one pair's angles, of every (RT / pairs)-th row (one search for their streams: 297,264 rows
+        // of one head 26.7 -> 20 us)
         const int r0 = (int)threadIdx.x / pairs, pair = (int)threadIdx.x - r0 * pairs, step = RT / pairs;
         const uint64_t turn = p.turn[pair];
-        for (int r = r0; r0 < step && r < nrows; r += step)
-            tab[r * pairs + pair] = turn_of(turn, p.rows.base[stream_of(p.rows, row0 + r)] + row0 + r, p.amplitude);
+        if (r0 < step && r0 < nrows) {
+            int s = stream_of(p.rows, row0 + r0);
+            int base = p.rows.base[s], next = s + 1 < p.rows.S ? p.rows.off[s + 1] : p.rows.n;
+            for (int r = r0; r < nrows; r += step) {
+                while (row0 + r >= next) {
+                    ++s;
+                    base = p.rows.base[s];
+                    next = s + 1 < p.rows.S ? p.rows.off[s + 1] : p.rows.n;
+                }
+                tab[r * pairs + pair] = turn_of(turn, base + row0 + r, p.amplitude);
+            }
+        }
     }
     __syncthreads();
     ptx::griddep_wait();
@@ -170,21 +181,25 @@ __device__ __forceinline__ int page_of(const int32_t *pt, int max_pages, int num
     return -1;
 }
 
-// One warp a row.  BF16 pages: lane l has latent values 8l .. 8l + 7 and 256 more of them further on, so that
-// loads and stores are whole lines; FP8 pages: values 16l .. 16l + 15, whose codes are 16 bytes.  Lane l turns rope
-// pair l.  The row's square sum is added in fp32, 16 values a lane and then across the warp.  BF16, 297,264 rows
-// (685 MB): 112 us, 0.90 of the measured copy rate (bare, without norm and rotation, 97); FP8: 116 us, 0.68.  Six blocks an
-// SM: with eight the registers spill (146 us), with five 116.
+// One warp a row: lane l has latent values 8l .. 8l + 7 and 256 more of them further on, so that loads and stores are
+// whole lines, and rope pair l.  The row's square sum is added in fp32, 16 values a lane and then across the warp.
+// BF16, 297,264 rows (685 MB): 102 to 103 us, 0.99 of the measured copy rate (bare, without norm and rotation, 97);
+// FP8 (534 MB): 106 us, 0.75: what the codes add to each row's chain (amax, scale, quotients) shows.  Six blocks an
+// SM: 109 and 110 us with five, 113 and 125 with seven, whose registers spill.  Two rows a warp: 104 and 124.
 template <bool FP8, bool HALF>
 __global__ void __launch_bounds__(256, 6) append_rope_kernel(const __grid_constant__ AppendParams p) {
+    __shared__ uint64_t turns[kRope / 2];
     ptx::griddep_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const int row = (int)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, w8 = threadIdx.x >> 5;
+    const int row = (int)blockIdx.x * 8 + w8;
+    // a parameter is read for one index at a time: 32 of them once a block, not once a row (112 us)
+    if (lane < 4) turns[4 * w8 + lane] = p.turn[4 * w8 + lane];
+    __syncthreads();
     if (row >= p.rows.n) return;
     const int s = stream_of(p.rows, row);
     const int pos = p.rows.base[s] + row;
     const uint16_t *src = p.x + row * p.x_row;
-    const int ca = FP8 ? 2 * lane : lane, cb = FP8 ? 2 * lane + 1 : lane + 32;   // 16-byte chunks
+    const int ca = lane, cb = lane + 32;   // 16-byte chunks (8 bytes as codes)
     ptx::griddep_wait();
     // the row is on its way while the page is looked up and the angle made
     const uint4 a = __ldg(reinterpret_cast<const uint4 *>(src) + ca), b = __ldg(reinterpret_cast<const uint4 *>(src) + cb);
@@ -194,7 +209,7 @@ __global__ void __launch_bounds__(256, 6) append_rope_kernel(const __grid_consta
     else
         kw = __ldg(reinterpret_cast<const uint32_t *>(src + kLat) + lane);
     const int page = page_of(p.pt, p.max_pages, p.num_pages, s, pos, p.err, lane == 0);
-    const float2 cs = p.rotate ? turn_of(p.turn[lane], pos, p.amplitude) : make_float2(1.f, 0.f);
+    const float2 cs = p.rotate ? turn_of(turns[lane], pos, p.amplitude) : make_float2(1.f, 0.f);
     if (page < 0) return;
     const int r = pos & (kPageRows - 1);
     float k0 = lo(kw), k1 = hi(kw);
@@ -228,15 +243,14 @@ __global__ void __launch_bounds__(256, 6) append_rope_kernel(const __grid_consta
         float amax = 0.0f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));   // of values >= 0: as their bits
         const float scale = __fdiv_rn(amax, 448.0f);
         uint32_t code[4] = {0u, 0u, 0u, 0u};
         if (amax > 0.0f) {
             // x / scale, correctly rounded: with y = 1 / scale rounded to nearest, q = x y and the remainder q scale - x
             // (exact by fma, and with this sign a zero keeps its own), q - remainder y is the nearest quotient (Markstein, 1990), as long as nothing underflows:
-            // a product's last bit is 2^-10 2^-23 2^-23 scale at least where the code is not 0.  297,264 rows take 116 us
-            // so and 157 with sixteen divisions a lane.
+            // a product's last bit is 2^-10 2^-23 2^-23 scale at least where the code is not 0.  297,264 rows take 106 us
+            // so and 135 with sixteen divisions a lane.
             if (scale >= 0x1p-90f) {
                 const float y = __frcp_rn(scale);
                 const float2 y2 = make_float2(y, y), ny2 = make_float2(-y, -y), s2 = make_float2(scale, scale);
@@ -257,7 +271,9 @@ __global__ void __launch_bounds__(256, 6) append_rope_kernel(const __grid_consta
                 }
             }
         }
-        reinterpret_cast<uint4 *>(pg + (size_t)r * kLat)[lane] = make_uint4(code[0], code[1], code[2], code[3]);
+        uint2 *dst = reinterpret_cast<uint2 *>(pg + (size_t)r * kLat);
+        dst[ca] = make_uint2(code[0], code[1]);
+        dst[cb] = make_uint2(code[2], code[3]);
         if (lane == 0) reinterpret_cast<float *>(pg + kF8ScaleOff)[r] = scale;
     } else {
         // without a norm the packed values are the bits that came
