@@ -47,12 +47,16 @@ struct Lay {
     static constexpr int QB = DQK / BOX, VB = DV / BOX;
     static constexpr int Q_TILE = BM * DQK * 2, K_TILE = BN * DQK * 2, UNIT = VH * DV * 2;
     static constexpr int KU = K_TILE / UNIT, BU = BN * 128 / UNIT;   // units of a key tile, of one of its boxes
+    // Groups of a key tile: boxes with a barrier of their own where the ring holds less than two steps, so that the
+    // next keys' first boxes come while the last values are still in use (2,048 rows behind 100,000: 4.80 ms with one group,
+    // 4.60 so; the halves of the values on their own as well: 4.77; at 128 wide, two steps and a half, 1.07 ms with one, 1.16 with two).
+    static constexpr int KG = DQK == 192 ? QB : 1;
     static constexpr int OFF_R = 2 * Q_TILE, BYTES = 229376, U = (BYTES - OFF_R) / UNIT;
     // a box does not wrap: it starts on a multiple of its own size, as keys and pairs of value halves do
     static_assert(U * UNIT + OFF_R == BYTES && U <= MAX_UNITS && K_TILE % UNIT == 0 && U % BU == 0 && 2 % BU == 0, "the ring's form");
 };
 
-// A place in the ring: group (a key tile or half of a value tile) number `g` modulo U, its phase, its first unit.
+// A place in the ring: group (of a key tile, or a value tile) number `g` modulo U, its phase, its first unit.
 template <int U>
 struct Ring {
     int g = 0, u = 0;
@@ -64,6 +68,11 @@ struct Ring {
         }
         u += units;
         if (u >= U) u -= U;
+    }
+    template <typename L>
+    __device__ __forceinline__ void keys() {
+#pragma unroll
+        for (int i = 0; i < L::KG; ++i) step(L::KU / L::KG);
     }
 };
 
@@ -395,7 +404,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
             auto group = [&](int units, bool is_keys) -> uint64_t * {
                 for (; room < units; tail.step(0)) {
                     if (!wait(&c.free[tail.g], tail.phase, &c.abort, p.err, 53)) return nullptr;
-                    room += (keys >> tail.g & 1) ? L::KU : 2;
+                    room += (keys >> tail.g & 1) ? L::KU / L::KG : 2;
                 }
                 room -= units;
                 keys = (keys & ~(1u << head.g)) | (uint32_t)is_keys << head.g;
@@ -403,20 +412,24 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                 return &c.full[head.g];
             };
             auto load_k = [&](int kt) {
-                uint64_t *bar = group(L::KU, true);
-                if (!bar) return false;
-                if (lane == 0) {
-                    ptx::mbar_arrive_expect_tx(bar, L::K_TILE);
-                    int u = head.u;
-                    for (int b = 0; b < L::QB; ++b) {
-                        const bool shared = p.has_kr && b == L::QB - 1;
-                        tma_load_3d(smem + L::OFF_R + u * L::UNIT, shared ? &p.kr : &p.k, bar, shared ? 0 : b * BOX, shared ? 0 : x.h,
-                                    x.krow + kt * BN);
-                        u = u + L::BU == L::U ? 0 : u + L::BU;
+#pragma unroll 1
+                for (int i = 0; i < L::KG; ++i) {
+                    uint64_t *bar = group(L::KU / L::KG, true);
+                    if (!bar) return false;
+                    if (lane == 0) {
+                        ptx::mbar_arrive_expect_tx(bar, L::K_TILE / L::KG);
+                        int u = head.u;
+#pragma unroll 1
+                        for (int b = i * L::QB / L::KG; b < (i + 1) * L::QB / L::KG; ++b) {
+                            const bool shared = p.has_kr && b == L::QB - 1;
+                            tma_load_3d(smem + L::OFF_R + u * L::UNIT, shared ? &p.kr : &p.k, bar, shared ? 0 : b * BOX, shared ? 0 : x.h,
+                                        x.krow + kt * BN);
+                            u = u + L::BU == L::U ? 0 : u + L::BU;
+                        }
                     }
+                    head.step(L::KU / L::KG);
+                    __syncwarp();
                 }
-                head.step(L::KU);
-                __syncwarp();
                 return true;
             };
             auto load_v = [&](int kt) {
@@ -496,19 +509,28 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
         Item x, y;
         Ring<L::U> keys, vals;
         bool early = false, known = false;   // the next item (y) is known, its first scores are made
-        // Scores of warpgroup w from the keys at `k`; `last`: the query tile's last product.
-        auto scores = [&](int w, const Ring<L::U> &k, bool pair, bool last) {
+        // Scores of warpgroup w from the keys at `k`; `last`: the query tile's last product; `look_first`: the keys may
+        // still be on their way.  (Loops are not unrolled here: every instruction of this warp is fetched again between items.
+        // Unrolled, 4,096 rows in eight prompts took 92 us for 72.)
+        auto scores = [&](int w, Ring<L::U> k, bool pair, bool last, bool look_first) {
             ptx::tc_fence_after();
             const uint64_t a = dq + (uint64_t)(((pair ? w : 0) * L::Q_TILE) >> 4);
-            int u = k.u;
+#pragma unroll 1
+            for (int g = 0; g < L::KG; ++g) {
+                if (look_first && !spin(&c.full[k.g], k.phase, &c.abort, p.err, 61)) return false;
+                int u = k.u;
 #pragma unroll
-            for (int i = 0; i < L::QB; ++i) {
-                ptx::mma4_bf16_ss_warp(tmem + w * BN, a + (uint64_t)((i * BM * 128) >> 4), dk + (uint64_t)((u * L::UNIT) >> 4), IQK, i == 0);
-                u = u + L::BU == L::U ? 0 : u + L::BU;
+                for (int b = 0; b < L::QB / L::KG; ++b) {
+                    const int i = g * (L::QB / L::KG) + b;
+                    ptx::mma4_bf16_ss_warp(tmem + w * BN, a + (uint64_t)((i * BM * 128) >> 4), dk + (uint64_t)((u * L::UNIT) >> 4), IQK, i == 0);
+                    u = u + L::BU == L::U ? 0 : u + L::BU;
+                }
+                if (g + 1 == L::KG) ptx::mma_commit_warp(&c.s_full[w]);
+                if (w == 1 || !pair) ptx::mma_commit_warp(&c.free[k.g]);
+                k.step(L::KU / L::KG);
             }
-            ptx::mma_commit_warp(&c.s_full[w]);
-            if (w == 1 || !pair) ptx::mma_commit_warp(&c.free[k.g]);
             if (last) ptx::mma_commit_warp(&c.q_free[pair ? w : 0]);
+            return true;
         };
         for (;;) {
             if (!known && !it.next(c, p, y, lane)) break;
@@ -521,13 +543,12 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
             // With two query tiles both warpgroups use a tile's keys, and the first to come takes them from the ring; so with
             // the values.
             auto qk = [&](int w, int j) {
-                if (w == 0 || !pair || j >= n0) {
-                    if (!spin(&c.full[r.g], r.phase, &c.abort, p.err, 61)) return false;
+                const bool first = w == 0 || !pair || j >= n0;
+                if (first) {
                     keys = r;
-                    r.step(L::KU);
+                    r.template keys<L>();
                 }
-                scores(w, keys, pair, pair ? j + 1 == (w ? n1 : n0) : w == (n1 == n0) && j + 1 == n0);
-                return true;
+                return scores(w, keys, pair, pair ? j + 1 == (w ? n1 : n0) : w == (n1 == n0) && j + 1 == n0, first);
             };
             // Once warpgroup 0 has had its last product, while warpgroup 1 still works: the first scores of the next item,
             // if all that they need is there.  Without them the tensor cores wait through the last softmax.
@@ -542,12 +563,17 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                 Ring<L::U> at = r;     // behind what this item still takes
                 if (pair) {
                     for (int j = left_j + 1; j < n1; ++j) {
-                        at.step(L::KU);
+                        at.template keys<L>();
                         at.step(2);
                     }
                 }
-                if (!look(&c.full[at.g], at.phase)) return;
-                scores(0, at, y.pair, y.pair ? y.n0 == 1 : y.n0 == 1 && y.n1 == 0);
+                const Ring<L::U> begin = at;
+#pragma unroll
+                for (int g = 0; g < L::KG; ++g) {
+                    if (!look(&c.full[at.g], at.phase)) return;
+                    at.step(L::KU / L::KG);
+                }
+                scores(0, begin, y.pair, y.pair ? y.n0 == 1 : y.n0 == 1 && y.n1 == 0, false);
                 early = true;
             };
             // The product of step j's P and values.  `whole`: not the warpgroup's last step, all keys count.
@@ -603,7 +629,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
             constexpr std::false_type none{};
             if (early) {
                 keys = r;
-                r.step(L::KU);
+                r.template keys<L>();
                 early = false;
             } else {
                 ok = wait(&c.q_full[0], nq0 & 1, &c.abort, p.err, 60);
