@@ -1044,8 +1044,11 @@ static int plan(Params &p, const int64_t *h_nq, const int64_t *h_nk, int S, int 
         p.nsp[i] = (int16_t)sp;
         p.chunk[i] = (int32_t)(sp > 1 ? chunk : std::max<int64_t>(1, e[i].tiles));
         // All heads side by side where their keys and values fit L2 together: the longest blocks of all come first then,
-        // and the last items are short.  Else as many as take a quarter of it.
-        p.hg[i] = (int16_t)(bytes * Hkv <= (96 << 20) ? Hkv : std::max<int64_t>(1, (32 << 20) / bytes));
+        // and the last items are short.  Else in groups of a like size that take up to 48 MB: a last group of few heads leaves
+        // SMs idle behind its longest blocks (16,384 rows of 16 heads: 815 us with groups of 32 MB and a rest,
+        // 714 so; 4,096 rows of 64 heads 235 and 209; like groups of 32, 64 and 90 MB: 220, 211 and 215).
+        const int64_t fit = std::max<int64_t>(1, (48 << 20) / bytes), groups = bytes * Hkv <= (96 << 20) ? 1 : (Hkv + fit - 1) / fit;
+        p.hg[i] = (int16_t)((Hkv + groups - 1) / groups);
         p.slot0[i] = sp > 1 ? (int32_t)out->slots : -1;
         const int64_t cnt = e[i].blocks * Hkv * sp;
         if (sp > 1) out->slots += cnt * 2;
