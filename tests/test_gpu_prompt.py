@@ -105,6 +105,14 @@ def test_one_prompt(pool, n, dqk, dv, kr):
     check([n], [n], *x, True, out, lse)
 
 
+def test_groups_of_heads(pool):
+    """Keys and values of all heads that do not fit L2 side by side: seven heads in groups of three, three and one."""
+    nq, nk, H = [300, 3], [60000, 70], 7
+    x = make(nq, nk, H, H, 64, 64, seed=70)
+    out, lse = call(pool, nq, nk, *x)
+    check(nq, nk, *x, True, out, lse)
+
+
 @pytest.mark.parametrize("H,Hkv", [(1, 1), (2, 1), (3, 1), (10, 2), (8, 1), (16, 2), (64, 1), (128, 1), (48, 1), (100, 1)])
 @pytest.mark.parametrize("causal", [True, False])
 def test_grouped_heads(pool, H, Hkv, causal):
