@@ -167,7 +167,7 @@ struct alignas(16) Item {
 struct Ctl {
     uint64_t q_full[2], q_free[2];
     uint64_t full[MAX_UNITS], free[MAX_UNITS];     // of the ring's groups
-    uint64_t s_full[2], p_full[2][2], o_full[2];   // P comes in halves of 64 keys
+    uint64_t s_full[2], p_full[2], o_full[2];
     uint64_t ml_full[2], ml_free[2]; // the rows' maxima and sums
     uint64_t o_free[2];              // the sums have been read
     uint64_t ask, answer;            // the question for another item
@@ -230,25 +230,41 @@ __device__ __forceinline__ void expect_warp(uint64_t *bar, uint32_t bytes) {
         : "memory");
 }
 
-// `n` (0 to 4) products of 16 keys: P from TMEM (8 columns a step), V MN-major (two 1 KB groups of 8 keys a step).
-__device__ __forceinline__ void pv_warp(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, int n) {
-    if (n == 4) {   // one block: a loop around single products issues them at half the pace of the tensor cores
-        asm volatile(
-            "{\n\t.reg .pred e, p;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
-            "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
-            "add.u64 b1, %2, 128;\n\tadd.u64 b2, %2, 256;\n\tadd.u64 b3, %2, 384;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "elect.sync _|e, 0xffffffff;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, 1;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, 1;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, 1;\n\t}" ::"r"(d),
-            "r"(a), "l"(b), "r"(idesc), "r"(acc)
-            : "memory");
-        return;
-    }
+// `n` products of 16 keys: P from TMEM (8 columns a step), V MN-major (two 1 KB groups of 8 keys a step; its halves'
+// descriptors are `b` and `b4`).
+__device__ __forceinline__ void pv_warp(uint32_t d, uint32_t a, uint64_t b, uint64_t b4, uint32_t idesc, uint32_t acc, int n) {
 #pragma unroll 1
-    for (int i = 0; i < n; ++i, a += 8, b += 2048 >> 4, acc = 1) ptx::mma_bf16_ts_warp(d, a, b, idesc, acc);
+    for (int i = 0; i < n; ++i, a += 8, b += 2048 >> 4, acc = 1) {
+        if (i == 4) b = b4;
+        ptx::mma_bf16_ts_warp(d, a, b, idesc, acc);
+    }
+}
+
+// All eight of a tile, in one block: the loop issues them at half the pace of the tensor cores.
+__device__ __forceinline__ void pv8_warp(uint32_t d, uint32_t a, uint64_t b, uint64_t b4, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred e, p;\n\t.reg .b32 a1, a2, a3, a4, a5, a6, a7;\n\t.reg .b64 b1, b2, b3, b5, b6, b7;\n\t"
+        "add.u32 a1, %1, 8;\n\t"
+        "add.u32 a2, %1, 16;\n\t"
+        "add.u32 a3, %1, 24;\n\t"
+        "add.u32 a4, %1, 32;\n\t"
+        "add.u32 a5, %1, 40;\n\t"
+        "add.u32 a6, %1, 48;\n\t"
+        "add.u32 a7, %1, 56;\n\t"
+        "add.u64 b1, %2, 128;\n\tadd.u64 b5, %3, 128;\n\t"
+        "add.u64 b2, %2, 256;\n\tadd.u64 b6, %3, 256;\n\t"
+        "add.u64 b3, %2, 384;\n\tadd.u64 b7, %3, 384;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %4, 1;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %4, 1;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %4, 1;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], %3, %4, 1;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], b5, %4, 1;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], b6, %4, 1;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], b7, %4, 1;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "l"(b4), "r"(idesc), "r"(acc)
+        : "memory");
 }
 
 // One look at a barrier.  Without a time to sleep it costs 38 cycles where the phase is complete, with one 70.
@@ -370,8 +386,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
             ptx::mbar_init(&c.q_full[i], 1);
             ptx::mbar_init(&c.q_free[i], 1);
             ptx::mbar_init(&c.s_full[i], 1);
-            ptx::mbar_init(&c.p_full[i][0], 4);
-            ptx::mbar_init(&c.p_full[i][1], 4);
+            ptx::mbar_init(&c.p_full[i], 4);
             ptx::mbar_init(&c.o_full[i], 1);
             ptx::mbar_init(&c.ml_full[i], 4);
             ptx::mbar_init(&c.ml_free[i], 4);
@@ -586,7 +601,9 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                 scores(0, begin, y.pair, y.pair ? y.n0 == 1 : y.n0 == 1 && y.n1 == 0, false);
                 early = true;
             };
-            // The product of step j's P and values.  `whole`: not the warpgroup's last step, all keys count.
+            // The product of step j's P and values.  `whole`: not the warpgroup's last step, all keys count; `alone`:
+            // warpgroup 0 has ended.  (P as a whole: handed over in halves it was taken 400 to 600 cycles late all the same, and
+            // this warp's longer code cost 40 prompts of 300 rows 240 us for 218; at length the two are alike.)
             auto pv = [&](int w, int j, auto is_whole, auto is_alone) {
                 constexpr bool whole = decltype(is_whole)::value, alone = decltype(is_alone)::value;
                 if (w == 0 || !pair || j >= n0) {
@@ -612,26 +629,28 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                     }
                 }
                 const uint32_t np = w ? np1 : np0, no = w ? no1 : no0;
-                if (alone) {   // warpgroup 0 has ended
+                if (alone) {
                     const long long t0 = clock64();
-                    for (uint32_t spins = 1; !look(&c.p_full[w][0], np & 1); ++spins) {
+                    for (uint32_t spins = 1; !look(&c.p_full[w], np & 1); ++spins) {
                         start_next(j);
                         if ((spins & 1023u) == 0 && expired(t0, 1ll << 31, &c.abort, p.err, 62)) return false;
                     }
-                } else if (!spin(&c.p_full[w][0], np & 1, &c.abort, p.err, 62)) {
+                } else if (!spin(&c.p_full[w], np & 1, &c.abort, p.err, 62)) {
                     return false;
                 }
                 // the sums of the item before are read out
                 if (j == 0 && no > 0 && !wait(&c.o_free[w], (no - 1) & 1, &c.abort, p.err, 66)) return false;
                 ptx::tc_fence_after();
                 const uint32_t ts = tmem + w * BN, to = tmem + 2 * BN + w * DV;
-                pv_warp(to, ts, dv + (uint64_t)((vals.u * L::UNIT) >> 4), IPV, j > 0, whole ? 4 : min(4, steps));
-                if (!spin(&c.p_full[w][1], np & 1, &c.abort, p.err, 62)) return false;
-                ptx::tc_fence_after();
                 const int u = vals.u + 1 == L::U ? 0 : vals.u + 1;
-                pv_warp(to, ts + 32, dv + (uint64_t)((u * L::UNIT) >> 4), IPV, 1, whole ? 4 : max(0, steps - 4));
+                const uint64_t b0 = dv + (uint64_t)((vals.u * L::UNIT) >> 4), b1 = dv + (uint64_t)((u * L::UNIT) >> 4);
+                if (whole) {
+                    pv8_warp(to, ts, b0, b1, IPV, j > 0);
+                } else {
+                    pv_warp(to, ts, b0, b1, IPV, j > 0, steps);
+                }
                 if (w == 1 || !pair) ptx::mma_commit_warp(&c.free[vals.g]);
-                if (!whole) ptx::mma_commit_warp(&c.o_full[w]);
+                if (!whole && j + 1 == (w ? n1 : n0)) ptx::mma_commit_warp(&c.o_full[w]);
                 if (w) ++np1; else ++np0;
                 return true;
             };
@@ -658,12 +677,12 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
             // the rest: warpgroup 0's last steps, then warpgroup 1's
 #pragma unroll 1
             for (; ok && j < n0; ++j) {
-                ok = j + 1 < n0 ? pv(0, j, yes, none) && qk(0, j + 1) : pv(0, j, none, none);
-                if (ok && j + 1 < n0 && j < n1) ok = pv(1, j, none, none);
+                ok = pv(0, j, none, none) && (j + 1 == n0 || qk(0, j + 1));
                 if (j + 1 == n0) break;
+                if (ok && j < n1) ok = pv(1, j, none, none);
             }
 #pragma unroll 1
-            for (; ok && j < n1; ++j) ok = j + 1 < n1 ? pv(1, j, yes, yes) && qk(1, j + 1) : pv(1, j, none, yes);
+            for (; ok && j < n1; ++j) ok = pv(1, j, none, yes) && (j + 1 == n1 || qk(1, j + 1));
             if (!ok) break;
             no0 += n0 > 0;
             no1 += n1 > 0;
@@ -701,7 +720,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                     break;
                 }
                 if (idle) {
-                    if (lane < 2) ptx::mbar_arrive(&c.p_full[w][lane]);
+                    if (lane == 0) ptx::mbar_arrive(&c.p_full[w]);
                     continue;
                 }
                 ptx::tc_fence_after();
@@ -763,11 +782,11 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                         pk[i] = ptx::pack_bf16x2(e.x, e.y);
                     }
                     ptx::tmem_st32(ts + 16 * q, pk);
-                    ptx::tmem_st_wait();   // with it what the maximum's move changed in O
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&c.p_full[w][q / 2]);
                 }
+                ptx::tmem_st_wait();   // with it what the maximum's move changed in O
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&c.p_full[w]);
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
             if (ok && n > 0) {
