@@ -105,6 +105,24 @@ def test_one_prompt(pool, n, dqk, dv, kr):
     check([n], [n], *x, True, out, lse)
 
 
+@pytest.mark.parametrize("dqk,dv", [(192, 128), (128, 128), (64, 64)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("row", [130, 255, 511, 699])
+def test_own_values_that_are_not_finite(pool, dqk, dv, value, row):
+    """A key leaves the rows before it as they are; so do values, but for rows whose last key lies in their tile."""
+    n = 700
+    q, k, v, _ = make([n], [n], 3, 3, dqk, dv, seed=1)
+    clean, lclean = call(pool, [n], [n], q, k, v)
+    for x, first in ((k, row), (v, row // 128 * 128)):
+        y = x.clone()
+        y[row, 1] = value
+        out, lse = call(pool, [n], [n], q, *((y, v) if x is k else (k, y)))
+        same = (bits(out) == bits(clean)).all(-1) & (lse.cpu() == lclean.cpu()).numpy()
+        assert same[:, [0, 2]].all() and same[:first, 1].all(), first
+        if value != value:
+            assert torch.isnan(out[row:, 1]).all()
+
+
 def test_groups_of_heads(pool):
     """Keys and values of all heads that do not fit L2 side by side: seven heads in groups of three, three and one."""
     nq, nk, H = [300, 3], [60000, 70], 7
