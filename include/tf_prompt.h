@@ -135,8 +135,9 @@ int tf_paged_read(tf_kvpool *pool, int32_t cache, const int32_t *d_pt, int32_t m
  * Scores are bf16 products summed in fp32, the softmax is fp32, its weights are rounded to bf16 for the second
  * product (relative 2^-8 each, as in tf_paged_mla_attend).  Work is dealt out by the batch's sizes, so a row's bits
  * may differ (within rounding) between batches, and are the same on every call of one batch.
- * What other streams hold, NaN included, never reaches a stream's outputs.  A NaN or infinity among a stream's
- * own values can reach the outputs of causal rows before it whose last key lies in the same 128-key tile.
+ * What other streams hold, NaN included, never reaches a stream's outputs.  A NaN or infinity in a stream's own
+ * keys reaches no causal row before it; one in its values v can reach the outputs of rows before it whose last key
+ * lies in the same 128-key tile.
  * d_ws: tf_prompt_workspace_bytes(...) bytes, 256-byte aligned (NULL if that is 0): partial sums of streams whose
  * keys are split.  Not to be shared by calls that may run at the same time.
  * pool: its device error word takes what a kernel records (a wait that ran out); its pages are not read.
