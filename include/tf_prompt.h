@@ -98,6 +98,10 @@ int tf_rope_apply(const tf_rope *rope, const int64_t *h_pos, const int64_t *h_n,
  *   rope     turned to its position by `rope`, a table of dim 64 (NULL: as it is)
  * each rounded once to bf16.  On FP8 pools the fp32 latent is quantized as in tf_paged_append (scale = amax / 448,
  * codes rounded to nearest even), without a rounding to bf16 before.
+ * Rows that are not finite: a NaN of the fp32 latent (with a gain one in the row makes every value NaN, and an
+ * infinity becomes NaN and the row's finite values 0) is NaN when it is read, on pages of either format; on FP8 pages
+ * its code is NaN, amax is that of the other values, which keep theirs, and an infinity without a gain makes the
+ * scale infinite, so that every value of its row is read as NaN.
  * The same row of a stream must not be written twice in a call (streams that share a page).  A table entry outside
  * the pool is recorded as TF_E_DEVICE and its rows are skipped.
  * Errors: TF_E_ARG for a null pool or host array, S outside [1, TF_MAX_STREAMS], max_pages < 1, a negative

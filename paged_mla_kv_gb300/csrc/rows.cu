@@ -157,6 +157,16 @@ __global__ void __launch_bounds__(RT) rope_kernel(const __grid_constant__ RopePa
     }
 }
 
+// The larger value; NaN if one of them is.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// The largest of a warp's absolute values: as their bits, of which those of a NaN are above all others.
+__device__ __forceinline__ float warp_amax(float a) { return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a))); }
+
 // ---- append of a projection's rows ----
 struct AppendParams {
     const int32_t *pt;       // [S][max_pages] or null (windows)
@@ -242,16 +252,24 @@ __global__ void __launch_bounds__(256, 6) append_rope_kernel(const __grid_consta
     if (FP8) {
         float amax = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
-        amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));   // of values >= 0: as their bits
+        for (int i = 0; i < 16; ++i) amax = max_or_nan(amax, fabsf(x[i]));
+        amax = warp_amax(amax);
+        const bool nan = amax != amax;
+        if (nan) {   // the scale is that of the other values, which keep theirs; 0 where there are none (or only zeros)
+            amax = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
+            amax = warp_amax(amax);
+        }
         const float scale = __fdiv_rn(amax, 448.0f);
         uint32_t code[4] = {0u, 0u, 0u, 0u};
-        if (amax > 0.0f) {
+        if (amax > 0.0f || nan) {
             // x / scale, correctly rounded: with y = 1 / scale rounded to nearest, q = x y and the remainder q scale - x
             // (exact by fma, and with this sign a zero keeps its own), q - remainder y is the nearest quotient (Markstein, 1990), as long as nothing underflows:
             // a product's last bit is 2^-10 2^-23 2^-23 scale at least where the code is not 0.  297,264 rows take 106 us
             // so and 135 with sixteen divisions a lane.
-            if (scale >= 0x1p-90f) {
+            // An infinite scale has no such remainder: finite values over it are 0, the infinite ones NaN.
+            if (scale >= 0x1p-90f && scale < INFINITY) {
                 const float y = __frcp_rn(scale);
                 const float2 y2 = make_float2(y, y), ny2 = make_float2(-y, -y), s2 = make_float2(scale, scale);
 #pragma unroll
@@ -264,7 +282,9 @@ __global__ void __launch_bounds__(256, 6) append_rope_kernel(const __grid_consta
             } else {
 #pragma unroll 1
                 for (int i = 0; i < 16; ++i) {   // (a dynamic index: few instructions for what never happens)
-                    const uint32_t c = __nv_cvt_float_to_fp8(__fdiv_rn(pick(x, i), scale), __NV_SATFINITE, __NV_E4M3);
+                    float v = pick(x, i);
+                    if (scale > 0.0f) v = __fdiv_rn(v, scale);   // else zeros and NaN, as they are
+                    const uint32_t c = __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         if (i >> 2 == k) code[k] |= c << (8 * (i & 3));
