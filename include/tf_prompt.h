@@ -98,6 +98,8 @@ int tf_rope_apply(const tf_rope *rope, const int64_t *h_pos, const int64_t *h_n,
  *   rope     turned to its position by `rope`, a table of dim 64 (NULL: as it is)
  * each rounded once to bf16.  On FP8 pools the fp32 latent is quantized as in tf_paged_append (scale = amax / 448,
  * codes rounded to nearest even), without a rounding to bf16 before.
+ * The norm is fp32 throughout: a square sum past fp32's largest value (values from some 2^59 on) is infinite, and a
+ * finite row comes out as zeros; squares below fp32's smallest count as 0 beside eps.
  * Rows that are not finite: a NaN of the fp32 latent (with a gain one in the row makes every value NaN, and an
  * infinity becomes NaN and the row's finite values 0) is NaN when it is read, on pages of either format; on FP8 pages
  * its code is NaN, amax is that of the other values, which keep theirs, and an infinity without a gain makes the
