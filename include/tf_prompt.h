@@ -140,7 +140,9 @@ int tf_paged_read(tf_kvpool *pool, int32_t cache, const int32_t *d_pt, int32_t m
  * d_kr + row * kr_row, the same for every head (a rotary key), and k holds the dqk - 64 others.
  * Scores are bf16 products summed in fp32, the softmax is fp32, its weights are rounded to bf16 for the second
  * product (relative 2^-8 each, as in tf_paged_mla_attend).  Work is dealt out by the batch's sizes, so a row's bits
- * may differ (within rounding) between batches, and are the same on every call of one batch.
+ * may differ (within rounding) between batches, and are the same on every call of one batch.  Keys are summed in parts
+ * of 131,072 at most (the tensor cores' sums are cut, not rounded, and lose up to 2^-10 over one) that fp32 joins: longer
+ * streams need a workspace.
  * What other streams hold, NaN included, never reaches a stream's outputs.  A NaN or infinity in a stream's own
  * keys reaches no causal row before it; one in its values v can reach the outputs of rows before it whose last key
  * lies in the same 128-key tile.

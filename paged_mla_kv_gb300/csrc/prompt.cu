@@ -76,6 +76,12 @@ struct Ring {
     }
 };
 
+// Key tiles of an item, at most.  The tensor cores cut an accumulated sum where fp32 would round it: a sum of values of
+// one sign loses 2^-23 of itself with every 16 keys.  Unsplit, 524,288 keys came out 0.4% low, as much as a rounding to
+// bf16, 2^20 keys 0.75%, 2^24 10%; in parts of 131,072, which are joined in fp32, any number loses 0.1%.  It also keeps an
+// item (3 to 4 million cycles then) far below the limit of the waits that last as long as one.
+constexpr int LONGEST = 1024;
+
 // Streams in the order of their work, the longest first.
 struct Params {
     CUtensorMap q, k, kr, v;
@@ -1034,6 +1040,7 @@ static int plan(Params &p, const int64_t *h_nq, const int64_t *h_nk, int S, int 
     // leave uneven.  An item's start and end count as START tiles, a split's partial sums as PART more, and the
     // launch that joins them as JOIN.
     constexpr int64_t START = 2, PART = 2, JOIN = 3;
+    most = std::min<int64_t>(most, LONGEST);
     int64_t chunk = most;
     double best = 1e300, whole = 0;
     for (int64_t c = most; c >= 1; c = c > 16 ? c - c / 8 : c - 1) {
