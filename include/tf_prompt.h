@@ -143,9 +143,10 @@ int tf_paged_read(tf_kvpool *pool, int32_t cache, const int32_t *d_pt, int32_t m
  * may differ (within rounding) between batches, and are the same on every call of one batch.  Keys are summed in parts
  * of 131,072 at most (the tensor cores' sums are cut, not rounded, and lose up to 2^-10 over one) that fp32 joins: longer
  * streams need a workspace.
- * What other streams hold, NaN included, never reaches a stream's outputs.  A NaN or infinity in a stream's own
- * keys reaches no causal row before it; one in its values v can reach the outputs of rows before it whose last key
- * lies in the same 128-key tile.
+ * What other streams hold, NaN included, never reaches a stream's outputs, and a NaN or infinity among its own keys or
+ * values reaches no row that does not see it: bits stay, but for the column of a value that is not finite in rows of the
+ * same 128-row query tile, which are made again and may be rounded in another way (slowly: a microsecond for some three
+ * keys of a row).  A row that sees a value that is not finite has NaN in its column, or that infinity.
  * d_ws: tf_prompt_workspace_bytes(...) bytes, 256-byte aligned (NULL if that is 0): partial sums of streams whose
  * keys are split.  Not to be shared by calls that may run at the same time.
  * pool: its device error word takes what a kernel records (a wait that ran out); its pages are not read.

@@ -88,6 +88,10 @@ struct Params {
     uint16_t *out;
     float *lse;
     float *part;                     // [slots][BM][DV], then (m, l) [slots][BM]
+    struct {                         // a tensor as plain memory, for outputs that are made again
+        const uint16_t *p;
+        int64_t row, head;
+    } mq, mk, mkr, mv;
     DevErr *err;
     int64_t out_row, out_head, slots;
     float scale_log2, thr;           // c; 8 / c
@@ -161,6 +165,8 @@ struct alignas(16) Item {
     __device__ __forceinline__ int seen(const Params &p, int t) const {
         return p.causal ? max(0, min(nk, lag + tok0 + t)) : nk;
     }
+    // One past the last key of its tiles.
+    __device__ __forceinline__ int stop() const { return (int)min((int64_t)nk, (int64_t)(c0 + (pair ? n1 : n0 + n1)) * BN); }
     // Key tile of warpgroup w's step j.
     __device__ __forceinline__ int key_tile(int w, int j) const { return pair ? c0 + j : c0 + 2 * j + w; }
     // Keys of that tile that any row of warpgroup w's query tile sees, rounded up to the 16 of a product step.
@@ -180,10 +186,10 @@ struct Ctl {
     uint64_t item_full[2], item_free[2];
     uint64_t drain;
     alignas(16) uint4 next;          // the answer
-    Item item[2];
+    Item item[4];                    // two on their way, and those that outputs are written of
     float2 ml[2][BM];                // (m, l) of each row
     uint32_t tmem;
-    int abort;
+    int abort, busy;                 // roles gave up; warps that make outputs again
 };
 constexpr int SMEM = 229376 + (int)((sizeof(Ctl) + 127) / 128 * 128);
 static_assert(SMEM <= 232448, "227 KB");
@@ -284,9 +290,11 @@ __device__ __forceinline__ bool look(uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, seen);
 }
 
-// Whether a wait that began at t0 is to be given up: past its limit (recorded), or as another role gave up.
-__device__ __forceinline__ bool expired(long long t0, long long limit, volatile int *abort, DevErr *err, int site) {
+// Whether a wait that began at t0 is to be given up: past its limit (recorded), or as another role gave up.  Outputs
+// that are made again (abort[1] warps at it, which wait for nobody) do not count.
+__device__ __forceinline__ bool expired(long long &t0, long long limit, volatile int *abort, DevErr *err, int site) {
     bool stop = *abort != 0;
+    if (abort[1] != 0) t0 = clock64();
     if (!stop && clock64() - t0 > limit) {
         ptx::record_error(err, TF_E_TIMEOUT, site);
         *abort = 1;
@@ -300,7 +308,7 @@ __device__ __forceinline__ bool expired(long long t0, long long limit, volatile 
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort, DevErr *err, int site,
                                      long long limit = 1ll << 31) {
     if (look(bar, parity)) return true;
-    const long long t0 = clock64();
+    long long t0 = clock64();
     for (uint32_t spins = 1;; ++spins) {
         if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
         if ((spins & 255u) == 0 && expired(t0, limit, abort, err, site)) return false;
@@ -350,11 +358,13 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t (&v)[8]) {
 
 // The same without sleeping, for the warp that the tensor cores wait for.
 __device__ __forceinline__ bool spin(uint64_t *bar, uint32_t parity, volatile int *abort, DevErr *err, int site) {
-    const long long t0 = clock64();
+    long long t0 = clock64();
     for (uint32_t spins = 1; !look(bar, parity); ++spins)
         if ((spins & 4095u) == 0 && expired(t0, 1ll << 31, abort, err, site)) return false;
     return true;
 }
+
+__device__ __forceinline__ __nv_bfloat162 as_bf16x2(const uint32_t &w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); }
 
 // The items of this CTA, as the roles that do not find them read them.
 struct Walk {
@@ -366,7 +376,7 @@ struct Walk {
         // through a shuffle, so that the compiler knows the values to be the same in all lanes: loops and descriptors
         // that hang on them then stay in uniform registers (8,192 rows of 64 heads
         // over 8 key heads: 768 us without it, 652 with)
-        const int *src = reinterpret_cast<const int *>(&c.item[b]);
+        const int *src = reinterpret_cast<const int *>(&c.item[count & 3]);
         int *dst = reinterpret_cast<int *>(&x);
         const int mine = src[min(lane, (int)(sizeof(Item) / 4) - 1)];
 #pragma unroll
@@ -377,6 +387,131 @@ struct Walk {
     }
 };
 
+// Two neighbouring bf16 values.
+__device__ __forceinline__ uint32_t load2(const uint16_t *at) {
+    uint32_t v;
+    asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(at));
+    return v;
+}
+
+// ---- outputs made again ----
+// P is 0 where the mask hides a key, but 0 times a NaN or an infinity is NaN: a value that is not finite reaches every row of a
+// query tile that its key tile is multiplied with.  Rows that do not see it get the columns that it spoilt from here, in
+// fp32 from the tensors themselves: a warp a row, eight keys at once, the row's maximum and sum as they are.  `rows`: the
+// warp's rows whose outputs hold a NaN; m and l: a row's, a lane each.
+// It runs only then, at some 600 cycles a key and row: a NaN in the last value row of 4,096 rows of 64 heads costs 41 ms,
+// NaN everywhere 0.9 (a row that sees a NaN among its last keys stays).  Looking for such rows costs outputs 0 to 4%, of some split
+// calls up to 8 (40 prompts of 300 rows 220 -> 227 us, 4,096 rows 216 -> 218).  Instead of it, a look by a warp of its own through
+// the tiles that the mask cuts, before their use: 254 us; the whole item again after such a look: 264, for the longer code that all
+// roles go through.
+template <int DQK, int DV>
+__device__ __forceinline__ void make_again(const Params &p, const Item &x, int w, int row0, uint32_t rows, float m, float l) {
+    constexpr int V = DV / 32;   // a lane's columns
+    const int lane = (int)threadIdx.x & 31, from = x.c0 * BN, stop = x.stop();
+    const uint16_t *vals = p.mv.p + (int64_t)x.krow * p.mv.row + x.h * p.mv.head + lane * V;
+    auto value = [&](int j, uint32_t (&v)[V]) {   // fp32 bits of key j's
+        uint32_t u[V / 2];
+        if (V == 4) {
+            const uint2 two = __ldg(reinterpret_cast<const uint2 *>(vals + j * p.mv.row));
+            u[0] = two.x, u[V / 2 - 1] = two.y;
+        } else {
+            u[0] = __ldg(reinterpret_cast<const uint32_t *>(vals + j * p.mv.row));
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[k] = k & 1 ? u[k / 2] & 0xFFFF0000u : u[k / 2] << 16;
+    };
+    auto sees = [&](int r, int &tok) {   // keys of these tiles that row r sees, behind the last one
+        tok = (row0 + r) / p.G + (x.pair ? w * p.tpt : 0);
+        return max(from, min(stop, x.seen(p, tok + 1)));
+    };
+    // Of each column: the last value that is not finite and the first NaN, from two tiles before the first row's last key on.
+    int bad[V], nan[V], tok;
+#pragma unroll
+    for (int k = 0; k < V; ++k) bad[k] = -1, nan[k] = INT_MAX;
+#pragma unroll 4
+    for (int j = max(from, sees(__ffs(rows) - 1, tok) - 2 * BN); j < stop; ++j) {
+        uint32_t v[V];
+        value(j, v);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const uint32_t size = v[k] & 0x7FFFFFFFu;
+            if (size >= 0x7F800000u) bad[k] = j;
+            if (size > 0x7F800000u) nan[k] = min(nan[k], j);
+        }
+    }
+#pragma unroll 1
+    for (; rows; rows &= rows - 1) {
+        const int r = __ffs(rows) - 1, upto = sees(r, tok);
+        uint32_t again = 0;   // a bit a column: spoilt by a value that the row does not see, and no NaN before that it sees
+#pragma unroll
+        for (int k = 0; k < V; ++k) again |= (uint32_t)(bad[k] >= upto && nan[k] >= upto) << k;
+        if (!__any_sync(0xffffffffu, again != 0)) continue;
+        const float mr = __shfl_sync(0xffffffffu, m, r), lr = __shfl_sync(0xffffffffu, l, r), cl = p.scale_log2;
+        const float mc = mr == -INFINITY ? 0.f : mr * cl;
+        const int head = x.h * p.G + (row0 + r) % p.G;
+        const int64_t token = (int64_t)x.qrow + tok;
+        constexpr int B = DQK / BOX;   // a lane has two neighbouring values of each box
+        const uint16_t *keys = p.mk.p + (int64_t)x.krow * p.mk.row + x.h * p.mk.head + 2 * lane;
+        const uint16_t *last = p.has_kr ? p.mkr.p + (int64_t)x.krow * p.mkr.row + 2 * lane : keys + (B - 1) * BOX;
+        const int64_t last_row = p.has_kr ? p.mkr.row : p.mk.row;
+        uint32_t q[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) q[i] = load2(p.mq.p + token * p.mq.row + head * p.mq.head + i * BOX + 2 * lane);
+        float acc[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] = 0.f;
+        // the keys' loads in flight together, then the values' (asm volatile: they are not moved to their uses)
+        constexpr int N = 8;
+#pragma unroll 1
+        for (int j0 = from; j0 < upto; j0 += N) {
+            uint32_t u[N][B];
+            float e[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int j = min(j0 + i, upto - 1);
+#pragma unroll
+                for (int d = 0; d < B; ++d) u[i][d] = load2(d + 1 < B ? keys + j * p.mk.row + d * BOX : last + j * last_row);
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                e[i] = 0.f;
+#pragma unroll
+                for (int d = 0; d < B; ++d) {
+                    e[i] = fmaf(__uint_as_float(u[i][d] << 16), __uint_as_float(q[d] << 16), e[i]);
+                    e[i] = fmaf(__uint_as_float(u[i][d] & 0xFFFF0000u), __uint_as_float(q[d] & 0xFFFF0000u), e[i]);
+                }
+            }
+            uint32_t v[N][V / 2];
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int k = 0; k < V / 2; ++k) v[i][k] = load2(vals + min(j0 + i, upto - 1) * p.mv.row + 2 * k);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                for (int i = 0; i < N; ++i) e[i] += __shfl_xor_sync(0xffffffffu, e[i], o);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float f = ptx::ex2(fmaf(e[i], cl, -mc));
+                if (j0 + i < upto) {
+#pragma unroll
+                    for (int k = 0; k < V; ++k)
+                        acc[k] = fmaf(f, __uint_as_float(k & 1 ? v[i][k / 2] & 0xFFFF0000u : v[i][k / 2] << 16), acc[k]);
+                }
+            }
+        }
+        const float inv = lr == 0.f ? 0.f : 1.f / lr;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            if (!(again >> k & 1)) continue;
+            const int col = lane * V + k;
+            if (x.slot >= 0) p.part[(((int64_t)x.slot + w) * BM + row0 + r) * DV + col] = acc[k];
+            else p.out[token * p.out_row + head * p.out_head + col] = (uint16_t)ptx::pack_bf16x2(acc[k] * inv, 0.f);
+        }
+        __syncwarp();
+    }
+}
+
 template <int DQK, int DV>
 __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constant__ Params p) {
     using L = Lay<DQK, DV>;
@@ -386,7 +521,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
 
     ptx::griddep_launch_dependents();
     if (threadIdx.x == 0) {
-        c.abort = 0;
+        c.abort = c.busy = 0;
         for (int i = 0; i < L::U; ++i) ptx::mbar_init(&c.full[i], 1), ptx::mbar_init(&c.free[i], 1);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&c.q_full[i], 1);
@@ -636,7 +771,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                 }
                 const uint32_t np = w ? np1 : np0, no = w ? no1 : no0;
                 if (alone) {
-                    const long long t0 = clock64();
+                    long long t0 = clock64();
                     for (uint32_t spins = 1; !look(&c.p_full[w], np & 1); ++spins) {
                         start_next(j);
                         if ((spins & 1023u) == 0 && expired(t0, 1ll << 31, &c.abort, p.err, 62)) return false;
@@ -855,6 +990,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                 uint16_t *out = p.out + orow * p.out_row + head * p.out_head;
                 const int64_t slot = (int64_t)x.slot + w;
                 float *part = p.part + (slot * BM + row) * DV;
+                __nv_bfloat162 nil = __float2bfloat162_rn(0.f);   // sums of products of outputs: NaN where one of them is
 #pragma unroll 1
                 for (int q = 0; q < DV; q += 16) {
                     uint32_t o[16];
@@ -879,6 +1015,8 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                         uint32_t v[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) v[i] = ptx::pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2) nil = __hfma2(as_bf16x2(v[i]), as_bf16x2(v[i + 1]), nil);
                         if (p.out32) {
                             store32(out + q, v);
                         } else {
@@ -891,6 +1029,9 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                             uint32_t v[8];
 #pragma unroll
                             for (int k = 0; k < 8; ++k) v[k] = o[i + k];
+#pragma unroll
+                            for (int k = 0; k < 8; k += 4)   // the upper halves are NaN where the whole is
+                                nil = __hfma2(as_bf16x2(__byte_perm(v[k], v[k + 1], 0x7632)), as_bf16x2(__byte_perm(v[k + 2], v[k + 3], 0x7632)), nil);
                             store32(part + q + i, v);
                         }
                     }
@@ -903,6 +1044,17 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                         reinterpret_cast<float2 *>(p.part + p.slots * BM * DV)[slot * BM + row] = make_float2(m, l);
                     else if (p.lse)
                         p.lse[orow * p.H + head] = l == 0.f ? -INFINITY : (m * cl + log2f(l)) * 0.69314718055994531f;
+                }
+                const uint32_t spoilt = __ballot_sync(0xffffffffu, __hisnan(__low2bfloat16(nil)) || __hisnan(__high2bfloat16(nil)));
+                if (spoilt && p.causal) {
+                    Item y;   // again, so that what only this needs takes no registers of the others
+                    const int *src = reinterpret_cast<const int *>(&c.item[(it.count - 1) & 3]);
+                    int *dst = reinterpret_cast<int *>(&y);
+#pragma unroll
+                    for (int k = 0; k < (int)(sizeof(Item) / 4); ++k) dst[k] = *const_cast<const volatile int *>(src + k);
+                    if (lane == 0) atomicAdd(&c.busy, 1);
+                    make_again<DQK, DV>(p, y, w, (warp & 3) * 32, spoilt, m, l);
+                    if (lane == 0) atomicAdd(&c.busy, -1);
                 }
             }
             if (!ok) break;
@@ -917,7 +1069,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
             x.decode(p, i);
             if (count >= 2 && !wait(&c.item_free[count & 1], (count / 2 - 1) & 1, &c.abort, p.err, 51)) break;
             if (lane == 0) {
-                c.item[count & 1] = x;
+                c.item[count & 3] = x;
                 ptx::mbar_arrive(&c.item_full[count & 1]);
             }
             if (i < 0) break;
@@ -1189,6 +1341,12 @@ int launch_prompt_attend(tf_kvpool *pool, const int64_t *h_nq, const int64_t *h_
         else if (!map(&p.kr, d_kr, kr_row, 64, 64, 1, keys, 1, BN)) return TF_E_CUDA;
     } else {
         p.k = p.kr = p.v = p.q;   // nothing is loaded through them
+    }
+    p.mq = {static_cast<const uint16_t *>(q->d_p), q->row, q->head};
+    if (keys > 0) {
+        p.mk = {static_cast<const uint16_t *>(k->d_p), k->row, k->head};
+        p.mkr = {static_cast<const uint16_t *>(d_kr), kr_row, 0};
+        p.mv = {static_cast<const uint16_t *>(v->d_p), v->row, v->head};
     }
     p.out = static_cast<uint16_t *>(out->d_p);
     p.out_row = out->row;

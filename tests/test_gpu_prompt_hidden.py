@@ -1,9 +1,13 @@
 """Attention of packed prompts: what a causal row does not see, NaN and infinities included, does not reach it.
 
-The expectation follows from the definition: a row that does not see a key keeps the bits of its output and lse,
-whatever key and value are; a row that sees it has, in the value's column, what the sum of positive weights times the
-values gives (NaN for a NaN or infinities of both signs, else the infinity; a weight below fp32's range times an infinity
-is NaN, which the tests' scores do not come near), and keeps the bits of its other columns.
+The expectation follows from the definition: a row that does not see a key keeps its output and lse, whatever key and
+value are; a row that sees it has, in the value's column, what the sum of positive weights times the values gives (NaN for
+a NaN or infinities of both signs, else the infinity; a weight below fp32's range times an infinity is NaN, which the
+tests' scores do not come near).  Bits stay but for one case: where a row does not see a value, but the last row of its
+query tile (128 rows: tokens times the heads of a key head) sees one of its 128-key tile or of a later one, the value's
+column may be rounded in another way.
+Both results are then within (u + 2^-10) sum p|v| + u |ref| of the definition (u = 2^-8; test_gpu_prompt.py has the reasons;
+2^-10 is far above the scores' and sums' errors of these inputs), so within 4.5 u sum p|v| of each other.
 """
 import numpy as np
 import pytest
@@ -61,6 +65,21 @@ def sees(nq, nk, s, key):
     return rows
 
 
+def share_a_tile(nq, nk, s, key, G):
+    """Rows of the packed call whose query tile is multiplied with the key's tile."""
+    off, per = sum(nq[:s]), 128 // G
+    rows = torch.zeros(sum(nq), dtype=torch.bool)
+    for i in range(nq[s]):
+        last = min(nq[s], (i // per + 1) * per) - 1
+        rows[off + i] = key < -(-max(0, nk[s] - nq[s] + last + 1) // 128) * 128
+    return rows
+
+
+def close(got, clean, size):
+    """Outputs that are rounded in another way; `size`: those of |v|, about sum p|v|."""
+    return ((got.float() - clean.float()).abs() <= 4.5 * 2.0 ** -8 * size.float()).all()
+
+
 def expected(pairs):
     """The sum of positive weights times (value or None): NaN, an infinity, or None where all are finite."""
     v = [x for x in pairs if x is not None]
@@ -74,6 +93,7 @@ def expected(pairs):
 def test_a_value_reaches_the_rows_that_see_it(pool, nq, nk, H, Hkv, dqk, dv, kr):
     q, k, v, rot = make(nq, nk, H, Hkv, dqk, dv, kr, seed=31)
     clean, lclean = call(pool, nq, nk, q, k, v, kr=rot)
+    size, _ = call(pool, nq, nk, q, k, v.abs(), kr=rot)
     G, h = H // Hkv, Hkv - 1
     s = len(nq) // 2 if len(nq) > 1 else 0
     base = sum(nk[:s])
@@ -86,7 +106,9 @@ def test_a_value_reaches_the_rows_that_see_it(pool, nq, nk, H, Hkv, dqk, dv, kr)
         assert torch.equal(lse, lclean)                       # (NaN compares unequal: there is none)
         seen = sees(nq, nk, s, key)
         changed = torch.tensor(bits(out) != bits(clean))
-        assert not changed[~seen].any(), key
+        near = share_a_tile(nq, nk, s, key, G) & ~seen
+        assert not changed[~seen & ~near].any(), key
+        assert close(out[near], clean[near], size[near]), key
         assert not changed[:, :h * G].any()
         for c in range(dv):
             if c not in kinds:
@@ -102,6 +124,7 @@ def test_several_values_at_once(pool, nq, nk, H, Hkv, dqk, dv, kr):
     """Every later half of a column's values not finite, and infinities of both signs met one after another."""
     q, k, v, rot = make(nq, nk, H, Hkv, dqk, dv, kr, seed=32)
     clean, lclean = call(pool, nq, nk, q, k, v, kr=rot)
+    size = call(pool, nq, nk, q, k, v.abs(), kr=rot)[0].float().cpu()
     G = H // Hkv
     y = v.clone()
     marks = {}                                                # (stream, column) -> [(key, value)]
@@ -114,13 +137,13 @@ def test_several_values_at_once(pool, nq, nk, H, Hkv, dqk, dv, kr):
             marks[s, c] = dict(keys).items()
     out, lse = call(pool, nq, nk, q, k, y, kr=rot)
     assert torch.equal(lse, lclean)
-    want, got, ref = torch.zeros(sum(nq), dv), out[:, :G].float().cpu(), clean[:, :G].float().cpu()
+    got, ref = out[:, :G].float().cpu(), clean[:, :G].float().cpu()
     for (s, c), keys in marks.items():
         off = sum(nq[:s])
         for i in range(nq[s]):
             e = expected([x for j, x in keys if j < nk[s] - nq[s] + i + 1])
             g = got[off + i, :, c]
-            assert torch.equal(g, ref[off + i, :, c]) if e is None else torch.isnan(g).all() if e != e else (g == e).all(), (s, i, c, e)
+            assert close(g, ref[off + i, :, c], size[off + i, :G, c]) if e is None else torch.isnan(g).all() if e != e else (g == e).all(), (s, i, c, e)
     other = [c for c in range(dv) if c not in (1, 2, dv - 2)]
     assert np.array_equal(bits(out[..., other]), bits(clean[..., other])) and np.array_equal(bits(out[:, G:]), bits(clean[:, G:]))
 
@@ -149,6 +172,7 @@ def test_many_items_and_long_ones(pool):
     H = 40
     q, k, v, rot = make(nq, nk, H, H, 192, 128, True, seed=34)
     clean, lclean = call(pool, nq, nk, q, k, v, kr=rot)
+    size, _ = call(pool, nq, nk, q, k, v.abs(), kr=rot)
     y = v.clone()
     bad = [(0, 0, 511), (2, 7, 200), (4, 39, 2099), (4, 3, 300), (4, 3, 1500), (5, 20, 128), (7, 11, 129)]
     first = {}
@@ -163,7 +187,12 @@ def test_many_items_and_long_ones(pool):
         assert torch.equal(lse, lclean)
         assert torch.equal(torch.isnan(out[..., 77]).cpu(), want)
         changed = torch.tensor(bits(out) != bits(clean))
-        assert torch.equal(changed[..., 77], want) and not changed[..., :77].any() and not changed[..., 78:].any()
+        assert not changed[..., :77].any() and not changed[..., 78:].any()
+        near = torch.zeros_like(want)
+        for s, h, key in bad:
+            near[:, h] |= share_a_tile(nq, nk, s, key, 1)
+        assert not changed[..., 77][~near].any()
+        assert close(out[..., 77].cpu()[~want], clean[..., 77].cpu()[~want], size[..., 77].cpu()[~want])
 
 
 def test_values_without_a_mask(pool):
@@ -177,3 +206,22 @@ def test_values_without_a_mask(pool):
     changed = torch.tensor(bits(out) != bits(clean))
     assert changed[:70, 1, 5:7].all() and changed.sum() == 140
     assert torch.isnan(out[:70, 1, 5]).all() and (out[:70, 1, 6] == INF).all()
+
+
+def test_a_row_made_again_over_many_keys(pool):
+    """Rows that are made again over 131,072 keys take longer than the kernel's other waits are allowed to: those know."""
+    n = m = 131072
+    H = 8
+    assert B.tf_prompt_plan_info([n], [m], H, H, 192, 128, sms=152)["splits"] == 1
+    q, k, v, rot = make([n], [m], H, H, 192, 128, True, seed=36)
+    clean, lclean = call(pool, [n], [m], q, k, v, kr=rot)
+    size = call(pool, [128], [m], q[-128:], k, v.abs(), kr=rot)[0]
+    v[m - 1, 3, 64] = NAN
+    out, lse = call(pool, [n], [m], q, k, v, kr=rot)
+    assert torch.equal(lse, lclean)
+    nan = torch.isnan(out)
+    assert nan.sum() == 1 and nan[n - 1, 3, 64]
+    changed = out.view(torch.int16) != clean.view(torch.int16)
+    assert not changed[:-128].any() and not changed[:, :3].any() and not changed[:, 4:].any()
+    assert not changed[..., :64].any() and not changed[..., 65:].any()
+    assert close(out[-128:-1, 3, 64], clean[-128:-1, 3, 64], size[:-1, 3, 64])
