@@ -877,6 +877,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             if (k + i >= limit) v[i] = 0xFF800000u;
+                        __syncwarp();
                         tmem_st16(ts + k, v);
                     }
                     ptx::tmem_st_wait();
@@ -896,6 +897,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                         m = top;
                         l *= f;
                     }
+                    __syncwarp();   // loads from TMEM are a whole warp's
                     if (j > 0) {   // O up to the tile before: its products are done, S of this one came after them
 #pragma unroll 1
                         for (int q = 0; q < DV; q += 32) {
@@ -994,6 +996,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
 #pragma unroll 1
                 for (int q = 0; q < DV; q += 16) {
                     uint32_t o[16];
+                    __syncwarp();   // after rows that are not live
                     if (x.n(w) > 0) {
                         tmem_ld16(to + w * DV + q, o);
                         ptx::tmem_ld_wait();
