@@ -142,7 +142,9 @@ int tf_paged_read(tf_kvpool *pool, int32_t cache, const int32_t *d_pt, int32_t m
  * product (relative 2^-8 each, as in tf_paged_mla_attend).  Work is dealt out by the batch's sizes, so a row's bits
  * may differ (within rounding) between batches, and are the same on every call of one batch.  Keys are summed in parts
  * of 131,072 at most (the tensor cores' sums are cut, not rounded, and lose up to 2^-10 over one) that fp32 joins: longer
- * streams need a workspace.
+ * streams need a workspace.  On a TF_POOL_BATCH_INVARIANT pool keys are split there alone, so that a stream has the same
+ * bits whatever else is in the batch (a few rows over a long context are slower: one SM a key head); the workspace is as
+ * on other pools or smaller, and tf_prompt_plan_info tells of the others.
  * What other streams hold, NaN included, never reaches a stream's outputs, and a NaN or infinity among its own keys or
  * values reaches no row that does not see it: bits stay, but for the column of a value that is not finite in rows of the
  * same 128-row query tile, which are made again and may be rounded in another way (slowly: a microsecond for some three

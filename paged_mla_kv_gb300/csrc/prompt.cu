@@ -1158,14 +1158,14 @@ __global__ void __launch_bounds__(128) prompt_combine_kernel(const __grid_consta
 
 // ---- the plan ----
 // Fills in what depends on the lengths.  Streams' keys are split where there are fewer items than SMs to
-// take them.
+// take them; with `invariant` only where a stream is longer than an item may be, at places that hang on nothing else.
 struct Plan {
     int64_t items = 0, slots = 0;
     int splits = 1;
 };
 
 static int plan(Params &p, const int64_t *h_nq, const int64_t *h_nk, int S, int H, int Hkv, int dqk, int dv, int causal,
-                int sms, Plan *out) {
+                int sms, bool invariant, Plan *out) {
     const int G = H / Hkv, tpt = BM / G;
     p.H = H;
     p.Hkv = Hkv;
@@ -1198,7 +1198,7 @@ static int plan(Params &p, const int64_t *h_nq, const int64_t *h_nk, int S, int 
     most = std::min<int64_t>(most, LONGEST);
     int64_t chunk = most;
     double best = 1e300, whole = 0;
-    for (int64_t c = most; c >= 1; c = c > 16 ? c - c / 8 : c - 1) {
+    for (int64_t c = most; c >= 1 && !invariant; c = c > 16 ? c - c / 8 : c - 1) {
         int64_t cnt = 0, load = 0, longest = 0, tail = 0;
         bool split = false;
         for (int i = n - 1; i >= 0; --i) {
@@ -1281,7 +1281,7 @@ int prompt_plan(const int64_t *h_nq, const int64_t *h_nk, int S, int H, int Hkv,
                 tf_prompt_plan *info, size_t *bytes) {
     prm::Plan pl;
     if (sms <= 0) sms = prompt_sms();
-    const int rc = prm::plan(prompt_params(), h_nq, h_nk, S, H, Hkv, dqk, dv, causal, std::min(sms, prm::MAX_SMS), &pl);
+    const int rc = prm::plan(prompt_params(), h_nq, h_nk, S, H, Hkv, dqk, dv, causal, std::min(sms, prm::MAX_SMS), false, &pl);
     if (rc != TF_OK) return rc;
     if (info) {
         info->items = pl.items;
@@ -1313,7 +1313,8 @@ int launch_prompt_attend(tf_kvpool *pool, const int64_t *h_nq, const int64_t *h_
         if (!ok) cudaGetLastError();
         return ok;
     });
-    const int rc = plan(p, h_nq, h_nk, S, H, Hkv, dqk, dv, causal, sms ? *sms : prompt_sms(), &pl);
+    const bool invariant = (pool->desc.flags & TF_POOL_BATCH_INVARIANT) != 0;   // never more slots than by default
+    const int rc = plan(p, h_nq, h_nk, S, H, Hkv, dqk, dv, causal, sms ? *sms : prompt_sms(), invariant, &pl);
     if (rc != TF_OK) return rc;
     const size_t need = ws_bytes_of(pl, dv);
     if (need > 0 && (!d_ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0))
