@@ -83,7 +83,7 @@ int tf_rope_make(const tf_rope_desc *desc, tf_rope *out);
  * Row j's head h starts at d_x + j * x_row + h * x_head (bf16 values; strides in values) and goes to
  * d_y + j * y_row + h * y_head; other values of y are left alone, so a part of a head is turned by pointers to
  * that part.  y may be x with the same strides (in place); it must not overlap x otherwise.  Strides may have
- * any sign and order as long as y's heads do not overlap each other.
+ * any sign and order as long as y's heads do not overlap each other (TF_E_ARG).
  * Errors: TF_E_ARG for a null pointer, a table not made by tf_rope_make, S outside [1, TF_MAX_STREAMS], H
  * outside [1, TF_MAX_HEADS], a negative h_n, or a pointer or stride that is not a multiple of 8 values;
  * TF_E_RANGE for a negative position or one past INT32_MAX; TF_E_UNSUPPORTED for more than 2^31 - 1 rows.  No rows:
@@ -119,7 +119,7 @@ int tf_paged_append_rope(tf_kvpool *pool, int32_t cache, const int32_t *d_pt, in
  * Rows h_from[s] .. h_from[s] + h_n[s] - 1 of every stream, packed: row j's 512 latent values go to
  * d_latent + j * lat_stride and its 64 rope values to d_rope + j * rope_stride (bf16; strides in values).
  * Either pointer may be NULL (that part is not read).  BF16 pages: the stored bits.  FP8 pages: bf16(code * scale),
- * as attention takes them.  Values between the rows are left alone.  A table entry outside the pool is recorded
+ * as attention takes them.  Values between the rows are left alone; the two outputs must not overlap each other.  A table entry outside the pool is recorded
  * as TF_E_DEVICE and its rows are left alone.
  * Errors: TF_E_ARG for a null pool or host array, both outputs NULL, S outside [1, TF_MAX_STREAMS], max_pages < 1, a negative
  * h_n, an output that is not 16-byte aligned or a stride that is not a multiple of 8 and at least 512 (64); TF_E_RANGE for a cache outside the
@@ -149,6 +149,7 @@ int tf_paged_read(tf_kvpool *pool, int32_t cache, const int32_t *d_pt, int32_t m
  * values reaches no row that does not see it: bits stay, but for the column of a value that is not finite in rows of the
  * same 128-row query tile, which are made again and may be rounded in another way (slowly: a microsecond for some three
  * keys of a row).  A row that sees a value that is not finite has NaN in its column, or that infinity.
+ * out's rows and heads may lie in any order but must not overlap each other (TF_E_ARG), nor anything that the call reads.
  * d_ws: tf_prompt_workspace_bytes(...) bytes, 256-byte aligned (NULL if that is 0): partial sums of streams whose
  * keys are split.  Not to be shared by calls that may run at the same time.
  * pool: its device error word takes what a kernel records (a wait that ran out); its pages are not read.

@@ -65,6 +65,19 @@ static int packed_checks(const int64_t *h_pos, const int64_t *h_n, int32_t S, in
 
 static bool unaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
+// Whether two of rows x heads blocks of `width` values, at r * row + h * head, have a value in common.
+static bool overlap(int64_t rows, int64_t row, int64_t heads, int64_t head, int64_t width) {
+    using wide = __int128;
+    const wide a = row < 0 ? -(wide)row : row, b = head < 0 ? -(wide)head : head;
+    if ((rows > 1 && a < width) || (heads > 1 && b < width)) return true;
+    if (rows <= 1 || heads <= 1 || a >= b * (heads - 1) + width || b >= a * (rows - 1) + width) return false;
+    // heads and rows that lie among one another: the rows nearest to each distance of two heads
+    for (int64_t h = 1; h < heads; ++h)
+        for (wide r = b * h / a, last = r + 1; r <= last; ++r)
+            if (r < rows && r * a - b * h < width && b * h - r * a < width) return true;
+    return false;
+}
+
 extern "C" int tf_rope_apply(const tf_rope *rope, const int64_t *h_pos, const int64_t *h_n, int32_t S, int32_t H,
                              const void *d_x, int64_t x_row, int64_t x_head, void *d_y, int64_t y_row, int64_t y_head,
                              void *stream) {
@@ -74,7 +87,7 @@ extern "C" int tf_rope_apply(const tf_rope *rope, const int64_t *h_pos, const in
     const int rc = packed_checks(h_pos, h_n, S, (int64_t)INT32_MAX + 1, &n);
     if (rc != TF_OK) return rc;
     if (n == 0) return TF_OK;
-    if (!d_x || !d_y || unaligned(d_x) || unaligned(d_y)) return TF_E_ARG;
+    if (!d_x || !d_y || unaligned(d_x) || unaligned(d_y) || overlap(n, y_row, H, y_head, rope->dim)) return TF_E_ARG;
     return no_throw([&] { return launch_rope(rope, h_pos, h_n, S, H, d_x, x_row, x_head, d_y, y_row, y_head, (cudaStream_t)stream); });
 }
 
@@ -177,7 +190,7 @@ extern "C" int tf_prompt_attend(tf_kvpool *p, const int64_t *h_nq, const int64_t
     if (keys > 0 && (bad_view(k->d_p, k->row, k->head, Hkv) || bad_view(v->d_p, v->row, v->head, Hkv) ||
                      (d_kr && bad_view(d_kr, kr_row, 8, 1))))
         return TF_E_ARG;
-    if (!out->d_p || unaligned(out->d_p) || out->row % 8 != 0 || out->head % 8 != 0) return TF_E_ARG;
+    if (!out->d_p || unaligned(out->d_p) || out->row % 8 != 0 || out->head % 8 != 0 || overlap(rows, out->row, H, out->head, dv)) return TF_E_ARG;
     return no_throw([&] {
         return launch_prompt_attend(p, h_nq, h_nk, S, H, Hkv, dqk, dv, q, k, keys > 0 ? d_kr : nullptr, kr_row, v, scale, causal, out,
                                     d_lse, d_ws, ws_bytes, (cudaStream_t)stream);
