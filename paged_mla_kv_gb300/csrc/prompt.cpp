@@ -180,14 +180,14 @@ extern "C" int tf_prompt_attend(tf_kvpool *p, const int64_t *h_nq, const int64_t
                                 int32_t dqk, int32_t dv, const tf_heads *q, const tf_heads *k, const void *d_kr,
                                 int64_t kr_row, const tf_heads *v, float scale, int32_t causal, const tf_heads *out,
                                 float *d_lse, void *d_ws, size_t ws_bytes, void *stream) {
-    if (!p || !q || !k || !v || !out || !(scale > 0.0f) || !std::isfinite(2.0f * scale)) return TF_E_ARG;
+    if (!p || !(scale > 0.0f) || !std::isfinite(2.0f * scale)) return TF_E_ARG;
     int64_t rows = 0, keys = 0;
     const int rc = prompt_checks(h_nq, h_nk, S, H, Hkv, dqk, dv, causal, &rows, &keys);
     if (rc != TF_OK) return rc;
     if (d_kr && dqk == 64) return TF_E_UNSUPPORTED;
     if (rows == 0) return TF_OK;
-    if (bad_view(q->d_p, q->row, q->head, H)) return TF_E_ARG;
-    if (keys > 0 && (bad_view(k->d_p, k->row, k->head, Hkv) || bad_view(v->d_p, v->row, v->head, Hkv) ||
+    if (!q || !out || bad_view(q->d_p, q->row, q->head, H)) return TF_E_ARG;
+    if (keys > 0 && (!k || !v || bad_view(k->d_p, k->row, k->head, Hkv) || bad_view(v->d_p, v->row, v->head, Hkv) ||
                      (d_kr && bad_view(d_kr, kr_row, 8, 1))))
         return TF_E_ARG;
     if (!out->d_p || unaligned(out->d_p) || out->row % 8 != 0 || out->head % 8 != 0 || overlap(rows, out->row, H, out->head, dv)) return TF_E_ARG;
