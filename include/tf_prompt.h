@@ -107,7 +107,7 @@ int tf_rope_apply(const tf_rope *rope, const int64_t *h_pos, const int64_t *h_n,
  * The same row of a stream must not be written twice in a call (streams that share a page).  A table entry outside
  * the pool is recorded as TF_E_DEVICE and its rows are skipped.
  * Errors: TF_E_ARG for a null pool or host array, S outside [1, TF_MAX_STREAMS], max_pages < 1, a negative
- * h_n, null or unaligned rows (16 bytes; row_stride a multiple of 8 and at least 576) or gain (16 bytes), a table not
+ * h_n, a page table that is not 4-byte aligned, null or unaligned rows (16 bytes; row_stride a multiple of 8 and at least 576) or gain (16 bytes), a table not
  * made by tf_rope_make or of another dim, with a gain an eps that is not a finite number > 0; TF_E_RANGE for a cache outside the pool, a
  * position outside the table or past INT32_MAX, or a NULL table wider than the pool; TF_E_UNSUPPORTED for more than 2^31 - 1 rows.
  * No rows: nothing is launched. */
@@ -122,7 +122,7 @@ int tf_paged_append_rope(tf_kvpool *pool, int32_t cache, const int32_t *d_pt, in
  * as attention takes them.  Values between the rows are left alone; the two outputs must not overlap each other.  A table entry outside the pool is recorded
  * as TF_E_DEVICE and its rows are left alone.
  * Errors: TF_E_ARG for a null pool or host array, both outputs NULL, S outside [1, TF_MAX_STREAMS], max_pages < 1, a negative
- * h_n, an output that is not 16-byte aligned or a stride that is not a multiple of 8 and at least 512 (64); TF_E_RANGE for a cache outside the
+ * h_n, a page table that is not 4-byte aligned, an output that is not 16-byte aligned or a stride that is not a multiple of 8 and at least 512 (64); TF_E_RANGE for a cache outside the
  * pool, rows outside the table or past INT32_MAX, or a NULL table wider than the pool; TF_E_UNSUPPORTED for more than 2^31 - 1 rows.
  * No rows: nothing is launched. */
 int tf_paged_read(tf_kvpool *pool, int32_t cache, const int32_t *d_pt, int32_t max_pages, const int64_t *h_from,
@@ -155,7 +155,7 @@ int tf_paged_read(tf_kvpool *pool, int32_t cache, const int32_t *d_pt, int32_t m
  * pool: its device error word takes what a kernel records (a wait that ran out); its pages are not read.
  * Errors: TF_E_ARG for a null pointer (k, v and kr may be NULL without keys; q and out without rows), S outside [1, TF_MAX_STREAMS],
  * H outside [1, TF_MAX_HEADS], Hkv that does not divide H, negative counts, a scale that is not a number > 0
- * (below 2^127), a causal other than 0 or 1, a pointer that is not 16-byte aligned or a stride that is not a multiple of 8 values, below 1 or
+ * (below 2^127), a causal other than 0 or 1, a pointer that is not 16-byte aligned (d_lse: 4) or a stride that is not a multiple of 8 values, below 1 or
  * above 2^36 (out's strides may be any multiple of 8; so may the head stride of a single head), an unaligned or missing workspace; TF_E_NOMEM for
  * one that is too small; TF_E_UNSUPPORTED for other dqk and dv, with d_kr a dqk of 64, or more than 2^31 - 1 rows, keys or tiles of work. */
 typedef struct {

@@ -63,7 +63,7 @@ static int packed_checks(const int64_t *h_pos, const int64_t *h_n, int32_t S, in
     return *rows > INT32_MAX ? TF_E_UNSUPPORTED : TF_OK;
 }
 
-static bool unaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+static bool unaligned(const void *p, uintptr_t to = 16) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
 // Whether two of rows x heads blocks of `width` values, at r * row + h * head, have a value in common.
 static bool overlap(int64_t rows, int64_t row, int64_t heads, int64_t head, int64_t width) {
@@ -94,7 +94,7 @@ extern "C" int tf_rope_apply(const tf_rope *rope, const int64_t *h_pos, const in
 // What the calls over pages refuse.
 static int paged_checks(const tf_kvpool *p, int32_t cache, const int32_t *d_pt, int32_t max_pages, const int64_t *h_pos,
                         const int64_t *h_n, int32_t S, int64_t *rows) {
-    if (!p || max_pages < 1) return TF_E_ARG;
+    if (!p || max_pages < 1 || unaligned(d_pt, 4)) return TF_E_ARG;
     const int64_t limit = std::min<int64_t>((int64_t)max_pages * kPageRows, (int64_t)INT32_MAX + 1);
     const int rc = packed_checks(h_pos, h_n, S, limit, rows);
     if (rc == TF_E_ARG) return rc;
@@ -180,7 +180,7 @@ extern "C" int tf_prompt_attend(tf_kvpool *p, const int64_t *h_nq, const int64_t
                                 int32_t dqk, int32_t dv, const tf_heads *q, const tf_heads *k, const void *d_kr,
                                 int64_t kr_row, const tf_heads *v, float scale, int32_t causal, const tf_heads *out,
                                 float *d_lse, void *d_ws, size_t ws_bytes, void *stream) {
-    if (!p || !(scale > 0.0f) || !std::isfinite(2.0f * scale)) return TF_E_ARG;
+    if (!p || unaligned(d_lse, 4) || !(scale > 0.0f) || !std::isfinite(2.0f * scale)) return TF_E_ARG;
     int64_t rows = 0, keys = 0;
     const int rc = prompt_checks(h_nq, h_nk, S, H, Hkv, dqk, dv, causal, &rows, &keys);
     if (rc != TF_OK) return rc;
