@@ -709,7 +709,8 @@ def tf_prompt_attend(pool: KVPool, nq, nk, q, k, v, scale: float, out, lse=None,
     rows, H, dqk = q.shape
     keys, Hkv, dv = v.shape
     what = "tf_prompt_attend"
-    if not (len(a) == len(b) and _sum(a) == rows and _sum(b) == keys and (lse is None or _dense(lse, f32, rows * H))):
+    if not (len(a) == len(b) and _sum(a) == rows and _sum(b) == keys and (lse is None or _dense(lse, f32, rows * H)) and
+            (ws is None or ws.is_contiguous())):
         _refuse(what)
     qr, qh = _strides(q, (rows, H, dqk), bf16, what)
     kr_, kh = _strides(k, (keys, Hkv, dqk if kr is None else dqk - 64), bf16, what)
