@@ -30,7 +30,8 @@ constexpr int BM = 128;              // rows of a query tile
 constexpr int BN = 128;              // keys of a tile
 constexpr int BOX = 64;              // values of a box's row: 128 bytes, one swizzle atom
 constexpr int VH = 64;               // keys of a half of a value tile
-// Warps: two softmax warpgroups, one for the outputs, the MMA warp, the TMA warp, and one that finds the next item.
+// Warps: two softmax warpgroups, one for the outputs, the MMA warp (for both warpgroups), the TMA warp, and the item warp, which
+// asks for the next item and works out what it is; the last one does nothing.
 constexpr int THREADS = 512;
 constexpr int OUT_WARP = 8, MMA_WARP = 12, TMA_WARP = 13, ITEM_WARP = 14;
 // Registers a thread: 128 at launch, of which the softmax takes more and the others less.
@@ -121,7 +122,7 @@ struct alignas(16) Item {
     int slot;                // slot of query tile 0, or -1
     int pair;                // two query tiles
 
-    // Item i (-1: none).  Divisions and a search: the TMA warp does it ahead of time and the others read the result.
+    // Item i (-1: none).  Divisions and a search: the item warp does it ahead of time and the others read the result.
     __device__ __forceinline__ void decode(const Params &p, int i) {
         if (i < 0) {
             n0 = n1 = -1;
@@ -182,7 +183,7 @@ struct Ctl {
     uint64_t s_full[2], p_full[2], o_full[2];
     uint64_t ml_full[2], ml_free[2]; // the rows' maxima and sums
     uint64_t o_free[2];              // the sums have been read
-    uint64_t ask, answer;            // the question for another item
+    uint64_t ask, answer;            // time to ask for another item (from the TMA warp); the answer has come
     uint64_t item_full[2], item_free[2];
     uint64_t drain;
     alignas(16) uint4 next;          // the answer
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
     ptx::griddep_wait();
 
     if (warp == TMA_WARP) {
-        // ================= TMA, and the question for the next item =================
+        // ================= TMA; it also says when the next item is to be asked for =================
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
         Ring<L::U> head, tail;     // the next group, the oldest that is not known to be free
         int room = L::U;           // free units
@@ -624,7 +625,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_kernel(const __grid_constan
                 return true;
             };
             if (x.n0 + x.n1 == 0) ask();
-            // in the order in which the MMA warps take them
+            // in the order in which the MMA warp takes them
             if (x.pair) {
                 if (x.n1 > 0) ok = load_q(0) && load_k(x.key_tile(1, 0)) && load_q(1);
                 for (int j = 0; ok && j < x.n1; ++j) {

@@ -194,8 +194,9 @@ __device__ __forceinline__ int page_of(const int32_t *pt, int max_pages, int num
 // One warp a row: lane l has latent values 8l .. 8l + 7 and 256 more of them further on, so that loads and stores are
 // whole lines, and rope pair l.  The row's square sum is added in fp32, 16 values a lane and then across the warp.
 // BF16, 297,264 rows (685 MB): 102 to 103 us, 0.99 of the measured copy rate (bare, without norm and rotation, 97);
-// FP8 (534 MB): 106 us, 0.75: what the codes add to each row's chain (amax, scale, quotients) shows.  Six blocks an
-// SM: 109 and 110 us with five, 113 and 125 with seven, whose registers spill.  Two rows a warp: 104 and 124.
+// FP8 (534 MB): 105 us, 0.75: what the codes add to each row's chain (amax, scale, quotients) shows.  Six blocks an
+// SM: 108 and 111 us with five, 113 and 104 to 113 with seven, which spill some 48 bytes (of the four forms one spills 8 at
+// six).  Two rows a warp: 104 and 124.
 template <bool FP8, bool HALF>
 __global__ void __launch_bounds__(256, 6) append_rope_kernel(const __grid_constant__ AppendParams p) {
     __shared__ uint64_t turns[kRope / 2];
