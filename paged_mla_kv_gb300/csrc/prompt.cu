@@ -425,6 +425,7 @@ __device__ __forceinline__ void make_again(const Params &p, const Item &x, int w
         tok = (row0 + r) / p.G + (x.pair ? w * p.tpt : 0);
         return max(from, min(stop, x.seen(p, tok + 1)));
     };
+    __syncwarp();   // the rows' own threads have written them
     // Of each column: the last value that is not finite and the first NaN, from two tiles before the first row's last key on.
     int bad[V], nan[V], tok;
 #pragma unroll
